@@ -1,0 +1,102 @@
+// gm_loss.h -- shared by the translation units of the losses over a large class
+// table (gm_loss.cu: kernels that read rows and entries, host driver;
+// gm_loss_prod.cu: the tensor-core products).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gm_internal.h"
+#include "gm_losses.h"
+
+namespace gm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Bits of the losses' status word (one a device, read by gm_loss_status).
+enum : int {
+  kLossTimeout = 1,    // a bounded wait inside a kernel gave up
+  kLossBadTarget = 2,  // a target outside [0, n_classes) that is not the ignored one
+  kLossBadTeacher = 4  // a malformed teacher row: see gm_distill_forward
+};
+
+// Products the kernel makes and what it does with a finished tile.
+enum class Prod {
+  kStats,  // Z = H W^T: each row's maximum and sums of exponentials over half a tile's columns
+  kGrad,   // Z = H W^T again: G = dloss/dZ in 16 bits (three planes of bf16 for fp32 operands)
+  kDh,     // G W
+  kDw      // G^T H
+};
+
+// Where a row's target stands.
+struct Targets {
+  const void* t;    // null: no labels
+  bool is64;
+  int64_t ignore;
+  int64_t n_cls;
+};
+
+// What the finished tile of a product is combined with.
+struct ProdArgs {
+  // tiles: m_tiles * n_tiles * splits, in groups of `group` row tiles, the column tiles
+  // of a group one after another, its row tiles innermost
+  int m_tiles, n_tiles, splits, group;
+  int k_blocks;      // blocks of 64 along the summed dimension
+  int k_per_split;   // blocks of a split
+  int planes;        // 1, or 3: each fp32 operand is the sum of three bf16 planes
+  bool bf16;
+  int a_row0, b_row0;  // first row of the operands that are not read from their start (row of the map)
+  int64_t m, n;      // rows and columns of the result
+  int* status;
+  // kStats, kGrad
+  int64_t cls0;      // class of column 0
+  Targets tgt;
+  const int64_t* ent_start;  // teacher: first entry of each row, its entries, their class and probability
+  const int32_t* ent_len;
+  const int2* ents;
+  float inv_t, c_t;  // 1 / T, log2(e) / T
+  float4* part;      // [half tile][row]: max, sum e^(z - max), sum e^((z - max) / T), sum q z
+  int64_t part_ld;
+  float* z_t;        // [row] logit of the target
+  const float4* row_c;  // [row] lse, factor of softmax(z), lse_T, factor of softmax(z / T)
+  const float* row_gl;  // [row] weight of the label
+  const unsigned* g_max;  // f16: bits of the largest |G| possible (null: no scale)
+  uint16_t* g;
+  int64_t g_ld, g_plane;
+  // kDh, kDw
+  float* acc;        // partial sums (null: out is written)
+  int64_t acc_ld, acc_split;
+  bool acc_add;
+  void* out;
+  int64_t out_ld;
+  int out_type;      // GM_LOSS_*
+};
+
+// Scale of G in f16: a power of two that brings the largest |G| possible to at most 2^14.
+__device__ __forceinline__ float g_scale_of(const unsigned* g_max) {
+  if (!g_max) return 1.0f;
+  const float m = __uint_as_float(*g_max);
+  if (!(m > 0.0f) || !(m < 3.0e38f)) return 1.0f;
+  int e;
+  frexpf(m, &e);
+  e = 14 - e;
+  return ldexpf(1.0f, e < -100 ? -100 : e > 100 ? 100 : e);
+}
+
+__device__ __forceinline__ int64_t row_target(const Targets& t, int64_t row) {  // -1: ignored, -2: out of range
+  const int64_t v = t.is64 ? static_cast<const int64_t*>(t.t)[row] : static_cast<const int32_t*>(t.t)[row];
+  return v == t.ignore ? -1 : (v >= 0 && v < t.n_cls) ? v : -2;
+}
+
+struct ProdMaps {
+  CUtensorMap a, b;
+};
+// Box height of the operands' maps (rows of a K-major box; MN-major boxes are 64 by 64).
+int prod_box_rows_a();
+int prod_box_rows_b(int cg, int bn);
+// Launches a product; cg: blocks a tile (1: 128 rows, 2: 256), bn: columns of a tile (64, 128 or 256).
+cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
+                        cudaStream_t s);
+
+}  // namespace gm
