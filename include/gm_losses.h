@@ -24,8 +24,9 @@
  *     (gm_logits, gm_labels, gm_csr, gm_loss_config) are host memory and only read
  *     during the call.
  *   - Work is queued on `stream`; a call does not wait for it unless
- *     GM_LOSS_CHECK is set. Workspace comes through gm_set_allocator's hooks, in
- *     stream order, and is given back before the call returns.
+ *     GM_LOSS_CHECK is set. Workspace is the caller's (gm_loss_config.workspace), or
+ *     comes through gm_set_allocator's hooks, in stream order, and is given back
+ *     before the call returns.
  *   - Every call returns a gm_status; nothing is thrown across the ABI.
  *   - Products are formed on the tensor cores with fp32 sums: bf16 and f16 operands
  *     as they are, f32 operands as three bf16 parts each. Maxima, sums of
@@ -80,13 +81,24 @@ typedef struct gm_loss_config {
   int64_t workspace_cap_bytes; /* bound on the piece of G a backward call holds; 0 = 256 MiB; the
                                   narrowest piece has 256 classes                                */
   int32_t flags;               /* GM_LOSS_CHECK                                                  */
+  void* workspace;             /* device memory for the call, 256-byte aligned (NULL: the hooks); it
+                                  may be reused once the call's work on the stream is done       */
+  int64_t workspace_bytes;     /* at least gm_loss_workspace's answer for the same call          */
 } gm_loss_config;
+
+/* Bytes of workspace a call needs (host only): of gm_xent_* with teacher_nnz < 0, of
+ * gm_distill_* with the teacher's entries; backward: 0 for a forward call, 1 for a
+ * backward one. For callers that own the memory, for example while work is captured
+ * into a CUDA graph. Errors: those of the call's arguments in z and cfg (whose flags and
+ * workspace do not matter), GM_ERR_INVALID_ARG for a NULL bytes. */
+gm_status gm_loss_workspace(const gm_logits* z, int64_t teacher_nnz, int32_t backward, const gm_loss_config* cfg,
+                            int64_t* bytes);
 
 /* loss and lse: device, n_rows floats, both written.
  * Errors: GM_ERR_INVALID_ARG (null or misaligned pointer, size out of range, ld < dim,
  * unknown type or flag), GM_ERR_INDEX_OVERFLOW (n_rows, n_classes or dim above its
- * limit), GM_ERR_OOM, GM_ERR_CUDA (a launch failed, or a CUDA error from earlier work
- * was still pending: left pending, nothing queued); with GM_LOSS_CHECK those of
+ * limit), GM_ERR_OOM, GM_ERR_WORKSPACE (the caller's workspace is too
+ * small), GM_ERR_CUDA (a launch failed, or a CUDA error from earlier work was still pending: left pending, nothing queued); with GM_LOSS_CHECK those of
  * gm_loss_status. */
 gm_status gm_xent_forward(const gm_logits* z, const gm_labels* labels, const gm_loss_config* cfg, void* stream,
                           float* loss, float* lse);

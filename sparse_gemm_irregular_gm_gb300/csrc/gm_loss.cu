@@ -8,8 +8,8 @@
 #include "gm_loss.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
-#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,73 +47,131 @@ __global__ void k_pack(const void* __restrict__ src, int64_t rows, int64_t dim, 
 }
 
 // ---- the teacher's rows -----------------------------------------------------------------
-template <class T>
-__device__ T block_reduce(T x, T* sh, bool maximum) {  // 128 threads; every thread gets the result
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <int W>
+__device__ __forceinline__ float group_max(float x, float* sh) {  // every thread of the W warps gets the result
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const T y = __shfl_xor_sync(kFull, x, d);
-    x = maximum ? (y > x ? y : x) : x + y;
+  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
+  if constexpr (W > 1) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = sh[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) x = fmaxf(x, sh[w]);
   }
-  __syncthreads();
-  if (lane == 0) sh[warp] = x;
-  __syncthreads();
-  x = sh[0];
-  for (int w = 1; w < 4; ++w) x = maximum ? (sh[w] > x ? sh[w] : x) : x + sh[w];
   return x;
 }
+template <int W>
+__device__ __forceinline__ float group_sum(float x, float* sh) {
+  x = warp_reduce_sum(x);
+  if constexpr (W > 1) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = sh[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) x += sh[w];
+  }
+  return x;
+}
+template <int W>
+__device__ __forceinline__ bool group_or(bool x) {
+  if constexpr (W > 1) return __syncthreads_or(x) != 0;
+  else return __any_sync(kFull, x);
+}
 
-// q = softmax of each row's stored values / T, one block a row; base[row] = sum q log q.
+// q = softmax of a row's stored values / T; base[row] = sum q log q. Bound by the latency
+// of a row's loads: a warp a row where rows are short; rows over kLongRow entries are
+// left to the whole block afterwards. The rows of a block lie a grid apart, since long rows
+// of a graph's product are neighbours. fp32: a thread sums a few hundred terms at most, and
+// an fp64 log or sum costs more here than the loads do.
+constexpr int kLongRow = 1024, kTeacherWarps = 32;
+
 template <class V, class R, class C>
-__global__ void __launch_bounds__(128) k_teacher(const R* __restrict__ rp, const C* __restrict__ col,
-                                                 const V* __restrict__ val, int64_t n_rows, int64_t n_cls, int64_t nnz,
-                                                 float inv_t, int64_t* __restrict__ start, int32_t* __restrict__ len,
-                                                 int2* __restrict__ ents, float* __restrict__ base,
-                                                 int* __restrict__ status) {
-  __shared__ double sh_d[4];
-  __shared__ float sh_f[4];
-  for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
-    const int64_t lo = static_cast<int64_t>(rp[row]), hi = static_cast<int64_t>(rp[row + 1]);
-    bool bad = lo < 0 || hi < lo || hi > nnz;
-    float m = -INFINITY;
-    if (!bad) {
-      int wrong = 0;
-      for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-        const int64_t c = static_cast<int64_t>(col[i]);
-        if (c < 0 || c >= n_cls || (i > lo && static_cast<int64_t>(col[i - 1]) >= c)) wrong = 1;
-        m = fmaxf(m, static_cast<float>(val[i] * inv_t));
+struct TeacherArgs {
+  const R* rp;
+  const C* col;
+  const V* val;
+  int64_t n_rows, n_cls, nnz;
+  float inv_t;
+  int64_t* start;
+  int32_t* len;
+  int2* ents;
+  float* base;
+  int* status;
+};
+
+template <int W, class V, class R, class C>
+__device__ __forceinline__ void teacher_row(const TeacherArgs<V, R, C>& a, int64_t row, int64_t lo, int64_t hi,
+                                            float* sh) {
+  constexpr int kGroup = 32 * W;
+  const int lane = threadIdx.x % kGroup;
+  bool bad = lo < 0 || hi < lo || hi > a.nnz;
+  float m = -INFINITY, sum = 0.f, b = 0.f;
+  if (!bad) {
+    bool wrong = false;
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += kGroup) {
+      const int64_t c = static_cast<int64_t>(a.col[i]);
+      if (c < 0 || c >= a.n_cls || (i > lo && static_cast<int64_t>(a.col[i - 1]) >= c)) wrong = true;
+      m = fmaxf(m, static_cast<float>(a.val[i] * a.inv_t));
+    }
+    bad = group_or<W>(wrong);
+    m = group_max<W>(m, sh);
+  }
+  // a NaN value leaves the maximum alone and makes the sum NaN, so the row counts as one with entries
+  if (!bad) {
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += kGroup) {
+      const float v = static_cast<float>(a.val[i] * a.inv_t);
+      sum += v == -INFINITY ? 0.f : expf(v - m);
+    }
+    sum = group_sum<W>(sum, sh);
+  }
+  const bool any = !bad && sum != 0.f;
+  if (any) {
+    const float log_sum = logf(sum), inv = 1.f / sum;
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += kGroup) {
+      const float v = static_cast<float>(a.val[i] * a.inv_t);
+      const float q = v == -INFINITY ? 0.f : expf(v - m) * inv;
+      a.ents[i] = make_int2(static_cast<int>(a.col[i]), __float_as_int(q));
+      if (q > 0.f || q != q) b += q * ((v - m) - log_sum);
+    }
+    b = group_sum<W>(b, sh);
+  }
+  if (lane == 0) {
+    a.start[row] = lo;
+    a.len[row] = any ? static_cast<int32_t>(hi - lo) : 0;
+    a.base[row] = bad ? NAN : b;
+    if (bad) atomicOr(a.status, kLossBadTeacher);
+  }
+}
+
+template <class V, class R, class C>
+__global__ void __launch_bounds__(32 * kTeacherWarps) k_teacher(const TeacherArgs<V, R, C> a) {
+  __shared__ float sh[kTeacherWarps];
+  __shared__ unsigned s_long;
+  const int warp = threadIdx.x >> 5;
+  for (int64_t row0 = blockIdx.x; row0 < a.n_rows; row0 += int64_t(gridDim.x) * kTeacherWarps) {
+    if (threadIdx.x == 0) s_long = 0;
+    __syncthreads();
+    const int64_t row = row0 + int64_t(warp) * gridDim.x;
+    if (row < a.n_rows) {
+      const int64_t lo = static_cast<int64_t>(a.rp[row]), hi = static_cast<int64_t>(a.rp[row + 1]);
+      if (lo >= 0 && hi <= a.nnz && hi - lo > kLongRow) {
+        if ((threadIdx.x & 31) == 0) atomicOr(&s_long, 1u << warp);
+      } else {
+        teacher_row<1>(a, row, lo, hi, sh);
       }
-      bad = __syncthreads_or(wrong) != 0;
-      m = block_reduce(m, sh_f, true);
     }
-    double sum = 0.0, log_sum = 0.0, b = 0.0;
-    // a NaN value leaves the maximum alone and makes the sum NaN, so the row counts as one with entries
-    bool any = false;
-    if (!bad) {
-      for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-        const float v = static_cast<float>(val[i] * inv_t);
-        sum += v == -INFINITY ? 0.0 : static_cast<double>(expf(v - m));
-      }
-      sum = block_reduce(sum, sh_d, false);
-      any = sum != 0.0;
+    __syncthreads();
+    for (unsigned left = s_long; left; left &= left - 1) {
+      const int64_t r = row0 + int64_t(__ffs(left) - 1) * gridDim.x;
+      teacher_row<kTeacherWarps>(a, r, static_cast<int64_t>(a.rp[r]), static_cast<int64_t>(a.rp[r + 1]), sh);
+      __syncthreads();
     }
-    if (any) {
-      log_sum = log(sum);
-      const float inv = static_cast<float>(1.0 / sum);
-      for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-        const float v = static_cast<float>(val[i] * inv_t);
-        const float q = v == -INFINITY ? 0.f : expf(v - m) * inv;
-        ents[i] = make_int2(static_cast<int>(col[i]), __float_as_int(q));
-        if (q > 0.f || q != q) b += static_cast<double>(q) * (static_cast<double>(v) - m - log_sum);
-      }
-      b = block_reduce(b, sh_d, false);
-    }
-    if (threadIdx.x == 0) {
-      start[row] = lo;
-      len[row] = any ? static_cast<int32_t>(hi - lo) : 0;
-      base[row] = bad ? NAN : static_cast<float>(b);
-      if (bad) atomicOr(status, kLossBadTeacher);
-    }
+    __syncthreads();
   }
 }
 
@@ -129,6 +187,7 @@ struct JoinArgs {
   float *loss, *lse, *kl, *lse_t;
   int* status;
 };
+// Bound by the latency of its loads: 4 of them in flight a thread.
 template <int ROWS>  // rows of a block; 256 / ROWS threads a row
 __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   constexpr int kSub = 256 / ROWS;
@@ -146,8 +205,18 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
     }
     m = mn;
   };
-  if (row < a.n_rows)
-    for (int64_t p = sub; p < a.n_parts; p += kSub) add(a.part[p * a.n_rows + row]);
+  if (row < a.n_rows) {
+    const float4* p = a.part + row;
+    int64_t i = sub;
+    for (; i + 3 * kSub < a.n_parts; i += 4 * kSub) {
+      float4 o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[q] = p[(i + q * kSub) * a.n_rows];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) add(o[q]);
+    }
+    for (; i < a.n_parts; i += kSub) add(p[i * a.n_rows]);
+  }
   __shared__ float4 sh[256];
   for (int d = kSub / 2; d > 0; d >>= 1) {
     if (sub >= d && sub < 2 * d) sh[threadIdx.x] = make_float4(m, s1, st, zq);
@@ -171,31 +240,22 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   }
 }
 
-// ---- what the backward pass needs of a row -------------------------------------------------
-__global__ void k_row_grads(int64_t n, Targets tgt, const float* __restrict__ lse, const float* __restrict__ g_loss,
-                            const float* __restrict__ g_lse, const int32_t* __restrict__ ent_len,
-                            const float* __restrict__ lse_t, const float* __restrict__ g_kl, float inv_t,
-                            float4* __restrict__ row_c, float* __restrict__ row_gl, unsigned* __restrict__ g_max,
-                            int* __restrict__ status) {
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; r < n; r += stride) {
-    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-    float gl = 0.f;
-    if (tgt.t) {
-      const int64_t t = row_target(tgt, r);
-      gl = t >= 0 ? g_loss[r] : 0.f;
-      c.x = lse[r];
-      c.y = gl + (g_lse ? g_lse[r] : 0.f);
-      if (t == -2) atomicOr(status, kLossBadTarget);
-    }
-    if (ent_len) {
-      c.z = lse_t[r];
-      c.w = ent_len[r] > 0 ? g_kl[r] * inv_t : 0.f;
-    }
-    row_c[r] = c;
-    row_gl[r] = gl;
-    // no product of the row's weights and probabilities is larger
-    if (g_max) atomicMax(g_max, __float_as_uint(fabsf(c.y) + fabsf(gl) + fabsf(c.w)));
+// ---- scale of G in f16 ------------------------------------------------------------------------
+// Bits of the largest |G| that the rows' weights allow, one block.
+__global__ void __launch_bounds__(1024) k_g_max(int64_t n, const RowGrads r, unsigned* __restrict__ g_max) {
+  float m = 0.f;
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+    const RowCoef c = row_coef(r, i);
+    m = fmaxf(m, fabsf(c.a) + fabsf(c.gl) + fabsf(c.b));
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+  __shared__ float sh[32];
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) m = fmaxf(m, sh[w]);
+    *g_max = __float_as_uint(m);
   }
 }
 
@@ -234,33 +294,65 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
-// 16-bit matrix of `planes` planes of rows x cols, ld elements a row.
+// Matrix of `planes` planes of rows x cols elements of 2 bytes (4: fp32), ld elements a row.
 struct Operand {
-  const uint16_t* p;
+  const void* p;
   int64_t rows, cols, ld, plane;
   int planes;
+  int bytes = 2;
 };
-// Boxes of box_rows rows of 64 elements, 128-byte swizzle; elements outside read as 0.
+// Boxes of box_rows rows of 128 bytes, 128-byte swizzle; elements outside read as 0.
 bool encode(CUtensorMap* m, const Operand& o, int box_rows) {
   const EncodeTiled fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
                               static_cast<cuuint64_t>(o.planes)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2, static_cast<cuuint64_t>(o.plane) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * o.bytes, static_cast<cuuint64_t>(o.plane) * o.bytes};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / o.bytes), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t*>(o.p), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(m, o.bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+            const_cast<void*>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
+constexpr int64_t kMostIndex = (int64_t(1) << 31) - 256;  // tile coordinates are int32
+constexpr int64_t kDefaultCap = int64_t(256) << 20;
+
+struct Call {
+  gm_logits z = {};
+  const gm_csr* teacher = nullptr;  // null: cross entropy alone
+  int64_t nnz = -1;                 // the teacher's entries, -1 without one
+  int32_t value_type = 0, index_type = 0;
+  float temperature = 1.f;
+  const gm_labels* labels = nullptr;
+  int64_t cap = kDefaultCap;
+  int32_t flags = 0;
+  void* workspace = nullptr;
+  int64_t workspace_bytes = 0;
+  cudaStream_t s = nullptr;
+  int sms = 0;
+  int* status = nullptr;
+};
+
 // One workspace block, carved in order.
 struct Arena {
-  DevBuf<unsigned char> buf;
+  DevBuf<unsigned char> buf;  // from the hooks, unless the caller brought memory
+  unsigned char* p = nullptr;
   size_t used = 0;
+  gm_status open(const Call& c) {
+    if (c.workspace) {
+      if (static_cast<int64_t>(used) > c.workspace_bytes) return GM_ERR_WORKSPACE;
+      p = static_cast<unsigned char*>(c.workspace);
+      return GM_OK;
+    }
+    if (!buf.alloc(used, c.s)) return GM_ERR_OOM;
+    p = buf.p;
+    return GM_OK;
+  }
   size_t add(int64_t bytes) {
     const size_t at = used;
     used += static_cast<size_t>(up(bytes, 256));
@@ -268,7 +360,7 @@ struct Arena {
   }
   template <class T>
   T* at(size_t off) const {
-    return reinterpret_cast<T*>(buf.p + off);
+    return reinterpret_cast<T*>(p + off);
   }
 };
 
@@ -280,21 +372,6 @@ struct NvtxRange {
 int64_t elem_bytes(int32_t type) { return type == GM_LOSS_F32 ? 4 : 2; }
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-constexpr int64_t kMostIndex = (int64_t(1) << 31) - 256;  // tile coordinates are int32
-constexpr int64_t kDefaultCap = int64_t(256) << 20;
-
-struct Call {
-  gm_logits z;
-  const gm_csr* teacher;  // null: cross entropy alone
-  int32_t value_type = 0, index_type = 0;
-  float temperature = 1.f;
-  const gm_labels* labels;
-  int64_t cap = kDefaultCap;
-  int32_t flags = 0;
-  cudaStream_t s = nullptr;
-  int sms = 0;
-  int* status = nullptr;
-};
 
 gm_status check(Call& c, const gm_logits* z, const gm_labels* labels, const gm_loss_config* cfg, void* stream) {
   if (!z) return GM_ERR_INVALID_ARG;
@@ -314,6 +391,9 @@ gm_status check(Call& c, const gm_logits* z, const gm_labels* labels, const gm_l
     if (cfg->workspace_cap_bytes < 0 || (cfg->flags & ~GM_LOSS_CHECK)) return GM_ERR_INVALID_ARG;
     if (cfg->workspace_cap_bytes) c.cap = cfg->workspace_cap_bytes;
     c.flags = cfg->flags;
+    if (cfg->workspace && (!aligned(cfg->workspace, 256) || cfg->workspace_bytes < 0)) return GM_ERR_INVALID_ARG;
+    c.workspace = cfg->workspace;
+    c.workspace_bytes = cfg->workspace_bytes;
   }
   c.s = static_cast<cudaStream_t>(stream);
   return GM_OK;
@@ -330,20 +410,31 @@ gm_status check_teacher(Call& c, const gm_csr* t, int32_t value_type, int32_t in
       !aligned(t->col_idx, index_type & GM_INDEX_COL64 ? 8 : 4) || !aligned(t->vals, value_type == GM_VALUE_F64 ? 8 : 4))
     return GM_ERR_INVALID_ARG;
   c.teacher = t;
+  c.nnz = t->nnz;
   c.value_type = value_type;
   c.index_type = index_type;
   c.temperature = temperature;
   return GM_OK;
 }
 
+// SMs of the current device, looked up once a device.
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // Device facts and a clear error state; GM_ERR_CUDA leaves a pending error to its owner.
 gm_status begin(Call& c) {
   if (cudaPeekAtLastError() != cudaSuccess) return GM_ERR_CUDA;
-  int dev = 0;
   void* st = nullptr;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaGetSymbolAddress(&st, g_loss_status) != cudaSuccess) {
+  c.sms = sm_count();
+  if (c.sms <= 0 || cudaGetSymbolAddress(&st, g_loss_status) != cudaSuccess) {
     cudaGetLastError();
     return GM_ERR_CUDA;
   }
@@ -381,7 +472,7 @@ struct Source {
     if (packed) off = a.add(planes() * rows * ld * 2);
   }
   Operand ready(const Arena& a, cudaStream_t s) const {
-    Operand o{static_cast<const uint16_t*>(p), rows, dim, ld, rows * ld, planes()};
+    Operand o{p, rows, dim, ld, rows * ld, planes()};
     if (packed) {
       o.p = a.at<uint16_t>(off);
       k_pack<<<grid_for(rows * ld, 256), 256, 0, s>>>(p, rows, dim, src_ld, type == GM_LOSS_F32, a.at<uint16_t>(off), ld);
@@ -394,19 +485,21 @@ struct Source {
 struct TeacherPlan {
   size_t start = 0, len = 0, ents = 0, base = 0;
   void plan(Arena& a, const Call& c) {
-    if (!c.teacher) return;
+    if (c.nnz < 0) return;
     start = a.add(c.z.n_rows * 8);
     len = a.add(c.z.n_rows * 4);
     base = a.add(c.z.n_rows * 4);
-    ents = a.add(c.teacher->nnz * 8);
+    ents = a.add(c.nnz * 8);
   }
   template <class V, class R, class C>
   void run(const Arena& a, const Call& c) const {
-    const int64_t blocks = std::min<int64_t>(c.z.n_rows, int64_t(c.sms) * 64);
-    k_teacher<V, R, C><<<static_cast<unsigned>(blocks), 128, 0, c.s>>>(
-        static_cast<const R*>(c.teacher->row_ptr), static_cast<const C*>(c.teacher->col_idx),
-        static_cast<const V*>(c.teacher->vals), c.z.n_rows, c.z.n_classes, c.teacher->nnz, 1.f / c.temperature,
-        a.at<int64_t>(start), a.at<int32_t>(len), a.at<int2>(ents), a.at<float>(base), c.status);
+    // rows a block: as many as its warps only when every SM then still has blocks
+    const int64_t blocks = std::min<int64_t>(c.z.n_rows, std::max<int64_t>(div_up(c.z.n_rows, kTeacherWarps), 2 * c.sms));
+    const TeacherArgs<V, R, C> args{static_cast<const R*>(c.teacher->row_ptr), static_cast<const C*>(c.teacher->col_idx),
+                                    static_cast<const V*>(c.teacher->vals), c.z.n_rows, c.z.n_classes, c.nnz,
+                                    1.f / c.temperature, a.at<int64_t>(start), a.at<int32_t>(len), a.at<int2>(ents),
+                                    a.at<float>(base), c.status};
+    k_teacher<V, R, C><<<static_cast<unsigned>(blocks), 32 * kTeacherWarps, 0, c.s>>>(args);
     note_launch();
   }
   template <class V>
@@ -424,11 +517,16 @@ struct TeacherPlan {
   }
 };
 
+// Stages (64 elements each) of a row of Z summed in TMEM at a time: 1024 elements leave an error
+// under 4e-7 of the row's log-sum; summing every stage apart would read TMEM 16 times as often.
+constexpr int kChunk = 16;
+
 void set_logits_args(ProdArgs& g, const Call& c, const Arena& a, const TeacherPlan& t) {
   g.tgt = targets_of(c);
   g.status = c.status;
   g.planes = c.z.type == GM_LOSS_F32 ? 3 : 1;
   g.bf16 = c.z.type != GM_LOSS_F16;
+  g.chunk = kChunk;
   g.inv_t = 1.f / c.temperature;
   g.c_t = kLog2e / c.temperature;
   if (c.teacher) {
@@ -444,25 +542,47 @@ int group_of(int64_t m_tiles, int64_t tile_rows, int64_t dim, int planes) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(m_tiles, (int64_t(40) << 20) / bytes)));
 }
 
+// How a forward call is cut, and where its workspace lies.
+struct ForwardPlan {
+  Arena a;
+  Source h, w;
+  TeacherPlan t;
+  int cg, bn;
+  int64_t n_tiles, n_parts;
+  size_t o_part, o_zt;
+  explicit ForwardPlan(const Call& c)
+      : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
+    const int64_t n = c.z.n_rows;
+    cg = n > 128 ? 2 : 1;
+    bn = prod_logits_cols(cg, h.planes());
+    n_tiles = div_up(c.z.n_classes, bn);
+    n_parts = 2 * n_tiles;
+    h.plan(a);
+    w.plan(a);
+    t.plan(a, c);
+    o_part = a.add(n_parts * n * 16);
+    o_zt = a.add(n * 4);
+  }
+};
+
 gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   gm_status rc = begin(c);
   if (rc != GM_OK) return rc;
   const int64_t n = c.z.n_rows;
   if (n == 0) return finish(c, true);
-  const int cg = n > 128 ? 2 : 1, bn = 256;
-  const int64_t n_tiles = div_up(c.z.n_classes, bn), n_parts = 2 * n_tiles;
-  Arena a;
-  Source h(c.z.h, n, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type);
-  TeacherPlan t;
-  h.plan(a);
-  w.plan(a);
-  t.plan(a, c);
-  const size_t o_part = a.add(n_parts * n * 16), o_zt = a.add(n * 4);
-  if (!a.buf.alloc(a.used, c.s)) return GM_ERR_OOM;
-  const Operand oh = h.ready(a, c.s), ow = w.ready(a, c.s);
+  ForwardPlan p(c);
+  Arena& a = p.a;
+  rc = a.open(c);
+  if (rc != GM_OK) return rc;
+  const TeacherPlan& t = p.t;
+  const int cg = p.cg, bn = p.bn;
+  const int64_t n_tiles = p.n_tiles, n_parts = p.n_parts;
+  const size_t o_part = p.o_part, o_zt = p.o_zt;
+  const Operand oh = p.h.ready(a, c.s), ow = p.w.ready(a, c.s);
   t.launch(a, c);
   ProdMaps maps;
   if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(cg, bn))) return GM_ERR_CUDA;
+  maps.o = maps.a;  // not used
   ProdArgs g = {};
   set_logits_args(g, c, a, t);
   g.m = n;
@@ -492,8 +612,9 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   j.status = c.status;
   if (ok) {
     // few rows: a block each, so that their half tiles are read by many threads
-    if (n <= 4 * c.sms) k_join<1><<<static_cast<unsigned>(n), 256, 0, c.s>>>(j);
-    else k_join<32><<<static_cast<unsigned>(div_up(n, 32)), 256, 0, c.s>>>(j);
+    // many: 8 rows a block, whose half tiles lie in whole 128-byte lines
+    if (n <= 2 * c.sms) k_join<1><<<static_cast<unsigned>(n), 256, 0, c.s>>>(j);
+    else k_join<8><<<static_cast<unsigned>(div_up(n, 8)), 256, 0, c.s>>>(j);
     note_launch();
   }
   return finish(c, ok);
@@ -507,6 +628,58 @@ struct Grads {
   int64_t dw_ld;
 };
 
+// Where a gradient goes: by TMA where its rows start on 16-byte boundaries.
+bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t dim, int64_t ld, int32_t type) {
+  const int es = static_cast<int>(elem_bytes(type));
+  g.out = out;
+  g.out_ld = ld;
+  g.out_type = type;
+  // half a tile of 64 columns of 2 bytes is less than a box
+  g.by_tma = aligned(out, 16) && (rows <= 1 || ld * es % 16 == 0) && (es == 4 || dim > 64);
+  if (!g.by_tma) return true;
+  if (rows <= 1) ld = up(dim, 16 / es);
+  return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
+}
+
+// How a backward call is cut, and where its workspace lies.
+struct BackwardPlan {
+  Arena a;
+  Source h, w;
+  TeacherPlan t;
+  int planes, bn_h, bn_w, cg_h, cg_w;
+  int64_t width;   // classes of a piece; rows of G are as long
+  int64_t splits;  // of dH's sum along a piece's classes
+  bool dh_direct;  // dH needs no sum over pieces or splits
+  int64_t acc_ld;
+  size_t o_max, o_g, o_acc;
+  explicit BackwardPlan(const Call& c)
+      : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
+    const int64_t n = c.z.n_rows, cls = c.z.n_classes, dim = c.z.dim;
+    planes = c.z.type == GM_LOSS_F32 ? 3 : 1;
+    // pieces of the classes: as few as the bound on G allows, of about equal width
+    const int64_t most = std::max<int64_t>(256, c.cap / (n * 2 * planes) / 256 * 256);
+    const int64_t n_pieces = div_up(cls, most);
+    width = std::min<int64_t>(most, up(div_up(cls, n_pieces), 256));
+    // tiles of dH: split along the classes when they are fewer than the SMs
+    bn_h = prod_sums_cols(dim, n, planes);
+    bn_w = prod_sums_cols(dim, cls, planes);
+    cg_h = bn_h == 256 && n > 128 ? 2 : 1;
+    cg_w = bn_w == 256 && cls > 128 ? 2 : 1;
+    const int64_t dh_tiles = div_up(n, 128 * cg_h) * div_up(dim, bn_h);
+    const int64_t kb = div_up(std::min(width, cls), 64);
+    splits = std::max<int64_t>(1, std::min<int64_t>(c.sms / cg_h / dh_tiles, kb / 8));
+    splits = div_up(kb, div_up(kb, splits));
+    dh_direct = n_pieces == 1 && splits == 1;
+    acc_ld = up(dim, 32);
+    h.plan(a);
+    w.plan(a);
+    t.plan(a, c);
+    o_max = a.add(4);
+    o_g = a.add(planes * n * width * 2);
+    o_acc = dh_direct ? 0 : a.add(splits * n * acc_ld * 4);
+  }
+};
+
 gm_status backward(Call& c, const Grads& q) {
   gm_status rc = begin(c);
   if (rc != GM_OK) return rc;
@@ -516,44 +689,26 @@ gm_status backward(Call& c, const Grads& q) {
     if (q.dw) ok = cudaMemset2DAsync(q.dw, q.dw_ld * es, 0, dim * es, cls, c.s) == cudaSuccess;
     return finish(c, ok);
   }
-  const int planes = c.z.type == GM_LOSS_F32 ? 3 : 1;
-  // pieces of the classes: as few as the bound on G allows, of about equal width
-  const int64_t most = std::max<int64_t>(256, c.cap / (n * 2 * planes) / 256 * 256);
-  const int64_t n_pieces = div_up(cls, most);
-  const int64_t width = std::min<int64_t>(most, up(div_up(cls, n_pieces), 256));
-  const int64_t g_ld = width;
-  // tiles of dH: split along the classes when they are fewer than the SMs
-  const int bn_d = dim > 128 ? 256 : dim > 64 ? 128 : 64;
-  const int cg_h = bn_d == 256 && n > 128 ? 2 : 1, cg_w = bn_d == 256 ? 2 : 1;
-  const int64_t dh_tiles = div_up(n, 128 * cg_h) * div_up(dim, bn_d);
-  const int64_t kb = div_up(std::min(width, cls), 64);
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(c.sms / cg_h / dh_tiles, kb / 8));
-  splits = div_up(kb, div_up(kb, splits));
-  const bool dh_direct = n_pieces == 1 && splits == 1;
-  const int64_t acc_ld = up(dim, 32);
-
-  Arena a;
-  Source h(c.z.h, n, dim, c.z.h_ld, c.z.type), w(c.z.w, cls, dim, c.z.w_ld, c.z.type);
-  TeacherPlan t;
-  h.plan(a);
-  w.plan(a);
-  t.plan(a, c);
-  const size_t o_rc = a.add(n * 16), o_gl = a.add(n * 4), o_max = a.add(4), o_g = a.add(planes * n * g_ld * 2);
-  const size_t o_acc = q.dh && !dh_direct ? a.add(splits * n * acc_ld * 4) : 0;
-  if (!a.buf.alloc(a.used, c.s)) return GM_ERR_OOM;
-  const Operand oh = h.ready(a, c.s), ow = w.ready(a, c.s);
+  BackwardPlan p(c);
+  Arena& a = p.a;
+  rc = a.open(c);
+  if (rc != GM_OK) return rc;
+  const TeacherPlan& t = p.t;
+  const int planes = p.planes, bn_h = p.bn_h, bn_w = p.bn_w, cg_h = p.cg_h, cg_w = p.cg_w;
+  const int64_t width = p.width, g_ld = p.width, splits = p.splits, acc_ld = p.acc_ld;
+  const bool dh_direct = p.dh_direct;
+  const size_t o_g = p.o_g, o_acc = p.o_acc;
+  const Operand oh = p.h.ready(a, c.s), ow = p.w.ready(a, c.s);
   t.launch(a, c);
   ProdArgs base = {};
   set_logits_args(base, c, a, t);
+  base.row = RowGrads{base.tgt, q.lse, q.g_loss, q.g_lse, base.ent_len, q.lse_t, q.g_kl, 1.f / c.temperature};
   unsigned* g_max = nullptr;
   if (c.z.type == GM_LOSS_F16) {
-    g_max = a.at<unsigned>(o_max);
-    if (cudaMemsetAsync(g_max, 0, 4, c.s) != cudaSuccess) return GM_ERR_CUDA;
+    g_max = a.at<unsigned>(p.o_max);
+    k_g_max<<<1, 1024, 0, c.s>>>(n, base.row, g_max);
+    note_launch();
   }
-  k_row_grads<<<grid_for(n, 256), 256, 0, c.s>>>(n, base.tgt, q.lse, q.g_loss, q.g_lse, base.ent_len, q.lse_t, q.g_kl,
-                                                 1.f / c.temperature, a.at<float4>(o_rc), a.at<float>(o_gl), g_max,
-                                                 c.status);
-  note_launch();
   base.g_max = g_max;
   uint16_t* g_mem = a.at<uint16_t>(o_g);
   bool ok = true;
@@ -563,23 +718,21 @@ gm_status backward(Call& c, const Grads& q) {
     ProdMaps maps;
     {
       const int cg = n > 128 ? 2 : 1;
-      if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(cg, 256))) return GM_ERR_CUDA;
+      const int bn = prod_logits_cols(cg, planes);
+      if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(cg, bn)) ||
+          !encode(&maps.o, og, 32))
+        return GM_ERR_CUDA;
       ProdArgs g = base;
       g.m = n;
       g.n = wid;
       g.m_tiles = static_cast<int>(div_up(n, 128 * cg));
-      g.n_tiles = static_cast<int>(div_up(wid, 256));
+      g.n_tiles = static_cast<int>(div_up(wid, bn));
       g.splits = 1;
       g.k_blocks = g.k_per_split = static_cast<int>(div_up(dim, 64));
       g.group = group_of(g.m_tiles, 128 * cg, dim, planes);
       g.b_row0 = static_cast<int>(c0);
       g.cls0 = c0;
-      g.row_c = a.at<float4>(o_rc);
-      g.row_gl = a.at<float>(o_gl);
-      g.g = g_mem;
-      g.g_ld = g_ld;
-      g.g_plane = og.plane;
-      ok = launch_prod(Prod::kGrad, cg, 256, maps, g, c.sms, c.s) == cudaSuccess;
+      ok = launch_prod(Prod::kGrad, cg, bn, maps, g, c.sms, c.s) == cudaSuccess;
     }
     if (ok && q.dh) {
       Operand piece = ow;  // the piece's rows alone: past them reads 0
@@ -589,23 +742,22 @@ gm_status backward(Call& c, const Grads& q) {
       g.m = n;
       g.n = dim;
       g.m_tiles = static_cast<int>(div_up(n, 128 * cg_h));
-      g.n_tiles = static_cast<int>(div_up(dim, bn_d));
+      g.n_tiles = static_cast<int>(div_up(dim, bn_h));
       g.k_blocks = static_cast<int>(div_up(wid, 64));
       g.k_per_split = static_cast<int>(div_up(g.k_blocks, splits));
       g.splits = static_cast<int>(div_up(g.k_blocks, g.k_per_split));
       g.group = 1;
       g.b_row0 = static_cast<int>(c0);
+      bool set;
       if (dh_direct) {
-        g.out = q.dh;
-        g.out_ld = q.dh_ld;
-        g.out_type = c.z.type;
+        set = set_result(&maps.o, g, q.dh, n, dim, q.dh_ld, c.z.type);
       } else {
-        g.acc = a.at<float>(o_acc);
-        g.acc_ld = acc_ld;
-        g.acc_split = n * acc_ld;
+        g.acc = g.by_tma = true;
         g.acc_add = c0 > 0;
+        set = encode(&maps.o, Operand{a.at<float>(o_acc), n, dim, acc_ld, n * acc_ld, static_cast<int>(splits), 4}, 32);
       }
-      ok = launch_prod(Prod::kDh, cg_h, bn_d, maps, g, c.sms, c.s) == cudaSuccess;
+      if (!set) return GM_ERR_CUDA;
+      ok = launch_prod(Prod::kDh, cg_h, bn_h, maps, g, c.sms, c.s) == cudaSuccess;
     }
     if (ok && q.dw) {
       if (!encode(&maps.a, og, 64) || !encode(&maps.b, oh, 64)) return GM_ERR_CUDA;
@@ -613,14 +765,13 @@ gm_status backward(Call& c, const Grads& q) {
       g.m = wid;
       g.n = dim;
       g.m_tiles = static_cast<int>(div_up(wid, 128 * cg_w));
-      g.n_tiles = static_cast<int>(div_up(dim, bn_d));
+      g.n_tiles = static_cast<int>(div_up(dim, bn_w));
       g.splits = 1;
       g.k_blocks = g.k_per_split = static_cast<int>(div_up(n, 64));
       g.group = 1;
-      g.out = static_cast<char*>(q.dw) + c0 * q.dw_ld * es;
-      g.out_ld = q.dw_ld;
-      g.out_type = c.z.type;
-      ok = launch_prod(Prod::kDw, cg_w, bn_d, maps, g, c.sms, c.s) == cudaSuccess;
+      if (!set_result(&maps.o, g, static_cast<char*>(q.dw) + c0 * q.dw_ld * es, wid, dim, q.dw_ld, c.z.type))
+        return GM_ERR_CUDA;
+      ok = launch_prod(Prod::kDw, cg_w, bn_w, maps, g, c.sms, c.s) == cudaSuccess;
     }
   }
   if (ok && q.dh && !dh_direct) {
@@ -653,9 +804,7 @@ gm_status check_grads(const Call& c, const Grads& q) {
 extern "C" gm_status gm_xent_forward(const gm_logits* z, const gm_labels* labels, const gm_loss_config* cfg,
                                      void* stream, float* loss, float* lse) {
   gm::NvtxRange range("gm_xent_forward");
-  gm::Call c = {};
-  c.cap = gm::kDefaultCap;
-  c.temperature = 1.f;
+  gm::Call c;
   if (!labels) return GM_ERR_INVALID_ARG;
   const gm_status rc = gm::check(c, z, labels, cfg, stream);
   if (rc != GM_OK) return rc;
@@ -667,9 +816,7 @@ extern "C" gm_status gm_xent_backward(const gm_logits* z, const gm_labels* label
                                       void* stream, const float* lse, const float* grad_loss, const float* grad_lse,
                                       void* dh, int64_t dh_ld, void* dw, int64_t dw_ld) {
   gm::NvtxRange range("gm_xent_backward");
-  gm::Call c = {};
-  c.cap = gm::kDefaultCap;
-  c.temperature = 1.f;
+  gm::Call c;
   if (!labels) return GM_ERR_INVALID_ARG;
   gm_status rc = gm::check(c, z, labels, cfg, stream);
   if (rc != GM_OK) return rc;
@@ -683,8 +830,7 @@ extern "C" gm_status gm_distill_forward(const gm_logits* z, const gm_csr* teache
                                         const gm_loss_config* cfg, void* stream, float* kl, float* lse_t, float* loss,
                                         float* lse) {
   gm::NvtxRange range("gm_distill_forward");
-  gm::Call c = {};
-  c.cap = gm::kDefaultCap;
+  gm::Call c;
   gm_status rc = gm::check(c, z, labels, cfg, stream);
   if (rc == GM_OK) rc = gm::check_teacher(c, teacher, value_type, index_type, temperature);
   if (rc != GM_OK) return rc;
@@ -701,14 +847,31 @@ extern "C" gm_status gm_distill_backward(const gm_logits* z, const gm_csr* teach
                                          const float* grad_kl, const float* lse, const float* grad_loss,
                                          const float* grad_lse, void* dh, int64_t dh_ld, void* dw, int64_t dw_ld) {
   gm::NvtxRange range("gm_distill_backward");
-  gm::Call c = {};
-  c.cap = gm::kDefaultCap;
+  gm::Call c;
   gm_status rc = gm::check(c, z, labels, cfg, stream);
   if (rc == GM_OK) rc = gm::check_teacher(c, teacher, value_type, index_type, temperature);
   if (rc != GM_OK) return rc;
   const gm::Grads q{lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dh_ld, dw, dw_ld};
   rc = gm::check_grads(c, q);
   return rc != GM_OK ? rc : gm::backward(c, q);
+}
+
+extern "C" gm_status gm_loss_workspace(const gm_logits* z, int64_t teacher_nnz, int32_t backward,
+                                       const gm_loss_config* cfg, int64_t* bytes) {
+  if (!bytes || (backward != 0 && backward != 1)) return GM_ERR_INVALID_ARG;
+  gm::Call c;
+  const gm_status rc = gm::check(c, z, nullptr, cfg, nullptr);
+  if (rc != GM_OK) return rc;
+  *bytes = 0;
+  if (c.z.n_rows == 0) return GM_OK;
+  c.nnz = teacher_nnz < 0 ? -1 : teacher_nnz;
+  c.sms = gm::sm_count();
+  if (c.sms <= 0) {
+    cudaGetLastError();
+    return GM_ERR_CUDA;
+  }
+  *bytes = static_cast<int64_t>(backward ? gm::BackwardPlan(c).a.used : gm::ForwardPlan(c).a.used);
+  return GM_OK;
 }
 
 extern "C" gm_status gm_loss_status(void* stream) {

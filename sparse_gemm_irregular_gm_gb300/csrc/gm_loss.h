@@ -37,6 +37,39 @@ struct Targets {
   int64_t n_cls;
 };
 
+__device__ __forceinline__ int64_t row_target(const Targets& t, int64_t row) {  // -1: ignored, -2: out of range
+  const int64_t v = t.is64 ? static_cast<const int64_t*>(t.t)[row] : static_cast<const int32_t*>(t.t)[row];
+  return v == t.ignore ? -1 : (v >= 0 && v < t.n_cls) ? v : -2;
+}
+
+// What a backward call is given of each row.
+struct RowGrads {
+  Targets tgt;
+  const float *lse, *g_loss, *g_lse;  // with labels; g_lse may be null
+  const int32_t* ent_len;             // null: no teacher
+  const float *lse_t, *g_kl;
+  float inv_t;
+};
+// G_ij = a e^(z - lse) - gl [j = t] + b (e^(z / T - lse_t) - q)
+struct RowCoef {
+  float lse, a, gl, lse_t, b;
+  int64_t t;
+};
+__device__ __forceinline__ RowCoef row_coef(const RowGrads& r, int64_t row) {
+  RowCoef c = {0.f, 0.f, 0.f, 0.f, 0.f, -1};
+  if (r.tgt.t) {
+    c.t = row_target(r.tgt, row);
+    c.gl = c.t >= 0 ? r.g_loss[row] : 0.f;
+    c.lse = r.lse[row];
+    c.a = c.gl + (r.g_lse ? r.g_lse[row] : 0.f);
+  }
+  if (r.ent_len) {
+    c.lse_t = r.lse_t[row];
+    c.b = r.ent_len[row] > 0 ? r.g_kl[row] * r.inv_t : 0.f;
+  }
+  return c;
+}
+
 // What the finished tile of a product is combined with.
 struct ProdArgs {
   // tiles: m_tiles * n_tiles * splits, in groups of `group` row tiles, the column tiles
@@ -44,6 +77,7 @@ struct ProdArgs {
   int m_tiles, n_tiles, splits, group;
   int k_blocks;      // blocks of 64 along the summed dimension
   int k_per_split;   // blocks of a split
+  int chunk;         // blocks summed in TMEM at a time (16-bit logits)
   int planes;        // 1, or 3: each fp32 operand is the sum of three bf16 planes
   bool bf16;
   int a_row0, b_row0;  // first row of the operands that are not read from their start (row of the map)
@@ -59,15 +93,12 @@ struct ProdArgs {
   float4* part;      // [half tile][row]: max, sum e^(z - max), sum e^((z - max) / T), sum q z
   int64_t part_ld;
   float* z_t;        // [row] logit of the target
-  const float4* row_c;  // [row] lse, factor of softmax(z), lse_T, factor of softmax(z / T)
-  const float* row_gl;  // [row] weight of the label
+  RowGrads row;
   const unsigned* g_max;  // f16: bits of the largest |G| possible (null: no scale)
-  uint16_t* g;
-  int64_t g_ld, g_plane;
   // kDh, kDw
-  float* acc;        // partial sums (null: out is written)
-  int64_t acc_ld, acc_split;
+  bool acc;          // the map of results is one of fp32 partial sums (by split), added to with acc_add
   bool acc_add;
+  bool by_tma;       // results go out by their map; else by plain stores to out
   void* out;
   int64_t out_ld;
   int out_type;      // GM_LOSS_*
@@ -84,17 +115,15 @@ __device__ __forceinline__ float g_scale_of(const unsigned* g_max) {
   return ldexpf(1.0f, e < -100 ? -100 : e > 100 ? 100 : e);
 }
 
-__device__ __forceinline__ int64_t row_target(const Targets& t, int64_t row) {  // -1: ignored, -2: out of range
-  const int64_t v = t.is64 ? static_cast<const int64_t*>(t.t)[row] : static_cast<const int32_t*>(t.t)[row];
-  return v == t.ignore ? -1 : (v >= 0 && v < t.n_cls) ? v : -2;
-}
-
 struct ProdMaps {
-  CUtensorMap a, b;
+  CUtensorMap a, b, o;  // operands, result (kGrad: G, boxes of 32 rows by 64; kDh, kDw with by_tma: 32 rows of 128 bytes)
 };
 // Box height of the operands' maps (rows of a K-major box; MN-major boxes are 64 by 64).
 int prod_box_rows_a();
 int prod_box_rows_b(int cg, int bn);
+// Columns of a tile: of the logits' products, and of the gradients' ones (rows: of their result).
+int prod_logits_cols(int cg, int planes);
+int prod_sums_cols(int64_t dim, int64_t rows, int planes);
 // Launches a product; cg: blocks a tile (1: 128 rows, 2: 256), bn: columns of a tile (64, 128 or 256).
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
                         cudaStream_t s);

@@ -6,10 +6,13 @@
 // Warp 0 loads operand tiles with TMA into a ring of 64-deep stages, one lane of warp
 // 1 issues tcgen05 products into one of two TMEM accumulators, and warps 4-11 read
 // the other accumulator: a thread holds one row, 32 columns at a time, so the row
-// reductions need no shuffles.
+// reductions need no shuffles. Results of 16 or 32 bits go through shared memory and
+// out by TMA, 128 bytes a row at a time.
 #include "gm_device.cuh"
 #include "gm_loss.h"
 #include "gm_umma.cuh"
+
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -20,22 +23,41 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+// Registers a thread where sums are held in registers (kParts, kSplit): the warps that load
+// and issue give theirs up to those that read results. 128 * 56 + 256 * 224 = 384 * 168, what a
+// block is launched with; launch_one checks that it is.
+constexpr int kLaunchRegs = 168, kIssueRegs = 56, kResultRegs = 224;
+static_assert(128 * kIssueRegs + 256 * kResultRegs <= kThreads * kLaunchRegs, "more registers than the launch brings");
 constexpr int kBK = 64;  // summed elements a stage: one 128-byte swizzled row
 
-// Order of the plane products of split fp32 operands (x = x0 + x1 + x2, bf16 each, by
-// falling size): the small ones first, so that they meet a small accumulator; x1 y2,
-// x2 y1 and x2 y2 lie under 2^-24 of x y and are left out.
-__device__ __constant__ const int kPlaneA[6] = {2, 0, 1, 1, 0, 0};
-__device__ __constant__ const int kPlaneB[6] = {0, 2, 1, 0, 1, 0};
+// How a tile's sum is kept.
+//   kWhole: in TMEM from the first stage to the last. The tensor cores cut each sum to
+//     24 bits instead of rounding it, so the error grows with the number of stages: 3.3e-7
+//     of a row's log-sum at dim 1024, 1.6e-6 at 4096 (the fp32 form: 4e-8).
+//   kParts: in TMEM over `chunk` stages, the parts added in registers, rounded: for logits of
+//     long rows, whose error goes into the losses as it is.
+//   kSplit: fp32 operands as three bf16 planes a stage, six products of planes a stage, in TMEM
+//     over one stage, the stages added in registers.
+enum { kWhole = 0, kParts = 1, kSplit = 2 };
 
-template <int CG, int BN>
+// Products of planes of split operands (x = x0 + x1 + x2 by falling size), the small ones
+// first, so that they meet a small accumulator; x1 y2, x2 y1 and x2 y2 lie under 2^-24
+// of x y and are left out.
+__device__ __forceinline__ constexpr int pair_a(int p) { return p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 1 : 0; }
+__device__ __forceinline__ constexpr int pair_b(int p) { return p == 0 ? 0 : p == 1 ? 2 : p == 2 ? 1 : p == 3 ? 0 : p == 4 ? 1 : 0; }
+
+template <int CG, int BN, int ACC>
 struct Shape {
-  static constexpr int kABytes = 128 * 128;            // this block's 128 rows of A
+  static constexpr int kPlanes = ACC == kSplit ? 3 : 1;
+  static constexpr int kABytes = 128 * 128;            // a plane of this block's 128 rows of A
   static constexpr int kBRows = BN / CG;               // its rows (columns) of B
   static constexpr int kBBytes = kBRows * 128;
-  static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 512;
+  static constexpr int kStage = kPlanes * (kABytes + kBBytes);
+  static constexpr int kMost = 196608 / kStage;        // 32 KB of the block's 227 hold results on their way out
+  static constexpr int kStages = kMost > 8 ? 8 : kMost;
+  static constexpr int kOut = kEpiWarps * 4096;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kOut + 512;
+  static_assert(kStages >= 2, "two stages at least");
 };
 
 struct Tile {
@@ -74,11 +96,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Teacher entries of a row, in step with the columns.
+// Teacher entries of a row, in step with the columns; one entry read ahead.
 struct Walk {
   const int2* e;
   int64_t at, end;
-  int2 next;
+  int2 next, after;
+  __device__ __forceinline__ int2 get(int64_t i) const { return i < end ? e[i] : make_int2(INT32_MAX, 0); }
   __device__ __forceinline__ void start(const ProdArgs& g, int64_t row, int64_t cls) {
     e = g.ents;
     at = end = 0;
@@ -87,60 +110,116 @@ struct Walk {
       end = lo + g.ent_len[row];
       at = first_entry(e, lo, end, cls);
     }
-    next = at < end ? e[at] : make_int2(INT32_MAX, 0);
+    next = get(at);
+    after = get(at + 1);
   }
   __device__ __forceinline__ void step() {
     ++at;
-    next = at < end ? e[at] : make_int2(INT32_MAX, 0);
+    next = after;
+    after = get(at + 1);
   }
 };
 
+// What a thread looks up of its row before the tile's sums are there.
+template <Prod KIND, bool LAB, bool DIS>
+struct RowState {
+  Walk w;
+  RowCoef c;
+  __device__ __forceinline__ void start(const ProdArgs& g, int64_t row, int64_t cls, bool first) {
+    if constexpr (KIND == Prod::kStats) {
+      c.t = LAB && row < g.m ? row_target(g.tgt, row) : -1;
+    } else if constexpr (KIND == Prod::kGrad) {
+      c = RowCoef{0.f, 0.f, 0.f, 0.f, 0.f, -1};
+      if (row < g.m) {
+        c = row_coef(g.row, row);
+        if (LAB && first && c.t == -2) atomicOr(g.status, kLossBadTarget);
+      }
+    }
+    if constexpr (DIS) w.start(g, row, cls);
+  }
+};
+
+// The sums of a thread's row, 32 columns at a time: from TMEM, the next 32 under way
+// while these are used, or from registers.
+template <int COLS>
+struct FromTmem {
+  uint32_t at;
+  float ahead[32];
+  __device__ __forceinline__ explicit FromTmem(uint32_t addr) : at(addr) { tmem_load32(at, ahead); }
+  template <int C>
+  __device__ __forceinline__ void get(float (&v)[32]) {
+    tmem_load_wait(ahead);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = ahead[j];
+    if constexpr (C + 32 < COLS) {
+      __syncwarp();
+      tmem_load32(at + C + 32, ahead);
+    }
+  }
+};
+template <int COLS>
+struct Held {
+  float acc[COLS];
+  template <int C>
+  __device__ __forceinline__ void get(float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = acc[C + j];
+  }
+};
+
+template <class Src>
+constexpr bool kHeld = false;
+template <int COLS>
+constexpr bool kHeld<Held<COLS>> = true;
+
+// Calls f with 0, 32, 64, ... below COLS as compile-time constants.
+template <int COLS, int C = 0, class F>
+__device__ __forceinline__ void each_32(F&& f) {
+  if constexpr (C < COLS) {
+    f(std::integral_constant<int, C>{});
+    each_32<COLS, C + 32>(f);
+  }
+}
+
 // ---- row statistics of half a tile -------------------------------------------------
-template <int BN, bool LAB, bool DIS>
-__device__ __forceinline__ void end_stats(const ProdArgs& g, uint32_t tmem, int64_t row, int n_tile, int half) {
+template <int BN, bool LAB, bool DIS, class Src>
+__device__ __forceinline__ void end_stats(const ProdArgs& g, Src& src, RowState<Prod::kStats, LAB, DIS>& rs, int64_t row,
+                                          int n_tile, int half) {
   constexpr int kCols = BN / 2;
   const int64_t cls = g.cls0 + int64_t(n_tile) * BN + half * kCols;  // class of the first column
   const int64_t end = g.cls0 + g.n;
   float m = -INFINITY, s1 = 0.f, st = 0.f, zq = 0.f;
-  int64_t t = -1;
-  if (LAB && row < g.m) t = row_target(g.tgt, row);
-  Walk w;
-  if (DIS) w.start(g, row, cls);
-#pragma unroll 1
-  for (int c = 0; c < kCols; c += 32) {
+  const int64_t t = rs.c.t;
+  each_32<kCols>([&](auto cc) {
+    constexpr int c = decltype(cc)::value;
     const int64_t k0 = cls + c;
-    if (k0 >= end) break;
     float v[32];
-    __syncwarp();
-    tmem_load32(tmem + half * kCols + c, v);
-    tmem_load_wait(v);
+    src.template get<c>(v);
+    if (k0 >= end) return;
     if (k0 + 32 > end) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (k0 + j >= end) v[j] = -INFINITY;
     }
-    float mx = v[0];
+    float m0 = fmaxf(v[0], v[1]), m1 = fmaxf(v[2], v[3]);
 #pragma unroll
-    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, v[j]);
-    const float mn = fmaxf(m, mx);
+    for (int j = 4; j < 32; j += 4) {
+      m0 = fmaxf(m0, fmaxf(v[j], v[j + 1]));
+      m1 = fmaxf(m1, fmaxf(v[j + 2], v[j + 3]));
+    }
+    const float mn = fmaxf(m, fmaxf(m0, m1));
     const float ref = mn == -INFINITY ? 0.f : mn;
     if (LAB) {
-      float a0 = 0.f, a1 = 0.f;
+      float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        a0 += ex2(fmaf(v[j], kLog2e, -ref * kLog2e));
-        a1 += ex2(fmaf(v[j + 1], kLog2e, -ref * kLog2e));
-      }
-      s1 = s1 * ex2((m - ref) * kLog2e) + (a0 + a1);
+      for (int j = 0; j < 32; ++j) a[j & 3] += ex2(fmaf(v[j], kLog2e, -ref * kLog2e));
+      s1 = s1 * ex2((m - ref) * kLog2e) + ((a[0] + a[1]) + (a[2] + a[3]));
     }
     if (DIS) {
-      float a0 = 0.f, a1 = 0.f;
+      float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        a0 += ex2(fmaf(v[j], g.c_t, -ref * g.c_t));
-        a1 += ex2(fmaf(v[j + 1], g.c_t, -ref * g.c_t));
-      }
-      st = st * ex2((m - ref) * g.c_t) + (a0 + a1);
+      for (int j = 0; j < 32; ++j) a[j & 3] += ex2(fmaf(v[j], g.c_t, -ref * g.c_t));
+      st = st * ex2((m - ref) * g.c_t) + ((a[0] + a[1]) + (a[2] + a[3]));
     }
     m = mn;
     if (LAB) {
@@ -154,6 +233,7 @@ __device__ __forceinline__ void end_stats(const ProdArgs& g, uint32_t tmem, int6
       }
     }
     if (DIS) {
+      Walk& w = rs.w;
       while (__any_sync(kFull, w.next.x < k0 + 32)) {
         const int rel = w.next.x < k0 + 32 ? static_cast<int>(w.next.x - k0) : -1;
         float z = 0.f;
@@ -167,49 +247,95 @@ __device__ __forceinline__ void end_stats(const ProdArgs& g, uint32_t tmem, int6
         }
       }
     }
-  }
+  });
   if (row < g.m) g.part[(int64_t(n_tile) * 2 + half) * g.part_ld + row] = make_float4(m, s1, st, zq);
 }
+
+// ---- results on their way out ------------------------------------------------------------
+// A warp's 32 rows of 128 bytes in shared memory, 16-byte pieces swizzled as the TMA store
+// expects them, so that neither side meets a bank twice.
+struct Outbox {
+  uint32_t buf;
+  int lane;
+  __device__ __forceinline__ void open() {  // the last store has read the buffer
+    if (lane == 0) tma_wait_read();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void put(int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    st_shared_v4(buf + lane * 128 + ((piece ^ (lane & 7)) << 4), a, b, c, d);
+  }
+  __device__ __forceinline__ void put16(int piece0, const float (&v)[32], bool bf16, uint32_t keep) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      put(piece0 + q, keep & pack2(v[8 * q], v[8 * q + 1], bf16), keep & pack2(v[8 * q + 2], v[8 * q + 3], bf16),
+          keep & pack2(v[8 * q + 4], v[8 * q + 5], bf16), keep & pack2(v[8 * q + 6], v[8 * q + 7], bf16));
+  }
+  __device__ __forceinline__ void put32(const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      put(q, __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+          __float_as_uint(v[4 * q + 3]));
+  }
+  __device__ __forceinline__ void send(const CUtensorMap* m, int x, int y, int z, bool add) {
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0) {
+      if (add) tma_add_3d(m, buf, x, y, z);
+      else tma_store_3d(m, buf, x, y, z);
+      tma_commit();
+    }
+  }
+  // The same by plain stores, for rows that do not start on 16-byte boundaries: the warp
+  // writes a row's columns together.
+  __device__ __forceinline__ void copy(void* out, int64_t ld, int es, int64_t row0, int64_t rows, int64_t col0,
+                                       int64_t cols) {
+    __syncwarp();
+#pragma unroll 1
+    for (int r = 0; r < 32 && row0 + r < rows; ++r) {
+      const uint32_t x = ld_shared_u32(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+      if (es == 4) {
+        if (lane < cols) static_cast<uint32_t*>(out)[(row0 + r) * ld + col0 + lane] = x;
+      } else {
+        uint16_t* p = static_cast<uint16_t*>(out) + (row0 + r) * ld + col0 + 2 * lane;
+        if (2 * lane < cols) p[0] = static_cast<uint16_t>(x);
+        if (2 * lane + 1 < cols) p[1] = static_cast<uint16_t>(x >> 16);
+      }
+    }
+    __syncwarp();
+  }
+};
 
 // ---- gradient of the logits ----------------------------------------------------------
 // G_ij = a_i e^(z - lse) - gl_i [j = t_i] + b_i (e^(z / T - lse_T) - q_ij), rounded to 16 bits as
 // the operand of the two products after it (times a power of two in f16, whose range
 // is too short for small probabilities times small weights); fp32 operands keep it in
-// three bf16 planes, 24 bits.
-template <int BN, bool LAB, bool DIS>
-__device__ __forceinline__ void end_grad(const ProdArgs& g, uint32_t tmem, int64_t row, int n_tile, int half) {
-  constexpr int kCols = BN / 2;
-  const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
-  const int64_t cls = g.cls0 + col0;
-  const bool in = row < g.m;
-  float4 rc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float gl = 0.f;
-  int64_t t = -1;
-  if (in) {
-    rc = g.row_c[row];
-    if (LAB) {
-      gl = g.row_gl[row];
-      t = row_target(g.tgt, row);
+// three bf16 planes, 24 bits. In 16 bits the factors go into the exponent.
+template <bool LAB, bool DIS, bool FINE>
+struct GradRow {
+  float a, b, gl, x1, xt, s1, st;
+  bool live;
+  __device__ __forceinline__ GradRow(const ProdArgs& g, const RowCoef& c) {
+    const float scale = g_scale_of(g.g_max);
+    a = c.a * scale, b = c.b * scale, gl = c.gl * scale;
+    live = a != 0.f || b != 0.f || gl != 0.f;
+    if (FINE) {
+      x1 = c.lse, xt = c.lse_t;
+    } else {  // 0 as a factor: 2^-inf
+      x1 = __log2f(fabsf(a)) - c.lse * kLog2e, xt = __log2f(fabsf(b)) - c.lse_t * kLog2e;
+      s1 = copysignf(1.f, a), st = copysignf(1.f, b);
     }
   }
-  const float scale = g_scale_of(g.g_max);
-  const float a = rc.y * scale, b = rc.w * scale;
-  gl *= scale;
-  Walk w;
-  if (DIS) w.start(g, row, cls);
-  if (cls >= g.cls0 + g.n) return;
-#pragma unroll 1
-  for (int c = 0; c < kCols; c += 32) {
-    const int64_t k0 = cls + c;
-    float v[32];
-    __syncwarp();
-    tmem_load32(tmem + half * kCols + c, v);
-    tmem_load_wait(v);
+  __device__ __forceinline__ void of(float (&v)[32], const ProdArgs& g, int64_t t, int64_t k0, Walk& w) const {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       float r = 0.f;
-      if (LAB) r = a != 0.f ? a * ex2((v[j] - rc.x) * kLog2e) : 0.f;
-      if (DIS) r += b != 0.f ? b * ex2(fmaf(v[j], g.inv_t, -rc.z) * kLog2e) : 0.f;
+      if (FINE) {
+        if (LAB) r = a * ex2((v[j] - x1) * kLog2e);
+        if (DIS) r = fmaf(b, ex2(fmaf(v[j], g.inv_t, -xt) * kLog2e), r);
+      } else {
+        if (LAB) r = s1 * ex2(fmaf(v[j], kLog2e, x1));
+        if (DIS) r = fmaf(st, ex2(fmaf(v[j], g.c_t, xt)), r);
+      }
       v[j] = r;
     }
     if (LAB) {
@@ -223,114 +349,126 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, uint32_t tmem, int64
     if (DIS) {
       while (__any_sync(kFull, w.next.x < k0 + 32)) {
         const int rel = w.next.x < k0 + 32 ? static_cast<int>(w.next.x - k0) : -1;
-        const float q = b != 0.f ? b * __int_as_float(w.next.y) : 0.f;
+        const float q = b * __int_as_float(w.next.y);
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (j == rel) v[j] -= q;
         if (rel >= 0) w.step();
       }
     }
-    if (!in) continue;
-    uint16_t* dst = g.g + row * g.g_ld + col0 + c;
+  }
+};
+
+template <int BN, bool LAB, bool DIS, class Src>
+__device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* map_o, Src& src,
+                                         RowState<Prod::kGrad, LAB, DIS>& rs, int64_t row, int n_tile, int half,
+                                         Outbox box) {
+  constexpr int kCols = BN / 2;
+  const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
+  const int64_t cls = g.cls0 + col0;
+  const int64_t row0 = row - box.lane;
+  const GradRow<LAB, DIS, kHeld<Src>> gr(g, rs.c);
+  const uint32_t keep = gr.live ? 0xffffffffu : 0u;  // a row without weight is 0 whatever its logits are
+  if constexpr (!kHeld<Src>) {
+    each_32<kCols>([&](auto cc) {
+      constexpr int c = decltype(cc)::value;
+      float v[32];
+      src.template get<c>(v);
+      gr.of(v, g, rs.c.t, cls + c, rs.w);
+      if constexpr (c % 64 == 0) box.open();
+      box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, keep);
+      if constexpr (c % 64 == 32) {
+        if (row0 < g.m && col0 + c - 32 < g.n)
+          box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), 0, false);
+      }
+    });
+  } else {
+    each_32<kCols>([&](auto cc) {
+      constexpr int c = decltype(cc)::value;
+      float v[32];
+      src.template get<c>(v);
+      gr.of(v, g, rs.c.t, cls + c, rs.w);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) src.acc[c + j] = v[j];
+    });
 #pragma unroll 1
     for (int p = 0; p < g.planes; ++p) {
+      each_32<kCols>([&](auto cc) {
+        constexpr int c = decltype(cc)::value;
+        float v[32];
+        src.template get<c>(v);
+        if constexpr (c % 64 == 0) box.open();
+        box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, keep);
+        if constexpr (c % 64 == 32) {
+          if (row0 < g.m && col0 + c - 32 < g.n)
+            box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), p, false);
+        }
+        if (p + 1 < g.planes) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint4 x;
-        x.x = pack2(v[8 * q + 0], v[8 * q + 1], g.bf16);
-        x.y = pack2(v[8 * q + 2], v[8 * q + 3], g.bf16);
-        x.z = pack2(v[8 * q + 4], v[8 * q + 5], g.bf16);
-        x.w = pack2(v[8 * q + 6], v[8 * q + 7], g.bf16);
-        reinterpret_cast<uint4*>(dst)[q] = x;
-      }
-      if (p + 1 < g.planes) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
-        dst += g.g_plane;
-      }
+          for (int j = 0; j < 32; ++j) src.acc[c + j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+        }
+      });
     }
   }
 }
 
 // ---- results of the gradient products ---------------------------------------------------
-template <int BN>
-__device__ __forceinline__ void end_sum(const ProdArgs& g, uint32_t tmem, int64_t row, int n_tile, int split,
-                                        int half) {
+template <int BN, class Src>
+__device__ __forceinline__ void end_sum(const ProdArgs& g, const CUtensorMap* map_o, Src& src, int64_t row, int n_tile,
+                                        int split, int half, Outbox box) {
   constexpr int kCols = BN / 2;
   const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
-  const float inv = g.acc ? 1.f : 1.f / g_scale_of(g.g_max);
-#pragma unroll 1
-  for (int c = 0; c < kCols; c += 32) {
-    const int64_t col = col0 + c;
-    if (col >= g.n) break;
+  const int64_t row0 = row - box.lane;
+  const bool sums = g.acc;
+  const float inv = sums ? 1.f : 1.f / g_scale_of(g.g_max);
+  const bool wide = sums || g.out_type == GM_LOSS_F32;
+  const bool bf = g.out_type == GM_LOSS_BF16;
+  each_32<kCols>([&](auto cc) {
+    constexpr int c = decltype(cc)::value;
     float v[32];
-    __syncwarp();
-    tmem_load32(tmem + half * kCols + c, v);
-    tmem_load_wait(v);
-    if (row >= g.m) continue;
-    const int64_t left = g.n - col;
-    if (g.acc) {  // acc_ld is a multiple of 4 and covers whole chunks
-      float4* dst = reinterpret_cast<float4*>(g.acc + split * g.acc_split + row * g.acc_ld + col);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float4 x = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        if (g.acc_add) {
-          const float4 o = dst[q];
-          x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
-        }
-        dst[q] = x;
-      }
-      continue;
-    }
+    src.template get<c>(v);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= inv;
-    const int es = g.out_type == GM_LOSS_F32 ? 4 : 2;
-    char* base = static_cast<char*>(g.out) + (row * g.out_ld + col) * es;
-    if (left >= 32 && (reinterpret_cast<uintptr_t>(base) & 15) == 0) {
-      if (es == 4) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          reinterpret_cast<float4*>(base)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-      } else {
-        const bool bf = g.out_type == GM_LOSS_BF16;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint4 x;
-          x.x = pack2(v[8 * q + 0], v[8 * q + 1], bf);
-          x.y = pack2(v[8 * q + 2], v[8 * q + 3], bf);
-          x.z = pack2(v[8 * q + 4], v[8 * q + 5], bf);
-          x.w = pack2(v[8 * q + 6], v[8 * q + 7], bf);
-          reinterpret_cast<uint4*>(base)[q] = x;
-        }
-      }
+    // 32 columns of 4 bytes or 64 of 2 fill the box; half a tile of 32 columns sends what it has
+    constexpr bool kPair = kCols >= 64;
+    constexpr int first = kPair ? c / 64 * 64 : c;
+    const int64_t col = col0 + (wide ? c : first);
+    if (wide) {
+      box.open();
+      box.put32(v);
     } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (j >= left) continue;
-        if (es == 4) reinterpret_cast<float*>(base)[j] = v[j];
-        else if (g.out_type == GM_LOSS_BF16) reinterpret_cast<__nv_bfloat16*>(base)[j] = __float2bfloat16_rn(v[j]);
-        else reinterpret_cast<__half*>(base)[j] = __float2half_rn(v[j]);
-      }
+      if (c == first) box.open();
+      box.put16(c == first ? 0 : 4, v, bf, 0xffffffffu);
+      if (kPair && c % 64 == 0) return;
     }
-  }
+    if (row0 >= g.m || col >= g.n) return;
+    if (g.by_tma) {
+      box.send(map_o, static_cast<int>(col), static_cast<int>(row0), split, g.acc_add);
+    } else {
+      const int64_t most = wide || !kPair ? 32 : 64;
+      box.copy(g.out, g.out_ld, wide ? 4 : 2, row0, g.m, col, min(most, g.n - col));
+    }
+  });
 }
 
-template <Prod KIND, int CG, int BN, bool LAB, bool DIS>
+template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>
 __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CUtensorMap map_a,
-                                                      const __grid_constant__ CUtensorMap map_b, const ProdArgs g) {
-  using S = Shape<CG, BN>;
+                                                      const __grid_constant__ CUtensorMap map_b,
+                                                      const __grid_constant__ CUtensorMap map_o, const ProdArgs g) {
+  using S = Shape<CG, BN, ACC>;
   constexpr bool kAmn = KIND == Prod::kDw;                        // G^T: rows of G run along the result's rows
   constexpr bool kBmn = KIND == Prod::kDw || KIND == Prod::kDh;   // H and W with the summed dimension outside
   extern __shared__ unsigned char smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bars = base + S::kStages * S::kStage;
+  const uint32_t out = base + S::kStages * S::kStage;
+  const uint32_t bars = out + S::kOut;
   const uint32_t full = bars, empty = bars + 8 * S::kStages, tfull = empty + 8 * S::kStages, tempty = tfull + 16,
                  spare = tempty + 16;
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  constexpr uint32_t kCols = 2 * BN;
+  constexpr uint32_t kTmemCols = 2 * BN;
 
   if (threadIdx.x == 0) {
     s_abort = 0;
@@ -347,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
   }
-  if (warp == 1) tmem_alloc<CG>(smem_addr(&s_tmem), kCols);
+  if (warp == 1) tmem_alloc<CG>(smem_addr(&s_tmem), kTmemCols);
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync_all();
@@ -356,107 +494,137 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
 
   const int n_tiles = g.m_tiles * g.n_tiles * g.splits;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
-  const int n_pairs = g.planes == 1 ? 1 : 6;
+  const int chunk = ACC == kWhole ? (1 << 30) : ACC == kSplit ? 1 : g.chunk;  // stages an accumulator takes
   volatile int* abort = &s_abort;
 
-  if (warp == 0 && lane == 0) {
-    // ---- loads
-    int st = 0, issued = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int t = first; ok && t < n_tiles; t += stride) {
-      const Tile tl = tile_at(g, t);
-      const int kb0 = tl.split * g.k_per_split, kb1 = min(g.k_blocks, kb0 + g.k_per_split);
-      const int m0 = tl.m * 128 * CG + static_cast<int>(rank) * 128;
-      const int n0 = tl.n * BN + static_cast<int>(rank) * S::kBRows;
-      for (int p = 0; ok && p < n_pairs; ++p) {
-        const int pa = n_pairs == 1 ? 0 : kPlaneA[p], pb = n_pairs == 1 ? 0 : kPlaneB[p];
+  if (warp < kEpiWarp0) {
+    if constexpr (ACC != kWhole) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 0) {
+      // ---- loads
+      const bool one = elect_one();
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; ok && t < n_tiles; t += stride) {
+        const Tile tl = tile_at(g, t);
+        const int kb0 = tl.split * g.k_per_split, kb1 = min(g.k_blocks, kb0 + g.k_per_split);
+        const int m0 = tl.m * 128 * CG + static_cast<int>(rank) * 128;
+        const int n0 = tl.n * BN + static_cast<int>(rank) * S::kBRows;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(empty + 8 * st, ph ^ 1, abort)) {
+          if (!__all_sync(kFull, mbar_wait(empty + 8 * st, ph ^ 1, abort))) {
             ok = false;
             break;
           }
-          const uint32_t a = base + st * S::kStage, b = a + S::kABytes;
-          const uint32_t bar = CG == 2 ? map_to_rank(full + 8 * st, 0) : full + 8 * st;
-          if (rank == 0) mbar_expect_tx(full + 8 * st, CG * S::kStage);
-          if constexpr (!kAmn) {
-            tma_load_3d<CG>(a, &map_a, kb * kBK, g.a_row0 + m0, pa, bar);
-          } else {
+          if (one) {
+            const uint32_t bar = CG == 2 ? map_to_rank(full + 8 * st, 0) : full + 8 * st;
+            if (rank == 0) mbar_expect_tx(full + 8 * st, CG * S::kStage);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, g.a_row0 + kb * kBK, pa, bar);
-          }
-          if constexpr (!kBmn) {
-            tma_load_3d<CG>(b, &map_b, kb * kBK, g.b_row0 + n0, pb, bar);
-          } else {
+            for (int p = 0; p < S::kPlanes; ++p) {
+              const uint32_t a = base + st * S::kStage + p * S::kABytes;
+              const uint32_t b = base + st * S::kStage + S::kPlanes * S::kABytes + p * S::kBBytes;
+              if constexpr (!kAmn) {
+                tma_load_3d<CG>(a, &map_a, kb * kBK, g.a_row0 + m0, p, bar);
+              } else {
 #pragma unroll
-            for (int i = 0; i < S::kBRows / 64; ++i)
-              tma_load_3d<CG>(b + i * 8192, &map_b, n0 + i * 64, g.b_row0 + kb * kBK, pb, bar);
+                for (int i = 0; i < 2; ++i)
+                  tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, g.a_row0 + kb * kBK, p, bar);
+              }
+              if constexpr (!kBmn) {
+                tma_load_3d<CG>(b, &map_b, kb * kBK, g.b_row0 + n0, p, bar);
+              } else {
+#pragma unroll
+                for (int i = 0; i < S::kBRows / 64; ++i)
+                  tma_load_3d<CG>(b + i * 8192, &map_b, n0 + i * 64, g.b_row0 + kb * kBK, p, bar);
+              }
+            }
           }
+          __syncwarp();
           ++issued;
           if (++st == S::kStages) st = 0, ph ^= 1;
         }
       }
-    }
-    // A block that gave up leaves only once the loads it issued have landed (the waits
-    // are bounded as well); rank 0's barriers count both blocks' loads.
-    if (!ok && rank == 0) {
-      int no_abort = 0;
-      for (int i = 0; i < S::kStages && i < issued; ++i) {
-        if (--st < 0) st = S::kStages - 1, ph ^= 1;
-        mbar_wait(full + 8 * st, ph, &no_abort);
-      }
-    }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ---- products
-    const uint32_t idesc = instr_desc(g.bf16, kAmn, kBmn, 128 * CG, BN);
-    int st = 0, buf = 0;
-    uint32_t ph = 0, bph = 0;
-    bool ok = true;
-    for (int t = first; ok && t < n_tiles; t += stride) {
-      const int split = t / (g.m_tiles * g.n_tiles);
-      const int kb0 = split * g.k_per_split, kb1 = min(g.k_blocks, kb0 + g.k_per_split);
-      const int steps = (kb1 - kb0) * n_pairs;
-      if (!mbar_wait(tempty + 8 * buf, bph ^ 1, abort)) break;
-      tc_fence_after();
-      for (int i = 0; i < steps; ++i) {
-        if (!mbar_wait(full + 8 * st, ph, abort)) {
-          ok = false;
-          break;
+      // A block that gave up leaves only once the loads it issued have landed (the waits
+      // are bounded as well); rank 0's barriers count both blocks' loads.
+      if (!ok && rank == 0) {
+        int no_abort = 0;
+        for (int i = 0; i < S::kStages && i < issued; ++i) {
+          if (--st < 0) st = S::kStages - 1, ph ^= 1;
+          mbar_wait(full + 8 * st, ph, &no_abort);
         }
-        tc_fence_after();
-        const uint32_t a = base + st * S::kStage, b = a + S::kABytes;
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---- products. The tensor cores wait for this loop when it is slow: the tile's
+      // buffer is waited for outside it, and a stage's operands are a constant away from
+      // the first one's descriptors.
+      const bool one = elect_one();
+      const uint32_t idesc = instr_desc(g.bf16, kAmn, kBmn, 128 * CG, BN);
+      const uint32_t b0 = base + S::kPlanes * S::kABytes;
+      const uint64_t desc_a = kAmn ? smem_desc(base, 8192, 1024) : smem_desc(base, 16, 1024);
+      const uint64_t desc_b = kBmn ? smem_desc(b0, 8192, 1024) : smem_desc(b0, 16, 1024);
+      constexpr int kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;  // 16 summed elements further
+      int st = 0, buf = 0;
+      uint32_t ph = 0, bph = 0;
+      bool ok = true;
+      for (int t = first; ok && t < n_tiles; t += stride) {
+        const int split = t / (g.m_tiles * g.n_tiles);
+        const int kb0 = split * g.k_per_split, steps = min(g.k_blocks, kb0 + g.k_per_split) - kb0;
+        for (int i0 = 0; ok && i0 < steps; i0 += chunk) {
+          if (!__all_sync(kFull, mbar_wait(tempty + 8 * buf, bph ^ 1, abort))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int n = min(chunk, steps - i0);
+          const uint32_t d = tmem + buf * BN;
+          for (int i = 0; i < n; ++i) {
+            if (!__all_sync(kFull, mbar_wait(full + 8 * st, ph, abort))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (one) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t da = kAmn ? smem_desc(a + k * 2048, 8192, 1024) : smem_desc(a + k * 32, 16, 1024);
-          const uint64_t db = kBmn ? smem_desc(b + k * 2048, 8192, 1024) : smem_desc(b + k * 32, 16, 1024);
-          tc_mma_f16<CG>(tmem + buf * BN, da, db, idesc, (i | k) != 0);
+              for (int p = 0; p < (ACC == kSplit ? 6 : 1); ++p) {
+                const int pa = ACC == kSplit ? pair_a(p) : 0, pb = ACC == kSplit ? pair_b(p) : 0;
+                const uint64_t da = desc_a + ((st * S::kStage + pa * S::kABytes) >> 4);
+                const uint64_t db = desc_b + ((st * S::kStage + pb * S::kBBytes) >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  tc_mma_f16<CG>(d, da + k * kStepA, db + k * kStepB, idesc, (i | p | k) != 0);
+              }
+              tc_commit<CG>(empty + 8 * st);
+            }
+            __syncwarp();
+            if (++st == S::kStages) st = 0, ph ^= 1;
+          }
+          if (!ok) break;
+          if (one) tc_commit<CG>(tfull + 8 * buf);
+          __syncwarp();
+          if (++buf == 2) buf = 0, bph ^= 1;
         }
-        tc_commit<CG>(empty + 8 * st);
-        if (++st == S::kStages) st = 0, ph ^= 1;
       }
-      if (!ok) break;
-      tc_commit<CG>(tfull + 8 * buf);
-      if (++buf == 2) buf = 0, bph ^= 1;
+      if (*abort) {  // the products still running read this block's shared memory
+        int no_abort = 0;
+        if (one) tc_commit<CG>(spare);
+        __syncwarp();
+        mbar_wait(spare, 0, &no_abort);
+      }
     }
-    if (*abort) {  // the products still running read this block's shared memory
-      int no_abort = 0;
-      tc_commit<CG>(spare);
-      mbar_wait(spare, 0, &no_abort);
-    }
-  } else if (warp >= kEpiWarp0) {
+  } else {
+    if constexpr (ACC != kWhole) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
     // ---- results
+    constexpr int kCols = BN / 2;
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    Outbox box{out + (warp - kEpiWarp0) * 4096, lane};
     int buf = 0;
     uint32_t bph = 0;
-    for (int t = first; t < n_tiles; t += stride) {
-      const Tile tl = tile_at(g, t);
-      if (!__all_sync(kFull, mbar_wait(tfull + 8 * buf, bph, abort))) break;
+    auto ready = [&] {
+      const bool ok = __all_sync(kFull, mbar_wait(tfull + 8 * buf, bph, abort));
       tc_fence_after();
-      const int64_t row = int64_t(tl.m) * 128 * CG + rank * 128 + quad * 32 + lane;
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * BN;
-      if constexpr (KIND == Prod::kStats) end_stats<BN, LAB, DIS>(g, acc, row, tl.n, half);
-      else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS>(g, acc, row, tl.n, half);
-      else end_sum<BN>(g, acc, row, tl.n, tl.split, half);
+      return ok;
+    };
+    auto done = [&] {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -464,23 +632,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
         else mbar_arrive(tempty + 8 * buf);
       }
       if (++buf == 2) buf = 0, bph ^= 1;
+    };
+    for (int t = first; t < n_tiles; t += stride) {
+      const Tile tl = tile_at(g, t);
+      const int64_t row = int64_t(tl.m) * 128 * CG + rank * 128 + quad * 32 + lane;
+      RowState<KIND, LAB, DIS> rs;
+      rs.start(g, row, g.cls0 + int64_t(tl.n) * BN + half * kCols, tl.n == 0 && half == 0);
+      auto finish = [&](auto& src) {
+        if constexpr (KIND == Prod::kStats) end_stats<BN, LAB, DIS>(g, src, rs, row, tl.n, half);
+        else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS>(g, &map_o, src, rs, row, tl.n, half, box);
+        else end_sum<BN>(g, &map_o, src, row, tl.n, tl.split, half, box);
+      };
+      if constexpr (ACC == kWhole) {
+        if (!ready()) break;
+        FromTmem<kCols> src(tmem + lanes + buf * BN + half * kCols);
+        finish(src);
+        done();
+      } else {
+        const int kb0 = tl.split * g.k_per_split, steps = min(g.k_blocks, kb0 + g.k_per_split) - kb0;
+        Held<kCols> src;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) src.acc[j] = 0.f;
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < steps; i += chunk) {
+          if (!ready()) {
+            ok = false;
+            break;
+          }
+          each_32<kCols>([&](auto cc) {
+            constexpr int c = decltype(cc)::value;
+            float v[32];
+            __syncwarp();
+            tmem_load32(tmem + lanes + buf * BN + half * kCols + c, v);
+            tmem_load_wait(v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) src.acc[c + j] += v[j];
+          });
+          done();
+        }
+        if (!ok) break;
+        finish(src);
+      }
     }
+    if (lane == 0) tma_wait_all();
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_free<CG>(tmem, kCols);
+  if (warp == 1) tmem_free<CG>(tmem, kTmemCols);
   if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kLossTimeout);
 }
 
-template <Prod KIND, int CG, int BN, bool LAB, bool DIS>
+template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>
 cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
-  using S = Shape<CG, BN>;
-  auto* k = k_prod<KIND, CG, BN, LAB, DIS>;
+  using S = Shape<CG, BN, ACC>;
+  auto* k = k_prod<KIND, CG, BN, LAB, DIS, ACC>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
+  if (ACC != kWhole) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, k);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
+  }
   const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
   const int groups = static_cast<int>(tiles < num_sms / CG ? tiles : num_sms / CG);
   cudaLaunchConfig_t cfg = {};
@@ -494,17 +711,42 @@ cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cud
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k, maps.a, maps.b, a);
+  e = cudaLaunchKernelEx(&cfg, k, maps.a, maps.b, maps.o, a);
   note_launch();
   return e;
 }
 
-template <Prod KIND, int CG, int BN>
+template <Prod KIND, int CG, int BN, int ACC>
 cudaError_t launch_modes(const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
-  const bool lab = a.tgt.t != nullptr, dis = a.ents != nullptr || a.ent_len != nullptr;
-  if (lab && dis) return launch_one<KIND, CG, BN, true, true>(maps, a, num_sms, s);
-  if (dis) return launch_one<KIND, CG, BN, false, true>(maps, a, num_sms, s);
-  return launch_one<KIND, CG, BN, true, false>(maps, a, num_sms, s);
+  const bool lab = a.tgt.t != nullptr, dis = a.ent_len != nullptr;
+  if (lab && dis) return launch_one<KIND, CG, BN, true, true, ACC>(maps, a, num_sms, s);
+  if (dis) return launch_one<KIND, CG, BN, false, true, ACC>(maps, a, num_sms, s);
+  return launch_one<KIND, CG, BN, true, false, ACC>(maps, a, num_sms, s);
+}
+
+template <Prod KIND>
+cudaError_t launch_logits(int cg, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
+  if (a.planes == 3)
+    return cg == 2 ? launch_modes<KIND, 2, 256, kSplit>(maps, a, num_sms, s)
+                   : launch_modes<KIND, 1, 128, kSplit>(maps, a, num_sms, s);
+  if (a.chunk < a.k_blocks)
+    return cg == 2 ? launch_modes<KIND, 2, 256, kParts>(maps, a, num_sms, s)
+                   : launch_modes<KIND, 1, 256, kParts>(maps, a, num_sms, s);
+  return cg == 2 ? launch_modes<KIND, 2, 256, kWhole>(maps, a, num_sms, s)
+                 : launch_modes<KIND, 1, 256, kWhole>(maps, a, num_sms, s);
+}
+
+template <Prod KIND>
+cudaError_t launch_sums(int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
+  if (a.planes == 3)
+    return cg == 2     ? launch_one<KIND, 2, 256, false, false, kSplit>(maps, a, num_sms, s)
+           : bn == 128 ? launch_one<KIND, 1, 128, false, false, kSplit>(maps, a, num_sms, s)
+                       : launch_one<KIND, 1, 64, false, false, kSplit>(maps, a, num_sms, s);
+  if (bn == 256)
+    return cg == 2 ? launch_one<KIND, 2, 256, false, false, kWhole>(maps, a, num_sms, s)
+                   : launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
+  return bn == 128 ? launch_one<KIND, 1, 128, false, false, kWhole>(maps, a, num_sms, s)
+                   : launch_one<KIND, 1, 64, false, false, kWhole>(maps, a, num_sms, s);
 }
 
 }  // namespace
@@ -512,27 +754,19 @@ cudaError_t launch_modes(const ProdMaps& maps, const ProdArgs& a, int num_sms, c
 int prod_box_rows_a() { return 128; }
 int prod_box_rows_b(int cg, int bn) { return bn / cg; }
 
+int prod_logits_cols(int cg, int planes) { return planes == 3 && cg == 1 ? 128 : 256; }
+int prod_sums_cols(int64_t dim, int64_t rows, int planes) {
+  const int bn = dim > 128 ? 256 : dim > 64 ? 128 : 64;
+  return planes == 3 && rows <= 128 ? (bn < 128 ? bn : 128) : bn;
+}
+
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
                         cudaStream_t s) {
   switch (kind) {
-    case Prod::kStats:
-      return cg == 2 ? launch_modes<Prod::kStats, 2, 256>(maps, a, num_sms, s)
-                     : launch_modes<Prod::kStats, 1, 256>(maps, a, num_sms, s);
-    case Prod::kGrad:
-      return cg == 2 ? launch_modes<Prod::kGrad, 2, 256>(maps, a, num_sms, s)
-                     : launch_modes<Prod::kGrad, 1, 256>(maps, a, num_sms, s);
-    case Prod::kDh:
-      if (bn == 256)
-        return cg == 2 ? launch_one<Prod::kDh, 2, 256, false, false>(maps, a, num_sms, s)
-                       : launch_one<Prod::kDh, 1, 256, false, false>(maps, a, num_sms, s);
-      return bn == 128 ? launch_one<Prod::kDh, 1, 128, false, false>(maps, a, num_sms, s)
-                       : launch_one<Prod::kDh, 1, 64, false, false>(maps, a, num_sms, s);
-    case Prod::kDw:
-      if (bn == 256)
-        return cg == 2 ? launch_one<Prod::kDw, 2, 256, false, false>(maps, a, num_sms, s)
-                       : launch_one<Prod::kDw, 1, 256, false, false>(maps, a, num_sms, s);
-      return bn == 128 ? launch_one<Prod::kDw, 1, 128, false, false>(maps, a, num_sms, s)
-                       : launch_one<Prod::kDw, 1, 64, false, false>(maps, a, num_sms, s);
+    case Prod::kStats: return launch_logits<Prod::kStats>(cg, maps, a, num_sms, s);
+    case Prod::kGrad: return launch_logits<Prod::kGrad>(cg, maps, a, num_sms, s);
+    case Prod::kDh: return launch_sums<Prod::kDh>(cg, bn, maps, a, num_sms, s);
+    case Prod::kDw: return launch_sums<Prod::kDw>(cg, bn, maps, a, num_sms, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -22,8 +22,12 @@ from .binding import DeviceCSR, GmError, gm_csr
 
 GM_LOSS_F32, GM_LOSS_BF16, GM_LOSS_F16 = 0, 1, 2
 GM_LOSS_CHECK = 1
-EXPORTS = ["gm_xent_forward", "gm_xent_backward", "gm_distill_forward", "gm_distill_backward", "gm_loss_status"]
+EXPORTS = ["gm_xent_forward", "gm_xent_backward", "gm_distill_forward", "gm_distill_backward", "gm_loss_workspace",
+           "gm_loss_status"]
 TYPES = {torch.float32: GM_LOSS_F32, torch.bfloat16: GM_LOSS_BF16, torch.float16: GM_LOSS_F16}
+_ROW_PTR = {torch.int64: 0, torch.int32: binding.GM_INDEX_ROWPTR32}
+_COL = {torch.int32: 0, torch.int64: binding.GM_INDEX_COL64}
+_VAL = {torch.float64: binding.GM_VALUE_F64, torch.float32: binding.GM_VALUE_F32}
 
 
 class gm_logits(ctypes.Structure):
@@ -37,7 +41,8 @@ class gm_labels(ctypes.Structure):
 
 
 class gm_loss_config(ctypes.Structure):
-    _fields_ = [("workspace_cap_bytes", ctypes.c_int64), ("flags", ctypes.c_int32)]
+    _fields_ = [("workspace_cap_bytes", ctypes.c_int64), ("flags", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -58,6 +63,7 @@ def load():
     lib.gm_xent_backward.argtypes = head + tail + [V, V, V] + out
     lib.gm_distill_forward.argtypes = head + teacher + tail + [V, V, V, V]
     lib.gm_distill_backward.argtypes = head + teacher + tail + [V, V, V, V, V] + out
+    lib.gm_loss_workspace.argtypes = head + [I64, I32, P(gm_loss_config), P(I64)]
     lib.gm_loss_status.argtypes = [V]
     for name in EXPORTS:
         getattr(lib, name).restype = ctypes.c_int
@@ -65,84 +71,99 @@ def load():
     return lib
 
 
-def _matrix(name, t, device=None, dtype=None, shape=None):
+def _matrix(name, t, like=None, shape=None):
     """A CUDA matrix whose rows are consecutive elements: (pointer, elements between rows)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in TYPES:
         raise ValueError(f"{name} must be a 2-d CUDA tensor of float32, bfloat16 or float16")
-    if (device is not None and t.device != device) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype} on {device}, not {t.dtype} on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}, not {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
     rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
         raise ValueError(f"{name}'s rows must be consecutive elements that do not overlap (strides {t.stride()})")
-    return (t.data_ptr() if t.numel() else None), (t.stride(0) if rows > 1 else max(cols, 1))
+    return t.data_ptr() or None, (ld if rows > 1 else max(cols, 1))
 
 
 def _vector(name, t, n, device, dtypes=(torch.float32,)):
     if t is None:
         return None
     if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype not in dtypes or t.dim() != 1
-            or t.numel() != n or not t.is_contiguous()):
+            or t.shape[0] != n or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous tensor of {n} elements of {' or '.join(map(str, dtypes))} on {device}")
-    return t.data_ptr() if n else None
+    return t.data_ptr() or None
 
 
-def _logits(h, w):
-    hp, h_ld = _matrix("h", h)
-    wp, w_ld = _matrix("w", w, h.device, h.dtype)
-    if h.shape[1] != w.shape[1]:
-        raise ValueError(f"h has rows of {h.shape[1]} elements, w of {w.shape[1]}")
-    return gm_logits(h.shape[0], w.shape[0], h.shape[1], hp, h_ld, wp, w_ld, TYPES[h.dtype])
+def _same_device(stream, device):
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return stream
 
 
-def _labels(h, target, ignore_index):
-    if target is None:
-        return None
-    p = _vector("target", target, h.shape[0], h.device, (torch.int64, torch.int32))
-    return gm_labels(p, int(ignore_index), int(target.dtype == torch.int32))
+class _Call:
+    """One call's checked arguments; ``with`` makes its device and stream current, so that what torch
+    allocates inside belongs to that stream."""
 
+    def __init__(self, h, w, target, ignore_index, teacher, check, workspace_cap_bytes, stream):
+        hp, h_ld = _matrix("h", h)
+        wp, w_ld = _matrix("w", w, h)
+        self.n, dim = h.shape
+        if dim != w.shape[1]:
+            raise ValueError(f"h has rows of {dim} elements, w of {w.shape[1]}")
+        self.h, self.w, self.device = h, w, h.device
+        self.z = gm_logits(self.n, w.shape[0], dim, hp, h_ld, wp, w_ld, TYPES[h.dtype])
+        self.labels = None
+        if target is not None:
+            p = _vector("target", target, self.n, self.device, (torch.int64, torch.int32))
+            self.labels = gm_labels(p, ignore_index, target.dtype == torch.int32)
+        self.cfg = gm_loss_config(workspace_cap_bytes, GM_LOSS_CHECK if check else 0, None, 0)
+        self.teacher = self._teacher(teacher) if teacher is not None else None
+        self.given = stream
+        self.on = None
 
-def _teacher(h, w, t: DeviceCSR):
-    """(descriptor, value type, index type) of a teacher of rows x classes."""
-    n, dev = h.shape[0], h.device
-    rp = {torch.int64: 0, torch.int32: binding.GM_INDEX_ROWPTR32}
-    col = {torch.int32: 0, torch.int64: binding.GM_INDEX_COL64}
-    val = {torch.float64: binding.GM_VALUE_F64, torch.float32: binding.GM_VALUE_F32}
-    for name, x, kinds in (("row_ptr", t.row_ptr, rp), ("col", t.col, col), ("val", t.val, val)):
-        if not isinstance(x, torch.Tensor) or x.device != dev or x.dtype not in kinds or not x.is_contiguous():
-            raise ValueError(f"the teacher's {name} must be a contiguous tensor of {' or '.join(map(str, kinds))} on {dev}")
-    if t.row_ptr.numel() != n + 1 or t.col.numel() != t.val.numel():
-        raise ValueError(f"the teacher has {t.row_ptr.numel()} row pointers for {n} rows, {t.col.numel()} columns and "
-                         f"{t.val.numel()} values")
-    return t.desc(), val[t.val.dtype], rp[t.row_ptr.dtype] | col[t.col.dtype]
-
-
-def _config(check, workspace_cap_bytes):
-    if not check and not workspace_cap_bytes:
-        return None
-    return gm_loss_config(int(workspace_cap_bytes), GM_LOSS_CHECK if check else 0)
-
-
-def _ref(x):
-    return ctypes.byref(x) if x is not None else None
-
-
-class _On:
-    """The tensors' device, and the stream that work and results belong to."""
-
-    def __init__(self, device, stream):
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors are on {device}")
-        self.on = torch.cuda.stream(self.stream)  # also makes the stream's device current
+    def _teacher(self, t):
+        for name, x, kinds in (("row_ptr", t.row_ptr, _ROW_PTR), ("col", t.col, _COL), ("val", t.val, _VAL)):
+            if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype not in kinds or not x.is_contiguous():
+                raise ValueError(f"the teacher's {name} must be a contiguous tensor of {' or '.join(map(str, kinds))} "
+                                 f"on {self.device}")
+        if t.row_ptr.numel() != self.n + 1 or t.col.numel() != t.val.numel():
+            raise ValueError(f"the teacher has {t.row_ptr.numel()} row pointers for {self.n} rows, {t.col.numel()} "
+                             f"columns and {t.val.numel()} values")
+        return t.desc(), _VAL[t.val.dtype], _ROW_PTR[t.row_ptr.dtype] | _COL[t.col.dtype]
 
     def __enter__(self):
-        self.on.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self.given is not None:
+            self.on = torch.cuda.stream(_same_device(self.given, self.device))  # also makes its device current
+        elif torch.cuda.current_device() != self.device.index:
+            self.on = torch.cuda.device(self.device)
+        if self.on is not None:
+            self.on.__enter__()
+        return self
 
     def __exit__(self, *a):
-        return self.on.__exit__(*a)
+        if self.on is not None:
+            self.on.__exit__(*a)
+
+    def vectors(self, k):
+        """k uninitialised results, a float a row (parts of one allocation)."""
+        return torch.empty((k, self.n), dtype=torch.float32, device=self.device).unbind(0)
+
+    def run(self, name, backward, *args):
+        lib = load()
+        need = ctypes.c_int64()
+        cfg = self.cfg
+        nnz = self.teacher[0].nnz if self.teacher is not None else -1
+        binding._check(lib.gm_loss_workspace(self.z, nnz, backward, cfg, need), name)
+        work = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        cfg.workspace, cfg.workspace_bytes = work.data_ptr() or None, need.value
+        stream = (self.given if self.given is not None else torch.cuda.current_stream(self.device.index)).cuda_stream
+        if self.teacher is None:
+            rc = getattr(lib, name)(self.z, self.labels, cfg, stream, *args)
+        else:
+            desc, value_type, index_type = self.teacher
+            rc = getattr(lib, name)(self.z, desc, value_type, index_type, self.temperature, self.labels, cfg, stream, *args)
+        binding._check(rc, name)
 
 
 def gm_loss_status(stream=None):
@@ -152,49 +173,48 @@ def gm_loss_status(stream=None):
 
 # ---- cross entropy -----------------------------------------------------------------------
 def gm_xent_forward(h, w, target, loss, lse, *, ignore_index=-100, check=False, stream=None):
-    z, lab = _logits(h, w), _labels(h, target, ignore_index)
-    n, dev = h.shape[0], h.device
-    with _On(dev, stream) as s:
-        binding._check(load().gm_xent_forward(_ref(z), _ref(lab), _ref(_config(check, 0)), s,
-                                              _vector("loss", loss, n, dev), _vector("lse", lse, n, dev)),
-                       "gm_xent_forward")
+    c = _Call(h, w, target, ignore_index, None, check, 0, stream)
+    with c:
+        c.run("gm_xent_forward", 0, _vector("loss", loss, c.n, c.device), _vector("lse", lse, c.n, c.device))
 
 
 def gm_xent_backward(h, w, target, lse, grad_loss, grad_lse, dh, dw, *, ignore_index=-100, workspace_cap_bytes=0,
                      check=False, stream=None):
-    z, lab = _logits(h, w), _labels(h, target, ignore_index)
-    n, dev = h.shape[0], h.device
-    dhp, dh_ld = _matrix("dh", dh, dev, h.dtype, h.shape) if dh is not None else (None, 0)
-    dwp, dw_ld = _matrix("dw", dw, dev, h.dtype, w.shape) if dw is not None else (None, 0)
-    with _On(dev, stream) as s:
-        binding._check(load().gm_xent_backward(
-            _ref(z), _ref(lab), _ref(_config(check, workspace_cap_bytes)), s, _vector("lse", lse, n, dev),
-            _vector("grad_loss", grad_loss, n, dev), _vector("grad_lse", grad_lse, n, dev), dhp, dh_ld, dwp, dw_ld),
-            "gm_xent_backward")
+    c = _Call(h, w, target, ignore_index, None, check, workspace_cap_bytes, stream)
+    with c:
+        _xent_backward(c, lse, grad_loss, grad_lse, dh, dw)
+
+
+def _xent_backward(c, lse, grad_loss, grad_lse, dh, dw):
+    n, dev = c.n, c.device
+    c.run("gm_xent_backward", 1, _vector("lse", lse, n, dev), _vector("grad_loss", grad_loss, n, dev),
+          _vector("grad_lse", grad_lse, n, dev), *_gradient("dh", dh, c.h), *_gradient("dw", dw, c.w))
+
+
+def _gradient(name, t, of):
+    return (None, 0) if t is None else _matrix(name, t, of, of.shape)
+
+
+def _like(x, need):
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device) if need else None
 
 
 def xent_forward(h, w, target, *, ignore_index=-100, check=False, stream=None):
     """(loss, lse) of each row: lse_i - z_i,target(i), and lse_i = log sum_j exp(z_ij), float32."""
-    _logits(h, w)
-    with _On(h.device, stream):
-        loss, lse = (torch.empty(h.shape[0], dtype=torch.float32, device=h.device) for _ in range(2))
-    gm_xent_forward(h, w, target, loss, lse, ignore_index=ignore_index, check=check, stream=stream)
+    c = _Call(h, w, target, ignore_index, None, check, 0, stream)
+    with c:
+        loss, lse = c.vectors(2)
+        c.run("gm_xent_forward", 0, loss.data_ptr() or None, lse.data_ptr() or None)
     return loss, lse
-
-
-def _grad_buffers(h, w, need_h, need_w, stream):
-    _logits(h, w)
-    with _On(h.device, stream):
-        return (torch.empty(h.shape, dtype=h.dtype, device=h.device) if need_h else None,
-                torch.empty(w.shape, dtype=w.dtype, device=w.device) if need_w else None)
 
 
 def xent_backward(h, w, target, lse, grad_loss, grad_lse=None, *, ignore_index=-100, need_h=True, need_w=True,
                   workspace_cap_bytes=0, check=False, stream=None):
     """(dh, dw) for the derivatives of an objective by loss and (optional) by lse."""
-    dh, dw = _grad_buffers(h, w, need_h, need_w, stream)
-    gm_xent_backward(h, w, target, lse, grad_loss, grad_lse, dh, dw, ignore_index=ignore_index,
-                     workspace_cap_bytes=workspace_cap_bytes, check=check, stream=stream)
+    c = _Call(h, w, target, ignore_index, None, check, workspace_cap_bytes, stream)
+    with c:
+        dh, dw = _like(h, need_h), _like(w, need_w)
+        _xent_backward(c, lse, grad_loss, grad_lse, dh, dw)
     return dh, dw
 
 
@@ -208,53 +228,54 @@ class Distilled(NamedTuple):
     lse: torch.Tensor | None
 
 
+def _distill_call(h, w, teacher, temperature, target, ignore_index, check, workspace_cap_bytes, stream):
+    c = _Call(h, w, target, ignore_index, teacher, check, workspace_cap_bytes, stream)
+    c.temperature = temperature
+    return c
+
+
 def gm_distill_forward(h, w, teacher, temperature, kl, lse_t, target=None, loss=None, lse=None, *, ignore_index=-100,
                        check=False, stream=None):
-    z, lab = _logits(h, w), _labels(h, target, ignore_index)
-    desc, vt, it = _teacher(h, w, teacher)
-    n, dev = h.shape[0], h.device
-    with _On(dev, stream) as s:
-        binding._check(load().gm_distill_forward(
-            _ref(z), _ref(desc), vt, it, float(temperature), _ref(lab), _ref(_config(check, 0)), s,
-            _vector("kl", kl, n, dev), _vector("lse_t", lse_t, n, dev), _vector("loss", loss, n, dev),
-            _vector("lse", lse, n, dev)), "gm_distill_forward")
+    c = _distill_call(h, w, teacher, temperature, target, ignore_index, check, 0, stream)
+    with c:
+        c.run("gm_distill_forward", 0, *(_vector(k, t, c.n, c.device) for k, t in
+                                         (("kl", kl), ("lse_t", lse_t), ("loss", loss), ("lse", lse))))
 
 
 def gm_distill_backward(h, w, teacher, temperature, lse_t, grad_kl, dh, dw, target=None, lse=None, grad_loss=None,
                         grad_lse=None, *, ignore_index=-100, workspace_cap_bytes=0, check=False, stream=None):
-    z, lab = _logits(h, w), _labels(h, target, ignore_index)
-    desc, vt, it = _teacher(h, w, teacher)
-    n, dev = h.shape[0], h.device
-    dhp, dh_ld = _matrix("dh", dh, dev, h.dtype, h.shape) if dh is not None else (None, 0)
-    dwp, dw_ld = _matrix("dw", dw, dev, h.dtype, w.shape) if dw is not None else (None, 0)
-    with _On(dev, stream) as s:
-        binding._check(load().gm_distill_backward(
-            _ref(z), _ref(desc), vt, it, float(temperature), _ref(lab), _ref(_config(check, workspace_cap_bytes)), s,
-            _vector("lse_t", lse_t, n, dev), _vector("grad_kl", grad_kl, n, dev), _vector("lse", lse, n, dev),
-            _vector("grad_loss", grad_loss, n, dev), _vector("grad_lse", grad_lse, n, dev), dhp, dh_ld, dwp, dw_ld),
-            "gm_distill_backward")
+    c = _distill_call(h, w, teacher, temperature, target, ignore_index, check, workspace_cap_bytes, stream)
+    with c:
+        _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dw)
+
+
+def _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dw):
+    n, dev = c.n, c.device
+    c.run("gm_distill_backward", 1, _vector("lse_t", lse_t, n, dev), _vector("grad_kl", grad_kl, n, dev),
+          _vector("lse", lse, n, dev), _vector("grad_loss", grad_loss, n, dev), _vector("grad_lse", grad_lse, n, dev),
+          *_gradient("dh", dh, c.h), *_gradient("dw", dw, c.w))
 
 
 def distill_forward(h, w, teacher: DeviceCSR, temperature=1.0, *, target=None, ignore_index=-100, check=False,
                     stream=None) -> Distilled:
     """Divergence of softmax(z / T) from the softmax of the teacher's stored values / T, a row; with ``target``
     also the rows' cross entropy at temperature 1, from the same pass."""
-    _logits(h, w)
-    with _On(h.device, stream):
-        out = [torch.empty(h.shape[0], dtype=torch.float32, device=h.device) for _ in range(2 if target is None else 4)]
-    out += [None] * (4 - len(out))
-    gm_distill_forward(h, w, teacher, temperature, out[0], out[1], target, out[2], out[3], ignore_index=ignore_index,
-                       check=check, stream=stream)
-    return Distilled(*out)
+    c = _distill_call(h, w, teacher, temperature, target, ignore_index, check, 0, stream)
+    with c:
+        out = c.vectors(2 if target is None else 4)
+        p = [t.data_ptr() or None for t in out]
+        c.run("gm_distill_forward", 0, *p, *[None] * (4 - len(p)))
+    return Distilled(*out, *[None] * (4 - len(out)))
 
 
 def distill_backward(h, w, teacher: DeviceCSR, lse_t, grad_kl, temperature=1.0, *, target=None, lse=None,
                      grad_loss=None, grad_lse=None, ignore_index=-100, need_h=True, need_w=True,
                      workspace_cap_bytes=0, check=False, stream=None):
     """(dh, dw) for the derivatives of an objective by kl and, with ``target``, by loss and (optional) lse."""
-    dh, dw = _grad_buffers(h, w, need_h, need_w, stream)
-    gm_distill_backward(h, w, teacher, temperature, lse_t, grad_kl, dh, dw, target, lse, grad_loss, grad_lse,
-                        ignore_index=ignore_index, workspace_cap_bytes=workspace_cap_bytes, check=check, stream=stream)
+    c = _distill_call(h, w, teacher, temperature, target, ignore_index, check, workspace_cap_bytes, stream)
+    with c:
+        dh, dw = _like(h, need_h), _like(w, need_w)
+        _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dw)
     return dh, dw
 
 
