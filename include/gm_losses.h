@@ -78,7 +78,7 @@ typedef struct gm_labels {
 
 /* Tuning; zero selects the automatic value. NULL is the same as all zeros. */
 typedef struct gm_loss_config {
-  int64_t workspace_cap_bytes; /* bound on the piece of G a backward call holds; 0 = 256 MiB; the
+  int64_t workspace_cap_bytes; /* bound on the piece of G a backward call holds; 0 = 512 MiB; the
                                   narrowest piece has 256 classes                                */
   int32_t flags;               /* GM_LOSS_CHECK                                                  */
   void* workspace;             /* device memory for the call, 256-byte aligned (NULL: the hooks); it

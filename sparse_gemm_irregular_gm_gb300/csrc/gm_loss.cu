@@ -26,22 +26,55 @@ __device__ int g_loss_status;
 
 // ---- operands that TMA cannot read in place ------------------------------------------
 // f32: three bf16 planes, x = x0 + x1 + x2 with x0 the nearest bf16 of x and so on, which
-// keeps all 24 bits; 16-bit types: one plane, copied. Rows are padded with zeros to ld.
-__global__ void k_pack(const void* __restrict__ src, int64_t rows, int64_t dim, int64_t src_ld, bool f32,
-                       uint16_t* __restrict__ dst, int64_t ld) {
-  const int64_t n = rows * ld, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
-    const int64_t r = i / ld, c = i - r * ld;
-    if (!f32) {
-      dst[i] = c < dim ? static_cast<const uint16_t*>(src)[r * src_ld + c] : 0;
-      continue;
+// keeps all 24 bits; 16-bit types: one plane, copied. Rows are padded with zeros to ld, a
+// multiple of 8: a thread writes 8 elements of each plane at once. VEC: the rows of src start
+// on 16-byte boundaries.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int64_t rows, int dim, int64_t src_ld,
+                                              uint16_t* __restrict__ dst, int ld) {
+  const unsigned per_row = static_cast<unsigned>(ld) / 8;
+  const int64_t n = rows * ld, pieces = rows * per_row, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
+    int64_t r;
+    int c;
+    if (pieces < (int64_t(1) << 32)) {
+      const unsigned q = static_cast<unsigned>(i) / per_row;
+      r = q, c = static_cast<int>((static_cast<unsigned>(i) - q * per_row) * 8);
+    } else {
+      r = i / per_row, c = static_cast<int>(i - r * per_row) * 8;
     }
-    float x = c < dim ? static_cast<const float*>(src)[r * src_ld + c] : 0.f;
-    const bool finite = fabsf(x) <= 3.4e38f;
-    for (int p = 0; p < 3; ++p) {
-      const __nv_bfloat16 b = __float2bfloat16_rn(x);
-      dst[p * n + i] = __bfloat16_as_ushort(b);
-      x = finite ? x - __bfloat162float(b) : 0.f;  // infinities and NaN stand in the first plane
+    const int left = dim - c;  // at least 1
+    if constexpr (!F32) {
+      const uint16_t* p = static_cast<const uint16_t*>(src) + r * src_ld + c;
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = (2 * j < left ? p[2 * j] : 0u) | (2 * j + 1 < left ? static_cast<uint32_t>(p[2 * j + 1]) << 16 : 0u);
+      *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+    } else {
+      const float* p = static_cast<const float*>(src) + r * src_ld + c;
+      float x[8];
+      if (VEC && left >= 8) {
+        const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < left ? p[j] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const __nv_bfloat16 a = __float2bfloat16_rn(x[j]), b = __float2bfloat16_rn(x[j + 1]);
+          y[j / 2] = __bfloat16_as_ushort(a) | (static_cast<uint32_t>(__bfloat16_as_ushort(b)) << 16);
+          // infinities, NaN and what rounds to infinity stand in the first plane
+          const float ra = __bfloat162float(a), rb = __bfloat162float(b);
+          x[j] = fabsf(ra) <= 3.4e38f ? x[j] - ra : 0.f;
+          x[j + 1] = fabsf(rb) <= 3.4e38f ? x[j + 1] - rb : 0.f;
+        }
+        *reinterpret_cast<uint4*>(dst + q * n + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
     }
   }
 }
@@ -301,18 +334,18 @@ struct Operand {
   int planes;
   int bytes = 2;
 };
-// Boxes of box_rows rows of 128 bytes, 128-byte swizzle; elements outside read as 0.
-bool encode(CUtensorMap* m, const Operand& o, int box_rows) {
+// Boxes of box_rows rows of row_bytes (128 or 64), swizzled over that width; elements outside read as 0.
+bool encode(CUtensorMap* m, const Operand& o, int box_rows, int row_bytes = 128) {
   const EncodeTiled fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
                               static_cast<cuuint64_t>(o.planes)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * o.bytes, static_cast<cuuint64_t>(o.plane) * o.bytes};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / o.bytes), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(row_bytes / o.bytes), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
   return fn(m, o.bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
             const_cast<void*>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -320,7 +353,7 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 constexpr int64_t kMostIndex = (int64_t(1) << 31) - 256;  // tile coordinates are int32
-constexpr int64_t kDefaultCap = int64_t(256) << 20;
+constexpr int64_t kDefaultCap = int64_t(512) << 20;
 
 struct Call {
   gm_logits z = {};
@@ -475,7 +508,13 @@ struct Source {
     Operand o{p, rows, dim, ld, rows * ld, planes()};
     if (packed) {
       o.p = a.at<uint16_t>(off);
-      k_pack<<<grid_for(rows * ld, 256), 256, 0, s>>>(p, rows, dim, src_ld, type == GM_LOSS_F32, a.at<uint16_t>(off), ld);
+      const unsigned grid = grid_for(rows * ld / 8, 256);
+      uint16_t* dst = a.at<uint16_t>(off);
+      const int d = static_cast<int>(dim), l = static_cast<int>(ld);
+      if (type != GM_LOSS_F32) k_pack<false, false><<<grid, 256, 0, s>>>(p, rows, d, src_ld, dst, l);
+      else if (aligned(p, 16) && (rows <= 1 || src_ld % 4 == 0))
+        k_pack<true, true><<<grid, 256, 0, s>>>(p, rows, d, src_ld, dst, l);
+      else k_pack<true, false><<<grid, 256, 0, s>>>(p, rows, d, src_ld, dst, l);
       note_launch();
     }
     return o;
@@ -720,7 +759,7 @@ gm_status backward(Call& c, const Grads& q) {
       const int cg = n > 128 ? 2 : 1;
       const int bn = prod_logits_cols(cg, planes);
       if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(cg, bn)) ||
-          !encode(&maps.o, og, 32))
+          !encode(&maps.o, og, 32, prod_grad_row_bytes(planes, base.chunk, static_cast<int>(div_up(dim, 64)))))
         return GM_ERR_CUDA;
       ProdArgs g = base;
       g.m = n;

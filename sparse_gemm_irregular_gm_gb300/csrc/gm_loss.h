@@ -116,7 +116,8 @@ __device__ __forceinline__ float g_scale_of(const unsigned* g_max) {
 }
 
 struct ProdMaps {
-  CUtensorMap a, b, o;  // operands, result (kGrad: G, boxes of 32 rows by 64; kDh, kDw with by_tma: 32 rows of 128 bytes)
+  CUtensorMap a, b, o;  // operands, result, boxes of 32 rows (kGrad: of
+                        // prod_grad_row_bytes; kDh, kDw with by_tma: of 128 bytes)
 };
 // Box height of the operands' maps (rows of a K-major box; MN-major boxes are 64 by 64).
 int prod_box_rows_a();
@@ -124,6 +125,7 @@ int prod_box_rows_b(int cg, int bn);
 // Columns of a tile: of the logits' products, and of the gradients' ones (rows: of their result).
 int prod_logits_cols(int cg, int planes);
 int prod_sums_cols(int64_t dim, int64_t rows, int planes);
+int prod_grad_row_bytes(int planes, int chunk, int k_blocks);
 // Launches a product; cg: blocks a tile (1: 128 rows, 2: 256), bn: columns of a tile (64, 128 or 256).
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
                         cudaStream_t s);

@@ -4,8 +4,8 @@
 //
 // One persistent kernel: blocks (or pairs of blocks) walk the tiles of the result.
 // Warp 0 loads operand tiles with TMA into a ring of 64-deep stages, one lane of warp
-// 1 issues tcgen05 products into one of two TMEM accumulators, and warps 4-11 read
-// the other accumulator: a thread holds one row, 32 columns at a time, so the row
+// 1 issues tcgen05 products into one of two TMEM accumulators, and warps from 4 on read
+// the other accumulator, 8 a tile: a thread holds one row, 32 columns at a time, so the row
 // reductions need no shuffles. Results of 16 or 32 bits go through shared memory and
 // out by TMA, 128 bytes a row at a time.
 #include "gm_device.cuh"
@@ -21,13 +21,12 @@ namespace gm {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;  // first warp that reads results, warps that read one tile
 // Registers a thread where sums are held in registers (kParts, kSplit): the warps that load
 // and issue give theirs up to those that read results. 128 * 56 + 256 * 224 = 384 * 168, what a
 // block is launched with; launch_one checks that it is.
 constexpr int kLaunchRegs = 168, kIssueRegs = 56, kResultRegs = 224;
-static_assert(128 * kIssueRegs + 256 * kResultRegs <= kThreads * kLaunchRegs, "more registers than the launch brings");
+static_assert(128 * kIssueRegs + 256 * kResultRegs <= 384 * kLaunchRegs, "more registers than the launch brings");
 constexpr int kBK = 64;  // summed elements a stage: one 128-byte swizzled row
 
 // How a tile's sum is kept.
@@ -46,8 +45,17 @@ enum { kWhole = 0, kParts = 1, kSplit = 2 };
 __device__ __forceinline__ constexpr int pair_a(int p) { return p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 1 : 0; }
 __device__ __forceinline__ constexpr int pair_b(int p) { return p == 0 ? 0 : p == 1 ? 2 : p == 2 ? 1 : p == 3 ? 0 : p == 4 ? 1 : 0; }
 
-template <int CG, int BN, int ACC>
+// Groups of 8 warps that read results. What is done with a logit (an exponential, a maximum,
+// a sum) is a chain of latencies that 2 warps a scheduler do not cover: with one group the
+// statistics of 512 x 256 x 1048576 took 332 us, the tensor cores 37 % busy. Two groups take
+// the tiles in turn, one accumulator each. Sums held in registers leave room for one group;
+// the gradients' results are only moved.
+template <Prod KIND, int ACC>
+constexpr int kGroups = ACC == kWhole && (KIND == Prod::kStats || KIND == Prod::kGrad) ? 2 : 1;
+
+template <Prod KIND, int CG, int BN, int ACC>
 struct Shape {
+  static constexpr int kThreads = 128 + 256 * kGroups<KIND, ACC>;
   static constexpr int kPlanes = ACC == kSplit ? 3 : 1;
   static constexpr int kABytes = 128 * 128;            // a plane of this block's 128 rows of A
   static constexpr int kBRows = BN / CG;               // its rows (columns) of B
@@ -55,7 +63,8 @@ struct Shape {
   static constexpr int kStage = kPlanes * (kABytes + kBBytes);
   static constexpr int kMost = 196608 / kStage;        // 32 KB of the block's 227 hold results on their way out
   static constexpr int kStages = kMost > 8 ? 8 : kMost;
-  static constexpr int kOut = kEpiWarps * 4096;
+  static constexpr int kBox = 4096 / kGroups<KIND, ACC>;  // a warp's results on their way out
+  static constexpr int kOut = 32768;
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kOut + 512;
   static_assert(kStages >= 2, "two stages at least");
 };
@@ -139,21 +148,29 @@ struct RowState {
   }
 };
 
-// The sums of a thread's row, 32 columns at a time: from TMEM, the next 32 under way
-// while these are used, or from registers.
-template <int COLS>
+// The sums of a thread's row, 32 columns at a time: from TMEM (AHEAD: the next 32 under way
+// while these are used), or from registers.
+template <int COLS, bool AHEAD>
 struct FromTmem {
   uint32_t at;
-  float ahead[32];
-  __device__ __forceinline__ explicit FromTmem(uint32_t addr) : at(addr) { tmem_load32(at, ahead); }
+  float ahead[AHEAD ? 32 : 1];
+  __device__ __forceinline__ explicit FromTmem(uint32_t addr) : at(addr) {
+    if constexpr (AHEAD) tmem_load32(at, ahead);
+  }
   template <int C>
   __device__ __forceinline__ void get(float (&v)[32]) {
-    tmem_load_wait(ahead);
+    if constexpr (AHEAD) {
+      tmem_load_wait(ahead);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = ahead[j];
-    if constexpr (C + 32 < COLS) {
+      for (int j = 0; j < 32; ++j) v[j] = ahead[j];
+      if constexpr (C + 32 < COLS) {
+        __syncwarp();
+        tmem_load32(at + C + 32, ahead);
+      }
+    } else {
       __syncwarp();
-      tmem_load32(at + C + 32, ahead);
+      tmem_load32(at + C, v);
+      tmem_load_wait(v);
     }
   }
 };
@@ -252,8 +269,9 @@ __device__ __forceinline__ void end_stats(const ProdArgs& g, Src& src, RowState<
 }
 
 // ---- results on their way out ------------------------------------------------------------
-// A warp's 32 rows of 128 bytes in shared memory, 16-byte pieces swizzled as the TMA store
-// expects them, so that neither side meets a bank twice.
+// A warp's 32 rows of 128 bytes (64: NARROW) in shared memory, 16-byte pieces swizzled as the
+// TMA store expects them, so that neither side meets a bank twice.
+template <bool NARROW>
 struct Outbox {
   uint32_t buf;
   int lane;
@@ -262,7 +280,8 @@ struct Outbox {
     __syncwarp();
   }
   __device__ __forceinline__ void put(int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    st_shared_v4(buf + lane * 128 + ((piece ^ (lane & 7)) << 4), a, b, c, d);
+    if constexpr (NARROW) st_shared_v4(buf + lane * 64 + ((piece ^ ((lane >> 1) & 3)) << 4), a, b, c, d);
+    else st_shared_v4(buf + lane * 128 + ((piece ^ (lane & 7)) << 4), a, b, c, d);
   }
   __device__ __forceinline__ void put16(int piece0, const float (&v)[32], bool bf16, uint32_t keep) {
 #pragma unroll
@@ -362,7 +381,7 @@ struct GradRow {
 template <int BN, bool LAB, bool DIS, class Src>
 __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* map_o, Src& src,
                                          RowState<Prod::kGrad, LAB, DIS>& rs, int64_t row, int n_tile, int half,
-                                         Outbox box) {
+                                         Outbox<!kHeld<Src>> box) {
   constexpr int kCols = BN / 2;
   const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
   const int64_t cls = g.cls0 + col0;
@@ -375,12 +394,9 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
       float v[32];
       src.template get<c>(v);
       gr.of(v, g, rs.c.t, cls + c, rs.w);
-      if constexpr (c % 64 == 0) box.open();
-      box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, keep);
-      if constexpr (c % 64 == 32) {
-        if (row0 < g.m && col0 + c - 32 < g.n)
-          box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), 0, false);
-      }
+      box.open();
+      box.put16(0, v, g.bf16, keep);
+      if (row0 < g.m && col0 + c < g.n) box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), 0, false);
     });
   } else {
     each_32<kCols>([&](auto cc) {
@@ -415,7 +431,7 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
 // ---- results of the gradient products ---------------------------------------------------
 template <int BN, class Src>
 __device__ __forceinline__ void end_sum(const ProdArgs& g, const CUtensorMap* map_o, Src& src, int64_t row, int n_tile,
-                                        int split, int half, Outbox box) {
+                                        int split, int half, Outbox<false> box) {
   constexpr int kCols = BN / 2;
   const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
   const int64_t row0 = row - box.lane;
@@ -452,10 +468,10 @@ __device__ __forceinline__ void end_sum(const ProdArgs& g, const CUtensorMap* ma
 }
 
 template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>
-__global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CUtensorMap map_a,
+__global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_prod(const __grid_constant__ CUtensorMap map_a,
                                                       const __grid_constant__ CUtensorMap map_b,
                                                       const __grid_constant__ CUtensorMap map_o, const ProdArgs g) {
-  using S = Shape<CG, BN, ACC>;
+  using S = Shape<KIND, CG, BN, ACC>;
   constexpr bool kAmn = KIND == Prod::kDw;                        // G^T: rows of G run along the result's rows
   constexpr bool kBmn = KIND == Prod::kDw || KIND == Prod::kDh;   // H and W with the summed dimension outside
   extern __shared__ unsigned char smem_raw[];
@@ -614,10 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
     if constexpr (ACC != kWhole) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
     // ---- results
     constexpr int kCols = BN / 2;
-    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    constexpr int kTurns = kGroups<KIND, ACC>;
+    const int quad = warp & 3, half = ((warp - kEpiWarp0) >> 2) & 1;
+    const int turn = kTurns == 2 ? (warp - kEpiWarp0) >> 3 : 0;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    Outbox box{out + (warp - kEpiWarp0) * 4096, lane};
-    int buf = 0;
+    Outbox<kTurns == 2 && KIND == Prod::kGrad> box{out + (warp - kEpiWarp0) * S::kBox, lane};
+    int buf = turn;
     uint32_t bph = 0;
     auto ready = [&] {
       const bool ok = __all_sync(kFull, mbar_wait(tfull + 8 * buf, bph, abort));
@@ -631,9 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
         if (CG == 2) mbar_arrive_cluster(map_to_rank(tempty + 8 * buf, 0));
         else mbar_arrive(tempty + 8 * buf);
       }
-      if (++buf == 2) buf = 0, bph ^= 1;
+      if (kTurns == 2) bph ^= 1;  // a group keeps to one accumulator
+      else if (++buf == 2) buf = 0, bph ^= 1;
     };
-    for (int t = first; t < n_tiles; t += stride) {
+    for (int t = first + turn * stride; t < n_tiles; t += kTurns * stride) {
       const Tile tl = tile_at(g, t);
       const int64_t row = int64_t(tl.m) * 128 * CG + rank * 128 + quad * 32 + lane;
       RowState<KIND, LAB, DIS> rs;
@@ -645,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
       };
       if constexpr (ACC == kWhole) {
         if (!ready()) break;
-        FromTmem<kCols> src(tmem + lanes + buf * BN + half * kCols);
+        FromTmem<kCols, kTurns == 1> src(tmem + lanes + buf * BN + half * kCols);
         finish(src);
         done();
       } else {
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prod(const __grid_constant__ CU
 
 template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>
 cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
-  using S = Shape<CG, BN, ACC>;
+  using S = Shape<KIND, CG, BN, ACC>;
   auto* k = k_prod<KIND, CG, BN, LAB, DIS, ACC>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
@@ -702,7 +721,7 @@ cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cud
   const int groups = static_cast<int>(tiles < num_sms / CG ? tiles : num_sms / CG);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -758,6 +777,10 @@ int prod_logits_cols(int cg, int planes) { return planes == 3 && cg == 1 ? 128 :
 int prod_sums_cols(int64_t dim, int64_t rows, int planes) {
   const int bn = dim > 128 ? 256 : dim > 64 ? 128 : 64;
   return planes == 3 && rows <= 128 ? (bn < 128 ? bn : 128) : bn;
+}
+
+int prod_grad_row_bytes(int planes, int chunk, int k_blocks) {
+  return planes == 3 || chunk < k_blocks ? 4096 / 32 / kGroups<Prod::kGrad, kParts> : 4096 / 32 / kGroups<Prod::kGrad, kWhole>;
 }
 
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
