@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   const bool lost = (*a.status & kLossTimeout) != 0;
   if (a.tgt.t) {
     const float l = lost ? NAN : m + logf(s1);
-    const int64_t t = row_target(a.tgt, row);
+    const int64_t t = check_target(a.tgt, raw_target(a.tgt, row));
     a.lse[row] = l;
     a.loss[row] = t == -1 ? 0.f : t == -2 ? NAN : l - a.z_t[row];
     if (t == -2) atomicOr(a.status, kLossBadTarget);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
 __global__ void __launch_bounds__(1024) k_g_max(int64_t n, const RowGrads r, unsigned* __restrict__ g_max) {
   float m = 0.f;
   for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-    const RowCoef c = row_coef(r, i);
+    const RowCoef c = row_coef(r, row_raw(r, i));
     m = fmaxf(m, fabsf(c.a) + fabsf(c.gl) + fabsf(c.b));
   }
 #pragma unroll

@@ -37,8 +37,7 @@ struct Targets {
   int64_t n_cls;
 };
 
-__device__ __forceinline__ int64_t row_target(const Targets& t, int64_t row) {  // -1: ignored, -2: out of range
-  const int64_t v = t.is64 ? static_cast<const int64_t*>(t.t)[row] : static_cast<const int32_t*>(t.t)[row];
+__device__ __forceinline__ int64_t check_target(const Targets& t, int64_t v) {  // -1: ignored, -2: out of range
   return v == t.ignore ? -1 : (v >= 0 && v < t.n_cls) ? v : -2;
 }
 
@@ -50,22 +49,46 @@ struct RowGrads {
   const float *lse_t, *g_kl;
   float inv_t;
 };
+// The row's values as they are in memory, read well before they are used.
+struct RowRaw {
+  int64_t t;
+  float lse, g_loss, g_lse, lse_t, g_kl;
+  int32_t len;
+};
+__device__ __forceinline__ int64_t raw_target(const Targets& t, int64_t row) {
+  return t.is64 ? static_cast<const int64_t*>(t.t)[row] : static_cast<const int32_t*>(t.t)[row];
+}
+__device__ __forceinline__ RowRaw row_raw(const RowGrads& r, int64_t row) {
+  RowRaw x = {0, 0.f, 0.f, 0.f, 0.f, 0.f, 0};
+  if (r.tgt.t) {
+    x.t = raw_target(r.tgt, row);
+    x.lse = r.lse[row];
+    x.g_loss = r.g_loss[row];
+    if (r.g_lse) x.g_lse = r.g_lse[row];
+  }
+  if (r.ent_len) {
+    x.len = r.ent_len[row];
+    x.lse_t = r.lse_t[row];
+    x.g_kl = r.g_kl[row];
+  }
+  return x;
+}
 // G_ij = a e^(z - lse) - gl [j = t] + b (e^(z / T - lse_t) - q)
 struct RowCoef {
   float lse, a, gl, lse_t, b;
   int64_t t;
 };
-__device__ __forceinline__ RowCoef row_coef(const RowGrads& r, int64_t row) {
+__device__ __forceinline__ RowCoef row_coef(const RowGrads& r, const RowRaw& x) {
   RowCoef c = {0.f, 0.f, 0.f, 0.f, 0.f, -1};
   if (r.tgt.t) {
-    c.t = row_target(r.tgt, row);
-    c.gl = c.t >= 0 ? r.g_loss[row] : 0.f;
-    c.lse = r.lse[row];
-    c.a = c.gl + (r.g_lse ? r.g_lse[row] : 0.f);
+    c.t = check_target(r.tgt, x.t);
+    c.gl = c.t >= 0 ? x.g_loss : 0.f;
+    c.lse = x.lse;
+    c.a = c.gl + x.g_lse;
   }
   if (r.ent_len) {
-    c.lse_t = r.lse_t[row];
-    c.b = r.ent_len[row] > 0 ? r.g_kl[row] * r.inv_t : 0.f;
+    c.lse_t = x.lse_t;
+    c.b = x.len > 0 ? x.g_kl * r.inv_t : 0.f;
   }
   return c;
 }

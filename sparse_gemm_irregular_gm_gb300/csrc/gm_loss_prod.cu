@@ -129,18 +129,25 @@ struct Walk {
   }
 };
 
-// What a thread looks up of its row before the tile's sums are there.
+// What a thread looks up of its row: read a tile ahead, used before the tile's sums are there.
 template <Prod KIND, bool LAB, bool DIS>
 struct RowState {
   Walk w;
   RowCoef c;
-  __device__ __forceinline__ void start(const ProdArgs& g, int64_t row, int64_t cls, bool first) {
-    if constexpr (KIND == Prod::kStats) {
-      c.t = LAB && row < g.m ? row_target(g.tgt, row) : -1;
-    } else if constexpr (KIND == Prod::kGrad) {
-      c = RowCoef{0.f, 0.f, 0.f, 0.f, 0.f, -1};
-      if (row < g.m) {
-        c = row_coef(g.row, row);
+  static __device__ __forceinline__ RowRaw read(const ProdArgs& g, int64_t row) {
+    RowRaw x = {};
+    if (row < g.m) {
+      if constexpr (KIND == Prod::kStats && LAB) x.t = raw_target(g.tgt, row);
+      if constexpr (KIND == Prod::kGrad) x = row_raw(g.row, row);
+    }
+    return x;
+  }
+  __device__ __forceinline__ void start(const ProdArgs& g, const RowRaw& x, int64_t row, int64_t cls, bool first) {
+    c = RowCoef{0.f, 0.f, 0.f, 0.f, 0.f, -1};
+    if (row < g.m) {
+      if constexpr (KIND == Prod::kStats && LAB) c.t = check_target(g.tgt, x.t);
+      if constexpr (KIND == Prod::kGrad) {
+        c = row_coef(g.row, x);
         if (LAB && first && c.t == -2) atomicOr(g.status, kLossBadTarget);
       }
     }
@@ -150,11 +157,13 @@ struct RowState {
 
 // The sums of a thread's row, 32 columns at a time: from TMEM (AHEAD: the next 32 under way
 // while these are used), or from registers.
-template <int COLS, bool AHEAD>
+// DONE is called once the last columns are read: the accumulator is free again.
+template <int COLS, bool AHEAD, class DONE>
 struct FromTmem {
   uint32_t at;
+  DONE& done;
   float ahead[AHEAD ? 32 : 1];
-  __device__ __forceinline__ explicit FromTmem(uint32_t addr) : at(addr) {
+  __device__ __forceinline__ FromTmem(uint32_t addr, DONE& d) : at(addr), done(d) {
     if constexpr (AHEAD) tmem_load32(at, ahead);
   }
   template <int C>
@@ -172,6 +181,7 @@ struct FromTmem {
       tmem_load32(at + C, v);
       tmem_load_wait(v);
     }
+    if constexpr (C + 32 >= COLS) done();
   }
 };
 template <int COLS>
@@ -652,11 +662,23 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       if (kTurns == 2) bph ^= 1;  // a group keeps to one accumulator
       else if (++buf == 2) buf = 0, bph ^= 1;
     };
-    for (int t = first + turn * stride; t < n_tiles; t += kTurns * stride) {
-      const Tile tl = tile_at(g, t);
-      const int64_t row = int64_t(tl.m) * 128 * CG + rank * 128 + quad * 32 + lane;
-      RowState<KIND, LAB, DIS> rs;
-      rs.start(g, row, g.cls0 + int64_t(tl.n) * BN + half * kCols, tl.n == 0 && half == 0);
+    using Row = RowState<KIND, LAB, DIS>;
+    auto row_of = [&](const Tile& x) { return int64_t(x.m) * 128 * CG + rank * 128 + quad * 32 + lane; };
+    Tile tl = {0, 0, 0};
+    RowRaw raw = {};
+    if (first + turn * stride < n_tiles) {
+      tl = tile_at(g, first + turn * stride);
+      raw = Row::read(g, row_of(tl));
+    }
+    Tile next = tl;
+    for (int t = first + turn * stride; t < n_tiles; t += kTurns * stride, tl = next) {
+      const int64_t row = row_of(tl);
+      Row rs;
+      rs.start(g, raw, row, g.cls0 + int64_t(tl.n) * BN + half * kCols, tl.n == 0 && half == 0);
+      if (t + kTurns * stride < n_tiles) {
+        next = tile_at(g, t + kTurns * stride);
+        raw = Row::read(g, row_of(next));
+      }
       auto finish = [&](auto& src) {
         if constexpr (KIND == Prod::kStats) end_stats<BN, LAB, DIS>(g, src, rs, row, tl.n, half);
         else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS>(g, &map_o, src, rs, row, tl.n, half, box);
@@ -664,9 +686,8 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       };
       if constexpr (ACC == kWhole) {
         if (!ready()) break;
-        FromTmem<kCols, kTurns == 1> src(tmem + lanes + buf * BN + half * kCols);
+        FromTmem<kCols, kTurns == 1, decltype(done)> src(tmem + lanes + buf * BN + half * kCols, done);
         finish(src);
-        done();
       } else {
         const int kb0 = tl.split * g.k_per_split, steps = min(g.k_blocks, kb0 + g.k_per_split) - kb0;
         Held<kCols> src;
