@@ -37,7 +37,13 @@ constexpr int kBK = 64;  // summed elements a stage: one 128-byte swizzled row
 //     long rows, whose error goes into the losses as it is.
 //   kSplit: fp32 operands as three bf16 planes a stage, six products of planes a stage, in TMEM
 //     over one stage, the stages added in registers.
-enum { kWhole = 0, kParts = 1, kSplit = 2 };
+//   kSplitWhole: the same, but in TMEM to the end: logits of at most two stages.
+enum { kWhole = 0, kParts = 1, kSplit = 2, kSplitWhole = 3 };
+constexpr int kWholeBlocks = 2;
+template <int ACC>
+constexpr bool three_planes = ACC == kSplit || ACC == kSplitWhole;
+template <int ACC>
+constexpr bool in_registers = ACC == kParts || ACC == kSplit;
 
 // Products of planes of split operands (x = x0 + x1 + x2 by falling size), the small ones
 // first, so that they meet a small accumulator; x1 y2, x2 y1 and x2 y2 lie under 2^-24
@@ -51,12 +57,12 @@ __device__ __forceinline__ constexpr int pair_b(int p) { return p == 0 ? 0 : p =
 // the tiles in turn, one accumulator each. Sums held in registers leave room for one group;
 // the gradients' results are only moved.
 template <Prod KIND, int ACC>
-constexpr int kGroups = ACC == kWhole && (KIND == Prod::kStats || KIND == Prod::kGrad) ? 2 : 1;
+constexpr int kGroups = !in_registers<ACC> && (KIND == Prod::kStats || KIND == Prod::kGrad) ? 2 : 1;
 
 template <Prod KIND, int CG, int BN, int ACC>
 struct Shape {
   static constexpr int kThreads = 128 + 256 * kGroups<KIND, ACC>;
-  static constexpr int kPlanes = ACC == kSplit ? 3 : 1;
+  static constexpr int kPlanes = three_planes<ACC> ? 3 : 1;
   static constexpr int kABytes = 128 * 128;            // a plane of this block's 128 rows of A
   static constexpr int kBRows = BN / CG;               // its rows (columns) of B
   static constexpr int kBBytes = kBRows * 128;
@@ -388,7 +394,7 @@ struct GradRow {
   }
 };
 
-template <int BN, bool LAB, bool DIS, class Src>
+template <int BN, bool LAB, bool DIS, bool FINE, class Src>
 __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* map_o, Src& src,
                                          RowState<Prod::kGrad, LAB, DIS>& rs, int64_t row, int n_tile, int half,
                                          Outbox<!kHeld<Src>> box) {
@@ -396,7 +402,7 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
   const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
   const int64_t cls = g.cls0 + col0;
   const int64_t row0 = row - box.lane;
-  const GradRow<LAB, DIS, kHeld<Src>> gr(g, rs.c);
+  const GradRow<LAB, DIS, FINE> gr(g, rs.c);
   const uint32_t keep = gr.live ? 0xffffffffu : 0u;  // a row without weight is 0 whatever its logits are
   if constexpr (!kHeld<Src>) {
     each_32<kCols>([&](auto cc) {
@@ -404,9 +410,16 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
       float v[32];
       src.template get<c>(v);
       gr.of(v, g, rs.c.t, cls + c, rs.w);
-      box.open();
-      box.put16(0, v, g.bf16, keep);
-      if (row0 < g.m && col0 + c < g.n) box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), 0, false);
+#pragma unroll
+      for (int p = 0; p < (FINE ? 3 : 1); ++p) {
+        box.open();
+        box.put16(0, v, g.bf16, keep);
+        if (row0 < g.m && col0 + c < g.n) box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), p, false);
+        if (FINE) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+        }
+      }
     });
   } else {
     each_32<kCols>([&](auto cc) {
@@ -520,11 +533,11 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
 
   const int n_tiles = g.m_tiles * g.n_tiles * g.splits;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
-  const int chunk = ACC == kWhole ? (1 << 30) : ACC == kSplit ? 1 : g.chunk;  // stages an accumulator takes
+  const int chunk = !in_registers<ACC> ? (1 << 30) : ACC == kSplit ? 1 : g.chunk;  // stages an accumulator takes
   volatile int* abort = &s_abort;
 
   if (warp < kEpiWarp0) {
-    if constexpr (ACC != kWhole) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if constexpr (in_registers<ACC>) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
       // ---- loads
       const bool one = elect_one();
@@ -610,8 +623,8 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
             tc_fence_after();
             if (one) {
 #pragma unroll
-              for (int p = 0; p < (ACC == kSplit ? 6 : 1); ++p) {
-                const int pa = ACC == kSplit ? pair_a(p) : 0, pb = ACC == kSplit ? pair_b(p) : 0;
+              for (int p = 0; p < (three_planes<ACC> ? 6 : 1); ++p) {
+                const int pa = three_planes<ACC> ? pair_a(p) : 0, pb = three_planes<ACC> ? pair_b(p) : 0;
                 const uint64_t da = desc_a + ((st * S::kStage + pa * S::kABytes) >> 4);
                 const uint64_t db = desc_b + ((st * S::kStage + pb * S::kBBytes) >> 4);
 #pragma unroll
@@ -637,7 +650,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       }
     }
   } else {
-    if constexpr (ACC != kWhole) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
+    if constexpr (in_registers<ACC>) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
     // ---- results
     constexpr int kCols = BN / 2;
     constexpr int kTurns = kGroups<KIND, ACC>;
@@ -681,10 +694,10 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       }
       auto finish = [&](auto& src) {
         if constexpr (KIND == Prod::kStats) end_stats<BN, LAB, DIS>(g, src, rs, row, tl.n, half);
-        else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS>(g, &map_o, src, rs, row, tl.n, half, box);
+        else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS, ACC != kWhole>(g, &map_o, src, rs, row, tl.n, half, box);
         else end_sum<BN>(g, &map_o, src, row, tl.n, tl.split, half, box);
       };
-      if constexpr (ACC == kWhole) {
+      if constexpr (!in_registers<ACC>) {
         if (!ready()) break;
         FromTmem<kCols, kTurns == 1, decltype(done)> src(tmem + lanes + buf * BN + half * kCols, done);
         finish(src);
@@ -732,7 +745,7 @@ cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cud
   auto* k = k_prod<KIND, CG, BN, LAB, DIS, ACC>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
-  if (ACC != kWhole) {
+  if (in_registers<ACC>) {
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, k);
     if (e != cudaSuccess) return e;
@@ -766,6 +779,9 @@ cudaError_t launch_modes(const ProdMaps& maps, const ProdArgs& a, int num_sms, c
 
 template <Prod KIND>
 cudaError_t launch_logits(int cg, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
+  if (a.planes == 3 && a.k_blocks <= kWholeBlocks)
+    return cg == 2 ? launch_modes<KIND, 2, 256, kSplitWhole>(maps, a, num_sms, s)
+                   : launch_modes<KIND, 1, 128, kSplitWhole>(maps, a, num_sms, s);
   if (a.planes == 3)
     return cg == 2 ? launch_modes<KIND, 2, 256, kSplit>(maps, a, num_sms, s)
                    : launch_modes<KIND, 1, 128, kSplit>(maps, a, num_sms, s);
@@ -801,7 +817,8 @@ int prod_sums_cols(int64_t dim, int64_t rows, int planes) {
 }
 
 int prod_grad_row_bytes(int planes, int chunk, int k_blocks) {
-  return planes == 3 || chunk < k_blocks ? 4096 / 32 / kGroups<Prod::kGrad, kParts> : 4096 / 32 / kGroups<Prod::kGrad, kWhole>;
+  const bool held = planes == 3 ? k_blocks > kWholeBlocks : chunk < k_blocks;
+  return held ? 128 / kGroups<Prod::kGrad, kParts> : 128 / kGroups<Prod::kGrad, kWhole>;
 }
 
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
