@@ -667,14 +667,15 @@ struct Grads {
   int64_t dw_ld;
 };
 
-// Where a gradient goes: by TMA where its rows start on 16-byte boundaries.
+// Where a gradient goes: by TMA where its rows start and end on 16-byte boundaries (a store
+// drops what lies outside the map by 16 bytes, not by elements).
 bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t dim, int64_t ld, int32_t type) {
   const int es = static_cast<int>(elem_bytes(type));
   g.out = out;
   g.out_ld = ld;
   g.out_type = type;
   // half a tile of 64 columns of 2 bytes is less than a box
-  g.by_tma = aligned(out, 16) && (rows <= 1 || ld * es % 16 == 0) && (es == 4 || dim > 64);
+  g.by_tma = aligned(out, 16) && (rows <= 1 || ld * es % 16 == 0) && dim * es % 16 == 0 && (es == 4 || dim > 64);
   if (!g.by_tma) return true;
   if (rows <= 1) ld = up(dim, 16 / es);
   return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
