@@ -22,7 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgm_spgemm.so")
 LIB_CHECKED = os.path.join(HERE, "libgm_spgemm_checked.so")
 SOURCES = ["gm_api.cu", "gm_analyze.cu", "gm_scan.cu", "gm_expand.cu", "gm_multisplit.cu", "gm_accum.cu", "gm_rowbitmap.cu",
-           "gm_stream.cu", "gm_noalloc.cu", "gm_loss.cu", "gm_loss_prod.cu"]
+           "gm_stream.cu", "gm_noalloc.cu", "gm_loss.cu", "gm_loss_prod.cu",
+           "gm_loss_skinny.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -292,16 +292,36 @@ __global__ void __launch_bounds__(1024) k_g_max(int64_t n, const RowGrads r, uns
   }
 }
 
-// dh = the splits' sums, rounded
-__global__ void k_sum_splits(const float* __restrict__ acc, int splits, int64_t split_stride, int64_t rows, int64_t dim,
-                             int64_t acc_ld, void* __restrict__ out, int64_t out_ld, int type,
-                             const unsigned* __restrict__ g_max, const int* __restrict__ status) {
-  const int64_t n = rows * dim, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+// dh = the splits' sums, rounded. SUB threads share the splits of an element (fixed order): 1
+// where there are few splits of many elements, 8 where it is the other way round.
+template <int SUB>
+__global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ acc, int splits, int64_t split_stride,
+                                                    int64_t rows, int64_t dim, int64_t acc_ld, void* __restrict__ out,
+                                                    int64_t out_ld, int type, const unsigned* __restrict__ g_max,
+                                                    const int* __restrict__ status) {
+  constexpr int kCols = 256 / SUB;
+  __shared__ float sh[SUB][kCols];
+  const int64_t n = rows * dim, stride = static_cast<int64_t>(gridDim.x) * kCols;
+  const int col = threadIdx.x % kCols, sub = threadIdx.x / kCols;
   const float inv = (*status & kLossTimeout) ? NAN : 1.f / g_scale_of(g_max);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kCols; i0 < n; i0 += stride) {
+    const int64_t i = i0 + col;
     const int64_t r = i / dim, c = i - r * dim;
     float x = 0.f;
-    for (int s = 0; s < splits; ++s) x += acc[s * split_stride + r * acc_ld + c];
+    if (i < n) {
+      const float* p = acc + r * acc_ld + c;
+#pragma unroll 4
+      for (int s = sub; s < splits; s += SUB) x += p[s * split_stride];
+    }
+    if constexpr (SUB > 1) {
+      __syncthreads();
+      sh[sub][col] = x;
+      __syncthreads();
+      if (sub != 0) continue;
+#pragma unroll
+      for (int s = 1; s < SUB; ++s) x += sh[s][col];
+    }
+    if (i >= n) continue;
     x *= inv;
     const int64_t o = r * out_ld + c;
     if (type == GM_LOSS_F32) static_cast<float*>(out)[o] = x;
@@ -581,11 +601,41 @@ int group_of(int64_t m_tiles, int64_t tile_rows, int64_t dim, int planes) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(m_tiles, (int64_t(40) << 20) / bytes)));
 }
 
+// Few rows go to kernels that read W once as it lies, instead of the tensor cores.
+bool skinny(const Call& c) { return c.z.n_rows <= skinny_rows(c.z.type) && c.z.dim <= kSkinnyDim; }
+// Elements of a load of matrices whose rows start at p, ld elements apart: 16 bytes, 4, or one element.
+int skinny_vec(const void* p, int64_t ld, int64_t dim, int64_t rows, int64_t es) {
+  if (rows <= 1) ld = dim;
+  if (aligned(p, 16) && ld * es % 16 == 0 && dim * es % 16 == 0) return static_cast<int>(16 / es);
+  return es == 2 && aligned(p, 4) && ld % 2 == 0 && dim % 2 == 0 ? 2 : 1;
+}
+SkinnyArgs skinny_args(const Call& c, const Arena& a, const TeacherPlan& t) {
+  SkinnyArgs g = {};
+  g.h = c.z.h;
+  g.w = c.z.w;
+  g.h_ld = c.z.h_ld;
+  g.w_ld = c.z.w_ld;
+  g.dim = c.z.dim;
+  g.n_cls = c.z.n_classes;
+  g.n = static_cast<int>(c.z.n_rows);
+  g.tgt = targets_of(c);
+  g.inv_t = 1.f / c.temperature;
+  g.c_t = kLog2e / c.temperature;
+  g.status = c.status;
+  if (c.teacher) {
+    g.ent_start = a.at<int64_t>(t.start);
+    g.ent_len = a.at<int32_t>(t.len);
+    g.ents = a.at<int2>(t.ents);
+  }
+  return g;
+}
+
 // How a forward call is cut, and where its workspace lies.
 struct ForwardPlan {
   Arena a;
   Source h, w;
   TeacherPlan t;
+  int blocks = 0;  // of the kernel for few rows; 0: the product
   int cg, bn;
   int64_t n_tiles, n_parts;
   size_t o_part, o_zt;
@@ -596,8 +646,12 @@ struct ForwardPlan {
     bn = prod_logits_cols(cg, h.planes());
     n_tiles = div_up(c.z.n_classes, bn);
     n_parts = 2 * n_tiles;
-    h.plan(a);
-    w.plan(a);
+    if (skinny(c)) {
+      n_parts = blocks = skinny_most_blocks(c.z.n_classes, c.sms);
+    } else {
+      h.plan(a);
+      w.plan(a);
+    }
     t.plan(a, c);
     o_part = a.add(n_parts * n * 16);
     o_zt = a.add(n * 4);
@@ -614,34 +668,44 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   rc = a.open(c);
   if (rc != GM_OK) return rc;
   const TeacherPlan& t = p.t;
-  const int cg = p.cg, bn = p.bn;
-  const int64_t n_tiles = p.n_tiles, n_parts = p.n_parts;
-  const size_t o_part = p.o_part, o_zt = p.o_zt;
-  const Operand oh = p.h.ready(a, c.s), ow = p.w.ready(a, c.s);
-  t.launch(a, c);
-  ProdMaps maps;
-  if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(cg, bn))) return GM_ERR_CUDA;
-  maps.o = maps.a;  // not used
-  ProdArgs g = {};
-  set_logits_args(g, c, a, t);
-  g.m = n;
-  g.n = c.z.n_classes;
-  g.m_tiles = static_cast<int>(div_up(n, 128 * cg));
-  g.n_tiles = static_cast<int>(n_tiles);
-  g.splits = 1;
-  g.k_blocks = g.k_per_split = static_cast<int>(div_up(c.z.dim, 64));
-  g.group = group_of(g.m_tiles, 128 * cg, c.z.dim, g.planes);
-  g.part = a.at<float4>(o_part);
-  g.part_ld = n;
-  g.z_t = a.at<float>(o_zt);
-  bool ok = launch_prod(Prod::kStats, cg, bn, maps, g, c.sms, c.s) == cudaSuccess;
+  float4* part = a.at<float4>(p.o_part);
+  float* z_t = a.at<float>(p.o_zt);
+  bool ok;
+  if (p.blocks) {
+    t.launch(a, c);
+    SkinnyArgs g = skinny_args(c, a, t);
+    g.part = part;
+    g.z_t = z_t;
+    const int vec = skinny_vec(g.w, g.w_ld, g.dim, g.n_cls, elem_bytes(c.z.type));
+    ok = launch_skinny(g, c.z.type, false, vec, &p.blocks, c.s) == cudaSuccess;
+    p.n_parts = p.blocks;
+  } else {
+    const Operand oh = p.h.ready(a, c.s), ow = p.w.ready(a, c.s);
+    t.launch(a, c);
+    ProdMaps maps;
+    if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(p.cg, p.bn))) return GM_ERR_CUDA;
+    maps.o = maps.a;  // not used
+    ProdArgs g = {};
+    set_logits_args(g, c, a, t);
+    g.m = n;
+    g.n = c.z.n_classes;
+    g.m_tiles = static_cast<int>(div_up(n, 128 * p.cg));
+    g.n_tiles = static_cast<int>(p.n_tiles);
+    g.splits = 1;
+    g.k_blocks = g.k_per_split = static_cast<int>(div_up(c.z.dim, 64));
+    g.group = group_of(g.m_tiles, 128 * p.cg, c.z.dim, g.planes);
+    g.part = part;
+    g.part_ld = n;
+    g.z_t = z_t;
+    ok = launch_prod(Prod::kStats, p.cg, p.bn, maps, g, c.sms, c.s) == cudaSuccess;
+  }
   JoinArgs j = {};
-  j.part = g.part;
-  j.n_parts = n_parts;
+  j.part = part;
+  j.n_parts = p.n_parts;
   j.n_rows = n;
-  j.tgt = g.tgt;
-  j.z_t = g.z_t;
-  j.ent_len = g.ent_len;
+  j.tgt = targets_of(c);
+  j.z_t = z_t;
+  j.ent_len = c.teacher ? a.at<int32_t>(t.len) : nullptr;
   j.base = c.teacher ? a.at<float>(t.base) : nullptr;
   j.inv_t = 1.f / c.temperature;
   j.loss = loss;
@@ -681,6 +745,17 @@ bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t di
   return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
 }
 
+void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const unsigned* g_max) {
+  const int64_t n = c.z.n_rows * c.z.dim, stride = c.z.n_rows * acc_ld;
+  if (splits >= 16)
+    k_sum_splits<8><<<grid_for(n, 32), 256, 0, c.s>>>(acc, splits, stride, c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld,
+                                                      c.z.type, g_max, c.status);
+  else
+    k_sum_splits<1><<<grid_for(n, 256), 256, 0, c.s>>>(acc, splits, stride, c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld,
+                                                       c.z.type, g_max, c.status);
+  note_launch();
+}
+
 // How a backward call is cut, and where its workspace lies.
 struct BackwardPlan {
   Arena a;
@@ -691,11 +766,18 @@ struct BackwardPlan {
   int64_t splits;  // of dH's sum along a piece's classes
   bool dh_direct;  // dH needs no sum over pieces or splits
   int64_t acc_ld;
-  size_t o_max, o_g, o_acc;
+  int blocks = 0;  // of the kernel for few rows; 0: the products
+  size_t o_max = 0, o_g = 0, o_acc = 0;
   explicit BackwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
     const int64_t n = c.z.n_rows, cls = c.z.n_classes, dim = c.z.dim;
     planes = c.z.type == GM_LOSS_F32 ? 3 : 1;
+    if (skinny(c)) {
+      blocks = skinny_most_blocks(cls, c.sms);
+      t.plan(a, c);
+      o_acc = a.add(blocks * n * dim * 4);
+      return;
+    }
     // pieces of the classes: as few as the bound on G allows, of about equal width
     const int64_t most = std::max<int64_t>(256, c.cap / (n * 2 * planes) / 256 * 256);
     const int64_t n_pieces = div_up(cls, most);
@@ -734,6 +816,22 @@ gm_status backward(Call& c, const Grads& q) {
   rc = a.open(c);
   if (rc != GM_OK) return rc;
   const TeacherPlan& t = p.t;
+  const RowGrads row{targets_of(c), q.lse,   q.g_loss, q.g_lse, c.teacher ? a.at<int32_t>(t.len) : nullptr,
+                     q.lse_t,       q.g_kl, 1.f / c.temperature};
+  if (p.blocks) {
+    t.launch(a, c);
+    SkinnyArgs g = skinny_args(c, a, t);
+    g.row = row;
+    g.dh = q.dh;
+    g.dw = q.dw;
+    g.dw_ld = q.dw_ld;
+    g.acc = a.at<float>(p.o_acc);
+    int vec = skinny_vec(g.w, g.w_ld, dim, cls, es);
+    if (q.dw) vec = std::min(vec, skinny_vec(q.dw, q.dw_ld, dim, cls, es));
+    const bool ok = launch_skinny(g, c.z.type, true, vec, &p.blocks, c.s) == cudaSuccess;
+    if (ok && q.dh) sum_splits(c, g.acc, p.blocks, dim, q, nullptr);
+    return finish(c, ok);
+  }
   const int planes = p.planes, bn_h = p.bn_h, bn_w = p.bn_w, cg_h = p.cg_h, cg_w = p.cg_w;
   const int64_t width = p.width, g_ld = p.width, splits = p.splits, acc_ld = p.acc_ld;
   const bool dh_direct = p.dh_direct;
@@ -742,7 +840,7 @@ gm_status backward(Call& c, const Grads& q) {
   t.launch(a, c);
   ProdArgs base = {};
   set_logits_args(base, c, a, t);
-  base.row = RowGrads{base.tgt, q.lse, q.g_loss, q.g_lse, base.ent_len, q.lse_t, q.g_kl, 1.f / c.temperature};
+  base.row = row;
   unsigned* g_max = nullptr;
   if (c.z.type == GM_LOSS_F16) {
     g_max = a.at<unsigned>(p.o_max);
@@ -814,11 +912,8 @@ gm_status backward(Call& c, const Grads& q) {
       ok = launch_prod(Prod::kDw, cg_w, bn_w, maps, g, c.sms, c.s) == cudaSuccess;
     }
   }
-  if (ok && q.dh && !dh_direct) {
-    k_sum_splits<<<grid_for(n * dim, 256), 256, 0, c.s>>>(a.at<float>(o_acc), static_cast<int>(splits), n * acc_ld, n,
-                                                          dim, acc_ld, q.dh, q.dh_ld, c.z.type, g_max, c.status);
-    note_launch();
-  }
+  if (ok && q.dh && !dh_direct)
+    sum_splits(c, a.at<float>(o_acc), static_cast<int>(splits), acc_ld, q, g_max);
   return finish(c, ok);
 }
 

@@ -153,4 +153,31 @@ int prod_grad_row_bytes(int planes, int chunk, int k_blocks);
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
                         cudaStream_t s);
 
+// ---- few rows (gm_loss_skinny.cu) --------------------------------------------------------
+constexpr int64_t kSkinnyDim = 4096;  // elements of a row of H at most: H and the sums of dH fit a block
+int skinny_rows(int type);            // rows at most
+struct SkinnyArgs {
+  const void *h, *w;
+  int64_t h_ld, w_ld, dim, n_cls;
+  int n;
+  int64_t per_warp, per_block;  // classes of a warp (forward), of a block (backward); set by the launch
+  Targets tgt;
+  const int64_t* ent_start;     // teacher; ent_len null: none
+  const int32_t* ent_len;
+  const int2* ents;
+  float inv_t, c_t;
+  int* status;
+  float4* part;                 // forward: [block][row]
+  float* z_t;
+  RowGrads row;                 // backward
+  void *dh, *dw;                // null: not wanted (dh: whether acc is written)
+  int64_t dw_ld;
+  float* acc;                   // [block][row][dim]
+};
+// Blocks of a launch at most, for the workspace.
+int skinny_most_blocks(int64_t n_cls, int sms);
+// vec: elements of a load of W (and store of dW): 16 bytes, 4 or one element, as rows allow.
+// *blocks: at most so many, then how many there are.
+cudaError_t launch_skinny(const SkinnyArgs& a, int type, bool backward, int vec, int* blocks, cudaStream_t s);
+
 }  // namespace gm

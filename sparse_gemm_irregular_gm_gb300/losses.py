@@ -146,8 +146,8 @@ class _Call:
             self.on.__exit__(*a)
 
     def vectors(self, k):
-        """k uninitialised results, a float a row (parts of one allocation)."""
-        return torch.empty((k, self.n), dtype=torch.float32, device=self.device).unbind(0)
+        """k uninitialised results, a float a row."""
+        return [torch.empty(self.n, dtype=torch.float32, device=self.device) for _ in range(k)]
 
     def run(self, name, backward, *args):
         lib = load()
