@@ -32,6 +32,7 @@ __device__ int g_loss_status;
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int64_t rows, int dim, int64_t src_ld,
                                               uint16_t* __restrict__ dst, int ld) {
+  chain_wait();
   const unsigned per_row = static_cast<unsigned>(ld) / 8;
   const int64_t n = rows * ld, pieces = rows * per_row, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) k_teacher(const TeacherArg
   __shared__ float sh[kTeacherWarps];
   __shared__ unsigned s_long;
   const int warp = threadIdx.x >> 5;
+  chain_wait();
   for (int64_t row0 = blockIdx.x; row0 < a.n_rows; row0 += int64_t(gridDim.x) * kTeacherWarps) {
     if (threadIdx.x == 0) s_long = 0;
     __syncthreads();
@@ -224,6 +226,7 @@ struct JoinArgs {
 template <int ROWS>  // rows of a block; 256 / ROWS threads a row
 __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   constexpr int kSub = 256 / ROWS;
+  chain_wait();
   const int rl = threadIdx.x % ROWS, sub = threadIdx.x / ROWS;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + rl;
   const bool dis = a.ent_len != nullptr;
@@ -276,6 +279,7 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
 // ---- scale of G in f16 ------------------------------------------------------------------------
 // Bits of the largest |G| that the rows' weights allow, one block.
 __global__ void __launch_bounds__(1024) k_g_max(int64_t n, const RowGrads r, unsigned* __restrict__ g_max) {
+  chain_wait();
   float m = 0.f;
   for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
     const RowCoef c = row_coef(r, row_raw(r, i));
@@ -301,6 +305,7 @@ __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ ac
                                                     const int* __restrict__ status) {
   constexpr int kCols = 256 / SUB;
   __shared__ float sh[SUB][kCols];
+  chain_wait();
   const int64_t n = rows * dim, stride = static_cast<int64_t>(gridDim.x) * kCols;
   const int col = threadIdx.x % kCols, sub = threadIdx.x / kCols;
   const float inv = (*status & kLossTimeout) ? NAN : 1.f / g_scale_of(g_max);
@@ -531,11 +536,9 @@ struct Source {
       const unsigned grid = grid_for(rows * ld / 8, 256);
       uint16_t* dst = a.at<uint16_t>(off);
       const int d = static_cast<int>(dim), l = static_cast<int>(ld);
-      if (type != GM_LOSS_F32) k_pack<false, false><<<grid, 256, 0, s>>>(p, rows, d, src_ld, dst, l);
-      else if (aligned(p, 16) && (rows <= 1 || src_ld % 4 == 0))
-        k_pack<true, true><<<grid, 256, 0, s>>>(p, rows, d, src_ld, dst, l);
-      else k_pack<true, false><<<grid, 256, 0, s>>>(p, rows, d, src_ld, dst, l);
-      note_launch();
+      const bool vec = aligned(p, 16) && (rows <= 1 || src_ld % 4 == 0);
+      launch_chained(type != GM_LOSS_F32 ? k_pack<false, false> : vec ? k_pack<true, true> : k_pack<true, false>, grid,
+                     256, 0, s, 1, p, rows, d, src_ld, dst, l);
     }
     return o;
   }
@@ -558,8 +561,7 @@ struct TeacherPlan {
                                     static_cast<const V*>(c.teacher->vals), c.z.n_rows, c.z.n_classes, c.nnz,
                                     1.f / c.temperature, a.at<int64_t>(start), a.at<int32_t>(len), a.at<int2>(ents),
                                     a.at<float>(base), c.status};
-    k_teacher<V, R, C><<<static_cast<unsigned>(blocks), 32 * kTeacherWarps, 0, c.s>>>(args);
-    note_launch();
+    launch_chained(k_teacher<V, R, C>, static_cast<unsigned>(blocks), 32 * kTeacherWarps, 0, c.s, 1, args);
   }
   template <class V>
   void run_indices(const Arena& a, const Call& c) const {
@@ -716,9 +718,8 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   if (ok) {
     // few rows: a block each, so that their half tiles are read by many threads
     // many: 8 rows a block, whose half tiles lie in whole 128-byte lines
-    if (n <= 2 * c.sms) k_join<1><<<static_cast<unsigned>(n), 256, 0, c.s>>>(j);
-    else k_join<8><<<static_cast<unsigned>(div_up(n, 8)), 256, 0, c.s>>>(j);
-    note_launch();
+    ok = (n <= 2 * c.sms ? launch_chained(k_join<1>, static_cast<unsigned>(n), 256, 0, c.s, 1, j)
+                         : launch_chained(k_join<8>, static_cast<unsigned>(div_up(n, 8)), 256, 0, c.s, 1, j)) == cudaSuccess;
   }
   return finish(c, ok);
 }
@@ -747,13 +748,9 @@ bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t di
 
 void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const unsigned* g_max) {
   const int64_t n = c.z.n_rows * c.z.dim, stride = c.z.n_rows * acc_ld;
-  if (splits >= 16)
-    k_sum_splits<8><<<grid_for(n, 32), 256, 0, c.s>>>(acc, splits, stride, c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld,
-                                                      c.z.type, g_max, c.status);
-  else
-    k_sum_splits<1><<<grid_for(n, 256), 256, 0, c.s>>>(acc, splits, stride, c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld,
-                                                       c.z.type, g_max, c.status);
-  note_launch();
+  const bool many = splits >= 16;
+  launch_chained(many ? k_sum_splits<8> : k_sum_splits<1>, grid_for(n, many ? 32 : 256), 256, 0, c.s, 1, acc, splits, stride,
+                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), g_max, c.status);
 }
 
 // How a backward call is cut, and where its workspace lies.
@@ -844,8 +841,7 @@ gm_status backward(Call& c, const Grads& q) {
   unsigned* g_max = nullptr;
   if (c.z.type == GM_LOSS_F16) {
     g_max = a.at<unsigned>(p.o_max);
-    k_g_max<<<1, 1024, 0, c.s>>>(n, base.row, g_max);
-    note_launch();
+    launch_chained(k_g_max, 1, 1024, 0, c.s, 1, n, base.row, g_max);
   }
   base.g_max = g_max;
   uint16_t* g_mem = a.at<uint16_t>(o_g);

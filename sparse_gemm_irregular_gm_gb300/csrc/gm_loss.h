@@ -12,6 +12,29 @@
 
 namespace gm {
 
+// Launches k so that its start overlaps the end of the kernel before it; k calls chain_wait
+// (gm_umma.cuh). cluster: blocks of a cluster.
+template <class... P, class... A>
+cudaError_t launch_chained(void (*k)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, unsigned cluster,
+                           A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, static_cast<A&&>(args)...);
+  note_launch();
+  return e;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Bits of the losses' status word (one a device, read by gm_loss_status).

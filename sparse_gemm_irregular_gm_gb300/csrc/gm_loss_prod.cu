@@ -530,6 +530,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  chain_wait();
 
   const int n_tiles = g.m_tiles * g.n_tiles * g.splits;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
@@ -753,20 +754,7 @@ cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cud
   }
   const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
   const int groups = static_cast<int>(tiles < num_sms / CG ? tiles : num_sms / CG);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k, maps.a, maps.b, maps.o, a);
-  note_launch();
-  return e;
+  return launch_chained(k, static_cast<unsigned>(groups * CG), S::kThreads, S::kSmem, s, CG, maps.a, maps.b, maps.o, a);
 }
 
 template <Prod KIND, int CG, int BN, int ACC>

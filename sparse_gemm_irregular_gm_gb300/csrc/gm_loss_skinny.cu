@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps) k_skinny_stats(const Skinn
   extern __shared__ __align__(16) float hs[];
   __shared__ float4 parts[kForwardWarps][N];
   const int pieces = static_cast<int>((a.dim + VEC - 1) / VEC);
+  chain_wait();
   stage_h<T, N, VEC>(a, hs, pieces);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(THREADS) k_skinny_grads(const SkinnyArgs a) {
   extern __shared__ __align__(16) float hs[];
   __shared__ __align__(16) float gs[kT][N];
   const int pieces = static_cast<int>((a.dim + VEC - 1) / VEC);
+  chain_wait();
   stage_h<T, N, VEC>(a, hs, pieces);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -424,9 +426,7 @@ cudaError_t run_forward(SkinnyArgs a, int* blocks, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t warps = int64_t(*blocks) * kForwardWarps, each = (a.n_cls + warps - 1) / warps;
   a.per_warp = (each + kClasses<N> - 1) / kClasses<N> * kClasses<N>;
-  k<<<*blocks, 32 * kForwardWarps, smem, s>>>(a);
-  note_launch();
-  return cudaPeekAtLastError();
+  return launch_chained(k, *blocks, 32 * kForwardWarps, smem, s, 1, a);
 }
 template <class T, int N, int VEC, int THREADS>
 cudaError_t run_backward(SkinnyArgs a, int* blocks, cudaStream_t s) {
@@ -437,9 +437,7 @@ cudaError_t run_backward(SkinnyArgs a, int* blocks, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t each = (a.n_cls + *blocks - 1) / *blocks;
   a.per_block = (each + kT - 1) / kT * kT;
-  k<<<*blocks, THREADS, smem, s>>>(a);
-  note_launch();
-  return cudaPeekAtLastError();
+  return launch_chained(k, *blocks, THREADS, smem, s, 1, a);
 }
 
 template <class T, int N, int VEC>

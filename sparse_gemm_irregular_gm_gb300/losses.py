@@ -182,13 +182,13 @@ def gm_xent_backward(h, w, target, lse, grad_loss, grad_lse, dh, dw, *, ignore_i
                      check=False, stream=None):
     c = _Call(h, w, target, ignore_index, None, check, workspace_cap_bytes, stream)
     with c:
-        _xent_backward(c, lse, grad_loss, grad_lse, dh, dw)
+        _xent_backward(c, lse, grad_loss, grad_lse, _gradient("dh", dh, h), _gradient("dw", dw, w))
 
 
 def _xent_backward(c, lse, grad_loss, grad_lse, dh, dw):
     n, dev = c.n, c.device
     c.run("gm_xent_backward", 1, _vector("lse", lse, n, dev), _vector("grad_loss", grad_loss, n, dev),
-          _vector("grad_lse", grad_lse, n, dev), *_gradient("dh", dh, c.h), *_gradient("dw", dw, c.w))
+          _vector("grad_lse", grad_lse, n, dev), *dh, *dw)
 
 
 def _gradient(name, t, of):
@@ -197,6 +197,11 @@ def _gradient(name, t, of):
 
 def _like(x, need):
     return torch.empty(x.shape, dtype=x.dtype, device=x.device) if need else None
+
+
+def _own(t):
+    """A gradient that _like made, as arguments."""
+    return (None, 0) if t is None else (t.data_ptr() or None, max(t.shape[1], 1))
 
 
 def xent_forward(h, w, target, *, ignore_index=-100, check=False, stream=None):
@@ -214,7 +219,7 @@ def xent_backward(h, w, target, lse, grad_loss, grad_lse=None, *, ignore_index=-
     c = _Call(h, w, target, ignore_index, None, check, workspace_cap_bytes, stream)
     with c:
         dh, dw = _like(h, need_h), _like(w, need_w)
-        _xent_backward(c, lse, grad_loss, grad_lse, dh, dw)
+        _xent_backward(c, lse, grad_loss, grad_lse, _own(dh), _own(dw))
     return dh, dw
 
 
@@ -246,14 +251,14 @@ def gm_distill_backward(h, w, teacher, temperature, lse_t, grad_kl, dh, dw, targ
                         grad_lse=None, *, ignore_index=-100, workspace_cap_bytes=0, check=False, stream=None):
     c = _distill_call(h, w, teacher, temperature, target, ignore_index, check, workspace_cap_bytes, stream)
     with c:
-        _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dw)
+        _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, _gradient("dh", dh, h), _gradient("dw", dw, w))
 
 
 def _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dw):
     n, dev = c.n, c.device
     c.run("gm_distill_backward", 1, _vector("lse_t", lse_t, n, dev), _vector("grad_kl", grad_kl, n, dev),
           _vector("lse", lse, n, dev), _vector("grad_loss", grad_loss, n, dev), _vector("grad_lse", grad_lse, n, dev),
-          *_gradient("dh", dh, c.h), *_gradient("dw", dw, c.w))
+          *dh, *dw)
 
 
 def distill_forward(h, w, teacher: DeviceCSR, temperature=1.0, *, target=None, ignore_index=-100, check=False,
@@ -275,7 +280,7 @@ def distill_backward(h, w, teacher: DeviceCSR, lse_t, grad_kl, temperature=1.0, 
     c = _distill_call(h, w, teacher, temperature, target, ignore_index, check, workspace_cap_bytes, stream)
     with c:
         dh, dw = _like(h, need_h), _like(w, need_w)
-        _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, dh, dw)
+        _distill_backward(c, lse_t, grad_kl, lse, grad_loss, grad_lse, _own(dh), _own(dw))
     return dh, dw
 
 
