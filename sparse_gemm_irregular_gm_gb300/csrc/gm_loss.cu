@@ -758,7 +758,7 @@ struct BackwardPlan {
   Arena a;
   Source h, w;
   TeacherPlan t;
-  int planes, bn_h, bn_w, cg_h, cg_w;
+  int planes, g_planes, bn_h, bn_w, cg_h, cg_w;
   int64_t width;   // classes of a piece; rows of G are as long
   int64_t splits;  // of dH's sum along a piece's classes
   bool dh_direct;  // dH needs no sum over pieces or splits
@@ -775,8 +775,9 @@ struct BackwardPlan {
       o_acc = a.add(blocks * n * dim * 4);
       return;
     }
+    g_planes = planes == 3 ? 3 : n <= 128 ? 2 : 1;
     // pieces of the classes: as few as the bound on G allows, of about equal width
-    const int64_t most = std::max<int64_t>(256, c.cap / (n * 2 * planes) / 256 * 256);
+    const int64_t most = std::max<int64_t>(256, c.cap / (n * 2 * g_planes) / 256 * 256);
     const int64_t n_pieces = div_up(cls, most);
     width = std::min<int64_t>(most, up(div_up(cls, n_pieces), 256));
     // tiles of dH: split along the classes when they are fewer than the SMs
@@ -794,7 +795,7 @@ struct BackwardPlan {
     w.plan(a);
     t.plan(a, c);
     o_max = a.add(4);
-    o_g = a.add(planes * n * width * 2);
+    o_g = a.add(g_planes * n * width * 2);
     o_acc = dh_direct ? 0 : a.add(splits * n * acc_ld * 4);
   }
 };
@@ -838,6 +839,7 @@ gm_status backward(Call& c, const Grads& q) {
   ProdArgs base = {};
   set_logits_args(base, c, a, t);
   base.row = row;
+  base.g_planes = p.g_planes;
   unsigned* g_max = nullptr;
   if (c.z.type == GM_LOSS_F16) {
     g_max = a.at<unsigned>(p.o_max);
@@ -848,7 +850,7 @@ gm_status backward(Call& c, const Grads& q) {
   bool ok = true;
   for (int64_t c0 = 0; ok && c0 < cls; c0 += width) {
     const int64_t wid = std::min(width, cls - c0);
-    const Operand og{g_mem, n, wid, g_ld, n * g_ld, planes};
+    const Operand og{g_mem, n, wid, g_ld, n * g_ld, p.g_planes};
     ProdMaps maps;
     {
       const int cg = n > 128 ? 2 : 1;

@@ -125,6 +125,10 @@ struct ProdArgs {
   int k_per_split;   // blocks of a split
   int chunk;         // blocks summed in TMEM at a time (16-bit logits)
   int planes;        // 1, or 3: each fp32 operand is the sum of three bf16 planes
+  // Planes of G: 3 of bf16 with fp32 operands; with 16-bit ones 1, rounded, or for at most 128 rows
+  // 2, value and remainder: there the gradients' products wait for W and dW, a second product
+  // a stage costs no time, and a gradient is then rounded once, like the plain form's.
+  int g_planes;
   bool bf16;
   int a_row0, b_row0;  // first row of the operands that are not read from their start (row of the map)
   int64_t m, n;      // rows and columns of the result

@@ -38,18 +38,31 @@ constexpr int kBK = 64;  // summed elements a stage: one 128-byte swizzled row
 //   kSplit: fp32 operands as three bf16 planes a stage, six products of planes a stage, in TMEM
 //     over one stage, the stages added in registers.
 //   kSplitWhole: the same, but in TMEM to the end: logits of at most two stages.
-enum { kWhole = 0, kParts = 1, kSplit = 2, kSplitWhole = 3 };
+//   kTwo: 16-bit operands, but G in two planes: gradients of few rows (see g_planes).
+enum { kWhole = 0, kParts = 1, kSplit = 2, kSplitWhole = 3, kTwo = 4 };
 constexpr int kWholeBlocks = 2;
 template <int ACC>
 constexpr bool three_planes = ACC == kSplit || ACC == kSplitWhole;
+template <int ACC>
+constexpr int kPlanesA = three_planes<ACC> ? 3 : ACC == kTwo ? 2 : 1;
+template <int ACC>
+constexpr int kPlanesB = three_planes<ACC> ? 3 : 1;
+template <int ACC>
+constexpr int kPairs = three_planes<ACC> ? 6 : kPlanesA<ACC>;  // products of planes a stage
 template <int ACC>
 constexpr bool in_registers = ACC == kParts || ACC == kSplit;
 
 // Products of planes of split operands (x = x0 + x1 + x2 by falling size), the small ones
 // first, so that they meet a small accumulator; x1 y2, x2 y1 and x2 y2 lie under 2^-24
 // of x y and are left out.
-__device__ __forceinline__ constexpr int pair_a(int p) { return p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 1 : 0; }
-__device__ __forceinline__ constexpr int pair_b(int p) { return p == 0 ? 0 : p == 1 ? 2 : p == 2 ? 1 : p == 3 ? 0 : p == 4 ? 1 : 0; }
+template <int ACC>
+__device__ __forceinline__ constexpr int pair_a(int p) {
+  return ACC == kTwo ? 1 - p : !three_planes<ACC> ? 0 : p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 1 : 0;
+}
+template <int ACC>
+__device__ __forceinline__ constexpr int pair_b(int p) {
+  return !three_planes<ACC> ? 0 : p == 0 ? 0 : p == 1 ? 2 : p == 2 ? 1 : p == 3 ? 0 : p == 4 ? 1 : 0;
+}
 
 // Groups of 8 warps that read results. What is done with a logit (an exponential, a maximum,
 // a sum) is a chain of latencies that 2 warps a scheduler do not cover: with one group the
@@ -62,11 +75,10 @@ constexpr int kGroups = !in_registers<ACC> && (KIND == Prod::kStats || KIND == P
 template <Prod KIND, int CG, int BN, int ACC>
 struct Shape {
   static constexpr int kThreads = 128 + 256 * kGroups<KIND, ACC>;
-  static constexpr int kPlanes = three_planes<ACC> ? 3 : 1;
   static constexpr int kABytes = 128 * 128;            // a plane of this block's 128 rows of A
   static constexpr int kBRows = BN / CG;               // its rows (columns) of B
   static constexpr int kBBytes = kBRows * 128;
-  static constexpr int kStage = kPlanes * (kABytes + kBBytes);
+  static constexpr int kStage = kPlanesA<ACC> * kABytes + kPlanesB<ACC> * kBBytes;
   static constexpr int kMost = 196608 / kStage;        // 32 KB of the block's 227 hold results on their way out
   static constexpr int kStages = kMost > 8 ? 8 : kMost;
   static constexpr int kBox = 4096 / kGroups<KIND, ACC>;  // a warp's results on their way out
@@ -109,6 +121,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
   }
   const __half2 r = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// What rounding to 16 bits leaves of a value.
+__device__ __forceinline__ float rest16(float v, bool bf16) {
+  return v - (bf16 ? __bfloat162float(__float2bfloat16_rn(v)) : __half2float(__float2half_rn(v)));
 }
 
 // Teacher entries of a row, in step with the columns; one entry read ahead.
@@ -410,14 +427,14 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
       float v[32];
       src.template get<c>(v);
       gr.of(v, g, rs.c.t, cls + c, rs.w);
-#pragma unroll
-      for (int p = 0; p < (FINE ? 3 : 1); ++p) {
+#pragma unroll 1
+      for (int p = 0; p < g.g_planes; ++p) {
         box.open();
         box.put16(0, v, g.bf16, keep);
         if (row0 < g.m && col0 + c < g.n) box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), p, false);
-        if (FINE) {
+        if (p + 1 < g.g_planes) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+          for (int j = 0; j < 32; ++j) v[j] = rest16(v[j], g.bf16);
         }
       }
     });
@@ -431,7 +448,7 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
       for (int j = 0; j < 32; ++j) src.acc[c + j] = v[j];
     });
 #pragma unroll 1
-    for (int p = 0; p < g.planes; ++p) {
+    for (int p = 0; p < g.g_planes; ++p) {
       each_32<kCols>([&](auto cc) {
         constexpr int c = decltype(cc)::value;
         float v[32];
@@ -442,9 +459,9 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
           if (row0 < g.m && col0 + c - 32 < g.n)
             box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), p, false);
         }
-        if (p + 1 < g.planes) {
+        if (p + 1 < g.g_planes) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) src.acc[c + j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+          for (int j = 0; j < 32; ++j) src.acc[c + j] = rest16(v[j], g.bf16);
         }
       });
     }
@@ -559,9 +576,8 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
             const uint32_t bar = CG == 2 ? map_to_rank(full + 8 * st, 0) : full + 8 * st;
             if (rank == 0) mbar_expect_tx(full + 8 * st, CG * S::kStage);
 #pragma unroll
-            for (int p = 0; p < S::kPlanes; ++p) {
+            for (int p = 0; p < kPlanesA<ACC>; ++p) {
               const uint32_t a = base + st * S::kStage + p * S::kABytes;
-              const uint32_t b = base + st * S::kStage + S::kPlanes * S::kABytes + p * S::kBBytes;
               if constexpr (!kAmn) {
                 tma_load_3d<CG>(a, &map_a, kb * kBK, g.a_row0 + m0, p, bar);
               } else {
@@ -569,6 +585,10 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
                 for (int i = 0; i < 2; ++i)
                   tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, g.a_row0 + kb * kBK, p, bar);
               }
+            }
+#pragma unroll
+            for (int p = 0; p < kPlanesB<ACC>; ++p) {
+              const uint32_t b = base + st * S::kStage + kPlanesA<ACC> * S::kABytes + p * S::kBBytes;
               if constexpr (!kBmn) {
                 tma_load_3d<CG>(b, &map_b, kb * kBK, g.b_row0 + n0, p, bar);
               } else {
@@ -598,7 +618,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       // the first one's descriptors.
       const bool one = elect_one();
       const uint32_t idesc = instr_desc(g.bf16, kAmn, kBmn, 128 * CG, BN);
-      const uint32_t b0 = base + S::kPlanes * S::kABytes;
+      const uint32_t b0 = base + kPlanesA<ACC> * S::kABytes;
       const uint64_t desc_a = kAmn ? smem_desc(base, 8192, 1024) : smem_desc(base, 16, 1024);
       const uint64_t desc_b = kBmn ? smem_desc(b0, 8192, 1024) : smem_desc(b0, 16, 1024);
       constexpr int kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;  // 16 summed elements further
@@ -624,8 +644,8 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
             tc_fence_after();
             if (one) {
 #pragma unroll
-              for (int p = 0; p < (three_planes<ACC> ? 6 : 1); ++p) {
-                const int pa = three_planes<ACC> ? pair_a(p) : 0, pb = three_planes<ACC> ? pair_b(p) : 0;
+              for (int p = 0; p < kPairs<ACC>; ++p) {
+                const int pa = pair_a<ACC>(p), pb = pair_b<ACC>(p);
                 const uint64_t da = desc_a + ((st * S::kStage + pa * S::kABytes) >> 4);
                 const uint64_t db = desc_b + ((st * S::kStage + pb * S::kBBytes) >> 4);
 #pragma unroll
@@ -786,6 +806,11 @@ cudaError_t launch_sums(int cg, int bn, const ProdMaps& maps, const ProdArgs& a,
     return cg == 2     ? launch_one<KIND, 2, 256, false, false, kSplit>(maps, a, num_sms, s)
            : bn == 128 ? launch_one<KIND, 1, 128, false, false, kSplit>(maps, a, num_sms, s)
                        : launch_one<KIND, 1, 64, false, false, kSplit>(maps, a, num_sms, s);
+  if (a.g_planes == 2)
+    return bn == 128  ? launch_one<KIND, 1, 128, false, false, kTwo>(maps, a, num_sms, s)
+           : bn == 64 ? launch_one<KIND, 1, 64, false, false, kTwo>(maps, a, num_sms, s)
+           : KIND == Prod::kDw && cg == 2 ? launch_one<Prod::kDw, 2, 256, false, false, kTwo>(maps, a, num_sms, s)
+                                          : launch_one<KIND, 1, 256, false, false, kTwo>(maps, a, num_sms, s);
   if (bn == 256)
     return cg == 2 ? launch_one<KIND, 2, 256, false, false, kWhole>(maps, a, num_sms, s)
                    : launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
