@@ -158,6 +158,24 @@ def test_strides_and_alignment(kind, d, pad, shift):
         assert torch.all(memory == 7.0)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,d,v,pad,shift,cap", [(100, 65, 700, 0, 0, 0), (100, 65, 700, 1, 1, 1), (9, 130, 513, 0, 2, 0),
+                                                 (128, 1029, 300, 0, 1, 1), (64, 1026, 257, 3, 0, 0), (17, 34, 900, 1, 3, 0),
+                                                 (12, 257, 1111, 0, 0, 1), (100, 300, 64, 7, 5, 0), (33, 1, 2000, 0, 1, 0)])
+def test_class_table_off_16_byte_boundaries_with_few_rows(kind, n, d, v, pad, shift, cap):
+    """NaN lies between and around its rows; pieces of 256 classes too."""
+    h, w, target = make(kind, n, d, v, pad=pad, shift=shift)
+    dev, host = make_teacher(n, v)
+    o = losses.distill_forward(h, w, dev, 2.0, target=target, check=True)
+    tn = target.cpu().numpy()
+    f = lo.forward(wide(h), wide(w), tn, -100, host, 2.0)
+    check_forward(f, h, w, 2.0, kl=o.kl, lse_t=o.lse_t, loss=o.loss, lse=o.lse)
+    (gk, gl), (gk_n, gl_n) = weights(n, 2, d, scale=64.0 if kind == "f16" else 1.0)
+    dh, dw = losses.distill_backward(h, w, dev, o.lse_t, gk, 2.0, target=target, lse=o.lse, grad_loss=gl,
+                                     workspace_cap_bytes=cap, check=True)
+    check_grads(f, lo.logit_grads(f, tn, -100, gl_n, None, 2.0, gk_n), h, w, kind, 2.0, dh, dw)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_pieces_change_nothing_but_roundings(kind):
     """A small bound on G cuts the classes into pieces of 256, the last one partial."""
