@@ -342,15 +342,25 @@ struct Outbox {
   __device__ __forceinline__ void copy(void* out, int64_t ld, int es, int64_t row0, int64_t rows, int64_t col0,
                                        int64_t cols) {
     __syncwarp();
+    const int n = static_cast<int>(min(int64_t(32), rows - row0));
+    const bool in0 = es == 4 ? lane < cols : 2 * lane < cols, in1 = 2 * lane + 1 < cols;
+    char* p = static_cast<char*>(out) + (row0 * ld + col0) * es + lane * 4;
+    const int64_t step = ld * es;
 #pragma unroll 1
-    for (int r = 0; r < 32 && row0 + r < rows; ++r) {
-      const uint32_t x = ld_shared_u32(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-      if (es == 4) {
-        if (lane < cols) static_cast<uint32_t*>(out)[(row0 + r) * ld + col0 + lane] = x;
-      } else {
-        uint16_t* p = static_cast<uint16_t*>(out) + (row0 + r) * ld + col0 + 2 * lane;
-        if (2 * lane < cols) p[0] = static_cast<uint16_t>(x);
-        if (2 * lane + 1 < cols) p[1] = static_cast<uint16_t>(x >> 16);
+    for (int r0 = 0; r0 < n; r0 += 16) {
+      uint32_t x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        x[i] = ld_shared_u32(buf + (r0 + i) * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+#pragma unroll
+      for (int i = 0; i < 16; ++i, p += step) {
+        const bool row = r0 + i < n;
+        if (es == 4) {
+          if (row && in0) *reinterpret_cast<uint32_t*>(p) = x[i];
+        } else {
+          if (row && in0) reinterpret_cast<uint16_t*>(p)[0] = static_cast<uint16_t>(x[i]);
+          if (row && in1) reinterpret_cast<uint16_t*>(p)[1] = static_cast<uint16_t>(x[i] >> 16);
+        }
       }
     }
     __syncwarp();
