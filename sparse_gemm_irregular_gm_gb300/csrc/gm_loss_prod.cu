@@ -114,18 +114,34 @@ __device__ __forceinline__ int64_t first_entry(const int2* e, int64_t lo, int64_
   return lo;
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
-  if (bf16) {
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&r);
   }
-  const __half2 r = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// What rounding to 16 bits leaves of a value.
-__device__ __forceinline__ float rest16(float v, bool bf16) {
-  return v - (bf16 ? __bfloat162float(__float2bfloat16_rn(v)) : __half2float(__float2half_rn(v)));
+// Rounds pairs of values to 16 bits; REST: leaves in v what the rounding took.
+template <bool BF16, bool REST>
+__device__ __forceinline__ void round16(float (&v)[32], uint32_t (&x)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    x[j] = pack2<BF16>(v[2 * j], v[2 * j + 1]);
+    if constexpr (REST) {
+      float a, b;
+      if constexpr (BF16) {
+        a = __uint_as_float(x[j] << 16), b = __uint_as_float(x[j] & 0xffff0000u);
+      } else {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+        a = y.x, b = y.y;
+      }
+      v[2 * j] -= a, v[2 * j + 1] -= b;
+    }
+  }
 }
 
 // Teacher entries of a row, in step with the columns; one entry read ahead.
@@ -316,11 +332,18 @@ struct Outbox {
     if constexpr (NARROW) st_shared_v4(buf + lane * 64 + ((piece ^ ((lane >> 1) & 3)) << 4), a, b, c, d);
     else st_shared_v4(buf + lane * 128 + ((piece ^ (lane & 7)) << 4), a, b, c, d);
   }
-  __device__ __forceinline__ void put16(int piece0, const float (&v)[32], bool bf16, uint32_t keep) {
+  // 32 columns of 16 bits; the values become what rounding took of them with rest.
+  __device__ __forceinline__ void put16(int piece0, float (&v)[32], bool bf16, bool rest, uint32_t keep) {
+    uint32_t x[16];
+    if (bf16) {
+      if (rest) round16<true, true>(v, x);
+      else round16<true, false>(v, x);
+    } else {
+      if (rest) round16<false, true>(v, x);
+      else round16<false, false>(v, x);
+    }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      put(piece0 + q, keep & pack2(v[8 * q], v[8 * q + 1], bf16), keep & pack2(v[8 * q + 2], v[8 * q + 3], bf16),
-          keep & pack2(v[8 * q + 4], v[8 * q + 5], bf16), keep & pack2(v[8 * q + 6], v[8 * q + 7], bf16));
+    for (int q = 0; q < 4; ++q) put(piece0 + q, keep & x[4 * q], keep & x[4 * q + 1], keep & x[4 * q + 2], keep & x[4 * q + 3]);
   }
   __device__ __forceinline__ void put32(const float (&v)[32]) {
 #pragma unroll
@@ -440,12 +463,8 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
 #pragma unroll 1
       for (int p = 0; p < g.g_planes; ++p) {
         box.open();
-        box.put16(0, v, g.bf16, keep);
+        box.put16(0, v, FINE || g.bf16, p + 1 < g.g_planes, keep);
         if (row0 < g.m && col0 + c < g.n) box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), p, false);
-        if (p + 1 < g.g_planes) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = rest16(v[j], g.bf16);
-        }
       }
     });
   } else {
@@ -464,14 +483,14 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
         float v[32];
         src.template get<c>(v);
         if constexpr (c % 64 == 0) box.open();
-        box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, keep);
+        box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, p + 1 < g.g_planes, keep);
         if constexpr (c % 64 == 32) {
           if (row0 < g.m && col0 + c - 32 < g.n)
             box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), p, false);
         }
         if (p + 1 < g.g_planes) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) src.acc[c + j] = rest16(v[j], g.bf16);
+          for (int j = 0; j < 32; ++j) src.acc[c + j] = v[j];
         }
       });
     }
@@ -504,7 +523,7 @@ __device__ __forceinline__ void end_sum(const ProdArgs& g, const CUtensorMap* ma
       box.put32(v);
     } else {
       if (c == first) box.open();
-      box.put16(c == first ? 0 : 4, v, bf, 0xffffffffu);
+      box.put16(c == first ? 0 : 4, v, bf, false, 0xffffffffu);
       if (kPair && c % 64 == 0) return;
     }
     if (row0 >= g.m || col >= g.n) return;
