@@ -187,7 +187,9 @@ struct SkinnyArgs {
   const void *h, *w;
   int64_t h_ld, w_ld, dim, n_cls;
   int n;
-  int64_t per_warp, per_block;  // classes of a warp (forward), of a block (backward); set by the launch
+  // set by the launch: classes of a warp (forward), of a block (backward), of a warp at a time
+  int64_t per_warp, per_block;
+  int take;
   Targets tgt;
   const int64_t* ent_start;     // teacher; ent_len null: none
   const int32_t* ent_len;

@@ -6,12 +6,13 @@
 // H stays in shared memory; a warp takes R classes at a time, so that one read of H serves
 // R rows of W. Forward: one pass over W. Backward: one pass that forms the logits again,
 // G in fp32, writes dW and sums dH, so W comes from HBM once and dW goes there once; the
-// second look at a tile's classes, for dH, finds them in L2.
+// second look at a tile's classes, for dH, finds them in L2 while all SMs' tiles fit there (rows
+// up to some 8 KB; past that W is read twice).
 //
 // Measured, kernels of a forward and a backward call together, these / the products:
 //   f32   1 x 4096 x 131072   1388 / 3857 us    8 x 4096 x 131072   2483 / 3752 us
 //   f32   1 x 80 x 400000      108 /  445 us    8 x 305 x 29546       96 /  160 us
-//   bf16  1 x 2650 x 26281     207 /  270 us    8 x 2650 x 26281     428 /  274 us
+//   bf16  1 x 2650 x 26281     198 /  270 us    8 x 2650 x 26281     428 /  274 us
 //   bf16  1 x 4096 x 131072    808 /  786 us    8 x 4096 x 131072   1783 /  708 us
 // so 16-bit operands come here with one row only. The forward pass of 1 x 4096 x 131072 f32
 // runs at 347 us, 91 % of the measured copy rate; the backward pass waits at its tiles' barriers.
@@ -60,7 +61,11 @@ struct Piece {
   __device__ __forceinline__ void set(int i, float v) { from_f32(v, &x[i]); }
 };
 
-// Classes a warp takes at a time: their logits with N rows fill at most a warp's lanes.
+// Classes a warp takes at a time, at most: their logits with N rows fill at most a warp's lanes.
+// How many it does take (SkinnyArgs.take) is cut in the backward pass so that a block's last turn is
+// as full as the others: 1 x 2650 x 26281 f32 had two turns of 103 blocks and none of 49, 517 us
+// instead of 322. Without the backward pass's barriers it costs more than it saves (137 -> 164 us
+// forward, 4 x 1240 x 144605 f32).
 template <int N>
 constexpr int kClasses = N == 8 ? 4 : 8;
 
@@ -99,18 +104,18 @@ __device__ __forceinline__ void stage_h(const SkinnyArgs& a, float* hs, int piec
   }
 }
 
-// A warp's way through its classes: batches of R, `step` apart, up to j_end. The next piece of
+// A warp's way through its classes: batches of `take` (at most R), `step` apart, up to j_end. The next piece of
 // each row is always under way, across the ends of rows and batches too, since a batch's end is a
 // chain of shuffles and exponentials that would leave the memory idle.
-template <class T, int N, int VEC>
+template <class T, int N, int VEC, bool CUT>  // CUT: take may be less than R
 struct Classes {
   static constexpr int R = kClasses<N>;
   const T* w;
   int64_t ld, j_end, step, j;  // j: batch of the piece under way
-  int pieces, turns, turn, lane;
+  int take, pieces, turns, turn, lane;
   Piece<T, VEC> ahead[R];
   __device__ __forceinline__ Classes(const SkinnyArgs& a, int64_t first, int64_t end, int64_t step, int pieces)
-      : w(static_cast<const T*>(a.w)), ld(a.w_ld), j_end(end), step(step), j(first), pieces(pieces),
+      : w(static_cast<const T*>(a.w)), ld(a.w_ld), j_end(end), step(step), j(first), take(a.take), pieces(pieces),
         turns((pieces + 31) / 32), turn(0), lane(threadIdx.x & 31) {
     fetch();
   }
@@ -119,7 +124,7 @@ struct Classes {
     const T* x = w + j * ld + int64_t(p) * VEC;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (p < pieces && j + r < j_end) ahead[r].load(x + r * ld);
+      if (p < pieces && (!CUT || r < take) && j + r < j_end) ahead[r].load(x + r * ld);
       else ahead[r].zero();
     }
   }
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps) k_skinny_stats(const Skinn
   const int64_t j_end = min(a.n_cls, j_first + a.per_warp);
   SkinnyWalk w;
   w.start(a, lane, j_first);
-  Classes<T, N, VEC> cls(a, j_first, j_end, R, pieces);
+  Classes<T, N, VEC, false> cls(a, j_first, j_end, R, pieces);
   float m = -INFINITY, s1 = 0.f, st = 0.f, zq = 0.f;
   for (int64_t j0 = j_first; j0 < j_end; j0 += R) {
     const float z = cls.logits(hs);
@@ -262,6 +267,7 @@ constexpr int kTile = THREADS / 32 * kClasses<N>;  // classes of a tile: one tur
 template <class T, int N, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_skinny_grads(const SkinnyArgs a) {
   constexpr int R = kClasses<N>, kPer = 32 / (R * N), kT = kTile<N, THREADS>, kGroups = kOwn / VEC;
+  const int take = a.take, turn = take * (THREADS / 32);  // classes of a warp, of the block at a time
   constexpr int Q = 4;  // classes taken together when dW and dH are formed
   extern __shared__ __align__(16) float hs[];
   __shared__ __align__(16) float gs[kT][N];
@@ -290,19 +296,19 @@ __global__ void __launch_bounds__(THREADS) k_skinny_grads(const SkinnyArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) dh[k][i][e] = 0.f;
   SkinnyWalk w;  // a warp's classes rise by tiles; entries of the classes between are passed over
-  w.start(a, lane, j_first + warp * R);
-  Classes<T, N, VEC> cls(a, j_first + warp * R, j_end, kT, pieces);
-  for (int64_t j0 = j_first; j0 < j_end; j0 += kT) {
-    const int64_t jw = j0 + warp * R;
+  w.start(a, lane, j_first + warp * take);
+  Classes<T, N, VEC, true> cls(a, j_first + warp * take, j_end, turn, pieces);
+  for (int64_t j0 = j_first; j0 < j_end; j0 += turn) {
+    const int64_t jw = j0 + warp * take;
     if (jw < j_end) {
       const float z = cls.logits(hs);
       float g = 0.f;
-      if (jw + r < j_end && live) {
+      if (r < take && jw + r < j_end && live) {
         if (a.tgt.t) g = rc.a * ex2((z - rc.lse) * kLog2e);
         if (a.ent_len) g = fmaf(rc.b, ex2(fmaf(z, a.inv_t, -rc.lse_t) * kLog2e), g);
         if (rc.t == jw + r) g -= rc.gl;
       }
-      const int64_t stop = min(jw + R, j_end);
+      const int64_t stop = min(jw + take, j_end);
       for (;;) {
         const bool mine = w.next.x < stop;
         const unsigned any = __ballot_sync(kFull, mine);
@@ -317,10 +323,10 @@ __global__ void __launch_bounds__(THREADS) k_skinny_grads(const SkinnyArgs a) {
           w.get(a);
         }
       }
-      if (lane % kPer == 0) gs[warp * R + r][n] = jw + r < j_end ? g : 0.f;
+      if (lane % kPer == 0 && r < take) gs[warp * take + r][n] = jw + r < j_end ? g : 0.f;
     }
     __syncthreads();
-    const int tile = static_cast<int>(min(int64_t(kT), j_end - j0));
+    const int tile = static_cast<int>(min(int64_t(turn), j_end - j0));
     if (owns) {
       for (int c0 = slice * Q; c0 < tile; c0 += slices * Q) {
         float g[Q][N];
@@ -435,8 +441,9 @@ cudaError_t run_backward(SkinnyArgs a, int* blocks, cudaStream_t s) {
   constexpr int kT = kTile<N, THREADS>;
   const cudaError_t e = fit_grid(k, THREADS, smem, (a.n_cls + kT - 1) / kT, *blocks, blocks);
   if (e != cudaSuccess) return e;
-  const int64_t each = (a.n_cls + *blocks - 1) / *blocks;
-  a.per_block = (each + kT - 1) / kT * kT;
+  a.per_block = (a.n_cls + *blocks - 1) / *blocks;
+  const int64_t turns = (a.per_block + kT - 1) / kT, share = turns * (THREADS / 32);
+  a.take = static_cast<int>((a.per_block + share - 1) / share);
   return launch_chained(k, *blocks, THREADS, smem, s, 1, a);
 }
 
