@@ -135,7 +135,7 @@ gm_status gm_distill_backward(const gm_logits* z, const gm_csr* teacher, int32_t
 
 /* Waits for the stream and returns what the losses' calls of this device have met since
  * the last gm_loss_status: GM_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; losses
- * and dH computed until this is read are NaN), GM_ERR_BAD_INDEX (a bad target or teacher
+ * computed until this is read are NaN, gradients incomplete), GM_ERR_BAD_INDEX (a bad target or teacher
  * row), GM_ERR_CUDA, or GM_OK. */
 gm_status gm_loss_status(void* stream);
 

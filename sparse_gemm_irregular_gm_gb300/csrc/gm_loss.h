@@ -130,7 +130,7 @@ struct ProdArgs {
   // a stage costs no time, and a gradient is then rounded once, like the plain form's.
   int g_planes;
   bool bf16;
-  int a_row0, b_row0;  // first row of the operands that are not read from their start (row of the map)
+  int b_row0;        // first row of W's map
   int64_t m, n;      // rows and columns of the result
   int* status;
   // kStats, kGrad

@@ -608,11 +608,11 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
             for (int p = 0; p < kPlanesA<ACC>; ++p) {
               const uint32_t a = base + st * S::kStage + p * S::kABytes;
               if constexpr (!kAmn) {
-                tma_load_3d<CG>(a, &map_a, kb * kBK, g.a_row0 + m0, p, bar);
+                tma_load_3d<CG>(a, &map_a, kb * kBK, m0, p, bar);
               } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                  tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, g.a_row0 + kb * kBK, p, bar);
+                  tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, kb * kBK, p, bar);
               }
             }
 #pragma unroll
