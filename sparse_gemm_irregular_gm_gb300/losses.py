@@ -16,6 +16,7 @@ import ctypes
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 from .binding import DeviceCSR, GmError, gm_csr
@@ -75,22 +76,26 @@ def _matrix(name, t, like=None, shape=None):
     """A CUDA matrix whose rows are consecutive elements: (pointer, elements between rows)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in TYPES:
         raise ValueError(f"{name} must be a 2-d CUDA tensor of float32, bfloat16 or float16")
-    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, not {t.dtype} on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
     rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {(rows, cols)}")
     ld, step = t.stride()
-    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name}'s rows must be consecutive elements that do not overlap (strides {t.stride()})")
-    return t.data_ptr() or None, (ld if rows > 1 else max(cols, 1))
+    return t.data_ptr() or None, (ld if rows > 1 else cols or 1)
 
 
-def _vector(name, t, n, device, dtypes=(torch.float32,)):
+_F32 = (torch.float32,)
+_INT = (torch.int64, torch.int32)
+
+
+def _vector(name, t, n, device, dtypes=_F32):
     if t is None:
         return None
-    if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype not in dtypes or t.dim() != 1
-            or t.shape[0] != n or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous()
+            or t.device != device):
         raise ValueError(f"{name} must be a contiguous tensor of {n} elements of {' or '.join(map(str, dtypes))} on {device}")
     return t.data_ptr() or None
 
@@ -115,7 +120,7 @@ class _Call:
         self.z = gm_logits(self.n, w.shape[0], dim, hp, h_ld, wp, w_ld, TYPES[h.dtype])
         self.labels = None
         if target is not None:
-            p = _vector("target", target, self.n, self.device, (torch.int64, torch.int32))
+            p = _vector("target", target, self.n, self.device, _INT)
             self.labels = gm_labels(p, ignore_index, target.dtype == torch.int32)
         self.cfg = gm_loss_config(workspace_cap_bytes, GM_LOSS_CHECK if check else 0, None, 0)
         self.teacher = self._teacher(teacher) if teacher is not None else None
@@ -151,19 +156,21 @@ class _Call:
 
     def run(self, name, backward, *args):
         lib = load()
-        need = ctypes.c_int64()
-        cfg = self.cfg
-        nnz = self.teacher[0].nnz if self.teacher is not None else -1
-        binding._check(lib.gm_loss_workspace(self.z, nnz, backward, cfg, need), name)
-        work = torch.empty(need.value, dtype=torch.uint8, device=self.device)
-        cfg.workspace, cfg.workspace_bytes = work.data_ptr() or None, need.value
+        z, cfg, need = self.z, self.cfg, ctypes.c_int64()
+        rc = lib.gm_loss_workspace(z, -1 if self.teacher is None else self.teacher[0].nnz, backward, cfg, need)
+        if rc:
+            raise GmError(rc, name)
+        size = need.value
+        work = torch.empty(size, dtype=torch.uint8, device=self.device)
+        cfg.workspace = work.data_ptr() or None
+        cfg.workspace_bytes = size
         stream = (self.given if self.given is not None else torch.cuda.current_stream(self.device.index)).cuda_stream
         if self.teacher is None:
-            rc = getattr(lib, name)(self.z, self.labels, cfg, stream, *args)
+            rc = getattr(lib, name)(z, self.labels, cfg, stream, *args)
         else:
-            desc, value_type, index_type = self.teacher
-            rc = getattr(lib, name)(self.z, desc, value_type, index_type, self.temperature, self.labels, cfg, stream, *args)
-        binding._check(rc, name)
+            rc = getattr(lib, name)(z, *self.teacher, self.temperature, self.labels, cfg, stream, *args)
+        if rc:
+            raise GmError(rc, name)
 
 
 def gm_loss_status(stream=None):
@@ -299,6 +306,7 @@ class _Xent(torch.autograd.Function):
         return loss, lse
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_loss, g_lse):
         h, w, target, lse = ctx.saved_tensors
         dh, dw = xent_backward(h, w, target, lse, _contiguous(g_loss, lse),
@@ -319,6 +327,7 @@ class _Distill(torch.autograd.Function):
         return tuple(f)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_kl, _, g_loss, g_lse):
         h, w, row_ptr, col, val, target, lse_t, lse = ctx.saved_tensors
         teacher = DeviceCSR(h.shape[0], w.shape[0], row_ptr, col, val)
