@@ -840,9 +840,12 @@ cudaError_t launch_sums(int cg, int bn, const ProdMaps& maps, const ProdArgs& a,
            : bn == 64 ? launch_one<KIND, 1, 64, false, false, kTwo>(maps, a, num_sms, s)
            : KIND == Prod::kDw && cg == 2 ? launch_one<Prod::kDw, 2, 256, false, false, kTwo>(maps, a, num_sms, s)
                                           : launch_one<KIND, 1, 256, false, false, kTwo>(maps, a, num_sms, s);
-  if (bn == 256)
-    return cg == 2 ? launch_one<KIND, 2, 256, false, false, kWhole>(maps, a, num_sms, s)
-                   : launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
+  if (bn == 256) {
+    if constexpr (KIND == Prod::kDw) {  // dH of at most 128 rows has two planes of G
+      if (cg == 1) return launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
+    }
+    return launch_one<KIND, 2, 256, false, false, kWhole>(maps, a, num_sms, s);
+  }
   return bn == 128 ? launch_one<KIND, 1, 128, false, false, kWhole>(maps, a, num_sms, s)
                    : launch_one<KIND, 1, 64, false, false, kWhole>(maps, a, num_sms, s);
 }
