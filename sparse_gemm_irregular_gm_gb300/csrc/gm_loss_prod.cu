@@ -8,6 +8,13 @@
 // the other accumulator, 8 a tile: a thread holds one row, 32 columns at a time, so the row
 // reductions need no shuffles. Results of 16 or 32 bits go through shared memory and
 // out by TMA, 128 bytes a row at a time.
+//
+// Why tiles of 256 by 256 over two blocks: a stage then brings 32 KB to an SM for 512 cycles of
+// products, the 64 bytes a cycle that L2 gives an SM; a 128 by 256 tile a block would need 96.
+// Measured, bf16, 2048 x 1024 x 65536 (2.75e11 operations each): statistics 136 us, the tensor
+// cores 95 % busy while tiles run; G 146; dH 154 (64 of 76 pairs have a tile); dW 151. Back to back
+// (8192 x 4096 x 131072) the power cap bounds them: 1.71 PFLOP/s. With dim 256 or less the
+// bytes of G bound the gradients: dH of 512 x 256 x 262144 66 us, 78 % of the DRAM rate.
 #include "gm_device.cuh"
 #include "gm_loss.h"
 #include "gm_umma.cuh"
