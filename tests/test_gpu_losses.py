@@ -541,3 +541,65 @@ def test_vertex_embedding_example_learns():
     means = example.train(scale=9, edge_factor=8, dim=32, batch=256, steps=60)
     assert torch.isfinite(means).all()
     assert means[-4:].mean() < 0.8 * means[:4].mean()  # chance is the logarithm of 512 vertices
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,d,v,cap", [(1, 33, 300, 0), (6, 130, 1000, 0), (100, 65, 513, 0), (300, 264, 1111, 0), (150, 129, 700, 1)])
+def test_workspace_is_as_large_as_said(kind, n, d, v, cap):
+    """The caller's workspace has gm_loss_workspace's bytes, and the memory around it is left alone."""
+    h, w, target = make(kind, n, d, v)
+    dev, _ = make_teacher(n, v)
+    (gk, gl), _ = weights(n, 2, 0)
+    want = losses.distill_forward(h, w, dev, 2.0, target=target)
+    want_g = losses.distill_backward(h, w, dev, want.lse_t, gk, 2.0, target=target, lse=want.lse, grad_loss=gl,
+                                     workspace_cap_bytes=cap)
+    lib = losses.load()
+    z = losses.gm_logits(n, v, d, h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), losses.TYPES[h.dtype])
+    lab = losses.gm_labels(target.data_ptr(), -100, 0)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    out = [torch.empty_like(t) for t in want]
+    dh, dw = torch.empty(n, d, dtype=h.dtype, device="cuda"), torch.empty(v, d, dtype=h.dtype, device="cuda")
+    for backward in (0, 1):
+        cfg = losses.gm_loss_config(cap, 0, None, 0)
+        need = ctypes.c_int64()
+        assert lib.gm_loss_workspace(z, dev.nnz, backward, cfg, need) == 0
+        memory = torch.full((need.value + 8192,), 0xa5, dtype=torch.uint8, device="cuda")
+        cfg.workspace, cfg.workspace_bytes = memory.data_ptr() + 4096, need.value
+        if backward:
+            rc = lib.gm_distill_backward(z, dev.desc(), 1, 0, 2.0, lab, cfg, stream, want.lse_t.data_ptr(), gk.data_ptr(),
+                                         want.lse.data_ptr(), gl.data_ptr(), None, dh.data_ptr(), d, dw.data_ptr(), d)
+        else:
+            rc = lib.gm_distill_forward(z, dev.desc(), 1, 0, 2.0, lab, cfg, stream, *(t.data_ptr() for t in out))
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.all(memory[:4096] == 0xa5) and torch.all(memory[4096 + need.value:] == 0xa5)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert torch.equal(dh, want_g[0]) and torch.equal(dw, want_g[1])
+
+
+def test_streams_at_once():
+    """Calls on several streams, other tensor-core work between them: the same results bit by bit."""
+    problems = []
+    for kind, n, d, v in (("bf16", 300, 264, 3000), ("f32", 200, 64, 5000), ("f16", 50, 129, 4000), ("bf16", 1, 512, 9000)):
+        h, w, target = make(kind, n, d, v, ignored=0.0)
+        dev, _ = make_teacher(n, v)
+        (gk, gl), _ = weights(n, 2, 0)
+        problems.append((h, w, target, dev, gk, gl))
+
+    def step(h, w, target, dev, gk, gl):
+        o = losses.distill_forward(h, w, dev, 2.0, target=target)
+        return (*o, *losses.distill_backward(h, w, dev, o.lse_t, gk, 2.0, target=target, lse=o.lse, grad_loss=gl))
+
+    want = [step(*p) for p in problems]
+    a = torch.randn(1024, 1024, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for turn in range(12):
+        for k, p in enumerate(problems):
+            with torch.cuda.stream(streams[(turn + k) % 3]):
+                got.append((k, step(*p)))
+                a @ a
+    torch.cuda.synchronize()
+    for k, o in got:
+        assert all(torch.equal(x, y) for x, y in zip(o, want[k]))
