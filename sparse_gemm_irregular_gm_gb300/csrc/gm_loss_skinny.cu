@@ -408,10 +408,11 @@ __global__ void __launch_bounds__(THREADS) k_skinny_grads(const SkinnyArgs a) {
 }
 
 // As many blocks as are resident at once, but none without work of its own; the workspace was
-// planned for `most`.
+// planned for `most`. The attribute belongs to the kernel on its device, not to the call: every call sets
+// the most its instance can ask for, so that threads with rows of other lengths do not take it back.
 template <class K>
-cudaError_t fit_grid(K* k, int threads, size_t smem, int64_t work, int most, int* blocks) {
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t fit_grid(K* k, int threads, int rows, size_t smem, int64_t work, int most, int* blocks) {
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(rows * kSkinnyDim * 4));
   int per_sm = 0, dev = 0, sms = 0;
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
@@ -428,7 +429,7 @@ cudaError_t run_forward(SkinnyArgs a, int* blocks, cudaStream_t s) {
   auto* k = k_skinny_stats<T, N, VEC>;
   const size_t smem = size_t(N) * ((a.dim + VEC - 1) / VEC) * VEC * 4;
   const int64_t batch = kForwardWarps * kClasses<N>;
-  const cudaError_t e = fit_grid(k, 32 * kForwardWarps, smem, (a.n_cls + batch - 1) / batch, *blocks, blocks);
+  const cudaError_t e = fit_grid(k, 32 * kForwardWarps, N, smem, (a.n_cls + batch - 1) / batch, *blocks, blocks);
   if (e != cudaSuccess) return e;
   const int64_t warps = int64_t(*blocks) * kForwardWarps, each = (a.n_cls + warps - 1) / warps;
   a.per_warp = (each + kClasses<N> - 1) / kClasses<N> * kClasses<N>;
@@ -439,7 +440,7 @@ cudaError_t run_backward(SkinnyArgs a, int* blocks, cudaStream_t s) {
   auto* k = k_skinny_grads<T, N, VEC, THREADS>;
   const size_t smem = size_t(N) * ((a.dim + VEC - 1) / VEC) * VEC * 4;
   constexpr int kT = kTile<N, THREADS>;
-  const cudaError_t e = fit_grid(k, THREADS, smem, (a.n_cls + kT - 1) / kT, *blocks, blocks);
+  const cudaError_t e = fit_grid(k, THREADS, N, smem, (a.n_cls + kT - 1) / kT, *blocks, blocks);
   if (e != cudaSuccess) return e;
   a.per_block = (a.n_cls + *blocks - 1) / *blocks;
   const int64_t turns = (a.per_block + kT - 1) / kT, share = turns * (THREADS / 32);

@@ -1,0 +1,48 @@
+"""What the losses promise where inputs, callers or memory are out of the ordinary: reports that belong to one call,
+masked classes, weights far apart, teachers with large values, malformed row pointers, bounded workspace."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+from sparse_gemm_irregular_gm_gb300 import losses
+from test_gpu_losses import make
+
+pytestmark = pytest.mark.gpu
+
+
+def test_host_threads_with_rows_of_different_lengths():
+    """The few-row kernels' shared memory goes with the row length: calls of several threads do not meet."""
+    lib = losses.load()
+    held, calls = [], []
+    for d in (64, 4096, 64, 4096):
+        h, w, target = make("f32", 8, d, 700, ignored=0.0)
+        want = losses.xent_forward(h, w, target)
+        z = losses.gm_logits(8, 700, d, h.data_ptr(), d, w.data_ptr(), d, losses.GM_LOSS_F32)
+        lab = losses.gm_labels(target.data_ptr(), -100, 0)
+        need = ctypes.c_int64()
+        assert lib.gm_loss_workspace(z, -1, 0, None, need) == 0
+        work = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+        cfg = losses.gm_loss_config(0, 0, work.data_ptr(), need.value)
+        got = [torch.empty_like(t) for t in want]
+        stream = torch.cuda.Stream()
+        held.append((h, w, target, work, stream, want, got))
+        calls.append((z, lab, cfg, ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p(got[0].data_ptr()),
+                      ctypes.c_void_p(got[1].data_ptr())))
+    torch.cuda.synchronize()
+    statuses = [set() for _ in calls]
+
+    def turn(k):
+        for _ in range(4000):
+            statuses[k].add(lib.gm_xent_forward(*calls[k]))
+
+    threads = [threading.Thread(target=turn, args=(k,)) for k in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert statuses == [{0}] * len(calls)
+    for *_, want, got in held:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
