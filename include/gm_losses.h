@@ -74,7 +74,8 @@ typedef struct gm_labels {
   int32_t target32;     /* 1: targets are int32                       */
 } gm_labels;
 
-#define GM_LOSS_CHECK 1 /* wait for the work and return its status (gm_loss_status) */
+#define GM_LOSS_CHECK 1 /* wait for the work and return what this call met (as gm_loss_status would, which then
+                           does not tell of it); other calls' reports stay where they are */
 
 /* Tuning; zero selects the automatic value. NULL is the same as all zeros. */
 typedef struct gm_loss_config {
@@ -133,10 +134,12 @@ gm_status gm_distill_backward(const gm_logits* z, const gm_csr* teacher, int32_t
                               const float* lse_t, const float* grad_kl, const float* lse, const float* grad_loss,
                               const float* grad_lse, void* dh, int64_t dh_ld, void* dw, int64_t dw_ld);
 
-/* Waits for the stream and returns what the losses' calls of this device have met since
- * the last gm_loss_status: GM_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; losses
- * computed until this is read are NaN, gradients incomplete), GM_ERR_BAD_INDEX (a bad target or teacher
- * row), GM_ERR_CUDA, or GM_OK. */
+/* Waits for the stream and returns what the losses' calls of this device, on any stream, have met
+ * since the last gm_loss_status, calls with GM_LOSS_CHECK apart: GM_ERR_DEVICE_TIMEOUT (a bounded wait in a
+ * kernel gave up: that call's losses and what it summed of dh are NaN, other gradients of it
+ * incomplete; other calls are not touched), GM_ERR_BAD_INDEX (a bad target or teacher row), GM_ERR_CUDA,
+ * GM_ERR_OOM (4 bytes could not be had; nothing is cleared), or GM_OK. Reading clears; a report that
+ * arrives meanwhile is told now or next time. */
 gm_status gm_loss_status(void* stream);
 
 #ifdef __cplusplus

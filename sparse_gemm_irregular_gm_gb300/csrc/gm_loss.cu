@@ -24,6 +24,9 @@ namespace {
 
 __device__ int g_loss_status;
 
+// Reads and clears in one step: what other streams' kernels set meanwhile is either told now or kept.
+__global__ void k_take_status(int* __restrict__ taken) { *taken = atomicExch(&g_loss_status, 0); }
+
 // ---- operands that TMA cannot read in place ------------------------------------------
 // f32: three bf16 planes, x = x0 + x1 + x2 with x0 the nearest bf16 of x and so on, which
 // keeps all 24 bits; 16-bit types: one plane, copied. Rows are padded with zeros to ld, a
@@ -212,6 +215,15 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) k_teacher(const TeacherArg
   }
 }
 
+// Whether this lane's part of a call's `lost` says that a product gave up (gm_loss_prod.cu); every warp
+// reads all of it. lost null: kernels that wait for nothing.
+__device__ __forceinline__ bool any_lost(const int* lost, int n) {
+  int x = 0;
+  if (lost)
+    for (int i = threadIdx.x & 31; i < n; i += 32) x |= lost[i];
+  return x != 0;
+}
+
 // ---- joining the half tiles of a row -----------------------------------------------------
 struct JoinArgs {
   const float4* part;
@@ -223,6 +235,8 @@ struct JoinArgs {
   float inv_t;
   float *loss, *lse, *kl, *lse_t;
   int* status;
+  const int* lost;
+  int n_lost;
 };
 // Bound by the latency of its loads: 4 of them in flight a thread (2000 rows, 1024 half tiles,
 // 33 MB: 22 us with one, 9 with four).
@@ -233,6 +247,7 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   const int rl = threadIdx.x % ROWS, sub = threadIdx.x / ROWS;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + rl;
   const bool dis = a.ent_len != nullptr;
+  const bool lost_here = any_lost(a.lost, a.n_lost);
   float m = -INFINITY, s1 = 0.f, st = 0.f, zq = 0.f;
   auto add = [&](float4 o) {
     const float mn = fmaxf(m, o.x), ref = mn == -INFINITY ? 0.f : mn;
@@ -263,8 +278,8 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
     if (sub < d) add(sh[threadIdx.x + d * ROWS]);
     __syncthreads();
   }
+  const bool lost = __any_sync(kFull, lost_here);
   if (sub != 0 || row >= a.n_rows) return;
-  const bool lost = (*a.status & kLossTimeout) != 0;
   if (a.tgt.t) {
     const float l = lost ? NAN : m + logf(s1);
     const int64_t t = check_target(a.tgt, raw_target(a.tgt, row));
@@ -306,13 +321,14 @@ template <int SUB>
 __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ acc, int splits, int64_t split_stride,
                                                     int64_t rows, int64_t dim, int64_t acc_ld, void* __restrict__ out,
                                                     int64_t out_ld, int type, const unsigned* __restrict__ g_max,
-                                                    const int* __restrict__ status) {
+                                                    const int* __restrict__ lost, int n_lost) {
   constexpr int kCols = 256 / SUB;
   __shared__ float sh[SUB][kCols];
   chain_wait();
   const int64_t n = rows * dim, stride = static_cast<int64_t>(gridDim.x) * kCols;
   const int col = threadIdx.x % kCols, sub = threadIdx.x / kCols;
-  const float inv = (*status & kLossTimeout) ? NAN : 1.f / g_scale_of(g_max);
+  const bool lost_here = any_lost(lost, n_lost);
+  const float inv = 1.f / g_scale_of(g_max);
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kCols; i0 < n; i0 += stride) {
     const int64_t i = i0 + col;
     const int64_t r = i / dim, c = i - r * dim;
@@ -330,8 +346,9 @@ __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ ac
 #pragma unroll
       for (int s = 1; s < SUB; ++s) x += sh[s][col];
     }
+    const bool gone = __any_sync(kFull, lost_here);  // a warp has one sub where SUB is over 1
     if (i >= n) continue;
-    x *= inv;
+    x = gone ? NAN : x * inv;
     const int64_t o = r * out_ld + c;
     if (type == GM_LOSS_F32) static_cast<float*>(out)[o] = x;
     else if (type == GM_LOSS_BF16) static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(x);
@@ -426,6 +443,15 @@ struct Arena {
   }
 };
 
+// The call's own words: lost (ProdArgs), and the report of a checked call.
+struct Words {
+  size_t lost = 0, status = 0;
+  void plan(Arena& a, const Call& c) {
+    lost = a.add(static_cast<int64_t>(c.sms) * 4);
+    status = a.add(4);
+  }
+};
+
 struct NvtxRange {
   explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
   ~NvtxRange() { nvtxRangePop(); }
@@ -504,9 +530,31 @@ gm_status begin(Call& c) {
   return GM_OK;
 }
 
-gm_status finish(const Call& c, bool launched) {
+gm_status status_of(int bits) {
+  if (bits & kLossTimeout) return GM_ERR_DEVICE_TIMEOUT;
+  return bits ? GM_ERR_BAD_INDEX : GM_OK;
+}
+
+// A checked call reports to a word of its own: it neither tells of other calls' rows nor keeps theirs from
+// gm_loss_status.
+gm_status own_status(Call& c, int* word) {
+  if (!(c.flags & GM_LOSS_CHECK)) return GM_OK;
+  c.status = word;
+  if (cudaMemsetAsync(word, 0, 4, c.s) == cudaSuccess) return GM_OK;
+  cudaGetLastError();
+  return GM_ERR_CUDA;
+}
+
+gm_status finish(const Call& c, bool launched, const int* word = nullptr) {
   if (cudaGetLastError() != cudaSuccess || !launched) return GM_ERR_CUDA;
-  return c.flags & GM_LOSS_CHECK ? gm_loss_status(c.s) : GM_OK;
+  if (!(c.flags & GM_LOSS_CHECK)) return GM_OK;
+  int bits = 0;
+  if ((word && cudaMemcpyAsync(&bits, word, 4, cudaMemcpyDeviceToHost, c.s) != cudaSuccess) ||
+      cudaStreamSynchronize(c.s) != cudaSuccess) {
+    cudaGetLastError();
+    return GM_ERR_CUDA;
+  }
+  return status_of(bits);
 }
 
 Targets targets_of(const Call& c) {
@@ -642,12 +690,14 @@ struct ForwardPlan {
   Source h, w;
   TeacherPlan t;
   int blocks = 0;  // of the kernel for few rows; 0: the product
+  Words own;
   int cg, bn;
   int64_t n_tiles, n_parts;
   size_t o_part, o_zt;
   explicit ForwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
     const int64_t n = c.z.n_rows;
+    own.plan(a, c);
     cg = n > 128 ? 2 : 1;
     bn = prod_logits_cols(cg, h.planes());
     n_tiles = div_up(c.z.n_classes, bn);
@@ -672,6 +722,9 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   ForwardPlan p(c);
   Arena& a = p.a;
   rc = a.open(c);
+  if (rc != GM_OK) return rc;
+  int *lost = a.at<int>(p.own.lost), *word = a.at<int>(p.own.status);
+  rc = own_status(c, word);
   if (rc != GM_OK) return rc;
   const TeacherPlan& t = p.t;
   float4* part = a.at<float4>(p.o_part);
@@ -703,6 +756,9 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
     g.part = part;
     g.part_ld = n;
     g.z_t = z_t;
+    g.lost = lost;
+    g.n_lost = c.sms;
+    g.lost_first = true;
     ok = launch_prod(Prod::kStats, p.cg, p.bn, maps, g, c.sms, c.s) == cudaSuccess;
   }
   JoinArgs j = {};
@@ -719,6 +775,8 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   j.kl = kl;
   j.lse_t = lse_t;
   j.status = c.status;
+  j.lost = p.blocks ? nullptr : lost;
+  j.n_lost = c.sms;
   if (ok) {
     // few rows: a block each, so that their half tiles are read by many threads; more: 2 a block,
     // a whole 32-byte sector (512 rows, 8192 half tiles: 45 -> 18 us); many: 8, a 128-byte line
@@ -728,7 +786,7 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
           : n <= 16 * c.sms ? launch_chained(k_join<2>, blocks2, 256, 0, c.s, 1, j)
                             : launch_chained(k_join<8>, blocks8, 256, 0, c.s, 1, j)) == cudaSuccess;
   }
-  return finish(c, ok);
+  return finish(c, ok, word);
 }
 
 struct Grads {
@@ -753,11 +811,12 @@ bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t di
   return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
 }
 
-void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const unsigned* g_max) {
+void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const unsigned* g_max,
+                const int* lost) {
   const int64_t n = c.z.n_rows * c.z.dim, stride = c.z.n_rows * acc_ld;
   const bool many = splits >= 16;
   launch_chained(many ? k_sum_splits<8> : k_sum_splits<1>, grid_for(n, many ? 32 : 256), 256, 0, c.s, 1, acc, splits, stride,
-                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), g_max, c.status);
+                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), g_max, lost, c.sms);
 }
 
 // How a backward call is cut, and where its workspace lies.
@@ -771,10 +830,12 @@ struct BackwardPlan {
   bool dh_direct;  // dH needs no sum over pieces or splits
   int64_t acc_ld;
   int blocks = 0;  // of the kernel for few rows; 0: the products
+  Words own;
   size_t o_max = 0, o_g = 0, o_acc = 0;
   explicit BackwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
     const int64_t n = c.z.n_rows, cls = c.z.n_classes, dim = c.z.dim;
+    own.plan(a, c);
     planes = c.z.type == GM_LOSS_F32 ? 3 : 1;
     if (skinny(c)) {
       blocks = skinny_most_blocks(cls, c.sms);
@@ -820,6 +881,9 @@ gm_status backward(Call& c, const Grads& q) {
   Arena& a = p.a;
   rc = a.open(c);
   if (rc != GM_OK) return rc;
+  int *lost = a.at<int>(p.own.lost), *word = a.at<int>(p.own.status);
+  rc = own_status(c, word);
+  if (rc != GM_OK) return rc;
   const TeacherPlan& t = p.t;
   const RowGrads row{targets_of(c), q.lse,   q.g_loss, q.g_lse, c.teacher ? a.at<int32_t>(t.len) : nullptr,
                      q.lse_t,       q.g_kl, 1.f / c.temperature};
@@ -834,8 +898,8 @@ gm_status backward(Call& c, const Grads& q) {
     int vec = skinny_vec(g.w, g.w_ld, dim, cls, es);
     if (q.dw) vec = std::min(vec, skinny_vec(q.dw, q.dw_ld, dim, cls, es));
     const bool ok = launch_skinny(g, c.z.type, true, vec, &p.blocks, c.s) == cudaSuccess;
-    if (ok && q.dh) sum_splits(c, g.acc, p.blocks, dim, q, nullptr);
-    return finish(c, ok);
+    if (ok && q.dh) sum_splits(c, g.acc, p.blocks, dim, q, nullptr, nullptr);
+    return finish(c, ok, word);
   }
   const int planes = p.planes, bn_h = p.bn_h, bn_w = p.bn_w, cg_h = p.cg_h, cg_w = p.cg_w;
   const int64_t width = p.width, g_ld = p.width, splits = p.splits, acc_ld = p.acc_ld;
@@ -847,6 +911,8 @@ gm_status backward(Call& c, const Grads& q) {
   set_logits_args(base, c, a, t);
   base.row = row;
   base.g_planes = p.g_planes;
+  base.lost = lost;
+  base.n_lost = c.sms;
   unsigned* g_max = nullptr;
   if (c.z.type == GM_LOSS_F16) {
     g_max = a.at<unsigned>(p.o_max);
@@ -875,6 +941,7 @@ gm_status backward(Call& c, const Grads& q) {
       g.group = group_of(g.m_tiles, 128 * cg, dim, planes);
       g.b_row0 = static_cast<int>(c0);
       g.cls0 = c0;
+      g.lost_first = c0 == 0;
       ok = launch_prod(Prod::kGrad, cg, bn, maps, g, c.sms, c.s) == cudaSuccess;
     }
     if (ok && q.dh) {
@@ -918,8 +985,8 @@ gm_status backward(Call& c, const Grads& q) {
     }
   }
   if (ok && q.dh && !dh_direct)
-    sum_splits(c, a.at<float>(o_acc), static_cast<int>(splits), acc_ld, q, g_max);
-  return finish(c, ok);
+    sum_splits(c, a.at<float>(o_acc), static_cast<int>(splits), acc_ld, q, g_max, lost);
+  return finish(c, ok, word);
 }
 
 gm_status check_grads(const Call& c, const Grads& q) {
@@ -1017,20 +1084,15 @@ extern "C" gm_status gm_loss_workspace(const gm_logits* z, int64_t teacher_nnz, 
 extern "C" gm_status gm_loss_status(void* stream) {
   if (cudaPeekAtLastError() != cudaSuccess) return GM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  gm::DevBuf<int> taken;
+  if (!taken.alloc(1, s)) return GM_ERR_OOM;
+  (gm::k_take_status<<<1, 1, 0, s>>>(taken.p), gm::note_launch());
   int bits = 0;
-  if (cudaMemcpyFromSymbolAsync(&bits, gm::g_loss_status, 4, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(&bits, taken.p, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess) {
     cudaGetLastError();
     return GM_ERR_CUDA;
   }
-  if (bits) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(gm::g_loss_status, &zero, 4, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess) {
-      cudaGetLastError();
-      return GM_ERR_CUDA;
-    }
-  }
-  if (bits & gm::kLossTimeout) return GM_ERR_DEVICE_TIMEOUT;
-  return bits ? GM_ERR_BAD_INDEX : GM_OK;
+  return gm::status_of(bits);
 }

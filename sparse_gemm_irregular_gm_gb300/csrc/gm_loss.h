@@ -37,7 +37,7 @@ cudaError_t launch_chained(void (*k)(P...), unsigned grid, unsigned block, size_
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Bits of the losses' status word (one a device, read by gm_loss_status).
+// Bits of a status word: the device's, which gm_loss_status reads, or a checked call's own.
 enum : int {
   kLossTimeout = 1,    // a bounded wait inside a kernel gave up
   kLossBadTarget = 2,  // a target outside [0, n_classes) that is not the ignored one
@@ -133,6 +133,9 @@ struct ProdArgs {
   int b_row0;        // first row of W's map
   int64_t m, n;      // rows and columns of the result
   int* status;
+  int* lost;         // [n_lost] of this call: 1 where a block gave up; n_lost: SMs, at least as many as blocks
+  int n_lost;
+  bool lost_first;   // the call's first product: writes all of them
   // kStats, kGrad
   int64_t cls0;      // class of column 0
   Targets tgt;

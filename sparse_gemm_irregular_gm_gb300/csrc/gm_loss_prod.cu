@@ -793,7 +793,15 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_free<CG>(tmem, kTmemCols);
-  if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kLossTimeout);
+  // The report may be read and cleared at any time, by other calls too; what later kernels of this
+  // call go by stays in its workspace.
+  if (threadIdx.x == 0) {
+    const int gave_up = s_abort;
+    if (gave_up) atomicOr(g.status, kLossTimeout);
+    if (g.lost_first)
+      for (int i = blockIdx.x; i < g.n_lost; i += gridDim.x) g.lost[i] = i == static_cast<int>(blockIdx.x) && gave_up;
+    else if (gave_up) g.lost[blockIdx.x] = 1;
+  }
 }
 
 template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>

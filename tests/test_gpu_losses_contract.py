@@ -6,8 +6,8 @@ import threading
 import pytest
 import torch
 
-from sparse_gemm_irregular_gm_gb300 import losses
-from test_gpu_losses import make
+from sparse_gemm_irregular_gm_gb300 import binding, losses
+from test_gpu_losses import make, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,30 @@ def test_host_threads_with_rows_of_different_lengths():
     assert statuses == [{0}] * len(calls)
     for *_, want, got in held:
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_checked_call_reports_its_own_rows_alone():
+    """Another call's bad target is neither raised by a checked call nor taken from gm_loss_status."""
+    h, w, target = make("bf16", 200, 72, 300, ignored=0.0)
+    bad = target.clone()
+    bad[11] = 300
+    one_h, one_target = h[:1], target[:1]
+    losses.xent_forward(h, w, bad)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    loss, lse = losses.xent_forward(h, w, target, check=True)
+    losses.xent_forward(one_h, w, one_target, check=True, stream=other)
+    (gl,), _ = weights(200, 1, 0)
+    losses.xent_backward(h, w, target, lse, gl, check=True)
+    none = h[:0]
+    losses.xent_forward(none, w, target[:0], check=True)
+    with pytest.raises(binding.GmError) as e:
+        losses.gm_loss_status()
+    assert e.value.status == 9  # GM_ERR_BAD_INDEX
+    losses.gm_loss_status()
+    for step in (lambda: losses.xent_forward(h, w, bad, check=True), lambda: losses.xent_backward(h, w, bad, lse, gl, check=True),
+                 lambda: losses.xent_backward(one_h, w, bad[11:12], lse[:1], gl[:1], check=True)):
+        with pytest.raises(binding.GmError) as e:
+            step()
+        assert e.value.status == 9
+        losses.gm_loss_status()  # told once, by the call itself
