@@ -66,8 +66,9 @@ typedef struct gm_logits {
 } gm_logits;
 
 /* The class each row should have. Rows with ignore_index have loss 0 and no
- * gradient. A target outside [0, n_classes) that is not ignore_index gives loss
- * NaN, no gradient, and GM_ERR_BAD_INDEX from gm_loss_status. */
+ * gradient by it; grad_lse, the derivative by their lse, counts. A target outside
+ * [0, n_classes) that is not ignore_index gives loss NaN, no gradient by loss or lse,
+ * and GM_ERR_BAD_INDEX from gm_loss_status. */
 typedef struct gm_labels {
   const void* target;   /* device, n_rows int64 (int32 with target32) */
   int64_t ignore_index;

@@ -107,7 +107,7 @@ __device__ __forceinline__ RowCoef row_coef(const RowGrads& r, const RowRaw& x) 
     c.t = check_target(r.tgt, x.t);
     c.gl = c.t >= 0 ? x.g_loss : 0.f;
     c.lse = x.lse;
-    c.a = c.gl + x.g_lse;
+    c.a = c.t == -2 ? 0.f : c.gl + x.g_lse;  // an ignored row has an lse like any other
   }
   if (r.ent_len) {
     c.lse_t = x.lse_t;

@@ -6,8 +6,9 @@ import threading
 import pytest
 import torch
 
+import loss_oracle as lo
 from sparse_gemm_irregular_gm_gb300 import binding, losses
-from test_gpu_losses import make, weights
+from test_gpu_losses import check_grads, make, weights, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,25 @@ def test_a_checked_call_reports_its_own_rows_alone():
             step()
         assert e.value.status == 9
         losses.gm_loss_status()  # told once, by the call itself
+
+
+@pytest.mark.parametrize("kind,n", [("bf16", 200), ("f16", 60), ("f32", 140), ("f32", 5), ("bf16", 1)])
+def test_rows_without_a_target_and_the_gradient_by_lse(kind, n):
+    """An ignored row's lse has its gradient; a row whose target is out of range has none at all."""
+    h, w, target = make(kind, n, 72, 300, ignored=0.0)
+    loss, lse = losses.xent_forward(h, w, target, check=True)
+    (gl, gs), (gl_n, gs_n) = weights(n, 2, 0, scale=64.0 if kind == "f16" else 1.0)
+    row = n // 2
+    target[row] = -100
+    tn = target.cpu().numpy()
+    f = lo.forward(wide(h), wide(w), tn)
+    dh, dw = losses.xent_backward(h, w, target, lse, gl, gs, check=True)
+    check_grads(f, lo.logit_grads(f, tn, -100, gl_n, gs_n), h, w, kind, 1.0, dh, dw)
+    assert torch.any(dh[row] != 0)
+    target[row] = 300
+    gs_n[row] = 0.0
+    dh, dw = losses.xent_backward(h, w, target, lse, gl, gs)
+    with pytest.raises(binding.GmError):
+        losses.gm_loss_status()
+    assert torch.all(dh[row] == 0)
+    check_grads(f, lo.logit_grads(f, tn, -100, gl_n, gs_n), h, w, kind, 1.0, dh, dw)
