@@ -85,17 +85,33 @@ __global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int6
 }
 
 // ---- the teacher's rows -----------------------------------------------------------------
-template <int W>
-__device__ __forceinline__ float group_max(float x, float* sh) {  // every thread of the W warps gets the result
+// The largest of values, to which NaN gives way. 64-bit ones by their bits as signed integers, those below
+// 0 turned over (2048 rows of 2500 values: 294 us for k_teacher with maxima in fp64, 92 so).
+__device__ __forceinline__ float key_of(float x) { return x; }
+__device__ __forceinline__ int64_t key_of(double x) {
+  const int64_t b = __double_as_longlong(x), size = b & INT64_MAX, inf = int64_t(0x7ff) << 52;
+  return size > inf ? INT64_MIN : b < 0 ? b ^ INT64_MAX : b;
+}
+__device__ __forceinline__ float value_of(float k) { return k; }
+__device__ __forceinline__ double value_of(int64_t k) {  // of what is less than any value: -inf
+  return k == INT64_MIN ? -INFINITY : __longlong_as_double(k < 0 ? k ^ INT64_MAX : k);
+}
+__device__ __forceinline__ float larger(float x, float y) { return fmaxf(x, y); }
+__device__ __forceinline__ int64_t larger(int64_t x, int64_t y) { return x > y ? x : y; }
+template <class V>
+using Key = decltype(key_of(V()));
+
+template <int W, class K>
+__device__ __forceinline__ K group_max(K x, K* sh) {  // every thread of the W warps gets the result
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
+  for (int d = 16; d > 0; d >>= 1) x = larger(x, __shfl_xor_sync(kFull, x, d));
   if constexpr (W > 1) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
     __syncthreads();
     x = sh[0];
 #pragma unroll
-    for (int w = 1; w < W; ++w) x = fmaxf(x, sh[w]);
+    for (int w = 1; w < W; ++w) x = larger(x, sh[w]);
   }
   return x;
 }
@@ -121,9 +137,11 @@ __device__ __forceinline__ bool group_or(bool x) {
 // q = softmax of a row's stored values / T; base[row] = sum q log q. Bound by the latency
 // of a row's loads: a warp a row where rows are short; rows over kLongRow entries are
 // left to the whole block afterwards. The rows of a block lie a grid apart, since long rows
-// of a graph's product are neighbours. fp32: a thread sums a few hundred terms at most, and
-// an fp64 log or sum costs more here than the loads do (8192 rows of 128 entries: 142 us with them,
-// 10 without; 1500 ragged rows, the longest of some 47,000 entries: 30 us).
+// of a graph's product are neighbours. A value counts by its distance to the row's largest, taken in
+// the values' own type (64-bit ones may be large and close). From there on fp32: a thread sums at most 32
+// terms of a short row and one in 1024 of a long one (1024 of a row over 2^20 classes), and an fp64 log
+// or sum costs more here than the loads do (8192 rows of 128 entries: 142 us with them, 10 without;
+// 1500 ragged rows, the longest of some 47,000 entries: 30 us).
 constexpr int kLongRow = 1024, kTeacherWarps = 32;
 
 template <class V, class R, class C>
@@ -142,29 +160,30 @@ struct TeacherArgs {
 
 template <int W, class V, class R, class C>
 __device__ __forceinline__ void teacher_row(const TeacherArgs<V, R, C>& a, int64_t row, int64_t lo, int64_t hi,
-                                            float* sh) {
+                                            Key<V>* sh_max, float* sh) {
   constexpr int kGroup = 32 * W;
   const int lane = threadIdx.x % kGroup;
   bool bad = lo < 0 || hi < lo || hi > a.nnz;
-  float m = -INFINITY, sum = 0.f, b = 0.f;
+  V m = 0;
+  float sum = 0.f, b = 0.f;
   if (!bad) {
     bool wrong = false;
+    Key<V> most = key_of(static_cast<V>(-INFINITY));
 #pragma unroll 4
     for (int64_t i = lo + lane; i < hi; i += kGroup) {
       const int64_t c = static_cast<int64_t>(a.col[i]);
       if (c < 0 || c >= a.n_cls || (i > lo && static_cast<int64_t>(a.col[i - 1]) >= c)) wrong = true;
-      m = fmaxf(m, static_cast<float>(a.val[i] * a.inv_t));
+      most = larger(most, key_of(a.val[i]));
     }
     bad = group_or<W>(wrong);
-    m = group_max<W>(m, sh);
+    m = value_of(group_max<W>(most, sh_max));
+    if (m == -INFINITY) m = 0;  // every exponential is 0, or NaN
   }
+  auto below = [&](V x) { return static_cast<float>(x - m) * a.inv_t; };
   // a NaN value leaves the maximum alone and makes the sum NaN, so the row counts as one with entries
   if (!bad) {
 #pragma unroll 4
-    for (int64_t i = lo + lane; i < hi; i += kGroup) {
-      const float v = static_cast<float>(a.val[i] * a.inv_t);
-      sum += v == -INFINITY ? 0.f : expf(v - m);
-    }
+    for (int64_t i = lo + lane; i < hi; i += kGroup) sum += expf(below(a.val[i]));
     sum = group_sum<W>(sum, sh);
   }
   const bool any = !bad && sum != 0.f;
@@ -172,10 +191,9 @@ __device__ __forceinline__ void teacher_row(const TeacherArgs<V, R, C>& a, int64
     const float log_sum = logf(sum), inv = 1.f / sum;
 #pragma unroll 4
     for (int64_t i = lo + lane; i < hi; i += kGroup) {
-      const float v = static_cast<float>(a.val[i] * a.inv_t);
-      const float q = v == -INFINITY ? 0.f : expf(v - m) * inv;
+      const float v = below(a.val[i]), q = expf(v) * inv;
       a.ents[i] = make_int2(static_cast<int>(a.col[i]), __float_as_int(q));
-      if (q > 0.f || q != q) b += q * ((v - m) - log_sum);
+      if (q > 0.f || q != q) b += q * (v - log_sum);
     }
     b = group_sum<W>(b, sh);
   }
@@ -189,6 +207,7 @@ __device__ __forceinline__ void teacher_row(const TeacherArgs<V, R, C>& a, int64
 
 template <class V, class R, class C>
 __global__ void __launch_bounds__(32 * kTeacherWarps) k_teacher(const TeacherArgs<V, R, C> a) {
+  __shared__ Key<V> sh_max[kTeacherWarps];
   __shared__ float sh[kTeacherWarps];
   __shared__ unsigned s_long;
   const int warp = threadIdx.x >> 5;
@@ -202,13 +221,13 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) k_teacher(const TeacherArg
       if (lo >= 0 && hi <= a.nnz && hi - lo > kLongRow) {
         if ((threadIdx.x & 31) == 0) atomicOr(&s_long, 1u << warp);
       } else {
-        teacher_row<1>(a, row, lo, hi, sh);
+        teacher_row<1>(a, row, lo, hi, sh_max, sh);
       }
     }
     __syncthreads();
     for (unsigned left = s_long; left; left &= left - 1) {
       const int64_t r = row0 + int64_t(__ffs(left) - 1) * gridDim.x;
-      teacher_row<kTeacherWarps>(a, r, static_cast<int64_t>(a.rp[r]), static_cast<int64_t>(a.rp[r + 1]), sh);
+      teacher_row<kTeacherWarps>(a, r, static_cast<int64_t>(a.rp[r]), static_cast<int64_t>(a.rp[r + 1]), sh_max, sh);
       __syncthreads();
     }
     __syncthreads();

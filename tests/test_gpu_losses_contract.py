@@ -3,12 +3,13 @@ masked classes, weights far apart, teachers with large values, malformed row poi
 import ctypes
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 import loss_oracle as lo
 from sparse_gemm_irregular_gm_gb300 import binding, losses
-from test_gpu_losses import check_grads, make, weights, wide
+from test_gpu_losses import check_forward, check_grads, make, make_teacher, near, weights, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,37 @@ def test_rows_without_a_target_and_the_gradient_by_lse(kind, n):
         losses.gm_loss_status()
     assert torch.all(dh[row] == 0)
     check_grads(f, lo.logit_grads(f, tn, -100, gl_n, gs_n), h, w, kind, 1.0, dh, dw)
+
+
+@pytest.mark.parametrize("offset", [1e9, -3e12, 1e300])
+@pytest.mark.parametrize("longest", [40, 3000])
+def test_teachers_values_are_large_and_close(offset, longest):
+    """64-bit values count by their distance to the row's largest, however large they are."""
+    n, v = 50, 3000
+    h, w, _ = make("bf16", n, 40, v)
+    dev, host = make_teacher(n, v, longest=longest, val=torch.float64)
+    dev.val.add_(offset)
+    host = lo.Teacher(host.row_ptr, host.col, dev.val.cpu().numpy())
+    o = losses.distill_forward(h, w, dev, 1.5, check=True)
+    f = lo.forward(wide(h), wide(w), None, -100, host, 1.5)
+    # the oracle divides by the temperature before it subtracts: as far apart as that rounds
+    spread = 2.0 ** -51 * abs(offset)
+    if spread < 1e-2:
+        bounds = lo.forward_bounds(f, wide(h), wide(w), 1.5)
+        near(o.kl, f["kl"], bounds["kl"] + 8 * spread * (np.abs(f["z"]).max(1) + np.abs(f["kl"]) + 1), "kl")
+    else:  # the values' own differences are rounded away: -inf and one value
+        q, base = lo.teacher_rows(lo.Teacher(host.row_ptr, host.col, np.where(np.isinf(host.val), host.val, 0.0)), 1.5, n, v)
+        kl = np.where(q.sum(1) > 0, base - (q * f["z"]).sum(1) / 1.5 + f["lse_t"], 0.0)
+        near(o.kl, kl, lo.forward_bounds(f, wide(h), wide(w), 1.5)["kl"], "kl")
+
+
+def test_teachers_lowest_values_over_a_small_temperature():
+    """Rows of nothing but the type's lowest value are uniform, as rows of any one value are."""
+    n, v = 40, 300
+    h, w, _ = make("bf16", n, 40, v)
+    dev, host = make_teacher(n, v, empty=0.0)
+    dev.val.fill_(torch.finfo(torch.float32).min)
+    host = lo.Teacher(host.row_ptr, host.col, np.zeros_like(host.val))
+    o = losses.distill_forward(h, w, dev, 0.5, check=True)
+    f = lo.forward(wide(h), wide(w), None, -100, host, 0.5)
+    check_forward(f, h, w, 0.5, kl=o.kl, lse_t=o.lse_t)
