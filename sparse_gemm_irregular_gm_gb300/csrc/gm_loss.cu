@@ -29,10 +29,25 @@ __global__ void k_take_status(int* __restrict__ taken) { *taken = atomicExch(&g_
 
 // ---- operands that TMA cannot read in place ------------------------------------------
 // f32: three bf16 planes, x = x0 + x1 + x2 with x0 the nearest bf16 of x and so on, which
-// keeps all 24 bits; 16-bit types: one plane, copied. Rows are padded with zeros to ld, a
+// keeps all 24 bits; an infinity stands in the third plane alone, which meets only the other operand's
+// first, its sign and size (in the first it would meet low planes that are 0: NaN where the product is
+// infinite); 16-bit types: one plane, copied. Rows are padded with zeros to ld, a
 // multiple of 8: a thread writes 8 elements of each plane at once. VEC: the rows of src start
 // on 16-byte boundaries. Bound by memory: 126425 x 1320 f32, 1.67 GB in and out, 245 us (6.8 TB/s);
 // 489196 x 437 f16, 0.86 GB, 132 us (6.5 TB/s).
+constexpr uint32_t kRoundsPast = 0x7f7f8000u;  // bits of |x| from which the nearest bf16 is none that is finite
+__device__ __forceinline__ uint32_t take_plane(float& x, bool third, bool ordinary) {  // leaves in x what is left of it
+  __nv_bfloat16 a = __float2bfloat16_rn(x);
+  float left = x - __bfloat162float(a);
+  if (!ordinary && !third) {
+    if (fabsf(x) == INFINITY) a = __ushort_as_bfloat16(0), left = x;
+    else if (x != x) left = 0.f;  // NaN stands in the first plane
+    else if ((__float_as_uint(x) & INT32_MAX) >= kRoundsPast) a = __float2bfloat16_rz(x), left = x - __bfloat162float(a);
+  }
+  x = left;
+  return __bfloat16_as_ushort(a);
+}
+
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int64_t rows, int dim, int64_t src_ld,
                                               uint16_t* __restrict__ dst, int ld) {
@@ -66,17 +81,17 @@ __global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int6
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = j < left ? p[j] : 0.f;
       }
+      uint32_t largest = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) largest = max(largest, __float_as_uint(x[j]) & INT32_MAX);
+      const bool ordinary = largest < kRoundsPast;
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
         uint32_t y[4];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const __nv_bfloat16 a = __float2bfloat16_rn(x[j]), b = __float2bfloat16_rn(x[j + 1]);
-          y[j / 2] = __bfloat16_as_ushort(a) | (static_cast<uint32_t>(__bfloat16_as_ushort(b)) << 16);
-          // infinities, NaN and what rounds to infinity stand in the first plane
-          const float ra = __bfloat162float(a), rb = __bfloat162float(b);
-          x[j] = fabsf(ra) <= 3.4e38f ? x[j] - ra : 0.f;
-          x[j + 1] = fabsf(rb) <= 3.4e38f ? x[j + 1] - rb : 0.f;
+          const uint32_t a = take_plane(x[j], q == 2, ordinary), b = take_plane(x[j + 1], q == 2, ordinary);
+          y[j / 2] = a | (b << 16);
         }
         *reinterpret_cast<uint4*>(dst + q * n + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
       }

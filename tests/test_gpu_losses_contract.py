@@ -131,3 +131,40 @@ def test_teachers_lowest_values_over_a_small_temperature():
     o = losses.distill_forward(h, w, dev, 0.5, check=True)
     f = lo.forward(wide(h), wide(w), None, -100, host, 0.5)
     check_forward(f, h, w, 0.5, kl=o.kl, lse_t=o.lse_t)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lowest", [False, True])
+@pytest.mark.parametrize("n,d", [(1, 65), (5, 65), (140, 65), (300, 129), (60, 200), (140, 1100)])
+def test_classes_masked_by_their_bias(kind, lowest, n, d):
+    """The last column of h is 1, that of w a bias: -inf, or the type's lowest value, takes a class out, and the rest are
+    as if it were not there."""
+    v = 400
+    h, w, target = make(kind, n, d, v)
+    h[:, -1] = 1
+    w[:, -1] = 0
+    keep = torch.arange(v) % 3 != 1
+    w[(~keep).cuda(), -1] = torch.finfo(w.dtype).min if lowest else -torch.inf
+    new = (torch.cumsum(keep, 0) - 1).numpy()
+    target = torch.where(target < 0, target, target // 3 * 3)
+    tn = target.cpu().numpy()
+    tn = np.where(tn < 0, tn, new[tn])
+    dev, host = make_teacher(n, v, longest=20)
+    dev.col.copy_(dev.col)
+    # entries on masked classes have probability 0
+    masked = ~keep.numpy()[host.col]
+    dev.val[torch.from_numpy(masked).cuda()] = -torch.inf
+    rows = np.repeat(np.arange(n), np.diff(host.row_ptr))[~masked]
+    rp = np.concatenate([[0], np.cumsum(np.bincount(rows, minlength=n))])
+    host = lo.Teacher(rp, new[host.col[~masked]], host.val[~masked])
+    wk = w[keep.cuda()]
+    o = losses.distill_forward(h, w, dev, 2.0, target=target, check=True)
+    f = lo.forward(wide(h), wide(wk), tn, -100, host, 2.0)
+    check_forward(f, h, wk, 2.0, kl=o.kl, lse_t=o.lse_t, loss=o.loss, lse=o.lse)
+    (gk, gl), (gk_n, gl_n) = weights(n, 2, d, scale=64.0 if kind == "f16" else 1.0)
+    dh, dw = losses.distill_backward(h, w, dev, o.lse_t, gk, 2.0, target=target, lse=o.lse, grad_loss=gl, check=True)
+    assert torch.all(dw[(~keep).cuda()] == 0)
+    # 0 times -inf spoils the column of biases, as in any product; f16's lowest times a G of 2^-24 does not
+    (eh, bh), (ew, bw) = lo.gradient_bounds(f, lo.logit_grads(f, tn, -100, gl_n, None, 2.0, gk_n), wide(h), wide(wk), kind, 2.0)
+    near(dh[:, :-1], eh[:, :-1], bh[:, :-1], "dh")
+    near(dw[keep.cuda()], ew, bw, "dw")
