@@ -80,8 +80,8 @@ typedef struct gm_labels {
 
 /* Tuning; zero selects the automatic value. NULL is the same as all zeros. */
 typedef struct gm_loss_config {
-  int64_t workspace_cap_bytes; /* bound on the piece of G a backward call holds; 0 = 512 MiB; the
-                                  narrowest piece has 256 classes                                */
+  int64_t workspace_cap_bytes; /* bound on the piece of G a backward call holds; 0 = 512 MiB, f16 (which
+                                  may keep G at two scales) 1 GiB; the narrowest piece has 256 classes */
   int32_t flags;               /* GM_LOSS_CHECK                                                  */
   void* workspace;             /* device memory for the call, 256-byte aligned (NULL: the hooks); it
                                   may be reused once the call's work on the stream is done       */

@@ -328,23 +328,28 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   }
 }
 
-// ---- scale of G in f16 ------------------------------------------------------------------------
-// Bits of the largest |G| that the rows' weights allow, one block: 2 us at 777 rows, its launch.
-__global__ void __launch_bounds__(1024) k_g_max(int64_t n, const RowGrads r, unsigned* __restrict__ g_max) {
+// ---- weights of the rows, for the scales of G in f16 -------------------------------------------
+// Bits of the largest (0: none) and of the smallest above 0 (infinity: none), one block: 2 us at 777
+// rows, its launch.
+__global__ void __launch_bounds__(1024) k_weights(int64_t n, const RowGrads r, unsigned* __restrict__ out) {
   chain_wait();
-  float m = 0.f;
+  float most = 0.f, least = INFINITY;
   for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-    const RowCoef c = row_coef(r, row_raw(r, i));
-    m = fmaxf(m, fabsf(c.a) + fabsf(c.gl) + fabsf(c.b));
+    const float x = weight_of(row_coef(r, row_raw(r, i)));
+    most = fmaxf(most, x);  // NaN gives way
+    if (x > 0.f) least = fminf(least, x);
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-  __shared__ float sh[32];
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  for (int d = 16; d > 0; d >>= 1) {
+    most = fmaxf(most, __shfl_xor_sync(kFull, most, d));
+    least = fminf(least, __shfl_xor_sync(kFull, least, d));
+  }
+  __shared__ float sh[2][32];
+  if ((threadIdx.x & 31) == 0) sh[0][threadIdx.x >> 5] = most, sh[1][threadIdx.x >> 5] = least;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 32; ++w) m = fmaxf(m, sh[w]);
-    *g_max = __float_as_uint(m);
+    for (int w = 1; w < 32; ++w) most = fmaxf(most, sh[0][w]), least = fminf(least, sh[1][w]);
+    out[0] = __float_as_uint(most), out[1] = __float_as_uint(least);
   }
 }
 
@@ -354,15 +359,14 @@ __global__ void __launch_bounds__(1024) k_g_max(int64_t n, const RowGrads r, uns
 template <int SUB>
 __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ acc, int splits, int64_t split_stride,
                                                     int64_t rows, int64_t dim, int64_t acc_ld, void* __restrict__ out,
-                                                    int64_t out_ld, int type, const unsigned* __restrict__ g_max,
-                                                    const int* __restrict__ lost, int n_lost) {
+                                                    int64_t out_ld, int type, const int* __restrict__ lost,
+                                                    int n_lost) {
   constexpr int kCols = 256 / SUB;
   __shared__ float sh[SUB][kCols];
   chain_wait();
   const int64_t n = rows * dim, stride = static_cast<int64_t>(gridDim.x) * kCols;
   const int col = threadIdx.x % kCols, sub = threadIdx.x / kCols;
   const bool lost_here = any_lost(lost, n_lost);
-  const float inv = 1.f / g_scale_of(g_max);
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kCols; i0 < n; i0 += stride) {
     const int64_t i = i0 + col;
     const int64_t r = i / dim, c = i - r * dim;
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ ac
     }
     const bool gone = __any_sync(kFull, lost_here);  // a warp has one sub where SUB is over 1
     if (i >= n) continue;
-    x = gone ? NAN : x * inv;
+    if (gone) x = NAN;
     const int64_t o = r * out_ld + c;
     if (type == GM_LOSS_F32) static_cast<float*>(out)[o] = x;
     else if (type == GM_LOSS_BF16) static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(x);
@@ -433,7 +437,7 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 constexpr int64_t kMostIndex = (int64_t(1) << 31) - 256;  // tile coordinates are int32
-constexpr int64_t kDefaultCap = int64_t(512) << 20;
+constexpr int64_t kDefaultCap = int64_t(512) << 20;  // f16: of each of the two sets of planes (Scales)
 
 struct Call {
   gm_logits z = {};
@@ -442,7 +446,7 @@ struct Call {
   int32_t value_type = 0, index_type = 0;
   float temperature = 1.f;
   const gm_labels* labels = nullptr;
-  int64_t cap = kDefaultCap;
+  int64_t cap = 0;                  // 0: the default
   int32_t flags = 0;
   void* workspace = nullptr;
   int64_t workspace_bytes = 0;
@@ -511,7 +515,7 @@ gm_status check(Call& c, const gm_logits* z, const gm_labels* labels, const gm_l
     return GM_ERR_INVALID_ARG;
   if (cfg) {
     if (cfg->workspace_cap_bytes < 0 || (cfg->flags & ~GM_LOSS_CHECK)) return GM_ERR_INVALID_ARG;
-    if (cfg->workspace_cap_bytes) c.cap = cfg->workspace_cap_bytes;
+    c.cap = cfg->workspace_cap_bytes;
     c.flags = cfg->flags;
     if (cfg->workspace && (!aligned(cfg->workspace, 256) || cfg->workspace_bytes < 0)) return GM_ERR_INVALID_ARG;
     c.workspace = cfg->workspace;
@@ -845,12 +849,11 @@ bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t di
   return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
 }
 
-void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const unsigned* g_max,
-                const int* lost) {
+void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const int* lost) {
   const int64_t n = c.z.n_rows * c.z.dim, stride = c.z.n_rows * acc_ld;
   const bool many = splits >= 16;
   launch_chained(many ? k_sum_splits<8> : k_sum_splits<1>, grid_for(n, many ? 32 : 256), 256, 0, c.s, 1, acc, splits, stride,
-                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), g_max, lost, c.sms);
+                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), lost, c.sms);
 }
 
 // How a backward call is cut, and where its workspace lies.
@@ -858,14 +861,14 @@ struct BackwardPlan {
   Arena a;
   Source h, w;
   TeacherPlan t;
-  int planes, g_planes, bn_h, bn_w, cg_h, cg_w;
+  int planes, g_planes, g_sets, bn_h, bn_w, cg_h, cg_w;
   int64_t width;   // classes of a piece; rows of G are as long
   int64_t splits;  // of dH's sum along a piece's classes
   bool dh_direct;  // dH needs no sum over pieces or splits
   int64_t acc_ld;
   int blocks = 0;  // of the kernel for few rows; 0: the products
   Words own;
-  size_t o_max = 0, o_g = 0, o_acc = 0;
+  size_t o_weights = 0, o_g = 0, o_acc = 0;
   explicit BackwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
     const int64_t n = c.z.n_rows, cls = c.z.n_classes, dim = c.z.dim;
@@ -878,8 +881,10 @@ struct BackwardPlan {
       return;
     }
     g_planes = planes == 3 ? 3 : n <= 128 ? 2 : 1;
+    g_sets = c.z.type == GM_LOSS_F16 ? 2 : 1;  // see Scales
+    const int64_t cap = c.cap ? c.cap : g_sets * kDefaultCap, g_bytes = n * 2 * g_planes * g_sets;  // of a class
     // pieces of the classes: as few as the bound on G allows, of about equal width
-    const int64_t most = std::max<int64_t>(256, c.cap / (n * 2 * g_planes) / 256 * 256);
+    const int64_t most = std::max<int64_t>(256, cap / g_bytes / 256 * 256);
     const int64_t n_pieces = div_up(cls, most);
     width = std::min<int64_t>(most, up(div_up(cls, n_pieces), 256));
     // tiles of dH: split along the classes when they are fewer than the SMs
@@ -896,8 +901,8 @@ struct BackwardPlan {
     h.plan(a);
     w.plan(a);
     t.plan(a, c);
-    o_max = a.add(4);
-    o_g = a.add(g_planes * n * width * 2);
+    o_weights = a.add(8);
+    o_g = a.add(g_bytes * width);
     o_acc = dh_direct ? 0 : a.add(splits * n * acc_ld * 4);
   }
 };
@@ -932,7 +937,7 @@ gm_status backward(Call& c, const Grads& q) {
     int vec = skinny_vec(g.w, g.w_ld, dim, cls, es);
     if (q.dw) vec = std::min(vec, skinny_vec(q.dw, q.dw_ld, dim, cls, es));
     const bool ok = launch_skinny(g, c.z.type, true, vec, &p.blocks, c.s) == cudaSuccess;
-    if (ok && q.dh) sum_splits(c, g.acc, p.blocks, dim, q, nullptr, nullptr);
+    if (ok && q.dh) sum_splits(c, g.acc, p.blocks, dim, q, nullptr);
     return finish(c, ok, word);
   }
   const int planes = p.planes, bn_h = p.bn_h, bn_w = p.bn_w, cg_h = p.cg_h, cg_w = p.cg_w;
@@ -947,17 +952,19 @@ gm_status backward(Call& c, const Grads& q) {
   base.g_planes = p.g_planes;
   base.lost = lost;
   base.n_lost = c.sms;
-  unsigned* g_max = nullptr;
   if (c.z.type == GM_LOSS_F16) {
-    g_max = a.at<unsigned>(p.o_max);
-    launch_chained(k_g_max, 1, 1024, 0, c.s, 1, n, base.row, g_max);
+    unsigned* weights = a.at<unsigned>(p.o_weights);
+    launch_chained(k_weights, 1, 1024, 0, c.s, 1, n, base.row, weights);
+    base.weights = weights;
+    // classes * 2^-25 / 2^(13 - near) <= 2^-11; with 2^27 classes and more no two exponents are near
+    base.near = 27;
+    while (base.near > 0 && (cls >> (27 - base.near)) > 0) --base.near;
   }
-  base.g_max = g_max;
   uint16_t* g_mem = a.at<uint16_t>(o_g);
   bool ok = true;
   for (int64_t c0 = 0; ok && c0 < cls; c0 += width) {
     const int64_t wid = std::min(width, cls - c0);
-    const Operand og{g_mem, n, wid, g_ld, n * g_ld, p.g_planes};
+    const Operand og{g_mem, n, wid, g_ld, n * g_ld, p.g_planes * p.g_sets};
     ProdMaps maps;
     {
       const int cg = n > 128 ? 2 : 1;
@@ -1019,7 +1026,7 @@ gm_status backward(Call& c, const Grads& q) {
     }
   }
   if (ok && q.dh && !dh_direct)
-    sum_splits(c, a.at<float>(o_acc), static_cast<int>(splits), acc_ld, q, g_max, lost);
+    sum_splits(c, a.at<float>(o_acc), static_cast<int>(splits), acc_ld, q, lost);
   return finish(c, ok, word);
 }
 

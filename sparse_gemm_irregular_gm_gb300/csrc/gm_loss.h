@@ -147,7 +147,8 @@ struct ProdArgs {
   int64_t part_ld;
   float* z_t;        // [row] logit of the target
   RowGrads row;
-  const unsigned* g_max;  // f16: bits of the largest |G| possible (null: no scale)
+  const unsigned* weights;  // f16: bits of the largest and the smallest of the rows' weights (null: no scale)
+  int near;                 // exponents that weights of one scale may lie apart
   // kDh, kDw
   bool acc;          // the map of results is one of fp32 partial sums (by split), added to with acc_add
   bool acc_add;
@@ -157,16 +158,31 @@ struct ProdArgs {
   int out_type;      // GM_LOSS_*
 };
 
-// Scale of G in f16: a power of two that brings the largest |G| possible to at most 2^14.
-__device__ __forceinline__ float g_scale_of(const unsigned* g_max) {
-  if (!g_max) return 1.0f;
-  const float m = __uint_as_float(*g_max);
-  if (!(m > 0.0f) || !(m < 3.0e38f)) return 1.0f;
+// Scales of G in f16, whose range is too short for small probabilities times small weights: powers
+// of two that bring the largest |G| possible, a row's weight, into [2^13, 2^14). What lies under
+// 2^-14 then loses bits, at most half of 2^-24 each: 2^-38 of the weight. While all rows' weights lie
+// within 2^near of the largest, its scale serves them all; near is such that the classes of a row
+// together lose no more than 2^-11 of its weight, f16's own rounding. Otherwise G is kept twice: with a
+// scale for each row for dH, whose rows are sums of their own, and with the largest weight's for dW.
+__device__ __forceinline__ float weight_of(const RowCoef& c) { return fabsf(c.a) + fabsf(c.gl) + fabsf(c.b); }
+__device__ __forceinline__ float scale_for(float weight) {
+  if (!(weight > 0.0f) || !(weight < 3.0e38f)) return 1.0f;
   int e;
-  frexpf(m, &e);
+  frexpf(weight, &e);
   e = 14 - e;
   return ldexpf(1.0f, e < -100 ? -100 : e > 100 ? 100 : e);
 }
+struct Scales {
+  float all = 1.0f;
+  bool apart = false;
+  __device__ __forceinline__ explicit Scales(const ProdArgs& g) {
+    if (!g.weights) return;
+    const unsigned most = g.weights[0], least = g.weights[1];
+    all = scale_for(__uint_as_float(most));
+    apart = static_cast<int>(most >> 23) - static_cast<int>(least >> 23) > g.near;
+  }
+  __device__ __forceinline__ float of(const RowCoef& c) const { return apart ? scale_for(weight_of(c)) : all; }
+};
 
 struct ProdMaps {
   CUtensorMap a, b, o;  // operands, result, boxes of 32 rows (kGrad: of

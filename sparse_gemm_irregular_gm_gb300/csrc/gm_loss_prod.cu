@@ -176,7 +176,8 @@ struct Walk {
 };
 
 // What a thread looks up of its row: read a tile ahead, used before the tile's sums are there.
-template <Prod KIND, bool LAB, bool DIS>
+// COEF: the row's weights, for its G or for the scale of it.
+template <Prod KIND, bool LAB, bool DIS, bool COEF>
 struct RowState {
   Walk w;
   RowCoef c;
@@ -184,7 +185,7 @@ struct RowState {
     RowRaw x = {};
     if (row < g.m) {
       if constexpr (KIND == Prod::kStats && LAB) x.t = raw_target(g.tgt, row);
-      if constexpr (KIND == Prod::kGrad) x = row_raw(g.row, row);
+      if constexpr (COEF) x = (KIND == Prod::kGrad || g.weights) ? row_raw(g.row, row) : x;
     }
     return x;
   }
@@ -192,8 +193,8 @@ struct RowState {
     c = RowCoef{0.f, 0.f, 0.f, 0.f, 0.f, -1};
     if (row < g.m) {
       if constexpr (KIND == Prod::kStats && LAB) c.t = check_target(g.tgt, x.t);
-      if constexpr (KIND == Prod::kGrad) {
-        c = row_coef(g.row, x);
+      if constexpr (COEF) {
+        if (KIND == Prod::kGrad || g.weights) c = row_coef(g.row, x);
         if (LAB && first && c.t == -2) atomicOr(g.status, kLossBadTarget);
       }
     }
@@ -256,7 +257,7 @@ __device__ __forceinline__ void each_32(F&& f) {
 
 // ---- row statistics of half a tile -------------------------------------------------
 template <int BN, bool LAB, bool DIS, class Src>
-__device__ __forceinline__ void end_stats(const ProdArgs& g, Src& src, RowState<Prod::kStats, LAB, DIS>& rs, int64_t row,
+__device__ __forceinline__ void end_stats(const ProdArgs& g, Src& src, RowState<Prod::kStats, LAB, DIS, false>& rs, int64_t row,
                                           int n_tile, int half) {
   constexpr int kCols = BN / 2;
   const int64_t cls = g.cls0 + int64_t(n_tile) * BN + half * kCols;  // class of the first column
@@ -352,6 +353,24 @@ struct Outbox {
 #pragma unroll
     for (int q = 0; q < 4; ++q) put(piece0 + q, keep & x[4 * q], keep & x[4 * q + 1], keep & x[4 * q + 2], keep & x[4 * q + 3]);
   }
+  // 32 columns in f16 at another scale: their values, or what rounding takes of them.
+  __device__ __forceinline__ void put_half(int piece0, const float (&v)[32], float scale, bool rest, uint32_t keep) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = v[8 * q + 2 * j] * scale, b = v[8 * q + 2 * j + 1] * scale;
+        x[j] = pack2<false>(a, b);
+        if (rest) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+          x[j] = pack2<false>(a - y.x, b - y.y);
+        }
+        x[j] &= keep;
+      }
+      put(piece0 + q, x[0], x[1], x[2], x[3]);
+    }
+  }
   __device__ __forceinline__ void put32(const float (&v)[32]) {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -399,15 +418,13 @@ struct Outbox {
 
 // ---- gradient of the logits ----------------------------------------------------------
 // G_ij = a_i e^(z - lse) - gl_i [j = t_i] + b_i (e^(z / T - lse_T) - q_ij), rounded to 16 bits as
-// the operand of the two products after it (times a power of two in f16, whose range
-// is too short for small probabilities times small weights); fp32 operands keep it in
+// the operand of the two products after it (in f16 times a power of two, see Scales); fp32 operands keep it in
 // three bf16 planes, 24 bits. In 16 bits the factors go into the exponent.
 template <bool LAB, bool DIS, bool FINE>
 struct GradRow {
   float a, b, gl, x1, xt, s1, st;
   bool live;
-  __device__ __forceinline__ GradRow(const ProdArgs& g, const RowCoef& c) {
-    const float scale = g_scale_of(g.g_max);
+  __device__ __forceinline__ GradRow(const RowCoef& c, float scale) {
     a = c.a * scale, b = c.b * scale, gl = c.gl * scale;
     live = a != 0.f || b != 0.f || gl != 0.f;
     if (FINE) {
@@ -451,16 +468,24 @@ struct GradRow {
   }
 };
 
-template <int BN, bool LAB, bool DIS, bool FINE, class Src>
+template <int BN, bool LAB, bool DIS, int ACC, class Src>
 __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* map_o, Src& src,
-                                         RowState<Prod::kGrad, LAB, DIS>& rs, int64_t row, int n_tile, int half,
+                                         RowState<Prod::kGrad, LAB, DIS, true>& rs, int64_t row, int n_tile, int half,
                                          Outbox<!kHeld<Src>> box) {
   constexpr int kCols = BN / 2;
+  constexpr bool FINE = ACC != kWhole, kHalf = !three_planes<ACC>;  // kHalf: may be f16
   const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
   const int64_t cls = g.cls0 + col0;
   const int64_t row0 = row - box.lane;
-  const GradRow<LAB, DIS, FINE> gr(g, rs.c);
+  float own = 1.f, to_all = NAN;  // the row's scale; from it to the one of all rows, NaN where that is the same for all
+  if constexpr (kHalf) {
+    const Scales scales(g);
+    own = scales.of(rs.c);
+    if (scales.apart) to_all = scales.all / own;
+  }
+  const GradRow<LAB, DIS, FINE> gr(rs.c, own);
   const uint32_t keep = gr.live ? 0xffffffffu : 0u;  // a row without weight is 0 whatever its logits are
+  const int first = kHalf && to_all == to_all ? -g.g_planes : 0;  // planes under 0: those of the scale of all rows
   if constexpr (!kHeld<Src>) {
     each_32<kCols>([&](auto cc) {
       constexpr int c = decltype(cc)::value;
@@ -468,10 +493,12 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
       src.template get<c>(v);
       gr.of(v, g, rs.c.t, cls + c, rs.w);
 #pragma unroll 1
-      for (int p = 0; p < g.g_planes; ++p) {
+      for (int p = first; p < g.g_planes; ++p) {
         box.open();
-        box.put16(0, v, FINE || g.bf16, p + 1 < g.g_planes, keep);
-        if (row0 < g.m && col0 + c < g.n) box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), p, false);
+        if (kHalf && p < 0) box.put_half(0, v, to_all, p != first, keep);
+        else box.put16(0, v, FINE || g.bf16, p + 1 < g.g_planes, keep);
+        if (row0 < g.m && col0 + c < g.n)
+          box.send(map_o, static_cast<int>(col0 + c), static_cast<int>(row0), p < 0 ? p - 2 * first : p, false);
       }
     });
   } else {
@@ -484,18 +511,20 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
       for (int j = 0; j < 32; ++j) src.acc[c + j] = v[j];
     });
 #pragma unroll 1
-    for (int p = 0; p < g.g_planes; ++p) {
+    for (int p = first; p < g.g_planes; ++p) {
+      const int plane = p < 0 ? p - 2 * first : p;
       each_32<kCols>([&](auto cc) {
         constexpr int c = decltype(cc)::value;
         float v[32];
         src.template get<c>(v);
         if constexpr (c % 64 == 0) box.open();
-        box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, p + 1 < g.g_planes, keep);
+        if (kHalf && p < 0) box.put_half(c % 64 == 0 ? 0 : 4, v, to_all, p != first, keep);
+        else box.put16(c % 64 == 0 ? 0 : 4, v, g.bf16, p + 1 < g.g_planes, keep);
         if constexpr (c % 64 == 32) {
           if (row0 < g.m && col0 + c - 32 < g.n)
-            box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), p, false);
+            box.send(map_o, static_cast<int>(col0 + c - 32), static_cast<int>(row0), plane, false);
         }
-        if (p + 1 < g.g_planes) {
+        if (p >= 0 && p + 1 < g.g_planes) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) src.acc[c + j] = v[j];
         }
@@ -507,12 +536,11 @@ __device__ __forceinline__ void end_grad(const ProdArgs& g, const CUtensorMap* m
 // ---- results of the gradient products ---------------------------------------------------
 template <int BN, class Src>
 __device__ __forceinline__ void end_sum(const ProdArgs& g, const CUtensorMap* map_o, Src& src, int64_t row, int n_tile,
-                                        int split, int half, Outbox<false> box) {
+                                        int split, int half, float inv, Outbox<false> box) {
   constexpr int kCols = BN / 2;
   const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
   const int64_t row0 = row - box.lane;
   const bool sums = g.acc;
-  const float inv = sums ? 1.f : 1.f / g_scale_of(g.g_max);
   const bool wide = sums || g.out_type == GM_LOSS_F32;
   const bool bf = g.out_type == GM_LOSS_BF16;
   each_32<kCols>([&](auto cc) {
@@ -595,6 +623,8 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
     if (warp == 0) {
       // ---- loads
       const bool one = elect_one();
+      int a_plane = 0;  // dW's planes of G
+      if constexpr (KIND == Prod::kDw && !three_planes<ACC>) a_plane = Scales(g).apart ? g.g_planes : 0;
       int st = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -619,7 +649,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
               } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                  tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, kb * kBK, p, bar);
+                  tma_load_3d<CG>(a + i * 8192, &map_a, m0 + i * 64, kb * kBK, a_plane + p, bar);
               }
             }
 #pragma unroll
@@ -732,7 +762,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       if (kTurns == 2) bph ^= 1;  // a group keeps to one accumulator
       else if (++buf == 2) buf = 0, bph ^= 1;
     };
-    using Row = RowState<KIND, LAB, DIS>;
+    using Row = RowState<KIND, LAB, DIS, KIND == Prod::kGrad || (KIND == Prod::kDh && !three_planes<ACC>)>;
     auto row_of = [&](const Tile& x) { return int64_t(x.m) * 128 * CG + rank * 128 + quad * 32 + lane; };
     Tile tl = {0, 0, 0};
     RowRaw raw = {};
@@ -751,8 +781,12 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       }
       auto finish = [&](auto& src) {
         if constexpr (KIND == Prod::kStats) end_stats<BN, LAB, DIS>(g, src, rs, row, tl.n, half);
-        else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS, ACC != kWhole>(g, &map_o, src, rs, row, tl.n, half, box);
-        else end_sum<BN>(g, &map_o, src, row, tl.n, tl.split, half, box);
+        else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS, ACC>(g, &map_o, src, rs, row, tl.n, half, box);
+        else {
+          float inv = 1.f;  // of the scale of G
+          if constexpr (!three_planes<ACC>) inv = 1.f / (KIND == Prod::kDh ? Scales(g).of(rs.c) : Scales(g).all);
+          end_sum<BN>(g, &map_o, src, row, tl.n, tl.split, half, inv, box);
+        }
       };
       if constexpr (!in_registers<ACC>) {
         if (!ready()) break;

@@ -168,3 +168,56 @@ def test_classes_masked_by_their_bias(kind, lowest, n, d):
     (eh, bh), (ew, bw) = lo.gradient_bounds(f, lo.logit_grads(f, tn, -100, gl_n, None, 2.0, gk_n), wide(h), wide(wk), kind, 2.0)
     near(dh[:, :-1], eh[:, :-1], bh[:, :-1], "dh")
     near(dw[keep.cuda()], ew, bw, "dw")
+
+
+@pytest.mark.parametrize("n,d,v", [(140, 64, 5000), (300, 1100, 3000), (90, 130, 5000), (12, 1100, 4000), (300, 200, 20000)])
+@pytest.mark.parametrize("cap", [0, 1])
+@pytest.mark.parametrize("labels", [True, False])
+def test_half_precision_with_weights_far_apart(n, d, v, cap, labels):
+    """Each row's dH is as near as its own weight asks, not the largest one's: what f16 cannot hold of a row's G is at
+    most 2^-11 of the row's weight, over all classes. dW's G is scaled by the largest weight, to at least 2^13, and loses
+    half a unit of 2^-24."""
+    h, w, target = make("f16", n, d, v, ignored=0.0)
+    h *= 0.25
+    w *= 4.0
+    tn = target.cpu().numpy()
+    weight = 2.0 ** (11 - np.arange(n) % 24)
+    given = torch.from_numpy(weight.astype(np.float32)).cuda()
+    if labels:
+        _, lse = losses.xent_forward(h, w, target, check=True)
+        f = lo.forward(wide(h), wide(w), tn)
+        dh, dw = losses.xent_backward(h, w, target, lse, given, workspace_cap_bytes=cap, check=True)
+        g, soft, hard = lo.logit_grads(f, tn, -100, weight)
+        weight, top = 2 * weight, np.abs(f["lse"])
+    else:
+        dev, host = make_teacher(n, v)
+        o = losses.distill_forward(h, w, dev, 1.0, check=True)
+        f = lo.forward(wide(h), wide(w), None, -100, host, 1.0)
+        dh, dw = losses.distill_backward(h, w, dev, o.lse_t, given, 1.0, workspace_cap_bytes=cap, check=True)
+        g, soft, hard = lo.logit_grads(f, temperature=1.0, g_kl=weight)
+        top = np.abs(f["lse_t"])
+    u = lo.ROUND["f16"]
+    dx = 2 * lo.logit_error(wide(h), wide(w)).max(1) + 2.0 ** -22 * (72 + 8 * np.abs(f["z"]).max(1) + 4 * top)
+    dg = soft * np.expm1(dx)[:, None] + 2.0 ** -22 * (soft + hard) + u * np.abs(g) * (1 + 2.0 ** -8)
+    small = weight[:, None] * 2.0 ** -11 * np.abs(wide(w)).max(0)
+    for got, a, x, da, lost, what in ((dh, g, wide(w), dg, small, "dh"), (dw, g.T, wide(h), dg.T + weight.max() * 2.0 ** -38, 0.0, "dw")):
+        exact = a @ x
+        bound = da @ np.abs(x) + (6 * (a.shape[1] / 16 + 1) + 16) * 2.0 ** -23 * (np.abs(a) @ np.abs(x)) + lost
+        near(got, exact, bound + u * np.abs(exact) * (1 + 2.0 ** -8) + 2.0 ** -24, what)
+
+
+@pytest.mark.parametrize("n", [60, 200])
+def test_half_precision_with_a_weight_that_is_not_finite(n):
+    """It spoils its own row of dH alone; weights of 0 beside it leave nothing."""
+    h, w, target = make("f16", n, 72, 300, ignored=0.0)
+    _, lse = losses.xent_forward(h, w, target)
+    (gl,), _ = weights(n, 1, 0, scale=64.0)
+    want, _ = losses.xent_backward(h, w, target, lse, gl)
+    gl[3] = 0
+    for x in (float("inf"), float("nan")):
+        gl[7] = x
+        dh, _ = losses.xent_backward(h, w, target, lse, gl, check=True)
+        assert not torch.isfinite(dh[7]).any() and torch.all(dh[3] == 0)
+        keep = [i for i in range(n) if i not in (3, 7)]
+        # another scale of G alone: two roundings of 11 bits at most
+        assert (dh[keep].double() - want[keep].double()).abs().max() <= 2.0 ** -9 * want.double().abs().max()
