@@ -81,7 +81,9 @@ typedef struct gm_labels {
 /* Tuning; zero selects the automatic value. NULL is the same as all zeros. */
 typedef struct gm_loss_config {
   int64_t workspace_cap_bytes; /* bound on the piece of G a backward call holds; 0 = 512 MiB, f16 (which
-                                  may keep G at two scales) 1 GiB; the narrowest piece has 256 classes */
+                                  may keep G at two scales) 1 GiB; the narrowest piece has 256 classes.
+                                  A forward call's row statistics, 16 bytes a row and 128 classes (f32 of at
+                                  most 128 rows: 64), keep to 512 MiB in pieces of two such at least */
   int32_t flags;               /* GM_LOSS_CHECK                                                  */
   void* workspace;             /* device memory for the call, 256-byte aligned (NULL: the hooks); it
                                   may be reused once the call's work on the stream is done       */

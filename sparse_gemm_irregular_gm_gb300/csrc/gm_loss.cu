@@ -1,10 +1,10 @@
 // gm_loss.cu -- losses over a large class table (include/gm_losses.h): the host
 // driver and the kernels around the tensor-core products of gm_loss_prod.cu.
 //
-// Forward: one product reduces Z = H W^T to a maximum and sums of exponentials for
-// each row and half tile, a second kernel joins them. Backward, for each piece of the
-// classes: the product again, its end writing the piece of G = dloss/dZ, then
-// dH += G W_piece and dW_piece = G^T H. Nothing of the size of Z is ever stored.
+// Forward, for each piece of the classes (usually one): the product reduces Z = H W^T to a
+// maximum and sums of exponentials for each row and half tile, a second kernel joins them.
+// Backward, for each piece of the classes: the product again, its end writing the piece of
+// G = dloss/dZ, then dH += G W_piece and dW_piece = G^T H. What is stored of Z's size has a bound.
 #include "gm_loss.h"
 
 #include <algorithm>
@@ -260,6 +260,7 @@ __device__ __forceinline__ bool any_lost(const int* lost, int n) {
 
 // ---- joining the half tiles of a row -----------------------------------------------------
 struct JoinArgs {
+  float4* carry;  // [row]: the sums so far, of a piece that is not the last; null: results
   const float4* part;
   int64_t n_parts, n_rows;
   Targets tgt;
@@ -314,6 +315,10 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   }
   const bool lost = __any_sync(kFull, lost_here);
   if (sub != 0 || row >= a.n_rows) return;
+  if (a.carry) {
+    a.carry[row] = make_float4(m, s1, st, zq);
+    return;
+  }
   if (a.tgt.t) {
     const float l = lost ? NAN : m + logf(s1);
     const int64_t t = check_target(a.tgt, raw_target(a.tgt, row));
@@ -437,7 +442,8 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 constexpr int64_t kMostIndex = (int64_t(1) << 31) - 256;  // tile coordinates are int32
-constexpr int64_t kDefaultCap = int64_t(512) << 20;  // f16: of each of the two sets of planes (Scales)
+constexpr int64_t kDefaultCap = int64_t(512) << 20;  // of G; f16: of each of the two sets of planes (Scales)
+constexpr int64_t kStatsCap = int64_t(512) << 20;    // of a forward call's row statistics
 
 struct Call {
   gm_logits z = {};
@@ -730,7 +736,9 @@ struct ForwardPlan {
   int blocks = 0;  // of the kernel for few rows; 0: the product
   Words own;
   int cg, bn;
-  int64_t n_tiles, n_parts;
+  int64_t n_tiles;      // of a row tile, in all
+  int64_t piece_tiles;  // of a piece of the classes
+  int64_t n_parts;      // [0]: with several pieces, the sums of those before; then half tiles
   size_t o_part, o_zt;
   explicit ForwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
@@ -739,7 +747,9 @@ struct ForwardPlan {
     cg = n > 128 ? 2 : 1;
     bn = prod_logits_cols(cg, h.planes());
     n_tiles = div_up(c.z.n_classes, bn);
-    n_parts = 2 * n_tiles;
+    const int64_t most = std::max<int64_t>(1, kStatsCap / (n * 32)), pieces = div_up(n_tiles, most);
+    piece_tiles = div_up(n_tiles, pieces);
+    n_parts = 2 * piece_tiles + (pieces > 1);
     if (skinny(c)) {
       n_parts = blocks = skinny_most_blocks(c.z.n_classes, c.sms);
     } else {
@@ -767,41 +777,7 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   const TeacherPlan& t = p.t;
   float4* part = a.at<float4>(p.o_part);
   float* z_t = a.at<float>(p.o_zt);
-  bool ok;
-  if (p.blocks) {
-    t.launch(a, c);
-    SkinnyArgs g = skinny_args(c, a, t);
-    g.part = part;
-    g.z_t = z_t;
-    const int vec = skinny_vec(g.w, g.w_ld, g.dim, g.n_cls, elem_bytes(c.z.type));
-    ok = launch_skinny(g, c.z.type, false, vec, &p.blocks, c.s) == cudaSuccess;
-    p.n_parts = p.blocks;
-  } else {
-    const Operand oh = p.h.ready(a, c.s), ow = p.w.ready(a, c.s);
-    t.launch(a, c);
-    ProdMaps maps;
-    if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(p.cg, p.bn))) return GM_ERR_CUDA;
-    maps.o = maps.a;  // not used
-    ProdArgs g = {};
-    set_logits_args(g, c, a, t);
-    g.m = n;
-    g.n = c.z.n_classes;
-    g.m_tiles = static_cast<int>(div_up(n, 128 * p.cg));
-    g.n_tiles = static_cast<int>(p.n_tiles);
-    g.splits = 1;
-    g.k_blocks = g.k_per_split = static_cast<int>(div_up(c.z.dim, 64));
-    g.group = group_of(g.m_tiles, 128 * p.cg, c.z.dim, g.planes);
-    g.part = part;
-    g.part_ld = n;
-    g.z_t = z_t;
-    g.lost = lost;
-    g.n_lost = c.sms;
-    g.lost_first = true;
-    ok = launch_prod(Prod::kStats, p.cg, p.bn, maps, g, c.sms, c.s) == cudaSuccess;
-  }
   JoinArgs j = {};
-  j.part = part;
-  j.n_parts = p.n_parts;
   j.n_rows = n;
   j.tgt = targets_of(c);
   j.z_t = z_t;
@@ -815,14 +791,57 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   j.status = c.status;
   j.lost = p.blocks ? nullptr : lost;
   j.n_lost = c.sms;
-  if (ok) {
-    // few rows: a block each, so that their half tiles are read by many threads; more: 2 a block,
-    // a whole 32-byte sector (512 rows, 8192 half tiles: 45 -> 18 us); many: 8, a 128-byte line
+  // few rows: a block each, so that their half tiles are read by many threads; more: 2 a block,
+  // a whole 32-byte sector (512 rows, 8192 half tiles: 45 -> 18 us); many: 8, a 128-byte line
+  auto join = [&](const float4* first, int64_t parts, float4* carry) {
+    j.part = first;
+    j.n_parts = parts;
+    j.carry = carry;
     const unsigned blocks1 = static_cast<unsigned>(n), blocks2 = static_cast<unsigned>(div_up(n, 2)),
                    blocks8 = static_cast<unsigned>(div_up(n, 8));
-    ok = (n <= 2 * c.sms    ? launch_chained(k_join<1>, blocks1, 256, 0, c.s, 1, j)
-          : n <= 16 * c.sms ? launch_chained(k_join<2>, blocks2, 256, 0, c.s, 1, j)
-                            : launch_chained(k_join<8>, blocks8, 256, 0, c.s, 1, j)) == cudaSuccess;
+    return (n <= 2 * c.sms    ? launch_chained(k_join<1>, blocks1, 256, 0, c.s, 1, j)
+            : n <= 16 * c.sms ? launch_chained(k_join<2>, blocks2, 256, 0, c.s, 1, j)
+                              : launch_chained(k_join<8>, blocks8, 256, 0, c.s, 1, j)) == cudaSuccess;
+  };
+  bool ok;
+  if (p.blocks) {
+    t.launch(a, c);
+    SkinnyArgs g = skinny_args(c, a, t);
+    g.part = part;
+    g.z_t = z_t;
+    const int vec = skinny_vec(g.w, g.w_ld, g.dim, g.n_cls, elem_bytes(c.z.type));
+    ok = launch_skinny(g, c.z.type, false, vec, &p.blocks, c.s) == cudaSuccess && join(part, p.blocks, nullptr);
+  } else {
+    const Operand oh = p.h.ready(a, c.s), ow = p.w.ready(a, c.s);
+    t.launch(a, c);
+    ProdMaps maps;
+    if (!encode(&maps.a, oh, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(p.cg, p.bn))) return GM_ERR_CUDA;
+    maps.o = maps.a;  // not used
+    ProdArgs g = {};
+    set_logits_args(g, c, a, t);
+    g.m = n;
+    g.m_tiles = static_cast<int>(div_up(n, 128 * p.cg));
+    g.splits = 1;
+    g.k_blocks = g.k_per_split = static_cast<int>(div_up(c.z.dim, 64));
+    g.group = group_of(g.m_tiles, 128 * p.cg, c.z.dim, g.planes);
+    const bool pieces = p.piece_tiles < p.n_tiles;
+    g.part = part + (pieces ? n : 0);
+    g.part_ld = n;
+    g.z_t = z_t;
+    g.lost = lost;
+    g.n_lost = c.sms;
+    ok = true;
+    for (int64_t t0 = 0; ok && t0 < p.n_tiles; t0 += p.piece_tiles) {
+      const int64_t tiles = std::min(p.piece_tiles, p.n_tiles - t0);
+      const bool first = t0 == 0, last = t0 + tiles == p.n_tiles;
+      g.n_tiles = static_cast<int>(tiles);
+      g.cls0 = t0 * p.bn;
+      g.b_row0 = static_cast<int>(g.cls0);
+      g.n = std::min(tiles * p.bn, c.z.n_classes - g.cls0);
+      g.lost_first = first;
+      ok = launch_prod(Prod::kStats, p.cg, p.bn, maps, g, c.sms, c.s) == cudaSuccess &&
+           join(first ? g.part : part, 2 * tiles + !first, last ? nullptr : part);
+    }
   }
   return finish(c, ok, word);
 }

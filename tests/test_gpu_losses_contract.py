@@ -221,3 +221,64 @@ def test_half_precision_with_a_weight_that_is_not_finite(n):
         keep = [i for i in range(n) if i not in (3, 7)]
         # another scale of G alone: two roundings of 11 bits at most
         assert (dh[keep].double() - want[keep].double()).abs().max() <= 2.0 ** -9 * want.double().abs().max()
+
+
+def test_workspace_of_a_forward_call_is_bounded():
+    lib = losses.load()
+    p = 1 << 20
+    for rows, classes in ((1 << 20, 1 << 20), (1 << 22, 1 << 22), (8192, 1 << 30)):
+        z = losses.gm_logits(rows, classes, 8, p, 8, p, 8, losses.GM_LOSS_BF16)
+        need = ctypes.c_int64()
+        assert lib.gm_loss_workspace(z, -1, 0, None, need) == 0
+        # the statistics' piece, and 64 bytes a row
+        assert need.value <= (512 << 20) + 64 * rows + 4096
+
+
+@pytest.mark.parametrize("kind,n,d,v", [("bf16", 40000, 16, 262221), ("f32", 40000, 8, 262221), ("bf16", 2000, 40, 2200001),
+                                        ("f16", 2000, 16, 4400001), ("bf16", 300, 8, 14400001), ("f32", 100, 8, 22000001)])
+def test_forward_in_pieces_of_the_classes(kind, n, d, v):
+    """Row statistics of more than 512 MiB: two to three pieces, whose sums are joined. The caller's workspace has
+    gm_loss_workspace's bytes, and the memory around it is left alone."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dtype = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[kind]
+    h = torch.randn(n, d, generator=g, device="cuda").to(dtype)
+    w = (torch.randn(v, d, generator=g, device="cuda") * (2.0 / d ** 0.5)).to(dtype)
+    target = torch.randint(0, v, (n,), generator=g, device="cuda")
+    target[0], target[-1], target[5] = 0, v - 1, -100
+    dev, _ = make_teacher(n, v // 64)
+    dev = binding.DeviceCSR(n, v, dev.row_ptr, dev.col * 64 + 63, dev.val)
+    temperature = 2.0
+    out = losses.distill_forward(h, w, dev, temperature, target=target, check=True)
+    lib = losses.load()
+    z = losses.gm_logits(n, v, d, h.data_ptr(), d, w.data_ptr(), d, losses.TYPES[dtype])
+    lab = losses.gm_labels(target.data_ptr(), -100, 0)
+    need = ctypes.c_int64()
+    assert lib.gm_loss_workspace(z, dev.nnz, 0, None, need) == 0
+    memory = torch.full((need.value + 8192,), 0xa5, dtype=torch.uint8, device="cuda")
+    cfg = losses.gm_loss_config(0, 0, memory.data_ptr() + 4096, need.value)
+    again = [torch.empty_like(t) for t in out]
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.gm_distill_forward(z, dev.desc(), 1, 0, temperature, lab, cfg, stream, *(t.data_ptr() for t in again)) == 0
+    torch.cuda.synchronize()
+    assert torch.all(memory[:4096] == 0xa5) and torch.all(memory[4096 + need.value:] == 0xa5)
+    assert all(torch.equal(a, b) for a, b in zip(again, out)) and all(torch.isfinite(t).all() for t in out)
+    loss, lse = losses.xent_forward(h, w, target, check=True)
+    W, rp = w.double(), dev.row_ptr.tolist()
+    for i in sorted({*range(0, n, max(1, n // 40)), 5, n - 1}):
+        zi = W @ h[i].double()
+        dz = (6 * (d / 16 + 1) + 8) * 2.0 ** -23 * float((W.abs() @ h[i].double().abs()).max())
+        big, want, want_t = float(zi.abs().max()), float(torch.logsumexp(zi, 0)), float(torch.logsumexp(zi / temperature, 0))
+        # loss_oracle.forward_bounds
+        bound = dz + 2.0 ** -22 * (64 + 4 * big + abs(want))
+        assert abs(float(lse[i]) - want) <= bound and abs(float(out.lse[i]) - want) <= bound
+        bound_t = dz / temperature + 2.0 ** -22 * (64 + 4 * big / temperature + abs(want_t))
+        assert abs(float(out.lse_t[i]) - want_t) <= bound_t
+        want_loss = 0.0 if i == 5 else want - float(zi[target[i]])
+        for x in (loss[i], out.loss[i]):
+            assert abs(float(x) - want_loss) <= bound + dz + 2.0 ** -22 * (big + abs(want))
+        val = dev.val[rp[i]:rp[i + 1]].double() / temperature
+        kl = 0.0
+        if val.numel() and not torch.all(val == -torch.inf):
+            q = torch.softmax(val, 0)
+            kl = float(torch.xlogy(q, q).sum() - q @ zi[dev.col[rp[i]:rp[i + 1]].long()] / temperature + want_t)
+        assert abs(float(out.kl[i]) - kl) <= bound_t + dz / temperature + 2.0 ** -20 * (8 + big / temperature + abs(want_t) + abs(kl))
