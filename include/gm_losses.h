@@ -120,7 +120,8 @@ gm_status gm_xent_backward(const gm_logits* z, const gm_labels* labels, const gm
  * its arrays' types. Columns of a row ascend strictly. A value of -inf has probability 0;
  * a row without entries, or with nothing but -inf, has kl 0 and no gradient. A row with a
  * column out of range or out of order, or row pointers that decrease or leave [0, nnz],
- * has kl NaN, no gradient, and GM_ERR_BAD_INDEX from gm_loss_status. temperature: finite,
+ * or that starts before the end of an earlier row, has kl NaN, no gradient, and
+ * GM_ERR_BAD_INDEX from gm_loss_status; other rows are as they would be without it. temperature: finite,
  * above 0. labels: NULL, or the rows' targets, whose cross entropy (at temperature 1) the
  * same pass then returns in loss and lse (both NULL without labels).
  * Errors: those of gm_xent_forward, and GM_ERR_DIM_MISMATCH when the teacher's sizes are

@@ -282,3 +282,49 @@ def test_forward_in_pieces_of_the_classes(kind, n, d, v):
             q = torch.softmax(val, 0)
             kl = float(torch.xlogy(q, q).sum() - q @ zi[dev.col[rp[i]:rp[i + 1]].long()] / temperature + want_t)
         assert abs(float(out.kl[i]) - kl) <= bound_t + dz / temperature + 2.0 ** -20 * (8 + big / temperature + abs(want_t) + abs(kl))
+
+
+@pytest.mark.parametrize("n,at", [(8, 0), (300, 7), (300, 290), (4097, 3), (4097, 4090), (9000, 5000), (200000, 199000)])
+@pytest.mark.parametrize("row_ptr", [torch.int64, torch.int32])
+@pytest.mark.parametrize("length", [10, 2500])
+def test_teacher_rows_that_share_entries(n, at, row_ptr, length):
+    """Row pointers fall back into the middle of row `at`: the rows that lie in it are refused, and it is not spoilt by
+    them, nor are those before and after. Row at + 3 is empty and has nothing to share."""
+    v = 3000
+    h, w, target = make("bf16", n, 16, v, ignored=0.0)
+    lens = np.full(n, 2)
+    lens[at] = length
+    lens[at + 1:at + 5] = (0, length // 2, 0, length - length // 2)
+    rp = np.concatenate([[0], np.cumsum(lens)])
+    g = torch.Generator().manual_seed(n)
+    # ascending in every row, those that share entries too
+    col = np.concatenate([np.arange(k) for k in lens])
+    val = torch.randn(int(rp[-1]), generator=g)
+    good = binding.DeviceCSR(n, v, torch.from_numpy(rp).to(row_ptr).cuda(), torch.from_numpy(col).int().cuda(), val.cuda())
+    want = losses.distill_forward(h, w, good, 2.0, check=True)
+    gk = torch.ones(n, device="cuda")
+    gk[at + 1:at + 5] = 0
+    want_h, want_w = losses.distill_backward(h, w, good, want.lse_t, gk, 2.0, check=True)
+    start = int(rp[at])
+    fall = rp.copy()
+    fall[at + 2:at + 5] = (start, start + length // 2, start + length // 2)
+    fall[at + 5:] -= length
+    fall = torch.from_numpy(fall).to(row_ptr).cuda()
+    # what row at held, then the rows after the four that lie in it
+    keep = torch.cat([torch.arange(start + length), torch.arange(start + 2 * length, int(rp[-1]))]).cuda()
+    bad = binding.DeviceCSR(n, v, fall, good.col[keep], good.val[keep])
+    assert fall[at + 1] == start + length and fall[at + 5] == start + length
+    spoilt = [at + 1, at + 2, at + 4]
+    for _ in range(3):
+        o = losses.distill_forward(h, w, bad, 2.0)
+        with pytest.raises(binding.GmError) as e:
+            losses.gm_loss_status()
+        assert e.value.status == 9  # GM_ERR_BAD_INDEX
+        assert torch.nonzero(torch.isnan(o.kl)).flatten().tolist() == spoilt
+        rest = torch.ones(n, dtype=torch.bool, device="cuda")
+        rest[at + 1:at + 5] = False
+        assert torch.equal(o.kl[rest], want.kl[rest]) and o.kl[at + 3] == 0 and torch.equal(o.lse_t, want.lse_t)
+        dh, dw = losses.distill_backward(h, w, bad, o.lse_t, torch.ones(n, device="cuda"), 2.0)
+        with pytest.raises(binding.GmError):
+            losses.gm_loss_status()
+        assert torch.equal(dh, want_h) and torch.equal(dw, want_w)
