@@ -345,8 +345,11 @@ def cross_entropy(h, w, target, *, ignore_index=-100):
 
 
 def distillation(h, w, teacher: DeviceCSR, temperature=1.0, *, target=None, ignore_index=-100) -> Distilled:
-    """``distill_forward`` differentiable by h and w through kl, loss and lse (not lse_t)."""
+    """``distill_forward`` differentiable by h and w through kl, loss and lse (not lse_t). The teacher is a constant:
+    values that want a gradient are refused (detach them)."""
     if teacher.n_rows != h.shape[0] or teacher.n_cols != w.shape[0]:
         raise GmError(2, f"the teacher is {teacher.n_rows} x {teacher.n_cols}, the logits {h.shape[0]} x {w.shape[0]}")
+    if torch.is_grad_enabled() and teacher.val.requires_grad:
+        raise ValueError("the teacher's values require a gradient, which distillation does not have; detach them")
     return Distilled(*_Distill.apply(h, w, teacher.row_ptr, teacher.col, teacher.val, target, float(temperature),
                                      ignore_index))

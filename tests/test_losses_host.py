@@ -138,3 +138,15 @@ def test_distillation_checks_the_teachers_sizes():
     t = binding.DeviceCSR(3, 5, None, None, None)
     with pytest.raises(binding.GmError):
         losses.distillation(torch.zeros(2, 8), torch.zeros(5, 8), t)
+
+
+def test_distillation_refuses_a_teacher_that_wants_a_gradient():
+    val = torch.zeros(2, requires_grad=True)
+    t = binding.DeviceCSR(2, 5, torch.tensor([0, 1, 2]), torch.tensor([0, 1], dtype=torch.int32), val)
+    h, w = torch.zeros(2, 8), torch.zeros(5, 8)
+    with pytest.raises(ValueError, match="detach"):
+        losses.distillation(h, w, t)
+    for call in (lambda: losses.distillation(h, w, binding.DeviceCSR(2, 5, t.row_ptr, t.col, val.detach())),
+                 lambda: torch.no_grad()(losses.distillation)(h, w, t)):
+        with pytest.raises(ValueError, match="CUDA tensor"):  # what tensors here are refused for
+            call()
