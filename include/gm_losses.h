@@ -122,7 +122,7 @@ gm_status gm_xent_backward(const gm_logits* z, const gm_labels* labels, const gm
  * column out of range or out of order, or row pointers that decrease or leave [0, nnz],
  * or that starts before the end of an earlier row, has kl NaN, no gradient, and
  * GM_ERR_BAD_INDEX from gm_loss_status; other rows are as they would be without it. temperature: finite,
- * above 0. labels: NULL, or the rows' targets, whose cross entropy (at temperature 1) the
+ * above 0 (log2(e) / T is finite too: T from 4.3e-39). labels: NULL, or the rows' targets, whose cross entropy (at temperature 1) the
  * same pass then returns in loss and lse (both NULL without labels).
  * Errors: those of gm_xent_forward, and GM_ERR_DIM_MISMATCH when the teacher's sizes are
  * not n_rows x n_classes. */

@@ -572,7 +572,7 @@ gm_status check_teacher(Call& c, const gm_csr* t, int32_t value_type, int32_t in
   if (t->n_rows != c.z.n_rows || t->n_cols != c.z.n_classes) return GM_ERR_DIM_MISMATCH;
   if (value_type != GM_VALUE_F64 && value_type != GM_VALUE_F32) return GM_ERR_INVALID_ARG;
   if (index_type & ~(GM_INDEX_ROWPTR32 | GM_INDEX_COL64)) return GM_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature)) return GM_ERR_INVALID_ARG;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature)) return GM_ERR_INVALID_ARG;
   if (t->nnz < 0 || !t->row_ptr || (t->nnz > 0 && (!t->col_idx || !t->vals))) return GM_ERR_INVALID_ARG;
   if (!aligned(t->row_ptr, index_type & GM_INDEX_ROWPTR32 ? 4 : 8) ||
       !aligned(t->col_idx, index_type & GM_INDEX_COL64 ? 8 : 4) || !aligned(t->vals, value_type == GM_VALUE_F64 ? 8 : 4))

@@ -150,3 +150,8 @@ def test_distillation_refuses_a_teacher_that_wants_a_gradient():
                  lambda: torch.no_grad()(losses.distillation)(h, w, t)):
         with pytest.raises(ValueError, match="CUDA tensor"):  # what tensors here are refused for
             call()
+
+
+def test_temperatures_whose_reciprocal_is_finite_but_not_its_exponent(lib):
+    for t in (3.5e-39, 4.2e-39):
+        assert lib.gm_distill_forward(logits(), csr(), 1, 0, t, None, None, None, P, P, None, None) == INVALID
