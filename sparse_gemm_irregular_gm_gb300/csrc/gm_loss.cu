@@ -285,13 +285,11 @@ __global__ void __launch_bounds__(32 * kTeacherWarps, 2) k_teacher(const Teacher
   }
 }
 
-// Whether this lane's part of a call's `lost` says that a product gave up (gm_loss_prod.cu); every warp
-// reads all of it. lost null: kernels that wait for nothing.
-__device__ __forceinline__ bool any_lost(const int* lost, int n) {
-  int x = 0;
-  if (lost)
-    for (int i = threadIdx.x & 31; i < n; i += 32) x |= lost[i];
-  return x != 0;
+// This lane's part of a call's `lost` (gm_loss_prod.cu): not 0 where a product gave up. A warp that writes
+// results reads all of it, early, and asks once it has its sums. lost null: kernels that wait for nothing.
+__device__ __forceinline__ uint64_t lost_word(const uint8_t* lost) {
+  static_assert(kMostBlocks == 8 * 32, "a word a lane");
+  return lost ? reinterpret_cast<const uint64_t*>(lost)[threadIdx.x & 31] : 0;
 }
 
 // ---- joining the half tiles of a row -----------------------------------------------------
@@ -306,8 +304,7 @@ struct JoinArgs {
   float inv_t;
   float *loss, *lse, *kl, *lse_t;
   int* status;
-  const int* lost;
-  int n_lost;
+  const uint8_t* lost;
 };
 // Bound by the latency of its loads: 4 of them in flight a thread (2000 rows, 1024 half tiles,
 // 33 MB: 22 us with one, 9 with four).
@@ -318,7 +315,7 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
   const int rl = threadIdx.x % ROWS, sub = threadIdx.x / ROWS;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + rl;
   const bool dis = a.ent_len != nullptr;
-  const bool lost_here = any_lost(a.lost, a.n_lost);
+  const uint64_t lost_here = threadIdx.x < 32 ? lost_word(a.lost) : 0;  // the warp with sub 0
   float m = -INFINITY, s1 = 0.f, st = 0.f, zq = 0.f;
   auto add = [&](float4 o) {
     const float mn = fmaxf(m, o.x), ref = mn == -INFINITY ? 0.f : mn;
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
     if (sub < d) add(sh[threadIdx.x + d * ROWS]);
     __syncthreads();
   }
-  const bool lost = __any_sync(kFull, lost_here);
+  const bool lost = __any_sync(kFull, lost_here != 0);
   if (sub != 0 || row >= a.n_rows) return;
   if (a.carry) {
     a.carry[row] = make_float4(m, s1, st, zq);
@@ -400,14 +397,13 @@ __global__ void __launch_bounds__(1024) k_weights(int64_t n, const RowGrads r, u
 template <int SUB>
 __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ acc, int splits, int64_t split_stride,
                                                     int64_t rows, int64_t dim, int64_t acc_ld, void* __restrict__ out,
-                                                    int64_t out_ld, int type, const int* __restrict__ lost,
-                                                    int n_lost) {
+                                                    int64_t out_ld, int type, const uint8_t* __restrict__ lost) {
   constexpr int kCols = 256 / SUB;
   __shared__ float sh[SUB][kCols];
   chain_wait();
   const int64_t n = rows * dim, stride = static_cast<int64_t>(gridDim.x) * kCols;
   const int col = threadIdx.x % kCols, sub = threadIdx.x / kCols;
-  const bool lost_here = any_lost(lost, n_lost);
+  const uint64_t lost_here = sub == 0 ? lost_word(lost) : 0;
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kCols; i0 < n; i0 += stride) {
     const int64_t i = i0 + col;
     const int64_t r = i / dim, c = i - r * dim;
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ ac
 #pragma unroll
       for (int s = 1; s < SUB; ++s) x += sh[s][col];
     }
-    const bool gone = __any_sync(kFull, lost_here);  // a warp has one sub where SUB is over 1
+    const bool gone = __any_sync(kFull, lost_here != 0);  // a warp has one sub where SUB is over 1
     if (i >= n) continue;
     if (gone) x = NAN;
     const int64_t o = r * out_ld + c;
@@ -526,8 +522,8 @@ struct Arena {
 // The call's own words: lost (ProdArgs), and the report of a checked call.
 struct Words {
   size_t lost = 0, status = 0;
-  void plan(Arena& a, const Call& c) {
-    lost = a.add(static_cast<int64_t>(c.sms) * 4);
+  void plan(Arena& a) {
+    lost = a.add(kMostBlocks);
     status = a.add(4);
   }
 };
@@ -585,7 +581,7 @@ gm_status check_teacher(Call& c, const gm_csr* t, int32_t value_type, int32_t in
   return GM_OK;
 }
 
-// SMs of the current device, looked up once a device.
+// SMs of the current device (at most kMostBlocks), looked up once a device.
 int sm_count() {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -593,6 +589,7 @@ int sm_count() {
   int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
   if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  n = std::min(n, kMostBlocks);
   if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
@@ -787,7 +784,7 @@ struct ForwardPlan {
   explicit ForwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
     const int64_t n = c.z.n_rows;
-    own.plan(a, c);
+    own.plan(a);
     cg = n > 128 ? 2 : 1;
     bn = prod_logits_cols(cg, h.planes());
     n_tiles = div_up(c.z.n_classes, bn);
@@ -815,7 +812,8 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   Arena& a = p.a;
   rc = a.open(c);
   if (rc != GM_OK) return rc;
-  int *lost = a.at<int>(p.own.lost), *word = a.at<int>(p.own.status);
+  uint8_t* lost = a.at<uint8_t>(p.own.lost);
+  int* word = a.at<int>(p.own.status);
   rc = own_status(c, word);
   if (rc != GM_OK) return rc;
   const TeacherPlan& t = p.t;
@@ -834,7 +832,6 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   j.lse_t = lse_t;
   j.status = c.status;
   j.lost = p.blocks ? nullptr : lost;
-  j.n_lost = c.sms;
   // few rows: a block each, so that their half tiles are read by many threads; more: 2 a block,
   // a whole 32-byte sector (512 rows, 8192 half tiles: 45 -> 18 us); many: 8, a 128-byte line
   auto join = [&](const float4* first, int64_t parts, float4* carry) {
@@ -873,7 +870,6 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
     g.part_ld = n;
     g.z_t = z_t;
     g.lost = lost;
-    g.n_lost = c.sms;
     ok = true;
     for (int64_t t0 = 0; ok && t0 < p.n_tiles; t0 += p.piece_tiles) {
       const int64_t tiles = std::min(p.piece_tiles, p.n_tiles - t0);
@@ -912,11 +908,11 @@ bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t di
   return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
 }
 
-void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const int* lost) {
+void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const uint8_t* lost) {
   const int64_t n = c.z.n_rows * c.z.dim, stride = c.z.n_rows * acc_ld;
   const bool many = splits >= 16;
   launch_chained(many ? k_sum_splits<8> : k_sum_splits<1>, grid_for(n, many ? 32 : 256), 256, 0, c.s, 1, acc, splits, stride,
-                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), lost, c.sms);
+                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), lost);
 }
 
 // How a backward call is cut, and where its workspace lies.
@@ -935,7 +931,7 @@ struct BackwardPlan {
   explicit BackwardPlan(const Call& c)
       : h(c.z.h, c.z.n_rows, c.z.dim, c.z.h_ld, c.z.type), w(c.z.w, c.z.n_classes, c.z.dim, c.z.w_ld, c.z.type) {
     const int64_t n = c.z.n_rows, cls = c.z.n_classes, dim = c.z.dim;
-    own.plan(a, c);
+    own.plan(a);
     planes = c.z.type == GM_LOSS_F32 ? 3 : 1;
     if (skinny(c)) {
       blocks = skinny_most_blocks(cls, c.sms);
@@ -983,7 +979,8 @@ gm_status backward(Call& c, const Grads& q) {
   Arena& a = p.a;
   rc = a.open(c);
   if (rc != GM_OK) return rc;
-  int *lost = a.at<int>(p.own.lost), *word = a.at<int>(p.own.status);
+  uint8_t* lost = a.at<uint8_t>(p.own.lost);
+  int* word = a.at<int>(p.own.status);
   rc = own_status(c, word);
   if (rc != GM_OK) return rc;
   const TeacherPlan& t = p.t;
@@ -1014,7 +1011,6 @@ gm_status backward(Call& c, const Grads& q) {
   base.row = row;
   base.g_planes = p.g_planes;
   base.lost = lost;
-  base.n_lost = c.sms;
   if (c.z.type == GM_LOSS_F16) {
     unsigned* weights = a.at<unsigned>(p.o_weights);
     launch_chained(k_weights, 1, 1024, 0, c.s, 1, n, base.row, weights);

@@ -44,6 +44,8 @@ enum : int {
   kLossBadTeacher = 4  // a malformed teacher row: see gm_distill_forward
 };
 
+constexpr int kMostBlocks = 256;  // of a product; a word of 8 a lane says whether any gave up
+
 // Products the kernel makes and what it does with a finished tile.
 enum class Prod {
   kStats,  // Z = H W^T: each row's maximum and sums of exponentials over half a tile's columns
@@ -133,8 +135,7 @@ struct ProdArgs {
   int b_row0;        // first row of W's map
   int64_t m, n;      // rows and columns of the result
   int* status;
-  int* lost;         // [n_lost] of this call: 1 where a block gave up; n_lost: SMs, at least as many as blocks
-  int n_lost;
+  uint8_t* lost;     // [kMostBlocks] of this call: 1 where a block gave up
   bool lost_first;   // the call's first product: writes all of them
   // kStats, kGrad
   int64_t cls0;      // class of column 0

@@ -833,7 +833,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
     const int gave_up = s_abort;
     if (gave_up) atomicOr(g.status, kLossTimeout);
     if (g.lost_first)
-      for (int i = blockIdx.x; i < g.n_lost; i += gridDim.x) g.lost[i] = i == static_cast<int>(blockIdx.x) && gave_up;
+      for (int i = blockIdx.x; i < kMostBlocks; i += gridDim.x) g.lost[i] = i == static_cast<int>(blockIdx.x) && gave_up;
     else if (gave_up) g.lost[blockIdx.x] = 1;
   }
 }
