@@ -6,7 +6,7 @@
  *
  *   Z = H W^T,   H: n_rows x dim (states),   W: n_classes x dim (class table),
  *
- * in pieces of the classes. The teacher of the distillation is a CSR matrix of
+ * in pieces of the classes where what is kept of their size would pass a bound. The teacher of the distillation is a CSR matrix of
  * n_rows x n_classes (gm_csr, as gm_spgemm writes it: columns ascending in a row),
  * so rows of a sparse product C = A * B serve as one without conversion.
  *
@@ -28,12 +28,14 @@
  *     comes through gm_set_allocator's hooks, in stream order, and is given back
  *     before the call returns.
  *   - Every call returns a gm_status; nothing is thrown across the ABI.
- *   - Products are formed on the tensor cores with fp32 sums: bf16 and f16 operands
- *     as they are, f32 operands as three bf16 parts each. Maxima, sums of
- *     exponentials and losses are fp32. G is rounded to the operands' 16-bit type
- *     (f32: three bf16 parts) before the gradient products; dH and dW are rounded
- *     once, from fp32 sums. The results do not depend on the launch (no atomics on
- *     values).
+ *   - One row, or up to 8 of f32, of dim up to 4096: fp32 arithmetic throughout, G too.
+ *     Others: products on the tensor cores with fp32 sums, which are cut, not rounded,
+ *     to 24 bits for up to 1024 elements at a time; bf16 and f16 operands as they are, f32
+ *     operands as three bf16 parts each. Before the gradient products G is rounded to
+ *     the operands' 16-bit type; with at most 128 rows the remainder is kept beside it in that
+ *     type, and f32's G is three bf16 parts. Maxima, sums of exponentials and losses
+ *     are fp32; dH and dW are rounded once, from fp32 sums. The results do not depend
+ *     on the launch (no atomics on values).
  *   - A row of H is read even when its target is the ignored one: such a row's
  *     values must be finite for dW to be, but they do not change any result.
  */

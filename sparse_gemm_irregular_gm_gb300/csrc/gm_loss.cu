@@ -155,7 +155,7 @@ __device__ __forceinline__ bool group_or(bool x) {
 // of a graph's product are neighbours. A value counts by its distance to the row's largest, taken in
 // the values' own type (64-bit ones may be large and close). From there on fp32: a thread sums at most 32
 // terms of a short row and one in 1024 of a long one (1024 of a row over 2^20 classes), and an fp64 log
-// or sum costs more here than the loads do (8192 rows of 128 entries: 142 us with them, 10 without;
+// or sum costs more here than the loads do (8192 rows of 128 entries: 142 us with them, 8 without;
 // 1500 ragged rows, the longest of some 47,000 entries: 30 us).
 constexpr int kLongRow = 1024, kTeacherWarps = 32;
 
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(1024) k_weights(int64_t n, const RowGrads r, u
   }
 }
 
-// dh = the splits' sums, rounded. SUB threads share the splits of an element (fixed order): 1
+// dh = the splits' sums (of a lost product: NaN), rounded. SUB threads share the splits of an element (fixed order): 1
 // where there are few splits of many elements, 8 where it is the other way round (7 x 80 elements
 // of 304 splits: 28 -> 5 us).
 template <int SUB>

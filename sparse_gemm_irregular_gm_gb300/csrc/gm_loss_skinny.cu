@@ -9,13 +9,22 @@
 // second look at a tile's classes, for dH, finds them in L2 while all SMs' tiles fit there (rows
 // up to some 8 KB; past that W is read twice).
 //
-// Measured, kernels of a forward and a backward call together, these / the products:
-//   f32   1 x 4096 x 131072   1388 / 3857 us    8 x 4096 x 131072   2483 / 3752 us
-//   f32   1 x 80 x 400000      108 /  445 us    8 x 305 x 29546       96 /  160 us
-//   bf16  1 x 2650 x 26281     198 /  270 us    8 x 2650 x 26281     428 /  274 us
-//   bf16  1 x 4096 x 131072    808 /  786 us    8 x 4096 x 131072   1783 /  708 us
-// so 16-bit operands come here with one row only. The forward pass of 1 x 4096 x 131072 f32
-// runs at 347 us, 91 % of the measured copy rate; the backward pass waits at its tiles' barriers.
+// Measured, kernels of a call, us, these / the products (more in profiles/losses_kernels.md):
+//                              forward        backward
+//   f32   1 x 4096 x 131072    333 / 1539    1037 / 2481
+//   f32   8 x 4096 x 131072    844 / 1366    1629 / 2300
+//   f32   1 x 80 x 400000       37 /  164      74 /  303
+//   f32   8 x 305 x 29546       25 /   37      68 /   85
+//   bf16  1 x 64 x 400000       33 /   21      79 /   89
+//   bf16  1 x 1024 x 32768      16 /   16      47 /   53
+//   bf16  1 x 2650 x 26281      46 /   86     178 /  170
+//   bf16  1 x 4096 x 131072    198 /  218     609 /  560
+// fp32 operands are faster here at every size measured. 16-bit ones need no layout for the products where
+// their rows lie on 16-byte boundaries: with one row they lose 58 % (dim 64) to gain 46 % forward and lie
+// within 22 % backward, and they come here; with 8 rows (both calls: 428 / 274 at 8 x 2650 x 26281,
+// 1783 / 708 at 8 x 4096 x 131072) they do not. 2 to 7 have not been measured. The forward pass of
+// 1 x 4096 x 131072 f32 runs at 95 % of the measured copy rate; the backward pass waits at its tiles'
+// barriers.
 #include <type_traits>
 
 #include <cuda_bf16.h>

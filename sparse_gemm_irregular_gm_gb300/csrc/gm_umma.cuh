@@ -233,7 +233,7 @@ __device__ __forceinline__ uint32_t instr_desc(bool bf16, bool a_mn, bool b_mn, 
 // is done and its writes are visible. Every chained kernel waits, so the order goes back to
 // the first. Letting the next kernel start earlier still (griddepcontrol.launch_dependents at a
 // kernel's start) was slower: its waiting blocks take registers that the running one's want
-// (28 x 288 x 789155 f16 forward 108 -> 162 us; a geometric mean over 36 cases of 287 -> 301 us).
+// (28 x 288 x 789155 f16 forward 108 -> 162 us).
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x

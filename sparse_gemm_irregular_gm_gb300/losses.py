@@ -8,7 +8,8 @@ columns ascending in a row: what ``binding.spgemm`` returns can be one.
 ``gm_*`` marshal tensors into the C ABI under its own names. ``xent_forward`` and the
 other functions of that kind also allocate the results; ``cross_entropy`` and
 ``distillation`` are the same under torch's autograd. Nothing waits for the GPU unless
-``check=True``, which raises ``binding.GmError`` for a bad target or teacher row.
+``check=True``, which raises ``binding.GmError`` for a bad target or teacher row of that call;
+``gm_loss_status`` raises for those of the calls without it.
 """
 from __future__ import annotations
 
