@@ -9,7 +9,7 @@
 // second look at a tile's classes, for dH, finds them in L2 while all SMs' tiles fit there (rows
 // up to some 8 KB; past that W is read twice).
 //
-// Measured, kernels of a call, us, these / the products (more in profiles/losses_kernels.md):
+// Measured, kernels of a call, us, these / the products:
 //                              forward        backward
 //   f32   1 x 4096 x 131072    333 / 1539    1037 / 2481
 //   f32   8 x 4096 x 131072    844 / 1366    1629 / 2300
