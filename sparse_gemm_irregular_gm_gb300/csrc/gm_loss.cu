@@ -8,14 +8,13 @@
 #include "gm_loss.h"
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include "gm_device.cuh"
+#include "gm_host.h"
 #include "gm_umma.cuh"
 
 namespace gm {
@@ -432,48 +431,6 @@ __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ ac
 }
 
 // ---- host -----------------------------------------------------------------------------------
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-
-// Matrix of `planes` planes of rows x cols elements of 2 bytes (4: fp32), ld elements a row.
-struct Operand {
-  const void* p;
-  int64_t rows, cols, ld, plane;
-  int planes;
-  int bytes = 2;
-};
-// Boxes of box_rows rows of row_bytes (128 or 64), swizzled over that width; elements outside read as 0.
-bool encode(CUtensorMap* m, const Operand& o, int box_rows, int row_bytes = 128) {
-  const EncodeTiled fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
-                              static_cast<cuuint64_t>(o.planes)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * o.bytes, static_cast<cuuint64_t>(o.plane) * o.bytes};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(row_bytes / o.bytes), static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t step[3] = {1, 1, 1};
-  return fn(m, o.bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-            const_cast<void*>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-int64_t div_up(int64_t x, int64_t m) { return (x + m - 1) / m; }
-
-constexpr int64_t kMostIndex = (int64_t(1) << 31) - 256;  // tile coordinates are int32
 constexpr int64_t kDefaultCap = int64_t(512) << 20;  // of G; f16: of each of the two sets of planes (Scales)
 constexpr int64_t kStatsCap = int64_t(512) << 20;    // of a forward call's row statistics
 
@@ -493,32 +450,6 @@ struct Call {
   int* status = nullptr;
 };
 
-// One workspace block, carved in order.
-struct Arena {
-  DevBuf<unsigned char> buf;  // from the hooks, unless the caller brought memory
-  unsigned char* p = nullptr;
-  size_t used = 0;
-  gm_status open(const Call& c) {
-    if (c.workspace) {
-      if (static_cast<int64_t>(used) > c.workspace_bytes) return GM_ERR_WORKSPACE;
-      p = static_cast<unsigned char*>(c.workspace);
-      return GM_OK;
-    }
-    if (!buf.alloc(used, c.s)) return GM_ERR_OOM;
-    p = buf.p;
-    return GM_OK;
-  }
-  size_t add(int64_t bytes) {
-    const size_t at = used;
-    used += static_cast<size_t>(up(bytes, 256));
-    return at;
-  }
-  template <class T>
-  T* at(size_t off) const {
-    return reinterpret_cast<T*>(p + off);
-  }
-};
-
 // The call's own words: lost (ProdArgs), and the report of a checked call.
 struct Words {
   size_t lost = 0, status = 0;
@@ -527,15 +458,6 @@ struct Words {
     status = a.add(4);
   }
 };
-
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
-
-int64_t elem_bytes(int32_t type) { return type == GM_LOSS_F32 ? 4 : 2; }
-bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
 
 gm_status check(Call& c, const gm_logits* z, const gm_labels* labels, const gm_loss_config* cfg, void* stream) {
   if (!z) return GM_ERR_INVALID_ARG;
@@ -546,7 +468,7 @@ gm_status check(Call& c, const gm_logits* z, const gm_labels* labels, const gm_l
   const int64_t es = elem_bytes(c.z.type);
   if (!c.z.w || !aligned(c.z.w, es) || (c.z.n_rows > 0 && (!c.z.h || !aligned(c.z.h, es)))) return GM_ERR_INVALID_ARG;
   if (c.z.h_ld < c.z.dim || c.z.w_ld < c.z.dim) return GM_ERR_INVALID_ARG;
-  if (c.z.h_ld > (int64_t(1) << 36) || c.z.w_ld > (int64_t(1) << 36)) return GM_ERR_INDEX_OVERFLOW;
+  if (c.z.h_ld > kMostLd || c.z.w_ld > kMostLd) return GM_ERR_INDEX_OVERFLOW;
   c.labels = labels;
   if (labels && ((c.z.n_rows > 0 && !labels->target) || (labels->target32 != 0 && labels->target32 != 1) ||
                  !aligned(labels->target, labels->target32 ? 4 : 8)))
@@ -581,24 +503,11 @@ gm_status check_teacher(Call& c, const gm_csr* t, int32_t value_type, int32_t in
   return GM_OK;
 }
 
-// SMs of the current device (at most kMostBlocks), looked up once a device.
-int sm_count() {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  n = std::min(n, kMostBlocks);
-  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 // Device facts and a clear error state; GM_ERR_CUDA leaves a pending error to its owner.
 gm_status begin(Call& c) {
   if (cudaPeekAtLastError() != cudaSuccess) return GM_ERR_CUDA;
   void* st = nullptr;
-  c.sms = sm_count();
+  c.sms = sm_count(kMostBlocks);
   if (c.sms <= 0 || cudaGetSymbolAddress(&st, g_loss_status) != cudaSuccess) {
     cudaGetLastError();
     return GM_ERR_CUDA;
@@ -810,7 +719,7 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
   if (n == 0) return finish(c, true);
   ForwardPlan p(c);
   Arena& a = p.a;
-  rc = a.open(c);
+  rc = a.open(c.workspace, c.workspace_bytes, c.s);
   if (rc != GM_OK) return rc;
   uint8_t* lost = a.at<uint8_t>(p.own.lost);
   int* word = a.at<int>(p.own.status);
@@ -977,7 +886,7 @@ gm_status backward(Call& c, const Grads& q) {
   }
   BackwardPlan p(c);
   Arena& a = p.a;
-  rc = a.open(c);
+  rc = a.open(c.workspace, c.workspace_bytes, c.s);
   if (rc != GM_OK) return rc;
   uint8_t* lost = a.at<uint8_t>(p.own.lost);
   int* word = a.at<int>(p.own.status);
@@ -1172,7 +1081,7 @@ extern "C" gm_status gm_loss_workspace(const gm_logits* z, int64_t teacher_nnz, 
   *bytes = 0;
   if (c.z.n_rows == 0) return GM_OK;
   c.nnz = teacher_nnz < 0 ? -1 : teacher_nnz;
-  c.sms = gm::sm_count();
+  c.sms = gm::sm_count(gm::kMostBlocks);
   if (c.sms <= 0) {
     cudaGetLastError();
     return GM_ERR_CUDA;

@@ -15,10 +15,10 @@ namespace gm {
 // Launches k so that its start overlaps the end of the kernel before it; k calls chain_wait
 // (gm_umma.cuh). cluster: blocks of a cluster.
 template <class... P, class... A>
-cudaError_t launch_chained(void (*k)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, unsigned cluster,
+cudaError_t launch_chained(void (*k)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, unsigned cluster,
                            A&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
