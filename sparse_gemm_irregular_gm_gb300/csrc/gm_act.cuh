@@ -1,0 +1,76 @@
+// gm_act.cuh -- activations of the layers and their slopes. FINE: for results of 32 bits, by CUDA's functions; else
+// to about 2^-22 absolutely with ex2 and rcp, well under half a step of 16 bits.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "gm_layers.h"
+#include "gm_umma.cuh"
+
+namespace gm {
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// exp(-z^2 / 2)
+template <bool FINE>
+__device__ __forceinline__ float bell(float z) {
+  if constexpr (FINE) return expf(-0.5f * z * z);
+  else return ex2(z * z * -0.72134752044f);
+}
+
+// Share of a standard normal below z: (1 + erf(z / sqrt 2)) / 2. In short: Abramowitz and Stegun 7.1.26,
+// erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0, off by 1.5e-7 at most; b: bell(z), which it shares
+// with the slope.
+template <bool FINE>
+__device__ __forceinline__ float normal_below(float z, float b) {
+  if constexpr (FINE) {
+    return 0.5f * erfcf(z * -0.70710678f);
+  } else {
+    const float t = rcp(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f), 0.5f * 1.421413741f),
+                                     0.5f * -0.284496736f), 0.5f * 0.254829592f);
+    const float tail = p * b;
+    return z < 0.f ? tail : 1.f - tail;
+  }
+}
+template <bool FINE>
+__device__ __forceinline__ float normal_below(float z) {
+  return normal_below<FINE>(z, FINE ? 0.f : bell<FINE>(z));
+}
+
+// 1 / (1 + exp(-x))
+template <bool FINE>
+__device__ __forceinline__ float logistic(float x) {
+  if constexpr (FINE) return 1.f / (1.f + expf(-x));
+  else return rcp(1.f + ex2(x * -1.44269504089f));
+}
+
+// (1 + tanh(u)) / 2 = logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3)
+constexpr float kTanhA = 1.5957691216f, kTanhB = 0.044715f;
+__device__ __forceinline__ float gelu_tanh_arg(float z) { return z * fmaf(z * z, kTanhA * kTanhB, kTanhA); }
+
+// act'(z)
+template <bool FINE>
+__device__ __forceinline__ float slope(float z, int act) {
+  if (act == GM_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if (act == GM_ACT_GELU) {
+    const float b = bell<FINE>(z);
+    return fmaf(z * 0.3989422804f, b, normal_below<FINE>(z, b));
+  }
+  if (act == GM_ACT_GELU_TANH) {
+    z = z > 30.f ? 30.f : z < -30.f ? -30.f : z;  // 1 and 0 long before; z^2 stays finite
+    const float s = logistic<FINE>(gelu_tanh_arg(z));
+    return fmaf(z * s * (1.f - s), fmaf(z * z, 3.f * kTanhA * kTanhB, kTanhA), s);
+  }
+  if (act == GM_ACT_SILU) {
+    const float s = logistic<FINE>(z);
+    return s * fmaf(z, 1.f - s, 1.f);
+  }
+  return 1.f;
+}
+
+}  // namespace gm

@@ -1,0 +1,533 @@
+// gm_linear.cu -- a product with bias, activation and residual (include/gm_layers.h): host driver, and the
+// kernels around the tensor-core products of gm_loss_prod.cu.
+//
+// Forward: one product whose end adds the bias, writes z if the backward call will want it, applies the activation and
+// adds the residual. Few tiles along a long row are split along it; the parts are joined by a second kernel with the same
+// end. Backward: dz = grad * act'(z) is laid out as an operand, its columns summed on the way (db), then dX = dz W
+// and dW = dz^T X are products of the kind that the losses' gradients are.
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gm_act.cuh"
+#include "gm_device.cuh"
+#include "gm_host.h"
+#include "gm_layers.h"
+#include "gm_loss.h"
+#include "gm_planes.cuh"
+#include "gm_umma.cuh"
+
+namespace gm {
+
+namespace {
+
+__device__ __forceinline__ float element(const void* p, int64_t i, int type) {
+  return type == GM_LOSS_F32    ? static_cast<const float*>(p)[i]
+         : type == GM_LOSS_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+                                : __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void set_element(void* p, int64_t i, int type, float x) {
+  if (type == GM_LOSS_F32) static_cast<float*>(p)[i] = x;
+  else if (type == GM_LOSS_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+  else static_cast<__half*>(p)[i] = __float2half_rn(x);
+}
+__device__ __forceinline__ float activated(float z, int act, bool fine) {
+  if (act == GM_ACT_RELU) return z < 0.f ? 0.f : z;
+  if (act == GM_ACT_GELU) return z * (fine ? normal_below<true>(z) : normal_below<false>(z));
+  if (act == GM_ACT_GELU_TANH) return z * (fine ? logistic<true>(gelu_tanh_arg(z)) : logistic<false>(gelu_tanh_arg(z)));
+  if (act == GM_ACT_SILU) return z * (fine ? logistic<true>(z) : logistic<false>(z));
+  return z;
+}
+
+// y and z from the parts of X W^T, a thread an element.
+__global__ void __launch_bounds__(256) k_linear_join(const float* __restrict__ acc, int splits, int64_t rows, int64_t outs,
+                                                     int64_t acc_ld, const LinearEnd e, void* y, int64_t y_ld, int type) {
+  chain_wait();
+  const int64_t n = rows * outs, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+    const int64_t r = i / outs, c = i - r * outs;
+    const float* p = acc + r * acc_ld + c;
+    float v = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) v += p[s * rows * acc_ld];
+    if (e.bias) v += element(e.bias, c, type);
+    if (e.keep) set_element(e.z, r * e.z_ld + c, type, v);
+    v = activated(v, e.act, type == GM_LOSS_F32);
+    if (e.residual) v += element(e.residual, r * e.residual_ld + c, type);
+    set_element(y, r * y_ld + c, type, v);
+  }
+}
+
+// dz = grad * act'(z), as an operand of the two products: 16 bits, with few rows a second plane of what rounding took; three
+// bf16 planes of f32. Sums of its columns over the block's rows, in fp32, go to sums[blockIdx.y]. A warp takes 256 columns of
+// a row, a thread 8 of them. Bound by memory.
+struct DzArgs {
+  const void *grad, *z;  // z null: dz is grad
+  int64_t grad_ld, z_ld, rows, outs, rows_a_block;
+  int act, type;
+  bool wide;             // rows start on 16-byte boundaries
+  uint16_t* dz;          // null: not wanted
+  int64_t ld, plane;
+  int planes;
+  float* sums;           // null: not wanted
+};
+constexpr int kDzWarps = 8, kDzColumns = 256;
+
+template <bool F32>
+__device__ __forceinline__ void read8(const void* p, int have, bool wide, bool bf16, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if constexpr (F32) {
+    if (wide && have >= 8) {
+      const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < have) v[i] = static_cast<const float*>(p)[i];
+    }
+  } else {
+    uint32_t w[4];
+    if (wide && have >= 8) {
+      const uint4 a = *static_cast<const uint4*>(p);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    } else {
+      const uint16_t* s = static_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (2 * i < have ? s[2 * i] : 0u) | (2 * i + 1 < have ? static_cast<uint32_t>(s[2 * i + 1]) << 16 : 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (bf16) {
+        v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = y.x, v[2 * i + 1] = y.y;
+      }
+    }
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(32 * kDzWarps) k_dz(const DzArgs a) {
+  __shared__ float sh[kDzWarps][kDzColumns];
+  chain_wait();
+  constexpr int kBytes = F32 ? 4 : 2;
+  constexpr int kAhead = 2;  // rows of a warp under way
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kDzColumns + lane * 8;
+  const int have = static_cast<int>(max(int64_t(0), min(int64_t(8), a.outs - col)));
+  const bool bf16 = a.type != GM_LOSS_F16;
+  const int64_t first = blockIdx.y * a.rows_a_block, end = min(a.rows, first + a.rows_a_block);
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int64_t r0 = first + warp; r0 < end; r0 += kDzWarps * kAhead) {
+    float g[kAhead][8], z[kAhead][8];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t r = r0 + k * kDzWarps;
+      const int in = r < end ? have : 0;
+      read8<F32>(static_cast<const char*>(a.grad) + (r * a.grad_ld + col) * kBytes, in, a.wide, bf16, g[k]);
+      if (a.z) read8<F32>(static_cast<const char*>(a.z) + (r * a.z_ld + col) * kBytes, in, a.wide, bf16, z[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t r = r0 + k * kDzWarps;
+      if (r >= end) break;
+      if (a.z) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[k][i] *= slope<F32>(z[k][i], a.act);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += i < have ? g[k][i] : 0.f;
+      if (a.dz && col < a.ld) {  // ld is a multiple of 8
+#pragma unroll 1
+        for (int p = 0; p < a.planes; ++p) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            float u[2] = {g[k][i], g[k][i + 1]};
+            uint32_t h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (i + j >= have) u[j] = 0.f;
+              if constexpr (F32) {
+                h[j] = take_plane(u[j], p == 2, (__float_as_uint(u[j]) & INT32_MAX) < kRoundsPast);
+              } else if (bf16) {
+                const __nv_bfloat16 y = __float2bfloat16_rn(u[j]);
+                h[j] = __bfloat16_as_ushort(y), u[j] -= __bfloat162float(y);
+              } else {
+                const __half y = __float2half_rn(u[j]);
+                h[j] = __half_as_ushort(y), u[j] -= __half2float(y);
+              }
+              g[k][i + j] = u[j];
+            }
+            w[i / 2] = h[0] | (h[1] << 16);
+          }
+          *reinterpret_cast<uint4*>(a.dz + p * a.plane + r * a.ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  if (!a.sums) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sh[warp][lane * 8 + i] = acc[i];
+  __syncthreads();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kDzColumns + threadIdx.x;
+  float x = 0.f;
+#pragma unroll
+  for (int w = 0; w < kDzWarps; ++w) x += sh[w][threadIdx.x];
+  if (c < a.outs) a.sums[blockIdx.y * a.outs + c] = x;
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+struct LinearCall {
+  gm_linear p = {};
+  gm_layer_config cfg = {};
+  cudaStream_t s = nullptr;
+  int sms = 0;
+  int* status = nullptr;
+  int planes() const { return p.type == GM_LOSS_F32 ? 3 : 1; }
+};
+
+gm_status check_matrix(const void* p, int64_t ld, int64_t cols, int64_t rows, int32_t type, bool needed) {
+  if (!p) return needed && rows > 0 ? GM_ERR_INVALID_ARG : GM_OK;
+  if (!aligned(p, elem_bytes(type)) || ld < cols) return GM_ERR_INVALID_ARG;
+  return ld > kMostLd ? GM_ERR_INDEX_OVERFLOW : GM_OK;
+}
+
+gm_status check_linear(LinearCall& c, const gm_linear* p, const gm_layer_config* cfg, void* stream) {
+  if (!p || p->n_rows < 0 || p->dim < 1 || p->n_outs < 1) return GM_ERR_INVALID_ARG;
+  if (p->n_rows > kMostIndex || p->dim > (int64_t(1) << 24) || p->n_outs > (int64_t(1) << 24)) return GM_ERR_INDEX_OVERFLOW;
+  if (p->type != GM_LOSS_F32 && p->type != GM_LOSS_BF16 && p->type != GM_LOSS_F16) return GM_ERR_INVALID_ARG;
+  if (p->activation < GM_ACT_NONE || p->activation > GM_ACT_SILU) return GM_ERR_INVALID_ARG;
+  gm_status rc = check_matrix(p->x, p->x_ld, p->dim, p->n_rows, p->type, true);
+  if (rc == GM_OK) rc = check_matrix(p->w, p->w_ld, p->dim, p->n_outs, p->type, true);
+  if (rc != GM_OK) return rc;
+  c.p = *p;
+  if (cfg) c.cfg = *cfg;
+  if (c.cfg.workspace && (!aligned(c.cfg.workspace, 256) || c.cfg.workspace_bytes < 0)) return GM_ERR_INVALID_ARG;
+  c.s = static_cast<cudaStream_t>(stream);
+  return GM_OK;
+}
+
+gm_status begin(LinearCall& c) {
+  if (cudaPeekAtLastError() != cudaSuccess) return GM_ERR_CUDA;
+  c.sms = sm_count(kMostBlocks);
+  c.status = loss_status_word();
+  if (c.sms > 0 && c.status) return GM_OK;
+  cudaGetLastError();
+  return GM_ERR_CUDA;
+}
+gm_status finish(bool launched) { return cudaGetLastError() != cudaSuccess || !launched ? GM_ERR_CUDA : GM_OK; }
+
+// Tiles of a product: blocks a tile, its columns, and how many parts its sum is cut into.
+struct Tiling {
+  int cg = 1, bn = 64;
+  int64_t splits = 1;
+};
+// The least of rounds of tiles times what a stage of one takes (in SM clocks: 64 bytes a clock from L2, or the products),
+// times stages, with a start and an end a round; parts cost their way through memory.
+Tiling tile_for(int64_t m, int64_t n, int64_t k_blocks, int planes, int sms) {
+  Tiling best;
+  double least = 1e300;
+  struct Kind { int cg, bn; double stage; };
+  const Kind kinds[] = {{2, 256, 512}, {1, 256, 768}, {1, 128, 512}, {1, 64, 384}};
+  for (const Kind& k : kinds) {
+    if (planes == 3 && k.cg == 1 && k.bn == 256) continue;
+    const int64_t slots = sms / k.cg, tiles = div_up(m, 128 * k.cg) * div_up(n, k.bn);
+    const double stage = planes == 3 ? (k.cg == 2 ? 3200 : k.bn == 128 ? 2000 : 1400) : k.stage;
+    for (int64_t want = 1; want <= 16; want *= 2) {
+      if (want > 1 && (tiles * want > slots || k_blocks / want < 8)) break;
+      const int64_t per = div_up(k_blocks, want), parts = div_up(k_blocks, per);
+      const double cost = div_up(tiles * parts, slots) * (per * stage + 2500.0 + 12.0 * k.bn) +
+                          (parts > 1 ? 6000.0 + static_cast<double>(m) * n * parts * 8 / (sms * 32.0) : 0.0);
+      if (cost < least) least = cost, best = Tiling{k.cg, k.bn, parts};
+    }
+  }
+  return best;
+}
+
+struct LinearForward {
+  Arena a;
+  Source x, w;
+  Tiling t;
+  size_t o_lost, o_acc = 0;
+  int64_t acc_ld = 0;
+  explicit LinearForward(const LinearCall& c)
+      : x(c.p.x, c.p.n_rows, c.p.dim, c.p.x_ld, c.p.type), w(c.p.w, c.p.n_outs, c.p.dim, c.p.w_ld, c.p.type) {
+    o_lost = a.add(kMostBlocks);
+    x.plan(a);
+    w.plan(a);
+    t = tile_for(c.p.n_rows, c.p.n_outs, div_up(c.p.dim, 64), c.planes(), c.sms);
+    if (t.splits > 1) {
+      acc_ld = up(c.p.n_outs, 32);
+      o_acc = a.add(t.splits * c.p.n_rows * acc_ld * 4);
+    }
+  }
+};
+
+// Rows of 32 elements from p on, read 16 bytes at a time.
+bool wide_rows(const void* p, int64_t ld, int64_t rows, int64_t es) { return aligned(p, 16) && (rows <= 1 || ld * es % 16 == 0); }
+// By TMA where its rows start and end on 16-byte boundaries; boxes of 32 rows of 32 elements.
+bool linear_result(CUtensorMap* m, bool* by_tma, void* out, int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+  *by_tma = wide_rows(out, ld, rows, es) && cols * es % 16 == 0;
+  if (!*by_tma) return true;
+  if (rows <= 1) ld = up(cols, 16 / es);
+  return encode(m, Operand{out, rows, cols, ld, rows * ld, 1, static_cast<int>(es)}, 32, static_cast<int>(32 * es));
+}
+
+gm_status forward(LinearCall& c, LinearEnd e, void* y, int64_t y_ld) {
+  gm_status rc = begin(c);
+  if (rc != GM_OK) return rc;
+  const int64_t m = c.p.n_rows, n = c.p.n_outs, es = elem_bytes(c.p.type);
+  LinearForward p(c);
+  rc = p.a.open(c.cfg.workspace, c.cfg.workspace_bytes, c.s);
+  if (rc != GM_OK) return rc;
+  const Operand ox = p.x.ready(p.a, c.s), ow = p.w.ready(p.a, c.s);
+  ProdMaps maps;
+  if (!encode(&maps.a, ox, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(p.t.cg, p.t.bn))) return GM_ERR_CUDA;
+  maps.o = maps.z = maps.a;
+  ProdArgs g = {};
+  g.planes = c.planes();
+  g.g_planes = 1;
+  g.bf16 = c.p.type != GM_LOSS_F16;
+  g.m = m;
+  g.n = n;
+  g.m_tiles = static_cast<int>(div_up(m, 128 * p.t.cg));
+  g.n_tiles = static_cast<int>(div_up(n, p.t.bn));
+  g.k_blocks = static_cast<int>(div_up(c.p.dim, 64));
+  g.k_per_split = static_cast<int>(div_up(g.k_blocks, p.t.splits));
+  g.splits = static_cast<int>(div_up(g.k_blocks, g.k_per_split));
+  g.group = group_of_tiles(g.m_tiles, 128 * p.t.cg, c.p.dim, g.planes);
+  g.status = c.status;
+  g.lost = p.a.at<uint8_t>(p.o_lost);
+  g.lost_first = true;
+  g.out = y;
+  g.out_ld = y_ld;
+  g.out_type = c.p.type;
+  e.bias_wide = aligned(e.bias, 16);
+  e.residual_wide = wide_rows(e.residual, e.residual_ld, m, es);
+  bool set;
+  float* acc = nullptr;
+  if (g.splits > 1) {
+    g.acc = true;
+    acc = p.a.at<float>(p.o_acc);
+    set = encode(&maps.o, Operand{acc, m, n, p.acc_ld, m * p.acc_ld, g.splits, 4}, 32);
+  } else {
+    set = linear_result(&maps.o, &g.by_tma, y, m, n, y_ld, es);
+    if (set && e.keep) set = linear_result(&maps.z, &e.z_by_tma, e.z, m, n, e.z_ld, es);
+  }
+  if (!set) return GM_ERR_CUDA;
+  g.lin = e;
+  bool ok = launch_prod(Prod::kLinear, p.t.cg, p.t.bn, maps, g, c.sms, c.s) == cudaSuccess;
+  if (ok && acc)
+    ok = launch_chained(k_linear_join, grid_for(m * n, 256), 256, 0, c.s, 1, static_cast<const float*>(acc), g.splits, m, n,
+                        p.acc_ld, e, y, y_ld, static_cast<int>(c.p.type)) == cudaSuccess;
+  return finish(ok);
+}
+
+struct LinearGrads {
+  const void* grad;
+  int64_t grad_ld;
+  const void* z;
+  int64_t z_ld;
+  void* dx;
+  int64_t dx_ld;
+  void* dw;
+  int64_t dw_ld;
+  void* db;
+};
+
+// One of the two products that read dz, and the sum of its parts.
+struct SumPlan {
+  int cg, bn;
+  int64_t splits, acc_ld, k_blocks;
+  size_t o_acc = 0;
+  SumPlan(Arena& a, int64_t rows, int64_t cols, int64_t k, int planes, int sms) {
+    bn = prod_sums_cols(cols, rows, planes);
+    cg = bn == 256 && rows > 128 ? 2 : 1;
+    k_blocks = div_up(k, 64);
+    const int64_t tiles = div_up(rows, 128 * cg) * div_up(cols, bn);
+    splits = std::max<int64_t>(1, std::min<int64_t>(sms / cg / tiles, k_blocks / 8));
+    splits = div_up(k_blocks, div_up(k_blocks, splits));
+    acc_ld = up(cols, 32);
+    if (splits > 1) o_acc = a.add(splits * rows * acc_ld * 4);
+  }
+};
+
+struct LinearBackward {
+  Arena a;
+  Source x, w;
+  int planes, dz_planes;
+  int64_t dz_ld, parts, rows_a_part;  // parts: of db's sum
+  SumPlan dx, dw;
+  size_t o_lost, o_dz, o_sums;
+  explicit LinearBackward(const LinearCall& c)
+      : x(c.p.x, c.p.n_rows, c.p.dim, c.p.x_ld, c.p.type),
+        w(c.p.w, c.p.n_outs, c.p.dim, c.p.w_ld, c.p.type),
+        planes(c.planes()),
+        dz_planes(planes == 3 ? 3 : c.p.activation != GM_ACT_NONE && c.p.n_rows <= 128 ? 2 : 1),
+        dx(a, c.p.n_rows, c.p.dim, c.p.n_outs, planes, c.sms),
+        dw(a, c.p.n_outs, c.p.dim, c.p.n_rows, planes, c.sms) {
+    const int64_t m = c.p.n_rows, n = c.p.n_outs;
+    x.plan(a);
+    w.plan(a);
+    o_lost = a.add(2 * kMostBlocks);
+    dz_ld = up(n, 8);
+    o_dz = a.add(dz_planes * m * dz_ld * 2);
+    const int64_t slabs = div_up(n, kDzColumns);
+    parts = std::max<int64_t>(1, std::min(div_up(8 * c.sms, slabs), div_up(m, 4 * kDzWarps)));
+    rows_a_part = div_up(m, parts);
+    parts = div_up(m, rows_a_part);
+    o_sums = a.add(parts * n * 4);
+  }
+};
+
+gm_status backward(LinearCall& c, const LinearGrads& q) {
+  gm_status rc = begin(c);
+  if (rc != GM_OK) return rc;
+  const int64_t m = c.p.n_rows, n = c.p.n_outs, dim = c.p.dim, es = elem_bytes(c.p.type);
+  const int32_t type = c.p.type;
+  if (m == 0) {
+    bool ok = true;
+    if (q.dw) ok = cudaMemset2DAsync(q.dw, q.dw_ld * es, 0, dim * es, n, c.s) == cudaSuccess;
+    if (ok && q.db) ok = cudaMemsetAsync(q.db, 0, n * es, c.s) == cudaSuccess;
+    return finish(ok);
+  }
+  LinearBackward p(c);
+  rc = p.a.open(c.cfg.workspace, c.cfg.workspace_bytes, c.s);
+  if (rc != GM_OK) return rc;
+  const bool act = c.p.activation != GM_ACT_NONE;
+  const bool in_place = !act && type != GM_LOSS_F32 && wide_rows(q.grad, q.grad_ld, m, 2);  // grad is dz, and an operand
+  const bool products = q.dx || q.dw;
+  Operand odz{q.grad, m, n, m <= 1 ? up(n, 8) : q.grad_ld, m * q.grad_ld, 1};
+  if ((products && !in_place) || q.db) {
+    DzArgs d = {};
+    d.grad = q.grad;
+    d.grad_ld = q.grad_ld;
+    d.z = act ? q.z : nullptr;
+    d.z_ld = q.z_ld;
+    d.rows = m;
+    d.outs = n;
+    d.rows_a_block = p.rows_a_part;
+    d.act = c.p.activation;
+    d.type = type;
+    d.wide = wide_rows(q.grad, q.grad_ld, m, es) && (!act || wide_rows(q.z, q.z_ld, m, es));
+    if (products && !in_place) {
+      d.dz = p.a.at<uint16_t>(p.o_dz);
+      d.ld = p.dz_ld;
+      d.plane = m * p.dz_ld;
+      d.planes = p.dz_planes;
+      odz = Operand{d.dz, m, n, d.ld, d.plane, d.planes};
+    }
+    if (q.db) d.sums = p.a.at<float>(p.o_sums);
+    const dim3 grid(static_cast<unsigned>(div_up(n, kDzColumns)), static_cast<unsigned>(p.parts));
+    if (launch_chained(type == GM_LOSS_F32 ? k_dz<true> : k_dz<false>, grid, 32 * kDzWarps, 0, c.s, 1, d) != cudaSuccess)
+      return finish(false);
+    if (q.db) sum_splits(d.sums, p.parts, 1, n, n, q.db, n, type, nullptr, c.s);
+  }
+  bool ok = true;
+  auto product = [&](Prod kind, const SumPlan& t, const Operand& b, int64_t rows, void* out, int64_t out_ld, uint8_t* lost) {
+    ProdMaps maps;
+    if (!encode(&maps.a, odz, kind == Prod::kDh ? prod_box_rows_a() : 64) || !encode(&maps.b, b, 64)) return false;
+    maps.z = maps.a;
+    ProdArgs g = {};
+    g.planes = p.planes;
+    g.g_planes = odz.planes;
+    g.bf16 = type != GM_LOSS_F16;
+    g.m = rows;
+    g.n = dim;
+    g.m_tiles = static_cast<int>(div_up(rows, 128 * t.cg));
+    g.n_tiles = static_cast<int>(div_up(dim, t.bn));
+    g.k_blocks = static_cast<int>(t.k_blocks);
+    g.k_per_split = static_cast<int>(div_up(t.k_blocks, t.splits));
+    g.splits = static_cast<int>(t.splits);
+    g.group = 1;
+    g.status = c.status;
+    g.lost = lost;
+    g.lost_first = true;
+    float* acc = nullptr;
+    bool set;
+    if (t.splits > 1) {
+      acc = p.a.at<float>(t.o_acc);
+      g.acc = g.by_tma = true;
+      set = encode(&maps.o, Operand{acc, rows, dim, t.acc_ld, rows * t.acc_ld, g.splits, 4}, 32);
+    } else {
+      set = set_result(&maps.o, g, out, rows, dim, out_ld, type);
+    }
+    if (!set || launch_prod(kind, t.cg, t.bn, maps, g, c.sms, c.s) != cudaSuccess) return false;
+    if (acc) sum_splits(acc, t.splits, rows, dim, t.acc_ld, out, out_ld, type, lost, c.s);
+    return true;
+  };
+  uint8_t* lost = p.a.at<uint8_t>(p.o_lost);
+  if (q.dx) ok = product(Prod::kDh, p.dx, p.w.ready(p.a, c.s), m, q.dx, q.dx_ld, lost);
+  if (ok && q.dw) ok = product(Prod::kDw, p.dw, p.x.ready(p.a, c.s), n, q.dw, q.dw_ld, lost + kMostBlocks);
+  return finish(ok);
+}
+
+}  // namespace
+
+}  // namespace gm
+
+extern "C" gm_status gm_linear_forward(const gm_linear* p, const gm_layer_config* cfg, void* stream, const void* bias,
+                                       const void* residual, int64_t residual_ld, void* y, int64_t y_ld, void* z,
+                                       int64_t z_ld) {
+  using namespace gm;
+  NvtxRange range("gm_linear_forward");
+  LinearCall c;
+  gm_status rc = check_linear(c, p, cfg, stream);
+  if (rc != GM_OK) return rc;
+  if (!aligned(bias, elem_bytes(p->type))) return GM_ERR_INVALID_ARG;
+  rc = check_matrix(residual, residual_ld, p->n_outs, p->n_rows, p->type, false);
+  if (rc == GM_OK) rc = check_matrix(y, y_ld, p->n_outs, p->n_rows, p->type, true);
+  if (rc == GM_OK) rc = check_matrix(z, z_ld, p->n_outs, p->n_rows, p->type, false);
+  if (rc != GM_OK) return rc;
+  if (y && y == residual && y_ld != residual_ld && p->n_rows > 1) return GM_ERR_INVALID_ARG;
+  if (p->n_rows == 0) return GM_OK;
+  LinearEnd e = {};
+  e.bias = bias;
+  e.residual = residual;
+  e.residual_ld = residual_ld;
+  e.act = p->activation;
+  e.keep = z != nullptr;
+  e.z = z;
+  e.z_ld = z_ld;
+  return forward(c, e, y, y_ld);
+}
+
+extern "C" gm_status gm_linear_backward(const gm_linear* p, const gm_layer_config* cfg, void* stream, const void* grad,
+                                        int64_t grad_ld, const void* z, int64_t z_ld, void* dx, int64_t dx_ld, void* dw,
+                                        int64_t dw_ld, void* dbias) {
+  using namespace gm;
+  NvtxRange range("gm_linear_backward");
+  LinearCall c;
+  gm_status rc = check_linear(c, p, cfg, stream);
+  if (rc == GM_OK) rc = check_matrix(grad, grad_ld, p->n_outs, p->n_rows, p->type, true);
+  if (rc == GM_OK) rc = check_matrix(z, z_ld, p->n_outs, p->n_rows, p->type, p->activation != GM_ACT_NONE);
+  if (rc == GM_OK) rc = check_matrix(dx, dx_ld, p->dim, p->n_rows, p->type, false);
+  if (rc == GM_OK) rc = check_matrix(dw, dw_ld, p->dim, p->n_outs, p->type, false);
+  if (rc != GM_OK) return rc;
+  if (!aligned(dbias, elem_bytes(p->type)) || (p->n_rows > 0 && !dx && !dw && !dbias)) return GM_ERR_INVALID_ARG;
+  return backward(c, LinearGrads{grad, grad_ld, z, z_ld, dx, dx_ld, dw, dw_ld, dbias});
+}
+
+extern "C" gm_status gm_linear_workspace(const gm_linear* p, int32_t backward, int64_t* bytes) {
+  using namespace gm;
+  if (!bytes || (backward != 0 && backward != 1)) return GM_ERR_INVALID_ARG;
+  LinearCall c;
+  const gm_status rc = check_linear(c, p, nullptr, nullptr);
+  if (rc != GM_OK) return rc;
+  *bytes = 0;
+  if (c.p.n_rows == 0) return GM_OK;
+  c.sms = sm_count(kMostBlocks);
+  if (c.sms <= 0) {
+    cudaGetLastError();
+    return GM_ERR_CUDA;
+  }
+  *bytes = static_cast<int64_t>(backward ? LinearBackward(c).a.used : LinearForward(c).a.used);
+  return GM_OK;
+}

@@ -15,6 +15,7 @@
 
 #include "gm_device.cuh"
 #include "gm_host.h"
+#include "gm_planes.cuh"
 #include "gm_umma.cuh"
 
 namespace gm {
@@ -34,19 +35,6 @@ __global__ void k_take_status(int* __restrict__ taken) { *taken = atomicExch(&g_
 // multiple of 8: a thread writes 8 elements of each plane at once. VEC: the rows of src start
 // on 16-byte boundaries. Bound by memory: 126425 x 1320 f32, 1.67 GB in and out, 245 us (6.8 TB/s);
 // 489196 x 437 f16, 0.86 GB, 132 us (6.5 TB/s).
-constexpr uint32_t kRoundsPast = 0x7f7f8000u;  // bits of |x| from which the nearest bf16 is none that is finite
-__device__ __forceinline__ uint32_t take_plane(float& x, bool third, bool ordinary) {  // leaves in x what is left of it
-  __nv_bfloat16 a = __float2bfloat16_rn(x);
-  float left = x - __bfloat162float(a);
-  if (!ordinary && !third) {
-    if (fabsf(x) == INFINITY) a = __ushort_as_bfloat16(0), left = x;
-    else if (x != x) left = 0.f;  // NaN stands in the first plane
-    else if ((__float_as_uint(x) & INT32_MAX) >= kRoundsPast) a = __float2bfloat16_rz(x), left = x - __bfloat162float(a);
-  }
-  x = left;
-  return __bfloat16_as_ushort(a);
-}
-
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int64_t rows, int dim, int64_t src_ld,
                                               uint16_t* __restrict__ dst, int ld) {
@@ -431,6 +419,64 @@ __global__ void __launch_bounds__(256) k_sum_splits(const float* __restrict__ ac
 }
 
 // ---- host -----------------------------------------------------------------------------------
+}  // namespace
+
+int* loss_status_word() {
+  void* st = nullptr;
+  if (cudaGetSymbolAddress(&st, g_loss_status) == cudaSuccess) return static_cast<int*>(st);
+  cudaGetLastError();
+  return nullptr;
+}
+
+Source::Source(const void* p, int64_t rows, int64_t dim, int64_t ld, int32_t type)
+    : p(p), rows(rows), dim(dim), ld(ld), type(type), src_ld(ld) {
+  packed = type == GM_LOSS_F32 || !aligned(p, 16) || (rows > 1 && ld % 8 != 0);
+  if (packed || rows <= 1) this->ld = up(dim, 8);
+}
+void Source::plan(Arena& a) {
+  if (packed) off = a.add(planes() * rows * ld * 2);
+}
+Operand Source::ready(const Arena& a, cudaStream_t s) const {
+  Operand o{p, rows, dim, ld, rows * ld, planes()};
+  if (packed) {
+    o.p = a.at<uint16_t>(off);
+    const unsigned grid = grid_for(rows * ld / 8, 256);
+    uint16_t* dst = a.at<uint16_t>(off);
+    const int d = static_cast<int>(dim), l = static_cast<int>(ld);
+    const bool vec = aligned(p, 16) && (rows <= 1 || src_ld % 4 == 0);
+    launch_chained(type != GM_LOSS_F32 ? k_pack<false, false> : vec ? k_pack<true, true> : k_pack<true, false>, grid, 256,
+                   0, s, 1, p, rows, d, src_ld, dst, l);
+  }
+  return o;
+}
+
+int group_of_tiles(int64_t m_tiles, int64_t tile_rows, int64_t dim, int planes) {
+  const int64_t bytes = tile_rows * dim * 2 * planes;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(m_tiles, (int64_t(40) << 20) / bytes)));
+}
+
+bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t dim, int64_t ld, int32_t type) {
+  const int es = static_cast<int>(elem_bytes(type));
+  g.out = out;
+  g.out_ld = ld;
+  g.out_type = type;
+  // half a tile of 64 columns of 2 bytes is less than a box
+  g.by_tma = aligned(out, 16) && (rows <= 1 || ld * es % 16 == 0) && dim * es % 16 == 0 && (es == 4 || dim > 64);
+  if (!g.by_tma) return true;
+  if (rows <= 1) ld = up(dim, 16 / es);
+  return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
+}
+
+void sum_splits(const float* acc, int64_t splits, int64_t rows, int64_t dim, int64_t acc_ld, void* out, int64_t out_ld,
+                int32_t type, const uint8_t* lost, cudaStream_t s) {
+  const int64_t n = rows * dim, stride = rows * acc_ld;
+  const bool many = splits >= 16;
+  launch_chained(many ? k_sum_splits<8> : k_sum_splits<1>, grid_for(n, many ? 32 : 256), 256, 0, s, 1, acc,
+                 static_cast<int>(splits), stride, rows, dim, acc_ld, out, out_ld, static_cast<int>(type), lost);
+}
+
+namespace {
+
 constexpr int64_t kDefaultCap = int64_t(512) << 20;  // of G; f16: of each of the two sets of planes (Scales)
 constexpr int64_t kStatsCap = int64_t(512) << 20;    // of a forward call's row statistics
 
@@ -506,14 +552,11 @@ gm_status check_teacher(Call& c, const gm_csr* t, int32_t value_type, int32_t in
 // Device facts and a clear error state; GM_ERR_CUDA leaves a pending error to its owner.
 gm_status begin(Call& c) {
   if (cudaPeekAtLastError() != cudaSuccess) return GM_ERR_CUDA;
-  void* st = nullptr;
   c.sms = sm_count(kMostBlocks);
-  if (c.sms <= 0 || cudaGetSymbolAddress(&st, g_loss_status) != cudaSuccess) {
-    cudaGetLastError();
-    return GM_ERR_CUDA;
-  }
-  c.status = static_cast<int*>(st);
-  return GM_OK;
+  c.status = loss_status_word();
+  if (c.sms > 0 && c.status) return GM_OK;
+  cudaGetLastError();
+  return GM_ERR_CUDA;
 }
 
 gm_status status_of(int bits) {
@@ -547,40 +590,6 @@ Targets targets_of(const Call& c) {
   if (!c.labels) return Targets{nullptr, true, 0, c.z.n_classes};
   return Targets{c.labels->target, c.labels->target32 == 0, c.labels->ignore_index, c.z.n_classes};
 }
-
-// H or W as a 16-bit operand, in place or laid out in workspace.
-struct Source {
-  const void* p;
-  int64_t rows, dim, ld;
-  int32_t type;
-  bool packed;
-  size_t off = 0;
-  Source(const void* p, int64_t rows, int64_t dim, int64_t ld, int32_t type)
-      : p(p), rows(rows), dim(dim), ld(ld), type(type) {
-    packed = type == GM_LOSS_F32 || !aligned(p, 16) || (rows > 1 && ld % 8 != 0);
-    if (rows <= 1) this->ld = up(dim, 8);
-    if (packed) this->ld = up(dim, 8);
-    src_ld = ld;
-  }
-  int64_t src_ld;
-  int planes() const { return type == GM_LOSS_F32 ? 3 : 1; }
-  void plan(Arena& a) {
-    if (packed) off = a.add(planes() * rows * ld * 2);
-  }
-  Operand ready(const Arena& a, cudaStream_t s) const {
-    Operand o{p, rows, dim, ld, rows * ld, planes()};
-    if (packed) {
-      o.p = a.at<uint16_t>(off);
-      const unsigned grid = grid_for(rows * ld / 8, 256);
-      uint16_t* dst = a.at<uint16_t>(off);
-      const int d = static_cast<int>(dim), l = static_cast<int>(ld);
-      const bool vec = aligned(p, 16) && (rows <= 1 || src_ld % 4 == 0);
-      launch_chained(type != GM_LOSS_F32 ? k_pack<false, false> : vec ? k_pack<true, true> : k_pack<true, false>, grid,
-                     256, 0, s, 1, p, rows, d, src_ld, dst, l);
-    }
-    return o;
-  }
-};
 
 struct TeacherPlan {
   size_t start = 0, len = 0, ents = 0, base = 0, falls = 0;
@@ -641,12 +650,6 @@ void set_logits_args(ProdArgs& g, const Call& c, const Arena& a, const TeacherPl
     g.ent_len = a.at<int32_t>(t.len);
     g.ents = a.at<int2>(t.ents);
   }
-}
-
-// Row tiles walked together: their rows of H stay in L2 while the class table streams by once.
-int group_of(int64_t m_tiles, int64_t tile_rows, int64_t dim, int planes) {
-  const int64_t bytes = tile_rows * dim * 2 * planes;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(m_tiles, (int64_t(40) << 20) / bytes)));
 }
 
 // Few rows go to kernels that read W once as it lies, instead of the tensor cores.
@@ -773,7 +776,7 @@ gm_status forward(Call& c, float* kl, float* lse_t, float* loss, float* lse) {
     g.m_tiles = static_cast<int>(div_up(n, 128 * p.cg));
     g.splits = 1;
     g.k_blocks = g.k_per_split = static_cast<int>(div_up(c.z.dim, 64));
-    g.group = group_of(g.m_tiles, 128 * p.cg, c.z.dim, g.planes);
+    g.group = group_of_tiles(g.m_tiles, 128 * p.cg, c.z.dim, g.planes);
     const bool pieces = p.piece_tiles < p.n_tiles;
     g.part = part + (pieces ? n : 0);
     g.part_ld = n;
@@ -802,27 +805,6 @@ struct Grads {
   void* dw;
   int64_t dw_ld;
 };
-
-// Where a gradient goes: by TMA where its rows start and end on 16-byte boundaries (a store
-// drops what lies outside the map by 16 bytes, not by elements).
-bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t dim, int64_t ld, int32_t type) {
-  const int es = static_cast<int>(elem_bytes(type));
-  g.out = out;
-  g.out_ld = ld;
-  g.out_type = type;
-  // half a tile of 64 columns of 2 bytes is less than a box
-  g.by_tma = aligned(out, 16) && (rows <= 1 || ld * es % 16 == 0) && dim * es % 16 == 0 && (es == 4 || dim > 64);
-  if (!g.by_tma) return true;
-  if (rows <= 1) ld = up(dim, 16 / es);
-  return encode(m, Operand{out, rows, dim, ld, rows * ld, 1, es}, 32);
-}
-
-void sum_splits(const Call& c, const float* acc, int splits, int64_t acc_ld, const Grads& q, const uint8_t* lost) {
-  const int64_t n = c.z.n_rows * c.z.dim, stride = c.z.n_rows * acc_ld;
-  const bool many = splits >= 16;
-  launch_chained(many ? k_sum_splits<8> : k_sum_splits<1>, grid_for(n, many ? 32 : 256), 256, 0, c.s, 1, acc, splits, stride,
-                 c.z.n_rows, c.z.dim, acc_ld, q.dh, q.dh_ld, static_cast<int>(c.z.type), lost);
-}
 
 // How a backward call is cut, and where its workspace lies.
 struct BackwardPlan {
@@ -906,7 +888,7 @@ gm_status backward(Call& c, const Grads& q) {
     int vec = skinny_vec(g.w, g.w_ld, dim, cls, es);
     if (q.dw) vec = std::min(vec, skinny_vec(q.dw, q.dw_ld, dim, cls, es));
     const bool ok = launch_skinny(g, c.z.type, true, vec, &p.blocks, c.s) == cudaSuccess;
-    if (ok && q.dh) sum_splits(c, g.acc, p.blocks, dim, q, nullptr);
+    if (ok && q.dh) sum_splits(g.acc, p.blocks, n, dim, dim, q.dh, q.dh_ld, c.z.type, nullptr, c.s);
     return finish(c, ok, word);
   }
   const int planes = p.planes, bn_h = p.bn_h, bn_w = p.bn_w, cg_h = p.cg_h, cg_w = p.cg_w;
@@ -947,7 +929,7 @@ gm_status backward(Call& c, const Grads& q) {
       g.n_tiles = static_cast<int>(div_up(wid, bn));
       g.splits = 1;
       g.k_blocks = g.k_per_split = static_cast<int>(div_up(dim, 64));
-      g.group = group_of(g.m_tiles, 128 * cg, dim, planes);
+      g.group = group_of_tiles(g.m_tiles, 128 * cg, dim, planes);
       g.b_row0 = static_cast<int>(c0);
       g.cls0 = c0;
       g.lost_first = c0 == 0;
@@ -994,7 +976,7 @@ gm_status backward(Call& c, const Grads& q) {
     }
   }
   if (ok && q.dh && !dh_direct)
-    sum_splits(c, a.at<float>(o_acc), static_cast<int>(splits), acc_ld, q, lost);
+    sum_splits(a.at<float>(o_acc), splits, n, dim, acc_ld, q.dh, q.dh_ld, c.z.type, lost, c.s);
   return finish(c, ok, word);
 }
 

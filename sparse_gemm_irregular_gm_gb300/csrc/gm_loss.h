@@ -1,13 +1,15 @@
 // gm_loss.h -- shared by the translation units of the losses over a large class
 // table (gm_loss.cu: kernels that read rows and entries, host driver;
-// gm_loss_prod.cu: the tensor-core products).
+// gm_loss_prod.cu: the tensor-core products) and of the layers that use the same products (gm_linear.cu).
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "gm_host.h"
 #include "gm_internal.h"
+#include "gm_layers.h"
 #include "gm_losses.h"
 
 namespace gm {
@@ -51,7 +53,8 @@ enum class Prod {
   kStats,  // Z = H W^T: each row's maximum and sums of exponentials over half a tile's columns
   kGrad,   // Z = H W^T again: G = dloss/dZ in 16 bits (three planes of bf16 for fp32 operands)
   kDh,     // G W
-  kDw      // G^T H
+  kDw,     // G^T H
+  kLinear  // X W^T with bias, activation and residual
 };
 
 // Where a row's target stands.
@@ -118,6 +121,19 @@ __device__ __forceinline__ RowCoef row_coef(const RowGrads& r, const RowRaw& x) 
   return c;
 }
 
+// What is done with a finished tile of X W^T: z = tile + bias, y = residual + act(z).
+struct LinearEnd {
+  const void* bias;      // null: none
+  const void* residual;  // null: none
+  int64_t residual_ld;
+  int32_t act;           // GM_ACT_*
+  bool bias_wide, residual_wide;  // read 16 bytes at a time
+  bool keep;             // z is written too
+  void* z;
+  int64_t z_ld;
+  bool z_by_tma;
+};
+
 // What the finished tile of a product is combined with.
 struct ProdArgs {
   // tiles: m_tiles * n_tiles * splits, in groups of `group` row tiles, the column tiles
@@ -157,6 +173,7 @@ struct ProdArgs {
   void* out;
   int64_t out_ld;
   int out_type;      // GM_LOSS_*
+  LinearEnd lin;     // kLinear
 };
 
 // Scales of G in f16, whose range is too short for small probabilities times small weights: powers
@@ -187,7 +204,9 @@ struct Scales {
 
 struct ProdMaps {
   CUtensorMap a, b, o;  // operands, result, boxes of 32 rows (kGrad: of
-                        // prod_grad_row_bytes; kDh, kDw with by_tma: of 128 bytes)
+                        // prod_grad_row_bytes; kDh, kDw with by_tma: of 128 bytes;
+                        // kLinear: of 32 elements)
+  CUtensorMap z;        // kLinear: z, like o
 };
 // Box height of the operands' maps (rows of a K-major box; MN-major boxes are 64 by 64).
 int prod_box_rows_a();
@@ -199,6 +218,31 @@ int prod_grad_row_bytes(int planes, int chunk, int k_blocks);
 // Launches a product; cg: blocks a tile (1: 128 rows, 2: 256), bn: columns of a tile (64, 128 or 256).
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
                         cudaStream_t s);
+
+// ---- around the products (gm_loss.cu) ------------------------------------------------------
+// Report word of the current device; null when it cannot be had.
+int* loss_status_word();
+// An operand of 16 bits for the tensor cores, in place or laid out in workspace.
+struct Source {
+  const void* p;
+  int64_t rows, dim, ld;
+  int32_t type;
+  bool packed;
+  size_t off = 0;
+  int64_t src_ld;
+  Source(const void* p, int64_t rows, int64_t dim, int64_t ld, int32_t type);
+  int planes() const { return type == GM_LOSS_F32 ? 3 : 1; }
+  void plan(Arena& a);
+  Operand ready(const Arena& a, cudaStream_t s) const;
+};
+// Where a result goes: by TMA where its rows start and end on 16-byte boundaries (a store
+// drops what lies outside the map by 16 bytes, not by elements).
+bool set_result(CUtensorMap* m, ProdArgs& g, void* out, int64_t rows, int64_t dim, int64_t ld, int32_t type);
+// out = the splits' sums (of a lost product: NaN), rounded.
+void sum_splits(const float* acc, int64_t splits, int64_t rows, int64_t dim, int64_t acc_ld, void* out, int64_t out_ld,
+                int32_t type, const uint8_t* lost, cudaStream_t s);
+// Row tiles walked together: their rows of A stay in L2 while B streams by once.
+int group_of_tiles(int64_t m_tiles, int64_t tile_rows, int64_t dim, int planes);
 
 // ---- few rows (gm_loss_skinny.cu) --------------------------------------------------------
 constexpr int64_t kSkinnyDim = 4096;  // elements of a row of H at most: H and the sums of dH fit a block

@@ -1,6 +1,6 @@
 // gm_loss_prod.cu -- the matrix products of the losses over a class table, each
 // with its own end: Z = H W^T reduced to row statistics, Z again turned into
-// G = dloss/dZ, dH = G W and dW = G^T H.
+// G = dloss/dZ, dH = G W and dW = G^T H; and of the layers' X W^T with bias, activation and residual.
 //
 // One persistent kernel: blocks (or pairs of blocks) walk the tiles of the result.
 // Warp 0 loads operand tiles with TMA into a ring of 64-deep stages, one lane of warp
@@ -15,6 +15,7 @@
 // cores 95 % busy while tiles run; G 146; dH 154 (64 of 76 pairs have a tile); dW 151. Back to back
 // (8192 x 4096 x 131072) the power cap bounds them: 1.71 PFLOP/s. With dim 256 or less the
 // bytes of G bound the gradients: dH of 512 x 256 x 262144 66 us, 78 % of the DRAM rate.
+#include "gm_act.cuh"
 #include "gm_device.cuh"
 #include "gm_loss.h"
 #include "gm_umma.cuh"
@@ -392,6 +393,28 @@ struct Outbox {
                                        int64_t cols) {
     __syncwarp();
     const int n = static_cast<int>(min(int64_t(32), rows - row0));
+    if constexpr (NARROW) {  // rows of 64 bytes, two at a time
+      const int l = lane & 15, r1 = lane >> 4;
+      const bool in0 = 2 * l < cols, in1 = 2 * l + 1 < cols;
+#pragma unroll 1
+      for (int r0 = 0; r0 < n; r0 += 16) {
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 2 * i + r1;
+          x[i] = ld_shared_u32(buf + r * 64 + (((l >> 2) ^ ((r >> 1) & 3)) << 4) + (l & 3) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 2 * i + r1;
+          uint16_t* p = static_cast<uint16_t*>(out) + (row0 + r) * ld + col0 + 2 * l;
+          if (r < n && in0) p[0] = static_cast<uint16_t>(x[i]);
+          if (r < n && in1) p[1] = static_cast<uint16_t>(x[i] >> 16);
+        }
+      }
+      __syncwarp();
+      return;
+    }
     const bool in0 = es == 4 ? lane < cols : 2 * lane < cols, in1 = 2 * lane + 1 < cols;
     char* p = static_cast<char*>(out) + (row0 * ld + col0) * es + lane * 4;
     const int64_t step = ld * es;
@@ -571,10 +594,136 @@ __device__ __forceinline__ void end_sum(const ProdArgs& g, const CUtensorMap* ma
   });
 }
 
+// ---- product with bias, activation and residual -------------------------------------------
+// act(z) of 32 columns; FINE: for results of 32 bits.
+template <bool FINE>
+__device__ __forceinline__ void activate(float (&v)[32], int act) {
+  if (act == GM_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
+  } else if (act == GM_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= normal_below<FINE>(v[j]);
+  } else if (act == GM_ACT_GELU_TANH) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= logistic<FINE>(gelu_tanh_arg(v[j]));
+  } else if (act == GM_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= logistic<FINE>(v[j]);
+  }
+}
+
+// 32 elements of 16 or 32 bits from p on, `have` of them; wide: 16 bytes at a time.
+template <bool F32>
+struct Piece32 {
+  uint32_t w[F32 ? 32 : 16];
+  __device__ __forceinline__ void read(const void* p, bool wide, int have) {
+    constexpr int kQuads = F32 ? 8 : 4, kEach = F32 ? 4 : 8;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (wide && (q + 1) * kEach <= have) {
+        x = static_cast<const uint4*>(p)[q];
+      } else if (q * kEach < have) {
+        uint32_t e[4];
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = q * 4 + i < have ? static_cast<const uint32_t*>(p)[q * 4 + i] : 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = q * 8 + 2 * i;
+            const uint16_t* s = static_cast<const uint16_t*>(p);
+            e[i] = (k < have ? s[k] : 0u) | (k + 1 < have ? static_cast<uint32_t>(s[k + 1]) << 16 : 0u);
+          }
+        }
+        x = make_uint4(e[0], e[1], e[2], e[3]);
+      }
+      w[4 * q] = x.x, w[4 * q + 1] = x.y, w[4 * q + 2] = x.z, w[4 * q + 3] = x.w;
+    }
+  }
+  __device__ __forceinline__ void add_to(float (&v)[32], bool bf16) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(w[j]);
+    } else if (bf16) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        v[j] += __uint_as_float(w[j / 2] << 16);
+        v[j + 1] += __uint_as_float(w[j / 2] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[j / 2]));
+        v[j] += y.x, v[j + 1] += y.y;
+      }
+    }
+  }
+};
+
+// A thread's row of z and y, 32 columns at a time. Of 16-bit results y and z have half the warp's room each.
+template <int BN, bool F32, class Src>
+__device__ __forceinline__ void end_linear(const ProdArgs& g, const CUtensorMap* map_o, const CUtensorMap* map_z, Src& src,
+                                           int64_t row, int n_tile, int split, int half, uint32_t buf, int lane) {
+  constexpr int kCols = BN / 2, kBytes = F32 ? 4 : 2;
+  const LinearEnd& e = g.lin;
+  const int64_t col0 = int64_t(n_tile) * BN + half * kCols;
+  const int64_t row0 = row - lane;
+  Outbox<!F32> box_y{buf, lane}, box_z{F32 ? buf : buf + 2048, lane};
+  auto put = [&](Outbox<!F32>& box, float (&v)[32]) {
+    if constexpr (F32) box.put32(v);
+    else box.put16(0, v, g.bf16, false, 0xffffffffu);
+  };
+  each_32<kCols>([&](auto cc) {
+    constexpr int c = decltype(cc)::value;
+    const int64_t col = col0 + c;
+    const int have = static_cast<int>(max(int64_t(0), min(int64_t(32), g.n - col)));
+    Piece32<F32> res;
+    const bool with = e.residual && !g.acc && row < g.m;
+    auto read_residual = [&] {
+      if (with) res.read(static_cast<const char*>(e.residual) + (row * e.residual_ld + col) * kBytes, e.residual_wide, have);
+    };
+    if constexpr (!F32) read_residual();  // ahead of the sums; 32 words more than f32's registers hold
+    float v[32];
+    src.template get<c>(v);
+    if (g.acc) {
+      Outbox<false> box{buf, lane};
+      box.open();
+      box.put32(v);
+      if (row0 < g.m && have) box.send(map_o, static_cast<int>(col), static_cast<int>(row0), split, false);
+      return;
+    }
+    if (e.bias) {
+      Piece32<F32> b;
+      b.read(static_cast<const char*>(e.bias) + col * kBytes, e.bias_wide, have);
+      b.add_to(v, g.bf16);
+    }
+    box_y.open();
+    if (e.keep) {
+      put(box_z, v);
+      if (row0 < g.m && have) {
+        if (e.z_by_tma) box_z.send(map_z, static_cast<int>(col), static_cast<int>(row0), 0, false);
+        else box_z.copy(e.z, e.z_ld, kBytes, row0, g.m, col, have);
+      }
+      if constexpr (F32) box_y.open();
+    }
+    activate<F32>(v, e.act);
+    if constexpr (F32) read_residual();
+    if (with) res.add_to(v, g.bf16);
+    put(box_y, v);
+    if (row0 < g.m && have) {
+      if (g.by_tma) box_y.send(map_o, static_cast<int>(col), static_cast<int>(row0), 0, false);
+      else box_y.copy(g.out, g.out_ld, kBytes, row0, g.m, col, have);
+    }
+  });
+}
+
 template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>
 __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_prod(const __grid_constant__ CUtensorMap map_a,
                                                       const __grid_constant__ CUtensorMap map_b,
-                                                      const __grid_constant__ CUtensorMap map_o, const ProdArgs g) {
+                                                      const __grid_constant__ CUtensorMap map_o,
+                                                      const __grid_constant__ CUtensorMap map_z, const ProdArgs g) {
   using S = Shape<KIND, CG, BN, ACC>;
   constexpr bool kAmn = KIND == Prod::kDw;                        // G^T: rows of G run along the result's rows
   constexpr bool kBmn = KIND == Prod::kDw || KIND == Prod::kDh;   // H and W with the summed dimension outside
@@ -781,6 +930,8 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
       }
       auto finish = [&](auto& src) {
         if constexpr (KIND == Prod::kStats) end_stats<BN, LAB, DIS>(g, src, rs, row, tl.n, half);
+        else if constexpr (KIND == Prod::kLinear)
+          end_linear<BN, three_planes<ACC>>(g, &map_o, &map_z, src, row, tl.n, tl.split, half, box.buf, lane);
         else if constexpr (KIND == Prod::kGrad) end_grad<BN, LAB, DIS, ACC>(g, &map_o, src, rs, row, tl.n, half, box);
         else {
           float inv = 1.f;  // of the scale of G
@@ -852,7 +1003,7 @@ cudaError_t launch_one(const ProdMaps& maps, const ProdArgs& a, int num_sms, cud
   }
   const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles * a.splits;
   const int groups = static_cast<int>(tiles < num_sms / CG ? tiles : num_sms / CG);
-  return launch_chained(k, static_cast<unsigned>(groups * CG), S::kThreads, S::kSmem, s, CG, maps.a, maps.b, maps.o, a);
+  return launch_chained(k, static_cast<unsigned>(groups * CG), S::kThreads, S::kSmem, s, CG, maps.a, maps.b, maps.o, maps.z, a);
 }
 
 template <Prod KIND, int CG, int BN, int ACC>
@@ -890,13 +1041,27 @@ cudaError_t launch_sums(int cg, int bn, const ProdMaps& maps, const ProdArgs& a,
            : KIND == Prod::kDw && cg == 2 ? launch_one<Prod::kDw, 2, 256, false, false, kTwo>(maps, a, num_sms, s)
                                           : launch_one<KIND, 1, 256, false, false, kTwo>(maps, a, num_sms, s);
   if (bn == 256) {
-    if constexpr (KIND == Prod::kDw) {  // dH of at most 128 rows has two planes of G
-      if (cg == 1) return launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
-    }
+    if (cg == 1) return launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
     return launch_one<KIND, 2, 256, false, false, kWhole>(maps, a, num_sms, s);
   }
   return bn == 128 ? launch_one<KIND, 1, 128, false, false, kWhole>(maps, a, num_sms, s)
                    : launch_one<KIND, 1, 64, false, false, kWhole>(maps, a, num_sms, s);
+}
+
+cudaError_t launch_linear(int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
+  constexpr Prod K = Prod::kLinear;
+  if (a.planes == 3 && a.k_blocks <= kWholeBlocks)
+    return cg == 2     ? launch_one<K, 2, 256, false, false, kSplitWhole>(maps, a, num_sms, s)
+           : bn == 128 ? launch_one<K, 1, 128, false, false, kSplitWhole>(maps, a, num_sms, s)
+                       : launch_one<K, 1, 64, false, false, kSplitWhole>(maps, a, num_sms, s);
+  if (a.planes == 3)
+    return cg == 2     ? launch_one<K, 2, 256, false, false, kSplit>(maps, a, num_sms, s)
+           : bn == 128 ? launch_one<K, 1, 128, false, false, kSplit>(maps, a, num_sms, s)
+                       : launch_one<K, 1, 64, false, false, kSplit>(maps, a, num_sms, s);
+  return cg == 2     ? launch_one<K, 2, 256, false, false, kWhole>(maps, a, num_sms, s)
+         : bn == 256 ? launch_one<K, 1, 256, false, false, kWhole>(maps, a, num_sms, s)
+         : bn == 128 ? launch_one<K, 1, 128, false, false, kWhole>(maps, a, num_sms, s)
+                     : launch_one<K, 1, 64, false, false, kWhole>(maps, a, num_sms, s);
 }
 
 }  // namespace
@@ -922,6 +1087,7 @@ cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const P
     case Prod::kGrad: return launch_logits<Prod::kGrad>(cg, maps, a, num_sms, s);
     case Prod::kDh: return launch_sums<Prod::kDh>(cg, bn, maps, a, num_sms, s);
     case Prod::kDw: return launch_sums<Prod::kDw>(cg, bn, maps, a, num_sms, s);
+    case Prod::kLinear: return launch_linear(cg, bn, maps, a, num_sms, s);
   }
   return cudaErrorInvalidValue;
 }

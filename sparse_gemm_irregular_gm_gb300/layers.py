@@ -18,12 +18,19 @@ from . import binding
 from .binding import GmError
 from .losses import TYPES, _gradient, _like, _matrix, _On
 
-EXPORTS = ["gm_norm_forward", "gm_norm_backward", "gm_norm_workspace"]
+EXPORTS = ["gm_linear_forward", "gm_linear_backward", "gm_linear_workspace", "gm_norm_forward", "gm_norm_backward", "gm_norm_workspace"]
 NORMS = {"rms": 0, "layer": 1}
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class gm_layer_config(ctypes.Structure):
     _fields_ = [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class gm_linear(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("n_outs", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("x_ld", ctypes.c_int64), ("w", ctypes.c_void_p), ("w_ld", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
 
 
 class gm_norm(ctypes.Structure):
@@ -49,7 +56,10 @@ def load():
     if _lib is not None:
         return _lib
     lib = binding.load()
-    P, V, I64 = ctypes.POINTER, ctypes.c_void_p, ctypes.c_int64
+    P, V, I64, I32 = ctypes.POINTER, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    lib.gm_linear_forward.argtypes = [P(gm_linear), P(gm_layer_config), V, V, V, I64, V, I64, V, I64]
+    lib.gm_linear_backward.argtypes = [P(gm_linear), P(gm_layer_config), V, V, I64, V, I64, V, I64, V, I64, V]
+    lib.gm_linear_workspace.argtypes = [P(gm_linear), I32, P(I64)]
     lib.gm_norm_forward.argtypes = [P(gm_norm), V, V, I64, V, I64, V]
     lib.gm_norm_backward.argtypes = [P(gm_norm), P(gm_layer_config), V, V, V, I64, V, I64, P(gm_norm_grads)]
     lib.gm_norm_workspace.argtypes = [P(gm_norm), P(I64)]
@@ -75,6 +85,101 @@ def _rows(name, t, like, shape=None):
 def _check(rc, where):
     if rc:
         raise GmError(rc, where)
+
+
+def _own(t):
+    """A matrix that was made for a result, as arguments."""
+    return (None, 0) if t is None else (t.data_ptr() or None, t.shape[1])
+
+
+# ---- product with bias, activation and residual ---------------------------------------------
+def _linear(x, w, activation):
+    xp, x_ld = _matrix("x", x)
+    wp, w_ld = _matrix("w", w, x)
+    n, dim = x.shape
+    if w.shape[1] != dim or dim < 1 or w.shape[0] < 1:
+        raise ValueError(f"x has rows of {dim} elements, w is {w.shape[0]} x {w.shape[1]}")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(map(str, ACTIVATIONS))}, not {activation!r}")
+    return gm_linear(n, dim, w.shape[0], xp, x_ld, wp, w_ld, TYPES[x.dtype], ACTIVATIONS[activation])
+
+
+def _linear_run(name, backward, a, device, s, *args):
+    lib, need = load(), ctypes.c_int64()
+    _check(lib.gm_linear_workspace(a, backward, need), name)
+    work = torch.empty(need.value, dtype=torch.uint8, device=device)
+    _check(getattr(lib, name)(a, gm_layer_config(work.data_ptr() or None, need.value), s, *args), name)
+
+
+def gm_linear_forward(x, w, bias, residual, y, z=None, *, activation=None, stream=None):
+    a = _linear(x, w, activation)
+    shape = (a.n_rows, a.n_outs)
+    args = (_row("bias", bias, a.n_outs, x), *_rows("residual", residual, x, shape), *_rows("y", y, x, shape), *_rows("z", z, x, shape))
+    with _On(x.device, stream) as s:
+        _linear_run("gm_linear_forward", 0, a, x.device, s, *args)
+
+
+def linear_forward(x, w, bias=None, *, activation=None, residual=None, keep=False, stream=None):
+    """(y, z): y = residual + act(z), z = x w^T + bias (x: rows x dim, w: outs x dim). z is None unless ``keep`` and an
+    activation, whose gradient reads it. ``activation``: relu, gelu, gelu_tanh, silu, or None."""
+    a = _linear(x, w, activation)
+    shape = (a.n_rows, a.n_outs)
+    args = _row("bias", bias, a.n_outs, x), *_rows("residual", residual, x, shape)
+    with _On(x.device, stream) as s:
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        z = torch.empty_like(y) if keep and a.activation else None
+        _linear_run("gm_linear_forward", 0, a, x.device, s, *args, *_own(y), *_own(z))
+    return y, z
+
+
+def gm_linear_backward(x, w, grad, z, dx, dw, dbias, *, activation=None, stream=None):
+    a = _linear(x, w, activation)
+    shape = (a.n_rows, a.n_outs)
+    args = (*_matrix("grad", grad, x, shape), *_rows("z", z, x, shape), *_gradient("dx", dx, x), *_gradient("dw", dw, w),
+            _row("dbias", dbias, a.n_outs, x))
+    with _On(x.device, stream) as s:
+        _linear_run("gm_linear_backward", 1, a, x.device, s, *args)
+
+
+def linear_backward(x, w, grad, *, activation=None, z=None, need_x=True, need_w=True, need_bias=False, stream=None):
+    """(dx, dw, dbias) for the gradient by y; the residual's is that gradient itself. ``z``: linear_forward's, with an activation."""
+    a = _linear(x, w, activation)
+    shape = (a.n_rows, a.n_outs)
+    args = *_matrix("grad", grad, x, shape), *_rows("z", z, x, shape)
+    with _On(x.device, stream) as s:
+        dx, dw = _like(x, need_x), _like(w, need_w)
+        db = torch.empty(a.n_outs, dtype=x.dtype, device=x.device) if need_bias else None
+        if need_x or need_w or need_bias:
+            _linear_run("gm_linear_backward", 1, a, x.device, s, *args, *_own(dx), *_own(dw), None if db is None else db.data_ptr())
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation):
+        ctx.activation = activation
+        y, z = linear_forward(x, w, bias, activation=activation, residual=residual, keep=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(x, w, z)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, w, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = linear_backward(x, w, _dense(g), activation=ctx.activation, z=z, need_x=need[0], need_w=need[1],
+                                     need_bias=need[2])
+        return dx, dw, db, g if need[3] else None, None
+
+
+def linear(x, w, bias=None, *, activation=None, residual=None):
+    """residual + act(x w^T + bias), differentiable by every tensor given."""
+    return _Linear.apply(x, w, bias, residual, activation)
+
+
+def _dense(g):
+    """A gradient whose rows are consecutive elements (an expanded one is not)."""
+    return g if g is None or (g.dim() == 2 and g.stride(1) == 1 and g.stride(0) >= g.shape[1]) else g.contiguous()
 
 
 # ---- norms around a residual ------------------------------------------------------------------
@@ -152,11 +257,6 @@ def residual_norm_forward(x, f=None, *, norm="rms", after=None, after_bias=None,
     return Normed(x if x2 is None else x2, y, stats)
 
 
-def _own(t):
-    """A matrix that _like made, as arguments."""
-    return (None, 0) if t is None else (t.data_ptr() or None, t.shape[1])
-
-
 def gm_norm_backward(x, f, stats, grad_x, grad_y, grads: NormGrads, *, norm="rms", after=None, after_bias=None, gate=None,
                      scale=1.0, before=None, before_bias=None, eps=1e-6, stream=None):
     a = _norm(x, f, norm, after, after_bias, gate, scale, before, before_bias, eps)
@@ -218,11 +318,6 @@ class _ResidualNorm(torch.autograd.Function):
         d = residual_norm_backward(x, f, _dense(g_x), _dense(g_y), stats, after=after, after_bias=after_bias, gate=gate,
                                    before=before, before_bias=before_bias, need=need, **ctx.rule)
         return *(getattr(d, k) for k in names), None, None, None
-
-
-def _dense(g):
-    """A gradient whose rows are consecutive elements (an expanded one is not)."""
-    return g if g is None or (g.dim() == 2 and g.stride(1) == 1 and g.stride(0) >= g.shape[1]) else g.contiguous()
 
 
 def residual_norm(x, f=None, *, norm="rms", after=None, after_bias=None, gate=None, scale=1.0, before=None,

@@ -1,0 +1,247 @@
+"""The product with bias, activation and residual on the GPU, every element against 64 bits within derived bounds."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import layer_oracle
+from layer_oracle import EPS32, HALF, LEAST
+from sparse_gemm_irregular_gm_gb300 import layers
+from sparse_gemm_irregular_gm_gb300.binding import GmError
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+# Steepest slope of an activation and of a slope: |act'| <= 1.13, |act''| <= 0.8 (relu: none; it is taken at the kept z's sign).
+SLOPE, BEND = 1.13, 0.8
+# fp32 sums on the tensor cores are cut, not rounded, to 24 bits: a whole unit, not half, an addition; additions of a stage's
+# 64 elements go 16 at a time. An activation in short form is within 2^-21 of its argument's size.
+ACT_ROOM = 2.0 ** -21
+
+
+def wide_of(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def sum_room(length, size):
+    return 2.0 ** -23 * (length / 16 + 24) * size
+
+
+def check(got, ref, room, kind):
+    got = wide_of(got)
+    assert got.shape == ref.shape
+    room = room * (1 + HALF[kind]) + HALF[kind] * np.abs(ref) * 1.01 + LEAST[kind]
+    bad = ~(np.abs(got - ref) <= room)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3], got[bad][:4], ref[bad][:4], room[bad][:4])
+
+
+def make(rows, dim, outs, kind, *, bias=True, residual=True, wide=0, offset=0, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed + 3)
+
+    def matrix(n, m, std):
+        big = torch.full((n * (m + wide) + offset,), float("nan"), device="cuda", dtype=TYPES[kind])
+        v = big[offset:].view(n, m + wide)[:, :m]
+        v.copy_(torch.randn(n, m, generator=g, device="cuda") * std)
+        return v
+
+    b = torch.empty(outs + offset, device="cuda", dtype=TYPES[kind])
+    b.copy_(torch.randn(outs + offset, generator=g, device="cuda") * 0.5)
+    return (matrix(rows, dim, 1.0), matrix(outs, dim, 1 / math.sqrt(dim)), b[offset:] if bias else None,
+            matrix(rows, outs, 2.0) if residual else None, matrix(rows, outs, 0.25))
+
+
+def both(x, w, b, r, grad, act, kind, got=None):
+    if got is None:
+        y, z = layers.linear_forward(x, w, b, activation=act, residual=r, keep=True)
+        dx, dw, db = layers.linear_backward(x, w, grad, activation=act, z=z, need_bias=True)
+    else:
+        y, z, dx, dw, db = got
+    assert (z is None) == (act == "none") or got is not None
+    rows, dim = x.shape
+    X, W, B, R, G = (wide_of(t) for t in (x, w, b, r, grad))
+    z64, zs = X @ W.T, np.abs(X) @ np.abs(W).T
+    if B is not None:
+        z64, zs = z64 + B, zs + np.abs(B)
+    zroom = sum_room(dim, zs)
+    if z is not None:
+        check(z, z64, zroom, kind)
+    a, _ = layer_oracle.act(z64, act)
+    y64 = a if R is None else a + R
+    check(y, y64, SLOPE * zroom + ACT_ROOM * np.abs(z64) + 4 * EPS32 * (np.abs(y64) + (0 if R is None else np.abs(R))), kind)
+    # gradients: the slope at z as it was kept
+    kept = z64 if z is None else wide_of(z)
+    s = layer_oracle.act(kept, act)[1]
+    dz = G * s
+    short = 0 if kind == "f32" or (act != "none" and rows <= 128) or act == "none" else HALF[kind]  # dz's own rounding
+    dz_room = np.abs(G) * (2.0 ** -21 * (1 + np.abs(kept)) if act not in ("none", "relu") else 4 * EPS32) + short * np.abs(dz) + 2 * LEAST[kind]
+    if rows <= 128 and act != "none" and kind != "f32":
+        dz_room = dz_room + HALF[kind] ** 2 * np.abs(dz)
+    check(dx, dz @ W, dz_room @ np.abs(W) + sum_room(w.shape[0], np.abs(dz) @ np.abs(W)), kind)
+    check(dw, dz.T @ X, dz_room.T @ np.abs(X) + sum_room(rows, np.abs(dz).T @ np.abs(X)), kind)
+    check(db, dz.sum(0), (dz_room - short * np.abs(dz)).sum(0) + EPS32 * (rows / 8 + 600) * np.abs(dz).sum(0), kind)
+    return y, z, dx, dw, db
+
+
+SHAPES = [(1, 1, 1), (1, 64, 64), (3, 7, 5), (16, 256, 1000), (33, 40, 200), (128, 128, 128), (129, 65, 257), (333, 129, 517),
+          (256, 1024, 512), (130, 2080, 72), (1000, 96, 24), (520, 520, 520), (2050, 136, 264), (5, 5000, 48), (300, 8, 2000)]
+
+
+@pytest.mark.parametrize("rows,dim,outs", SHAPES)
+@pytest.mark.parametrize("kind", TYPES)
+def test_sizes(rows, dim, outs, kind):
+    act = ACTS[(rows + dim) % 5]
+    both(*make(rows, dim, outs, kind, seed=rows), act, kind)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("bias,residual", [(True, True), (False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("rows", [40, 200])
+def test_parts(act, kind, bias, residual, rows):
+    both(*make(rows, 136, 152, kind, bias=bias, residual=residual), act, kind)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("wide,offset", [(8, 0), (3, 0), (0, 1), (5, 2), (4, 4)])
+@pytest.mark.parametrize("rows,dim,outs", [(70, 72, 96), (150, 33, 47), (9, 1032, 200)])
+def test_strides(kind, wide, offset, rows, dim, outs):
+    both(*make(rows, dim, outs, kind, wide=wide, offset=offset), "gelu", kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("wide,offset", [(0, 0), (5, 0), (8, 8), (8, 1)])
+@pytest.mark.parametrize("rows,dim,outs", [(150, 200, 136), (20, 40, 33), (5, 6000, 64)])
+def test_results_into_the_callers_rows(kind, wide, offset, rows, dim, outs):
+    x, w, b, r, grad = make(rows, dim, outs, kind)
+
+    def room(n, m):
+        big = torch.full((n * (m + wide) + offset + 32,), 7.0, device="cuda", dtype=TYPES[kind])
+        return big, big[offset:offset + n * (m + wide)].view(n, m + wide)[:, :m]
+
+    (by, y), (bz, z), (bx, dx), (bw, dw) = room(rows, outs), room(rows, outs), room(rows, dim), room(outs, dim)
+    db = torch.empty(outs, device="cuda", dtype=TYPES[kind])
+    layers.gm_linear_forward(x, w, b, r, y, z, activation="silu")
+    layers.gm_linear_backward(x, w, grad, z, dx, dw, db, activation="silu")
+    both(x, w, b, r, grad, "silu", kind, (y, z, dx, dw, db))
+    for big, m in ((by, y), (bz, z), (bx, dx), (bw, dw)):  # nothing else was written
+        m.fill_(7.0)
+        assert (big == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,dim,outs", [(200, 64, 320), (4, 5000, 64)])
+def test_result_over_the_residual(rows, dim, outs):
+    x, w, b, r, _ = make(rows, dim, outs, "bf16")
+    y, _ = layers.linear_forward(x, w, b, activation="gelu", residual=r)
+    layers.gm_linear_forward(x, w, b, r, r, activation="gelu")
+    assert torch.equal(y, r)
+
+
+@pytest.mark.parametrize("rows", [100, 400])
+def test_one_gradient_at_a_time_and_runs_repeat(rows):
+    x, w, b, r, grad = make(rows, 300, 520, "bf16")
+    _, z = layers.linear_forward(x, w, b, activation="gelu", keep=True)
+    k = dict(activation="gelu", z=z)
+    whole = layers.linear_backward(x, w, grad, need_bias=True, **k)
+    again = layers.linear_backward(x, w, grad, need_bias=True, **k)
+    for i in range(3):
+        assert torch.equal(whole[i], again[i])
+        one = layers.linear_backward(x, w, grad, need_x=i == 0, need_w=i == 1, need_bias=i == 2, **k)
+        assert [t is not None for t in one] == [i == 0, i == 1, i == 2]
+        assert torch.equal(whole[i], one[i])
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+def test_far_and_special_arguments(kind, act):
+    """Where an activation's pieces would overflow, it has its limit; infinities and NaN stay in their rows and columns."""
+    big = 60000.0 if kind == "f16" else 1e30
+    x = torch.tensor([[1.0], [-1.0], [0.0], [1e-4]], device="cuda", dtype=TYPES[kind])
+    w = torch.tensor([[big], [30.0], [10.0], [1.0]], device="cuda", dtype=TYPES[kind])
+    y, z = layers.linear_forward(x, w, activation=act, keep=True)
+    ref, s = layer_oracle.act(wide_of(x) @ wide_of(w).T, act)
+    assert y.isfinite().all()
+    check(y, ref, 2.0 ** -20 * np.abs(wide_of(x) @ wide_of(w).T) * (np.abs(wide_of(x) @ wide_of(w).T) < 100), kind)
+    dx, _, db = layers.linear_backward(x, w, torch.ones_like(y), activation=act, z=z, need_bias=True)
+    assert db.isfinite().all()
+    x[1, 0] = float("nan")
+    x[3, 0] = float("inf")
+    y2, _ = layers.linear_forward(x, w, activation=act)
+    assert y2[1].isnan().all() and torch.equal(y2[[0, 2]], y[[0, 2]])
+    assert (y2[3] == float("inf")).all()
+
+
+def test_no_rows():
+    x, w, b, r, grad = make(0, 48, 72, "bf16")
+    y, _ = layers.linear_forward(x, w, b, residual=r)
+    assert y.shape == (0, 72)
+    dx, dw, db = layers.linear_backward(x, w, grad, need_bias=True)
+    assert dx.shape == (0, 48) and (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_autograd_against_differences(act):
+    x, w, b, r, grad = make(5, 9, 7, "f32", seed=1)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b, r)]
+    (layers.linear(*leaves[:3], activation=act, residual=leaves[3]) * grad).sum().backward()
+    base = [wide_of(t.detach()) for t in leaves]
+    G = wide_of(grad)
+
+    def total(x, w, b, r):
+        return ((layer_oracle.act(x @ w.T + b, act)[0] + r) * G).sum()
+
+    for k, t in enumerate(leaves):
+        slope = np.zeros(t.shape)
+        for i in np.ndindex(*t.shape):
+            up, down = ([v.copy() for v in base] for _ in range(2))
+            up[k][i] += 1e-6
+            down[k][i] -= 1e-6
+            slope[i] = (total(*up) - total(*down)) / 2e-6
+        assert np.allclose(wide_of(t.grad), slope, rtol=1e-4, atol=1e-5 * np.abs(slope).max()), k
+
+
+def test_autograd_asks_only_for_what_is_wanted():
+    x, w, b, r, _ = make(40, 24, 32, "bf16")
+    r.requires_grad_()
+    y = layers.linear(x, w, b, activation="relu", residual=r)
+    y.sum().backward()  # an expanded gradient
+    assert (r.grad == 1).all()
+    w.requires_grad_()
+    layers.linear(x, w).sum().backward()
+    assert torch.equal(w.grad, layers.linear_backward(x, w.detach(), torch.ones_like(y), need_x=False)[1])
+
+
+@pytest.mark.parametrize("rows,dim,outs", [(64, 512, 256), (3, 8192, 128), (300, 100, 60)])
+def test_other_stream_and_graph(rows, dim, outs):
+    x, w, b, r, grad = make(rows, dim, outs, "bf16")
+
+    def run(stream=None):
+        y, z = layers.linear_forward(x, w, b, activation="silu", residual=r, keep=True, stream=stream)
+        return [y, z, *layers.linear_backward(x, w, grad, activation="silu", z=z, need_bias=True, stream=stream)]
+
+    here = run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    there = run(s)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(here, there))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = run()
+    for t, u in zip((x, w, b, r, grad), make(rows, dim, outs, "bf16", seed=9)):
+        t.copy_(u)
+    g.replay()
+    assert all(torch.equal(p, q) for p, q in zip(held, run()))
+
+
+def test_refusals():
+    x, w, b, r, grad = make(4, 16, 24, "bf16")
+    for bad in (lambda: layers.linear_forward(x, w.float()), lambda: layers.linear_forward(x, w[:, :8]),
+                lambda: layers.linear_forward(x.t(), w), lambda: layers.linear_forward(x, w, b[:5]),
+                lambda: layers.linear_forward(x, w, residual=r[:2]), lambda: layers.linear_forward(x, w, activation="tanh"),
+                lambda: layers.linear_forward(x.cpu(), w), lambda: layers.linear_backward(x, w, grad[:, :4])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(GmError):
+        layers.linear_backward(x, w, grad, activation="gelu")  # without z

@@ -135,3 +135,48 @@ def test_oracle_of_the_norms_against_differences(norm, gate):
             down[name][i] -= 1e-6
             slope[i] = (total(up) - total(down)) / 2e-6
         assert np.allclose(slope, ref["d" + name][0], rtol=1e-5, atol=1e-7), name
+
+
+def linear(**k):
+    a = dict(n_rows=4, dim=8, n_outs=6, x=P, x_ld=8, w=P, w_ld=8, type=1, activation=2)
+    a.update(k)
+    return layers.gm_linear(*a.values())
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"n_rows": -1}, INVALID), ({"dim": 0}, INVALID), ({"n_outs": 0}, INVALID), ({"type": 3}, INVALID), ({"activation": 5}, INVALID),
+    ({"activation": -1}, INVALID), ({"x": None}, INVALID), ({"w": None}, INVALID), ({"x": P + 1}, INVALID), ({"w": P + 1}, INVALID),
+    ({"x_ld": 7}, INVALID), ({"w_ld": 7}, INVALID), ({"type": 0, "w": P + 2}, INVALID), ({"n_rows": 1 << 31}, OVERFLOW),
+    ({"dim": 1 << 25, "x_ld": 1 << 25, "w_ld": 1 << 25}, OVERFLOW), ({"n_outs": 1 << 25}, OVERFLOW), ({"x_ld": 1 << 40}, OVERFLOW)])
+def test_bad_products(lib, change, status):
+    p = linear(**change)
+    assert lib.gm_linear_forward(p, None, None, P, P, 1 << 26, P, 1 << 26, None, 0) == status
+    assert lib.gm_linear_backward(p, None, None, P, 1 << 26, P, 1 << 26, P, 1 << 26, P, 1 << 26, P) == status
+    assert lib.gm_linear_workspace(p, 0, ctypes.c_int64()) == status
+
+
+def test_bad_product_arrays(lib):
+    f = lambda bias=P, r=P, r_ld=6, y=P + 4096, y_ld=6, z=None, z_ld=0, cfg=None: lib.gm_linear_forward(  # noqa: E731
+        linear(), cfg, None, bias, r, r_ld, y, y_ld, z, z_ld)
+    for bad in (dict(bias=P + 1), dict(r=P + 1), dict(r_ld=5), dict(y=None), dict(y=P + 1), dict(y_ld=5), dict(z=P + 1, z_ld=6),
+                dict(z=P, z_ld=5), dict(y=P, y_ld=7), dict(cfg=layers.gm_layer_config(P + 128, 1 << 20)), dict(cfg=layers.gm_layer_config(P, -1))):
+        assert f(**bad) == INVALID, bad
+    assert f(y_ld=1 << 40) == OVERFLOW
+    b = lambda g=P, g_ld=6, z=P, z_ld=6, dx=P, dx_ld=8, dw=P, dw_ld=8, db=P: lib.gm_linear_backward(  # noqa: E731
+        linear(), None, None, g, g_ld, z, z_ld, dx, dx_ld, dw, dw_ld, db)
+    for bad in (dict(g=None), dict(g=P + 1), dict(g_ld=5), dict(z=None), dict(z_ld=5), dict(dx=P + 1), dict(dx_ld=7), dict(dw_ld=7),
+                dict(db=P + 1), dict(dx=None, dw=None, db=None)):
+        assert b(**bad) == INVALID, bad
+    assert lib.gm_linear_workspace(linear(), 2, ctypes.c_int64()) == INVALID
+    assert lib.gm_linear_workspace(linear(), 0, None) == INVALID
+    need = ctypes.c_int64(7)
+    assert lib.gm_linear_workspace(linear(n_rows=0, x=None), 1, need) == OK and need.value == 0
+    assert lib.gm_linear_forward(linear(n_rows=0, x=None), None, None, None, None, 0, None, 6, None, 0) == OK
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_oracle_of_the_activations_against_differences(act):
+    z = np.linspace(-6, 6, 481) + 0.003
+    a, s = layer_oracle.act(z, act)
+    up, down = layer_oracle.act(z + 1e-6, act)[0], layer_oracle.act(z - 1e-6, act)[0]
+    assert np.allclose((up - down) / 2e-6, s, atol=1e-8)
