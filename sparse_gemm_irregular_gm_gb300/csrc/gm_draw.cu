@@ -1,13 +1,16 @@
 // gm_draw.cu -- a class drawn from each row of logits (include/gm_sampling.h).
 //
 // A row is read from memory once, into the shared memory of a block or of a cluster of blocks, and
-// everything else works there: its maximum; for top-k and top-p a border found digit by digit (below),
-// never a sort; the kept weights' sum; the class at which u is passed. Nothing is written but the results.
+// everything else works there: its maximum; for top-k and top-p a border found by histograms, never a
+// sort; the kept weights' sum; the class at which u is passed. Nothing is written but the results.
 //
 // Borders. Classes are compared by D, the distance of their ordered bits from the row's largest: 16 bits, or 32 of
-// f32. A histogram of D's upper 11 bits (counts for top-k, sums of weights for top-p) shows the digit in
-// which the border lies, one of the next 11 bits within that digit its next, until D is
-// known; of the classes that have just that D the first so many are kept, in class order.
+// f32. A border is a D and how many of the classes that have just that D are kept, in class order.
+//   Long rows of 16 bits (KEYS): how often each of the 65536 values occurs is counted while the row is read, 128 KB of
+//   16-bit counts. Counts, and sums of counts times weights, of 1024 lines of 64 values then lead to the border: a weight is
+//   computed for each value that occurs, not for each class, and looked up when classes are summed.
+//   Others: a histogram of D's upper 11 bits shows the digit in which the border lies, one of the next
+//   11 bits within that digit its next, until D is known.
 //
 // Weights are integers: w = 2^(t), t = (z - max) log2(e) / T <= 0, as a multiple of 2^-B with B such that all of a row
 // add up in 64 bits. So sums are exact, in any order, and every pass sees the same ones.
@@ -28,7 +31,8 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kBins = 2048;
+constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) - kLog2e
+
 constexpr int kMostCluster = 8;
 constexpr int kPer = 8;  // classes a thread takes at a time: 16 bytes of a 16-bit type
 constexpr int kTable = 33;
@@ -47,43 +51,68 @@ struct DrawArgs {
 };
 
 // ---- ordered bits of a logit ----------------------------------------------------------------------
-// Larger logits have larger keys; -0 has 0's, a NaN of either sign the largest of all.
+// A logit's place: 16 bits, or 32 of f32, that grow as logits fall. The bits of positive ones are turned over, of negative
+// ones less 1, which brings -0 to 0's place and leaves the others apart. NaN lies before inf's place or after -inf's. Two
+// 16-bit ones at a time.
+__device__ __forceinline__ uint32_t place_pair(uint32_t w) {
+  const uint32_t m = (w >> 15) & 0x00010001u;
+  return (w ^ ((0x00010001u - m) * 0x7fffu)) - m;
+}
 template <int TYPE>
-__device__ __forceinline__ uint32_t key_of(uint32_t bits) {
+__device__ __forceinline__ uint32_t place_of(uint32_t bits) {
   if constexpr (TYPE == GM_LOSS_F32) {
-    const uint32_t size = bits & 0x7fffffffu;
-    if (size > 0x7f800000u) return 0xffffffffu;
-    if (size == 0) return 0x80000000u;
-    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+    const uint32_t m = bits >> 31;
+    return (bits ^ ((1u - m) * 0x7fffffffu)) - m;
   } else {
-    constexpr uint32_t inf = TYPE == GM_LOSS_BF16 ? 0x7f80u : 0x7c00u;
-    const uint32_t size = bits & 0x7fffu;
-    if (size > inf) return 0xffffu;
-    if (size == 0) return 0x8000u;
-    return bits & 0x8000u ? 0xffffu - bits : bits | 0x8000u;
+    return place_pair(bits) & 0xffffu;
   }
 }
 template <int TYPE>
-constexpr uint32_t kInfKey = TYPE == GM_LOSS_F32 ? 0xff800000u : TYPE == GM_LOSS_BF16 ? 0xff80u : 0xfc00u;
+constexpr uint32_t kInfBits = TYPE == GM_LOSS_F32 ? 0x7f800000u : TYPE == GM_LOSS_BF16 ? 0x7f80u : 0x7c00u;
 template <int TYPE>
-constexpr uint32_t kNoneKey = TYPE == GM_LOSS_F32 ? 0x007fffffu : TYPE == GM_LOSS_BF16 ? 0x007fu : 0x03ffu;  // -inf's
+constexpr uint32_t kZero = TYPE == GM_LOSS_F32 ? 0x7fffffffu : 0x7fffu;  // 0's place
 template <int TYPE>
-__device__ __forceinline__ float value_of(uint32_t key) {
-  if constexpr (TYPE == GM_LOSS_F32) {
-    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-  } else {
-    const uint32_t b = key & 0x8000u ? key & 0x7fffu : 0xffffu - key;
-    if constexpr (TYPE == GM_LOSS_BF16) return __uint_as_float(b << 16);
-    else return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-  }
+constexpr uint32_t kInfPlace = kZero<TYPE> - kInfBits<TYPE>;
+template <int TYPE>
+constexpr uint32_t kNonePlace = kZero<TYPE> + kInfBits<TYPE>;  // -inf's
+template <int TYPE>
+__device__ __forceinline__ float value_of(uint32_t place) {
+  const uint32_t size = place <= kZero<TYPE> ? kZero<TYPE> - place : place - kZero<TYPE>;
+  const float x = TYPE == GM_LOSS_F32    ? __uint_as_float(size)
+                  : TYPE == GM_LOSS_BF16 ? __uint_as_float(size << 16)
+                                         : __half2float(__ushort_as_half(static_cast<unsigned short>(size)));
+  return place <= kZero<TYPE> ? x : -x;
 }
-// Key of the smallest logit that is at least x.
+// Place of the smallest logit that is at least x + y + y_low.
 template <int TYPE>
-__device__ __forceinline__ uint32_t key_from(double x) {
-  const float f = __double2float_ru(x);
-  if constexpr (TYPE == GM_LOSS_F32) return key_of<TYPE>(__float_as_uint(f));
-  else if constexpr (TYPE == GM_LOSS_BF16) return key_of<TYPE>(__bfloat16_as_ushort(__float2bfloat16_ru(f)));
-  else return key_of<TYPE>(__half_as_ushort(__float2half_ru(f)));
+__device__ __forceinline__ uint32_t place_from(float x, float y, float y_low) {
+  float f = x + y;
+  const float b = f - x;
+  const float rest = (x - (f - b)) + (y - b) + y_low;  // what the sum's rounding took
+  if (rest > 0.f) f = nextafterf(f, INFINITY);
+  if constexpr (TYPE == GM_LOSS_F32) return place_of<TYPE>(__float_as_uint(f));
+  else if constexpr (TYPE == GM_LOSS_BF16) return place_of<TYPE>(__bfloat16_as_ushort(__float2bfloat16_ru(f)));
+  else return place_of<TYPE>(__half_as_ushort(__float2half_ru(f)));
+}
+
+// The whole part of f * n for f in [0, 1], and whether something is left: in integers, since 64-bit floating point is
+// 1 / 70 as fast as 32-bit here (all threads of a block dividing by T so took 5 us).
+__device__ __forceinline__ u64 whole_times(float f, u64 n, bool& left) {
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits;
+  const int s = e ? 150 - static_cast<int>(e) : 149;  // f = m 2^-s, 23 <= s
+  const u64 lo = m * n, hi = __umul64hi(m, n);
+  if (s >= 128) {
+    left = (lo | hi) != 0;
+    return 0;
+  }
+  if (s >= 64) {
+    const u64 w = hi >> (s - 64);
+    left = lo != 0 || (w << (s - 64)) != hi;
+    return w;
+  }
+  left = (lo & ((u64(1) << s) - 1)) != 0;
+  return (hi << (64 - s)) | (lo >> s);
 }
 
 // ---- weights ---------------------------------------------------------------------------------------
@@ -91,13 +120,21 @@ __device__ __forceinline__ uint32_t key_from(double x) {
 // own. Its fraction f in [-1/2, 1/2], in units of 2^-31, is split into the nearest 32nd, whose power is in a table of
 // 31-bit integers, and a rest g with |g| <= 1/64, whose 2^g - 1 = g ln 2 + (g ln 2)^2 / 2 + ... is at
 // most 0.011, so that fp32 gives it to 2^-31. About 30 instructions; exact at t = 0.
+// 2^(31 + (j - 16) / 32), rounded
+__constant__ uint32_t kPowers[kTable] = {
+    1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u,
+    1729250827u, 1767116489u, 1805811301u, 1845353420u, 1885761398u, 1927054196u,
+    1969251188u, 2012372174u, 2056437387u, 2101467502u, 2147483648u, 2194507417u,
+    2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
+    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u,
+    2908241642u, 2971923842u, 3037000500u};
 struct Weigher {
   float top, c, c_low;
-  uint32_t top_key;
+  uint32_t top_place;
   int bits;
   const uint32_t* table;
-  __device__ __forceinline__ u64 operator()(uint32_t key, float z) const {
-    if (key == top_key) return u64(1) << bits;
+  __device__ __forceinline__ u64 operator()(uint32_t place, float z) const {
+    if (place == top_place) return u64(1) << bits;
     const float d = z - top;
     const float t = __fmul_rn(d, c);  // a product of its own: its error is taken from it below
     if (!(t > -static_cast<float>(bits) - 2.f)) return 0;
@@ -120,20 +157,39 @@ struct Weigher {
 };
 
 // ---- sums over the block and the cluster --------------------------------------------------------------
+constexpr int kGroups = 64;                          // of bins, or of lines: the first step of a search
+constexpr int kBins = 2048, kGroupBins = kBins / kGroups;
+constexpr int kLine = 64, kLines = 65536 / kLine, kGroupLines = kLines / kGroups;
+constexpr int kWeights = 16384;                      // KEYS: weights that take the counts' place
+constexpr int kCountBytes = 65536 * 2;               // KEYS: counts of all values, in front of the held part
+
 struct Share {  // what a block tells the others of its part
   u64 sum;      // weights of the classes above the border
   uint32_t ties, above;
 };
+// Classes kept: those with D < d, and of those with D = d the first `ties`.
+struct Border {
+  uint32_t d;
+  int64_t ties;
+  __device__ __forceinline__ bool all() const { return ties == INT64_MAX; }
+};
+template <bool KEYS>
 struct Shared {
   uint32_t table[kTable + 1];
   Share told[kMostCluster];
-  u64 told_top[kMostCluster];
-  u64 warp_sum[33];
-  uint32_t warp_top[33], warp_ties[33], warp_above[33];
-  uint32_t low[kBins], high[kBins];  // counts, or the two words of sums
-  u64 before;                        // what lies above the digit found
-  uint32_t digit;
-  u64 in_digit;
+  u64 told_ends[kMostCluster];
+  float least_log, least_log_low;  // T log(min_p)
+  double log_total;
+  Border border;
+  uint32_t digit;                  // !KEYS: D's digits found so far
+  bool found;
+  u64 before, goal;
+  u64 warp_sum[32];
+  uint32_t warp_top[32], warp_last[32], warp_ties[32], warp_above[32];
+  u64 coarse[kMostCluster][kGroups];
+  // !KEYS: counts, or the two words of sums; KEYS: sums of the lines
+  uint32_t low[KEYS ? 1 : kBins], high[KEYS ? 1 : kBins];
+  u64 line[KEYS ? kLines : 1];
 };
 
 __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
@@ -141,191 +197,318 @@ __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_addr(p), rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ u64 remote_u64(const void* p, uint32_t rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_addr(p), rank)) : "memory");
+  return v;
+}
 __device__ __forceinline__ void put_remote_u64(void* p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(map_to_rank(smem_addr(p), rank)), "l"(v) : "memory");
 }
+// f(rank) for every block of the row, all under way before the first is used; their sum.
+template <class F>
+__device__ __forceinline__ u64 from_each(int blocks, F&& f) {
+  decltype(f(0)) v[kMostCluster];
+#pragma unroll
+  for (int r = 0; r < kMostCluster; ++r) v[r] = r < blocks ? f(r) : 0;
+  u64 sum = 0;
+#pragma unroll
+  for (int r = 0; r < kMostCluster; ++r) sum += v[r];
+  return sum;
+}
 
-template <int TYPE>
+// A warp's way to the place at which a sum reaches the goal: the sum before what was found so far, the sum of all.
+struct Search {
+  u64 before, total, goal;
+  // the first lane at which `before` and the sum of v up to and with it reach the goal (the last, where there is none)
+  __device__ __forceinline__ uint32_t step(u64 v) {
+    const u64 to = warp_inclusive_scan(v);
+    const unsigned at = __ballot_sync(kFull, before + to >= goal);
+    const int l = at ? __ffs(at) - 1 : 31;
+    before += __shfl_sync(kFull, to - v, l);
+    return l;
+  }
+  // the same of two values a lane
+  __device__ __forceinline__ uint32_t step2(u64 a, u64 b) {
+    const uint32_t l = step(a + b);
+    const u64 first = __shfl_sync(kFull, a, l);
+    if (before + first >= goal) return 2 * l;
+    before += first;
+    return 2 * l + 1;
+  }
+};
+
+template <int TYPE, bool KEYS>
 struct Row {
-  Shared& sh;
+  static constexpr int kWords = TYPE == GM_LOSS_F32 ? 8 : 4;  // of a piece
+  Shared<KEYS>& sh;
   const DrawArgs& a;
+  uint32_t* counts;       // KEYS: of the values at each place, two a word
   int blocks, rank;       // of the cluster
-  const void* data;       // of this block's part: class c at element c + phase
-  int n, phase;           // classes of the part, their first one's place within 16 bytes
+  const void* data;       // of this block's part, from piece 0 on: places where they are held, else logits
+  int n, phase;           // classes of the part, their first one's element in piece 0
   __device__ __forceinline__ void meet() const {
     if (blocks > 1) cluster_sync_all();
     else __syncthreads();
   }
   __device__ __forceinline__ int pieces() const { return (phase + n + kPer - 1) / kPer; }
-  // Keys of a piece; outside the part: none's.
-  __device__ __forceinline__ void keys(int piece, uint32_t (&k)[kPer]) const {
-    const int c0 = piece * kPer - phase;
-    uint32_t w[8];
-    if (a.held || (c0 >= 0 && c0 + kPer <= n)) {
-      const uint4* p = static_cast<const uint4*>(data);
-      if constexpr (TYPE == GM_LOSS_F32) {
-        const uint4 x = p[2 * piece], y = p[2 * piece + 1];
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-      } else {
-        const uint4 x = p[piece];
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  // Places of a piece; outside the part: none's.
+  __device__ __forceinline__ void places(int piece, uint32_t (&q)[kPer]) const {
+    uint32_t w[kWords];
+    if (a.held) {
+#pragma unroll
+      for (int h = 0; h < kWords / 4; ++h) {
+        const uint4 x = static_cast<const uint4*>(data)[piece * (kWords / 4) + h];
+        w[4 * h] = x.x, w[4 * h + 1] = x.y, w[4 * h + 2] = x.z, w[4 * h + 3] = x.w;
       }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        k[i] = key_of<TYPE>(TYPE == GM_LOSS_F32 ? w[i] : i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
     } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) k[i] = c0 + i >= 0 && c0 + i < n ? key_of<TYPE>(element(c0 + i)) : kNoneKey<TYPE>;
+      read(data, piece, w);
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) q[i] = TYPE == GM_LOSS_F32 ? w[i % kWords] : i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
   }
-  __device__ __forceinline__ uint32_t element(int c) const {  // of the part, in memory or held
-    if constexpr (TYPE == GM_LOSS_F32) return static_cast<const uint32_t*>(data)[phase + c];
-    else return static_cast<const uint16_t*>(data)[phase + c];
+  // A piece of the row in memory, as places: 16 bytes at a time, the ends by elements. base: of piece 0.
+  __device__ __forceinline__ void read(const void* base, int piece, uint32_t (&w)[kWords]) const {
+    const int c0 = piece * kPer - phase;
+    if (c0 >= 0 && c0 + kPer <= n) {
+#pragma unroll
+      for (int h = 0; h < kWords / 4; ++h) {
+        const uint4 x = static_cast<const uint4*>(base)[piece * (kWords / 4) + h];
+        w[4 * h] = x.x, w[4 * h + 1] = x.y, w[4 * h + 2] = x.z, w[4 * h + 3] = x.w;
+      }
+    } else {
+      constexpr uint32_t none = kZero<TYPE> + 1 + kInfBits<TYPE>;  // -inf's bits
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const bool in = c0 + i >= 0 && c0 + i < n;
+        const int at = piece * kPer + i;
+        if constexpr (TYPE == GM_LOSS_F32) w[i] = in ? static_cast<const uint32_t*>(base)[at] : none;
+        else w[i / 2] |= (in ? static_cast<const uint16_t*>(base)[at] : none) << (i & 1 ? 16 : 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = TYPE == GM_LOSS_F32 ? place_of<TYPE>(w[i]) : place_pair(w[i]);
   }
-  // f(key) for every class, in any order
+  // f(place) for every class, in any order
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
     for (int p = threadIdx.x; p < pieces(); p += blockDim.x) {
-      uint32_t k[kPer];
-      keys(p, k);
+      uint32_t q[kPer];
+      places(p, q);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) f(k[i]);
+      for (int i = 0; i < kPer; ++i) f(q[i]);
     }
   }
+  __device__ __forceinline__ uint32_t count_at(uint32_t place) const {
+    return reinterpret_cast<const uint16_t*>(counts)[place];
+  }
 
-  // One digit of a border. The histogram has been filled; target(total) is what the border's sum is to reach. Finds the
-  // first digit at which the sum from digit 0 on, and `before` it, is at least the target.
-  template <bool MASS, class T>
-  __device__ __forceinline__ void find(u64 before, T&& target) const {
-    meet();  // histograms are complete
-    const int per = kBins / blockDim.x;  // blockDim.x: 128 .. 1024
-    const int b0 = threadIdx.x * per;
-    u64 mine = 0;
-    auto bin = [&](int b) {
-      u64 x = 0;
-      for (int r = 0; r < blocks; ++r) {
-        if (blocks > 1) x += MASS ? u64(remote_u32(&sh.low[b], r)) + (u64(remote_u32(&sh.high[b], r)) << 32) : remote_u32(&sh.low[b], r);
-        else x += MASS ? u64(sh.low[b]) + (u64(sh.high[b]) << 32) : sh.low[b];
-      }
-      return x;
-    };
-    for (int i = 0; i < per; ++i) mine += bin(b0 + i);
-    u64 total;
-    u64 at = before + block_exclusive_scan(mine, sh.warp_sum, &total);
-    const double goal = target(before + total);
-    const bool last = threadIdx.x == blockDim.x - 1;
-    // a thread's bins hold the border when the sum before them falls short of it and the sum with them does not; the last
-    // one's do where rounding leaves no other
-    if (static_cast<double>(at) < goal && (static_cast<double>(at + mine) >= goal || last)) {
-      for (int i = 0; i < per; ++i) {
-        const u64 x = bin(b0 + i);
-        if (static_cast<double>(at + x) >= goal || (i == per - 1)) {
-          sh.digit = b0 + i;
-          sh.before = at;
-          sh.in_digit = x;
-          break;
-        }
-        at += x;
-      }
+  // A group's sum goes to every block; t: lane or thread, one for each block.
+  __device__ __forceinline__ void tell(int g, u64 sum, int t) const {
+    if (t >= blocks) return;
+    if (blocks > 1) put_remote_u64(&sh.coarse[rank][g], t, sum);
+    else sh.coarse[0][g] = sum;
+  }
+  // One warp: the group in which the goal is reached. goal_of: from the sum of all.
+  template <class G>
+  __device__ __forceinline__ uint32_t group(Search& s, G&& goal_of) const {
+    const int lane = threadIdx.x & 31;
+    const u64 x = from_each(blocks, [&](int r) { return sh.coarse[r][2 * lane]; });
+    const u64 y = from_each(blocks, [&](int r) { return sh.coarse[r][2 * lane + 1]; });
+    s.total = s.before + warp_reduce_sum(x + y);
+    s.goal = goal_of(s.total);
+    return s.step2(x, y);
+  }
+
+  // !KEYS: a digit of the border, from the histogram that the block's threads have filled. One warp calls
+  // then(search, digit), whose results all threads may read afterwards.
+  template <bool MASS, class G, class F>
+  __device__ __forceinline__ void digit(u64 before, G&& goal_of, F&& then) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    __syncthreads();
+    for (int g = warp; g < kGroups; g += warps) {
+      const int b = g * kGroupBins + lane;
+      tell(g, warp_reduce_sum(MASS ? u64(sh.low[b]) + (u64(sh.high[b]) << 32) : u64(sh.low[b])), lane);
     }
-    meet();  // found, and the histograms are read
+    meet();
+    if (warp == 0) {
+      Search s{before, 0, 0};
+      const uint32_t g = group(s, goal_of), b = g * kGroupBins + lane;
+      const u64 x = from_each(blocks, [&](int r) {
+        if (blocks == 1) return MASS ? u64(sh.low[b]) + (u64(sh.high[b]) << 32) : u64(sh.low[b]);
+        return MASS ? u64(remote_u32(&sh.low[b], r)) + (u64(remote_u32(&sh.high[b], r)) << 32) : u64(remote_u32(&sh.low[b], r));
+      });
+      const uint32_t d = g * kGroupBins + s.step(x);
+      then(s, d);
+    }
+    meet();  // histograms and sums are read
   }
   __device__ __forceinline__ void clear() const {
     for (int i = threadIdx.x; i < kBins; i += blockDim.x) sh.low[i] = sh.high[i] = 0;
     __syncthreads();
   }
+
+  // KEYS: the border's D, from the counts of values from place `top` to last_d further on. value(D, count): what so many
+  // classes of it add; COUNTS: their number. One warp calls then(search, D).
+  template <bool COUNTS, class V, class G, class F>
+  __device__ __forceinline__ void border_of(uint32_t top, uint32_t last_d, V&& value, G&& goal_of, F&& then) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int line0 = static_cast<int>(top / kLine), line1 = static_cast<int>(min(top + last_d, 0xffffu) / kLine);
+    auto of_line = [&](uint32_t line, uint32_t even, uint32_t odd, u64& x, u64& y) {
+      const uint32_t d = line * kLine + 2 * lane - top;  // wraps for values above the largest, whose counts are 0
+      x = even ? value(d, even) : 0, y = odd ? value(d + 1, odd) : 0;
+    };
+    // four lines at a time: eight lanes read one
+    for (int l = 4 * warp; l < kLines; l += 4 * warps) {
+      const uint4 c = reinterpret_cast<const uint4*>(counts)[l * 8 + lane];
+      if constexpr (COUNTS) {
+        uint32_t n_ = 0;
+#pragma unroll
+        for (const uint32_t w : {c.x, c.y, c.z, c.w}) n_ += (w & 0xffffu) + (w >> 16);
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) n_ += __shfl_xor_sync(kFull, n_, d);
+        if ((lane & 7) == 0) sh.line[l + lane / 8] = n_;
+      } else {
+        const unsigned some = __ballot_sync(kFull, (c.x | c.y | c.z | c.w) != 0);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          u64 sum = 0;
+          if ((some >> (8 * i) & 0xffu) && l + i >= line0 && l + i <= line1) {
+            const uint32_t word = counts[(l + i) * 32 + lane];
+            u64 x, y;
+            of_line(l + i, word & 0xffffu, word >> 16, x, y);
+            sum = warp_reduce_sum(x + y);
+          }
+          if (lane == 0) sh.line[l + i] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < kGroups) {
+      u64 sum = 0;
+#pragma unroll
+      for (int i = 0; i < kGroupLines; ++i) sum += sh.line[threadIdx.x * kGroupLines + i];
+      for (int r = 0; r < blocks; ++r) tell(threadIdx.x, sum, r);
+    }
+    meet();
+    if (warp == 0) {
+      Search s{0, 0, 0};
+      const uint32_t g = group(s, goal_of);
+      const u64 x = from_each(blocks, [&](int r) {
+        if (lane >= kGroupLines) return u64(0);
+        return blocks == 1 ? sh.line[g * kGroupLines + lane] : remote_u64(&sh.line[g * kGroupLines + lane], r);
+      });
+      const uint32_t line = g * kGroupLines + s.step(x);
+      const u64 both = from_each(blocks, [&](int r) {
+        const uint32_t w = blocks == 1 ? counts[line * 32 + lane] : remote_u32(&counts[line * 32 + lane], r);
+        return u64(w & 0xffffu) | (u64(w >> 16) << 32);
+      });
+      u64 even, odd;
+      of_line(line, static_cast<uint32_t>(both), static_cast<uint32_t>(both >> 32), even, odd);
+      then(s, line * kLine + s.step2(even, odd) - top);
+    }
+    meet();  // lines and sums are read
+  }
 };
 
-// Classes kept: those with D < d, and of those with D = d the first `ties`.
-struct Border {
-  uint32_t d;
-  int64_t ties;
-};
-
-template <int TYPE>
+template <int TYPE, bool KEYS>
 __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs a) {
-  extern __shared__ __align__(16) unsigned char part_mem[];
-  __shared__ Shared sh;
-  constexpr int kBytes = TYPE == GM_LOSS_F32 ? 4 : 2;
+  extern __shared__ __align__(16) unsigned char dynamic_mem[];
+  __shared__ Shared<KEYS> sh;
+  using R = Row<TYPE, KEYS>;
+  constexpr int kBytes = TYPE == GM_LOSS_F32 ? 4 : 2, kWords = R::kWords;
   constexpr int kDigits = TYPE == GM_LOSS_F32 ? 3 : 2;
+  uint32_t* counts = reinterpret_cast<uint32_t*>(dynamic_mem);
+  unsigned char* part_mem = dynamic_mem + (KEYS ? kCountBytes : 0);
   uint32_t blocks;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(blocks));
   const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
   const int64_t row_i = blockIdx.x / blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if (threadIdx.x < kTable)
-    sh.table[threadIdx.x] = static_cast<uint32_t>(__double2ll_rn(2147483648.0 * exp2((static_cast<int>(threadIdx.x) - 16) * 0.03125)));
+  if (threadIdx.x < kTable) sh.table[threadIdx.x] = kPowers[threadIdx.x];
+  if constexpr (KEYS) {
+    for (int i = threadIdx.x; i < kCountBytes / 16; i += blockDim.x) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  } else {
+    for (int i = threadIdx.x; i < kBins; i += blockDim.x) sh.low[i] = sh.high[i] = 0;
+  }
   chain_wait();
 
-  // ---- the part of the row, and its largest key
-  const int first = static_cast<int>(min(int64_t(rank) * a.part, int64_t(a.n_classes)));
-  const int n = min(a.part, a.n_classes - first);
-  const char* src = static_cast<const char*>(a.z) + (row_i * a.ld + first) * kBytes;
-  const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(src) % (kPer * kBytes) / kBytes);
-  Row<TYPE> row{sh, a, static_cast<int>(blocks), static_cast<int>(rank), a.held ? static_cast<const void*>(part_mem) : src - phase * kBytes, n, phase};
-  uint32_t top = 0;
-  if (a.held) {
-    // whole pieces as they lie; the ends by elements, and none's logit around them
-    const char* base = src - phase * kBytes;
-    for (int p = threadIdx.x; p < row.pieces(); p += blockDim.x) {
-      const int c0 = p * kPer - phase;
-      uint4 x[kBytes / 2];
-      if (c0 >= 0 && c0 + kPer <= n) {
-#pragma unroll
-        for (int h = 0; h < kBytes / 2; ++h) x[h] = __ldcs(reinterpret_cast<const uint4*>(base) + p * (kBytes / 2) + h);
-      } else {
-        uint32_t w[2 * kBytes];
-#pragma unroll
-        for (int i = 0; i < 2 * kBytes; ++i) w[i] = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const bool in = c0 + i >= 0 && c0 + i < n;
-          if constexpr (TYPE == GM_LOSS_F32) {
-            w[i] = in ? reinterpret_cast<const uint32_t*>(src)[c0 + i] : 0xff800000u;
-          } else {
-            const uint32_t v = in ? reinterpret_cast<const uint16_t*>(src)[c0 + i] : TYPE == GM_LOSS_BF16 ? 0xff80u : 0xfc00u;
-            w[i / 2] |= v << (i & 1 ? 16 : 0);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < kBytes / 2; ++h) x[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-      }
-#pragma unroll
-      for (int h = 0; h < kBytes / 2; ++h) {
-        reinterpret_cast<uint4*>(part_mem)[p * (kBytes / 2) + h] = x[h];
-        const uint32_t w[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (TYPE == GM_LOSS_F32) top = max(top, key_of<TYPE>(w[i]));
-          else top = max(top, max(key_of<TYPE>(w[i] & 0xffffu), key_of<TYPE>(w[i] >> 16)));
-        }
-      }
-    }
-  } else {
-    row.each([&](uint32_t k) { top = max(top, k); });
-  }
-  for (int i = threadIdx.x; i < kBins; i += blockDim.x) sh.low[i] = sh.high[i] = 0;
-  top = __reduce_max_sync(kFull, top);
-  if (lane == 0) sh.warp_top[warp] = top;
-  __syncthreads();
-  top = sh.warp_top[lane < warps ? lane : 0];
-  top = __reduce_max_sync(kFull, top);
-  if (blocks > 1) {
-    if (threadIdx.x < blocks) put_remote_u64(&sh.told_top[rank], threadIdx.x, top);
-    cluster_sync_all();
-    for (int r = 0; r < blocks; ++r) top = max(top, static_cast<uint32_t>(sh.told_top[r]));
-  }
-
-  // ---- the row's rule
+  // the row's rule; T log(min_p), in 64 bits, is one thread's work while the row is on its way
   const float temp = a.rule.temperature ? a.rule.temperature[row_i] : a.rule.all_temperature;
   const float top_p = a.rule.top_p ? a.rule.top_p[row_i] : a.rule.all_top_p;
   const float min_p = a.rule.min_p ? a.rule.min_p[row_i] : a.rule.all_min_p;
   int64_t top_k = a.rule.top_k ? a.rule.top_k[row_i] : a.rule.all_top_k;
   const float u = a.u[row_i];
-  const double c = temp > 0.f ? 1.4426950408889634 / static_cast<double>(temp) : 0.0;
-  const float c_high = static_cast<float>(c);
-  const bool fine = top > kNoneKey<TYPE> && top <= kInfKey<TYPE> && u >= 0.f && u < 1.f && temp >= 0.f && temp < INFINITY &&
-                    c_high < INFINITY && top_k >= 0 && top_p >= 0.f && top_p <= 1.f && min_p >= 0.f && min_p <= 1.f;
+
+  // ---- the part of the row, and the places of its largest and smallest
+  const int first = static_cast<int>(min(int64_t(rank) * a.part, int64_t(a.n_classes)));
+  const int n = min(a.part, a.n_classes - first);
+  const char* src = static_cast<const char*>(a.z) + (row_i * a.ld + first) * kBytes;
+  const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(src) % (kPer * kBytes) / kBytes);
+  src -= phase * kBytes;  // piece 0
+  const R row{sh, a, counts, static_cast<int>(blocks), static_cast<int>(rank), a.held ? static_cast<const void*>(part_mem) : src, n, phase};
+  const int pieces = row.pieces();
+  uint32_t top = 0xffffffffu, last = 0;
+  constexpr int kAhead = TYPE == GM_LOSS_F32 ? 2 : 4;  // pieces of a thread under way
+  for (int p0 = threadIdx.x; p0 < pieces; p0 += kAhead * blockDim.x) {
+    uint32_t w[kAhead][kWords];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (p0 + j * static_cast<int>(blockDim.x) < pieces) row.read(src, p0 + j * blockDim.x, w[j]);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int p = p0 + j * blockDim.x;
+      if (p >= pieces) break;
+      if (a.held) {
+#pragma unroll
+        for (int h = 0; h < kWords / 4; ++h)
+          reinterpret_cast<uint4*>(part_mem)[p * (kWords / 4) + h] =
+              make_uint4(w[j][4 * h], w[j][4 * h + 1], w[j][4 * h + 2], w[j][4 * h + 3]);
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t x = w[j][i];
+        if constexpr (TYPE == GM_LOSS_F32) {
+          top = min(top, x), last = max(last, x);
+        } else {  // two at a time, taken apart at the end
+          top = __vminu2(top, x), last = __vmaxu2(last, x);
+        }
+        if constexpr (KEYS) {
+          atomicAdd(&counts[(x & 0xffffu) >> 1], 1u + (x & 1u) * 0xffffu);
+          atomicAdd(&counts[x >> 17], 1u + (x >> 16 & 1u) * 0xffffu);
+        }
+      }
+    }
+  }
+  if constexpr (TYPE != GM_LOSS_F32) top = min(top & 0xffffu, top >> 16), last = max(last & 0xffffu, last >> 16);
+  if (threadIdx.x == blockDim.x - 1 && min_p > 0.f) {
+    const double x = static_cast<double>(temp) * log(static_cast<double>(min_p));
+    sh.least_log = static_cast<float>(x);
+    sh.least_log_low = static_cast<float>(x - static_cast<double>(sh.least_log));
+  }
+  top = __reduce_min_sync(kFull, top);
+  last = __reduce_max_sync(kFull, last);
+  if (lane == 0) sh.warp_top[warp] = top, sh.warp_last[warp] = last;
+  __syncthreads();
+  top = __reduce_min_sync(kFull, sh.warp_top[lane < warps ? lane : 0]);
+  last = __reduce_max_sync(kFull, sh.warp_last[lane < warps ? lane : 0]);
+  if (blocks > 1) {
+    if (threadIdx.x < blocks) put_remote_u64(&sh.told_ends[rank], threadIdx.x, (u64(last) << 32) | top);
+    cluster_sync_all();
+    for (int r = 0; r < blocks; ++r) {
+      top = min(top, static_cast<uint32_t>(sh.told_ends[r]));
+      last = max(last, static_cast<uint32_t>(sh.told_ends[r] >> 32));
+    }
+  }
+
+  // log2(e) / T in two parts
+  const float c_high = temp > 0.f ? kLog2e / temp : 0.f;
+  const float c_low = temp > 0.f ? (fmaf(-c_high, temp, kLog2e) + kLog2eLow) / temp : 0.f;
+  const bool fine = top < kNonePlace<TYPE> && top >= kInfPlace<TYPE> && last <= kNonePlace<TYPE> && u >= 0.f && u < 1.f && temp >= 0.f &&
+                    temp < INFINITY && c_high < INFINITY && top_k >= 0 && top_p >= 0.f && top_p <= 1.f && min_p >= 0.f && min_p <= 1.f;
   if (!fine) {  // the same for every block of the row
     if (rank == 0 && threadIdx.x == 0) {
       a.index[row_i] = -1;
@@ -336,205 +519,317 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   }
   if (temp == 0.f) top_k = 1;
   const float top_z = value_of<TYPE>(top);
-  const Weigher weigh{top_z, c_high, static_cast<float>(c - static_cast<double>(c_high)), top, a.bits, sh.table};
+  const Weigher weigh{top_z, c_high, c_low, top, a.bits, sh.table};
+  auto weight = [&](uint32_t d) { return weigh(top + d, value_of<TYPE>(top + d)); };
 
   // what is not -inf, and passes min-p
-  Border border{top - kNoneKey<TYPE> - 1, INT64_MAX};
+  Border border{kNonePlace<TYPE> - top - 1, INT64_MAX};
   uint32_t by_min = border.d;
-  if (min_p > 0.f && temp > 0.f && top < kInfKey<TYPE>) {
-    const uint32_t least = key_from<TYPE>(static_cast<double>(top_z) + static_cast<double>(temp) * log(static_cast<double>(min_p)));
-    by_min = min(by_min, top - min(top, least));
+  if (min_p > 0.f && temp > 0.f && top > kInfPlace<TYPE>) {
+    const uint32_t from = place_from<TYPE>(top_z, sh.least_log, sh.least_log_low);
+    by_min = min(by_min, max(from, top) - top);
   } else if (min_p > 0.f) {
     by_min = 0;  // T = 0, or +inf: w is 1 or 0
   }
+  constexpr bool kLong = TYPE == GM_LOSS_F32;
+  auto shift_of = [](int g) { return kLong ? (g == 0 ? 21 : g == 1 ? 10 : 0) : (g == 0 ? 5 : 0); };
 
   // ---- top-k
   if (top_k > 0 && top_k < a.n_classes) {
-    u64 before = 0;
-    uint32_t lo = 0;  // digits found so far
-#pragma unroll 1
-    for (int g = 0; g < kDigits; ++g) {
-      const int shift = TYPE == GM_LOSS_F32 ? (g == 0 ? 21 : g == 1 ? 10 : 0) : (g == 0 ? 5 : 0);
-      const int shift0 = TYPE == GM_LOSS_F32 ? (g == 1 ? 21 : 10) : 5;  // of the digit before
-      if (g > 0) row.clear();
-      row.each([&](uint32_t k) {
-        const uint32_t d = top - k;
-        if (g == 0 || (d >> shift0) == (lo >> shift0)) atomicAdd(&sh.low[(d - lo) >> shift], 1u);
+    auto goal = [&](u64) { return static_cast<u64>(top_k); };
+    if constexpr (KEYS) {
+      row.template border_of<true>(top, 0xffffu, [](uint32_t, uint32_t count) { return u64(count); }, goal, [&](const Search& s, uint32_t d) {
+        if (lane == 0) sh.border = Border{d, top_k - static_cast<int64_t>(s.before)};
       });
-      row.template find<false>(before, [&](u64) { return static_cast<double>(top_k); });
-      lo += sh.digit << shift;
-      before = sh.before;
+    } else {
+      uint32_t d = 0;
+      u64 before = 0;
+#pragma unroll 1
+      for (int g = 0; g < kDigits; ++g) {
+        const int shift = shift_of(g), done = g > 0 ? shift_of(g - 1) : 0;
+        if (g > 0) row.clear();
+        row.each([&](uint32_t q) {
+          const uint32_t x = q - top;
+          if (g == 0 || (x >> done) == (d >> done)) atomicAdd(&sh.low[(x - d) >> shift], 1u);
+        });
+        row.template digit<false>(before, goal, [&](const Search& s, uint32_t x) {
+          if (lane == 0) sh.border = Border{d + (x << shift), top_k - static_cast<int64_t>(s.before)}, sh.before = s.before;
+        });
+        d = sh.border.d, before = sh.before;
+      }
+      if (top_p < 1.f) row.clear();
     }
-    if (lo <= border.d) border = Border{lo, top_k - static_cast<int64_t>(before)};
-    if (top_p < 1.f) row.clear();
+    if (sh.border.d <= border.d) border = sh.border;
   }
 
   // ---- top-p
   if (top_p < 1.f) {
-    u64 before = 0;
-    uint32_t lo = 0;
-    double goal = 0.0;
-    // of the classes at the border itself only `ties` count, which one thread adds at once where they are not all
-    const bool all = border.ties == INT64_MAX;
-    const u64 w_border = weigh(top - border.d, value_of<TYPE>(top - border.d));
-    auto add = [&](uint32_t at, u64 w) {
-      const uint32_t l = static_cast<uint32_t>(w), old = atomicAdd(&sh.low[at], l);
-      const uint32_t h = static_cast<uint32_t>(w >> 32) + (old + l < old);
-      if (h) atomicAdd(&sh.high[at], h);
+    // the classes at a border of top-k, of which only some count, come after all others and are not in the sums
+    const Border old = border;
+    const u64 extra = old.all() ? 0 : weight(old.d) * static_cast<u64>(old.ties);
+    auto goal = [&](u64 total) {
+      bool left;
+      const u64 w = whole_times(top_p, total + extra, left);
+      return max(w + left, u64(1));
     };
-#pragma unroll 1
-    for (int g = 0; g < kDigits; ++g) {
-      const int shift = TYPE == GM_LOSS_F32 ? (g == 0 ? 21 : g == 1 ? 10 : 0) : (g == 0 ? 5 : 0);
-      const int shift0 = TYPE == GM_LOSS_F32 ? (g == 1 ? 21 : 10) : 5;
-      if (g > 0) row.clear();
-      row.each([&](uint32_t k) {
-        const uint32_t d = top - k;
-        if (d > border.d || (d == border.d && !all)) return;
-        if (g > 0 && (d >> shift0) != (lo >> shift0)) return;
-        const u64 w = weigh(k, value_of<TYPE>(k));
-        if (w) add((d - lo) >> shift, w);
-      });
-      if (!all && rank == 0 && threadIdx.x == 0 && (g == 0 || (border.d >> shift0) == (lo >> shift0)))
-        add((border.d - lo) >> shift, w_border * static_cast<u64>(border.ties));
-      row.template find<true>(before, [&](u64 total) {
-        if (g == 0) goal = fmax(static_cast<double>(top_p) * static_cast<double>(total), 1.0);
-        return goal;
-      });
-      lo += sh.digit << shift;
-      before = sh.before;
-    }
     // so many of the classes with this very D
-    const u64 w = weigh(top - lo, value_of<TYPE>(top - lo)), have = w ? sh.in_digit / w : 0;
-    u64 ties = w ? static_cast<u64>(ceil((goal - static_cast<double>(before)) / static_cast<double>(w))) : 1;
-    ties = max(u64(1), min(ties, max(have, u64(1))));
-    if (lo < border.d || static_cast<int64_t>(ties) < border.ties) border = Border{lo, static_cast<int64_t>(ties)};
+    auto at = [&](const Search& s, uint32_t d) {
+      const bool stays = s.total < s.goal;  // all others fall short
+      if (stays) d = old.d;
+      const u64 w = weight(d), from = stays ? s.total : s.before;
+      const u64 ties = w ? max(u64(1), (s.goal - from + w - 1) / w) : 1;
+      if (lane == 0) sh.border = Border{d, static_cast<int64_t>(ties)};
+    };
+    if constexpr (KEYS) {
+      row.template border_of<false>(top, old.d, [&](uint32_t x, uint32_t count) {
+        return x < old.d || (x == old.d && old.all()) ? weight(x) * count : u64(0);
+      }, goal, at);
+    } else {
+      auto add = [&](uint32_t bin, u64 w) {
+        const uint32_t l = static_cast<uint32_t>(w), was = atomicAdd(&sh.low[bin], l);
+        const uint32_t h = static_cast<uint32_t>(w >> 32) + (was + l < was);
+        if (h) atomicAdd(&sh.high[bin], h);
+      };
+      uint32_t d = 0;
+      u64 before = 0, reach = 0;
+#pragma unroll 1
+      for (int g = 0; g < kDigits; ++g) {
+        const int shift = shift_of(g), done = g > 0 ? shift_of(g - 1) : 0;
+        if (g > 0) row.clear();
+        row.each([&](uint32_t q) {
+          const uint32_t x = q - top;
+          if (x > old.d || (x == old.d && !old.all())) return;
+          if (g > 0 && (x >> done) != (d >> done)) return;
+          const u64 w = weigh(q, value_of<TYPE>(q));
+          if (w) add((x - d) >> shift, w);
+        });
+        row.template digit<true>(before, [&](u64 total) { return g == 0 ? goal(total) : reach; }, [&](const Search& s, uint32_t x) {
+          const bool stays = s.total < s.goal;
+          if (stays || g == kDigits - 1) at(s, d + (x << shift));
+          if (lane == 0) sh.digit = d + (x << shift), sh.before = s.before, sh.goal = s.goal, sh.found = stays;
+        });
+        if (sh.found) break;
+        d = sh.digit, before = sh.before, reach = sh.goal;
+      }
+    }
+    if (sh.border.d < border.d || sh.border.ties < border.ties) border = sh.border;
   }
 
   // ---- min-p
   if (by_min < border.d) border = Border{by_min, INT64_MAX};
 
+  // KEYS: the weights of the values that occur in this part, in place of their counts, by D: those up to the border and a
+  // 0 after it; where the border lies further on, those nearest to the largest and those nearest to the border, backwards
+  // from it. What lies between, beyond 64 powers of two from either, is around 0 and rare; `sparse` where there is any. A class
+  // at the border has its mark in place of a weight.
+  constexpr u64 kTie = u64(1) << 54;  // a thread sums at most 64 weights of 2^46
+  const u64* weights = reinterpret_cast<const u64*>(counts);
+  constexpr uint32_t kNear = kWeights / 2;
+  const bool whole = border.d + 2 <= kWeights;
+  uint32_t above = 0, ties = 0;
+  bool sparse = false;
+  if constexpr (KEYS) {
+    ties = row.count_at(top + border.d);
+    // classes above the border, eight places at a time
+    uint32_t n_above = 0;
+    bool between = false;
+    const uint32_t end = top + border.d;  // not this
+    for (uint32_t i = top / 8 + threadIdx.x; i * 8 < end; i += blockDim.x) {
+      const uint4 c = reinterpret_cast<const uint4*>(counts)[i];
+      if ((c.x | c.y | c.z | c.w) == 0) continue;
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t q = i * 8 + j, m = j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu, d = q - top;
+        if (q >= end) continue;
+        n_above += m;
+        between = between || (m && !whole && d >= kNear && end - q >= kNear - 1);
+      }
+    }
+    n_above = __reduce_add_sync(kFull, n_above);
+    if (lane == 0) sh.warp_above[warp] = n_above;
+    auto d_of = [&](uint32_t i) { return whole || i < kNear ? i : border.d - (i - kNear); };
+    u64 occurs = 0;
+    const uint32_t entries = whole ? border.d : kWeights - 1;
+    for (uint32_t i = threadIdx.x, j = 0; i < entries; i += blockDim.x, ++j)
+      if (row.count_at(top + d_of(i))) occurs |= u64(1) << j;
+    sparse = __syncthreads_or(between);
+    for (uint32_t i = threadIdx.x, j = 0; i < entries; i += blockDim.x, ++j)
+      if (occurs >> j & 1) reinterpret_cast<u64*>(counts)[i] = weight(d_of(i));
+    above = __reduce_add_sync(kFull, lane < warps ? sh.warp_above[lane] : 0u);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      reinterpret_cast<u64*>(counts)[whole ? border.d : kNear] = kTie;
+      reinterpret_cast<u64*>(counts)[whole ? border.d + 1 : kWeights - 1] = 0;
+    }
+    __syncthreads();
+  }
+
   // ---- sums of what is kept, by warps: a warp takes pieces that follow one another
-  const int per_warp = (row.pieces() + warps - 1) / warps;
-  const int p0 = min(warp * per_warp, row.pieces()), p1 = min(p0 + per_warp, row.pieces());
-  const u64 w_tie = weigh(top - border.d, value_of<TYPE>(top - border.d));
-  u64 sum = 0;
-  uint32_t ties = 0, above = 0;
-  for (int p = p0 + lane; p < p1; p += 32) {
-    uint32_t k[kPer];
-    row.keys(p, k);
+  const int per_warp = (pieces + warps - 1) / warps;
+  const int p0 = min(warp * per_warp, pieces), p1 = min(p0 + per_warp, pieces);
+  const u64 w_tie = weight(border.d);
+  // weights above the border of a piece, and how many classes are at it
+  auto sum_of = [&](int p, uint32_t& n_ties, uint32_t& n_above) {
+    uint32_t q[kPer];
+    row.places(p, q);
+    u64 x = 0;
+    if (KEYS && !sparse) {
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x += weights[min(q[i] - top, border.d + 1)];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const uint32_t d = q[i] - top;
+          x += weights[d < kNear ? d : d > border.d ? kWeights - 1 : kNear + border.d - d];
+        }
+      }
+      n_ties += static_cast<uint32_t>(x / kTie);
+      return x % kTie;
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const uint32_t d = top - k[i];
-      if (d < border.d) sum += weigh(k[i], value_of<TYPE>(k[i])), ++above;
-      else if (d == border.d) ++ties;
+      const uint32_t d = q[i] - top;
+      n_ties += d == border.d;
+      if (d < border.d) ++n_above, x += weigh(q[i], value_of<TYPE>(q[i]));
     }
-  }
+    return x;
+  };
+  u64 sum = 0;
+  uint32_t warp_ties = 0, warp_above = 0;
+  for (int p = p0 + lane; p < p1; p += 32) sum += sum_of(p, warp_ties, warp_above);
   sum = warp_reduce_sum(sum);
-  ties = __reduce_add_sync(kFull, ties);
-  above = __reduce_add_sync(kFull, above);
-  if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_ties[warp] = ties, sh.warp_above[warp] = above;
-  __syncthreads();
-  Share mine = {0, 0, 0};
-  u64 sum_before = 0;  // of this warp, in its block
-  uint32_t ties_before = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w == warp) sum_before = mine.sum, ties_before = mine.ties;
-    mine.sum += sh.warp_sum[w], mine.ties += sh.warp_ties[w], mine.above += sh.warp_above[w];
+  warp_ties = __reduce_add_sync(kFull, warp_ties);
+  if constexpr (!KEYS) warp_above = __reduce_add_sync(kFull, warp_above);
+  if (lane == 0) {
+    sh.warp_sum[warp] = sum, sh.warp_ties[warp] = warp_ties;
+    if constexpr (!KEYS) sh.warp_above[warp] = warp_above;
   }
-  u64 total = mine.sum;
-  int64_t all_ties = mine.ties, kept = mine.above;
+  __syncthreads();
+  u64 sum_before, total;  // of this warp in its block, of the block
+  uint32_t ties_before;
+  {
+    const u64 x = lane < warps ? sh.warp_sum[lane] : 0;
+    const uint32_t t = lane < warps ? sh.warp_ties[lane] : 0;
+    const u64 x_to = warp_inclusive_scan(x);
+    const uint32_t t_to = warp_inclusive_scan(t);
+    sum_before = __shfl_sync(kFull, x_to - x, warp), ties_before = __shfl_sync(kFull, t_to - t, warp);
+    total = __shfl_sync(kFull, x_to, 31), ties = __shfl_sync(kFull, t_to, 31);
+    if constexpr (!KEYS) above = __reduce_add_sync(kFull, lane < warps ? sh.warp_above[lane] : 0u);
+  }
+  int64_t all_ties = ties, kept = above;
+  u64 part_from = 0, part_sum = total;  // of the row's sum: before this block's part, of the part
+  int64_t part_ties = ties, part_ties_from = 0;
   if (blocks > 1) {
     if (threadIdx.x < blocks) {
-      put_remote_u64(&sh.told[rank].sum, threadIdx.x, mine.sum);
-      put_remote_u64(&sh.told[rank].ties, threadIdx.x, (u64(mine.above) << 32) | mine.ties);
+      put_remote_u64(&sh.told[rank].sum, threadIdx.x, total);
+      put_remote_u64(&sh.told[rank].ties, threadIdx.x, (u64(above) << 32) | ties);
     }
     cluster_sync_all();
     total = 0, all_ties = kept = 0;
     for (int r = 0; r < blocks; ++r) {
-      if (r == rank) sum_before += total, ties_before += static_cast<uint32_t>(all_ties);
+      if (r == rank) part_from = total, part_ties_from = all_ties;
       total += sh.told[r].sum, all_ties += sh.told[r].ties, kept += sh.told[r].above;
     }
   }
   const int64_t most = min(border.ties, all_ties);
   total += static_cast<u64>(most) * w_tie;
   kept += most;
-  const double goal = static_cast<double>(u) * static_cast<double>(total);
+  bool left;
+  const u64 goal = whole_times(u, total, left);  // more than u * total: more than its whole part
   auto tied = [&](int64_t before, int64_t n_ties) {  // of n_ties after `before` others, how many are kept
     return static_cast<u64>(max(int64_t(0), min(most - before, n_ties)));
   };
-  sum_before += static_cast<u64>(min(most, int64_t(ties_before))) * w_tie;
-  sum += tied(ties_before, ties) * w_tie;
-  if (!(static_cast<double>(sum_before) <= goal && static_cast<double>(sum_before + sum) > goal)) return;
+  part_sum += tied(part_ties_from, part_ties) * w_tie;
+  part_from += tied(0, part_ties_from) * w_tie;
+  if (part_from > goal || part_from + part_sum <= goal) return;  // in another block's part
+  sum_before += part_from + tied(part_ties_from, ties_before) * w_tie;
+  sum += tied(part_ties_from + ties_before, warp_ties) * w_tie;
 
-  // ---- the one warp in which the sum passes u: 32 pieces at a time, then the lane, then the class
-  int64_t tie = ties_before;
-  u64 at = sum_before;
-  for (int p = p0; p < p1; p += 32) {
-    uint32_t k[kPer];
-    u64 own = 0;
-    uint32_t own_ties = 0;
-    const bool in = p + lane < p1;
-    if (in) {
-      row.keys(p + lane, k);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t d = top - k[i];
-        if (d < border.d) own += weigh(k[i], value_of<TYPE>(k[i]));
-        else if (d == border.d) ++own_ties;
+  // ---- the one warp in which the sum passes u: 32 pieces at a time, then the lane, then the class. The logarithm
+  // of the sum is another warp's work meanwhile, in 64 bits.
+  const bool here = sum_before <= goal && sum_before + sum > goal;
+  int at_class = -1;
+  uint32_t at_place = 0;
+  if (here) {
+    int64_t tie = part_ties_from + ties_before;
+    u64 at = sum_before;
+    for (int p = p0; p < p1; p += 32) {
+      u64 own = 0;
+      uint32_t own_ties = 0, unused = 0;
+      if (p + lane < p1) own = sum_of(p + lane, own_ties, unused);
+      __syncwarp();
+      const uint32_t ties_to = warp_inclusive_scan(own_ties);
+      int64_t tie_at = tie + ties_to - own_ties;
+      own += tied(tie_at, own_ties) * w_tie;
+      const u64 to = warp_inclusive_scan(own);
+      const unsigned passed = __ballot_sync(kFull, at + to > goal);
+      if (!passed) {
+        at += __shfl_sync(kFull, to, 31);
+        tie += __shfl_sync(kFull, ties_to, 31);
+        continue;
       }
-    }
-    const uint32_t ties_to = warp_inclusive_scan(own_ties);
-    int64_t tie_at = tie + ties_to - own_ties;
-    own += tied(tie_at, own_ties) * w_tie;
-    const u64 to = warp_inclusive_scan(own);
-    const unsigned passed = __ballot_sync(kFull, static_cast<double>(at + to) > goal);
-    if (!passed) {
-      at += __shfl_sync(kFull, to, 31);
-      tie += __shfl_sync(kFull, ties_to, 31);
-      continue;
-    }
-    if (lane != __ffs(passed) - 1) return;
-    at += to - own;
+      if (lane == __ffs(passed) - 1) {
+        at += to - own;
+        uint32_t q[kPer];
+        row.places(p + lane, q);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t d = top - k[i];
-      u64 w = 0;
-      if (d < border.d) w = weigh(k[i], value_of<TYPE>(k[i]));
-      else if (d == border.d) w = tied(tie_at, 1) * w_tie, ++tie_at;
-      at += w;
-      if (w && static_cast<double>(at) > goal) {
-        a.index[row_i] = first + (p + lane) * kPer - phase + i;
-        const double log_w = k[i] == top ? 0.0 : (static_cast<double>(value_of<TYPE>(k[i])) - static_cast<double>(top_z)) / static_cast<double>(temp);
-        a.logprob[row_i] = static_cast<float>(log_w - log(ldexp(static_cast<double>(total), -a.bits)));
-        a.kept[row_i] = static_cast<int32_t>(kept);
-        return;
+        for (int i = 0; i < kPer; ++i) {
+          const uint32_t d = q[i] - top;
+          u64 w = 0;
+          if (d < border.d) w = weigh(q[i], value_of<TYPE>(q[i]));
+          else if (d == border.d) w = tied(tie_at, 1) * w_tie, ++tie_at;
+          at += w;
+          if (at_class < 0 && w && at > goal) at_class = (p + lane) * kPer - phase + i, at_place = q[i];
+        }
       }
+      break;
     }
-    return;
+  } else if (lane == 0) {
+    // any warp but that one will do: all agree
+    if (warp == 0 || (warp == 1 && warps > 1)) sh.log_total = log(ldexp(static_cast<double>(total), -a.bits));
+  }
+  __syncthreads();
+  if (at_class >= 0) {
+    const double log_w = at_place == top ? 0.0 : (static_cast<double>(value_of<TYPE>(at_place)) - static_cast<double>(top_z)) / static_cast<double>(temp);
+    a.index[row_i] = first + at_class;
+    a.logprob[row_i] = static_cast<float>(log_w - sh.log_total);
+    a.kept[row_i] = static_cast<int32_t>(kept);
   }
 }
 
 // ---- host ---------------------------------------------------------------------------------------------
 constexpr int64_t kMostClasses = int64_t(1) << 24;
-constexpr int kHeldBytes = 196608;  // of a row in a block's shared memory
+constexpr int kHeldBytes = 204800;          // of a block's shared memory: counts, and its part of the row
+// Rows from here on are searched by counts of all values: clearing and reading them costs what so many atomics do.
+constexpr int64_t kLeastCounted = 16384;
+constexpr int64_t kMostCounted = 65512;     // classes of a part: a value's count has 16 bits, up to 14 places are none's
 
-template <int TYPE>
-cudaError_t launch(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
-  const int64_t es = TYPE == GM_LOSS_F32 ? 4 : 2, n = a.n_classes;
-  const cudaError_t e = cudaFuncSetAttribute(k_draw<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldBytes);
+template <int TYPE, bool KEYS>
+cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
+  const int64_t es = TYPE == GM_LOSS_F32 ? 4 : 2, n = a.n_classes, room = kHeldBytes - (KEYS ? kCountBytes : 0);
+  const cudaError_t e = cudaFuncSetAttribute(k_draw<TYPE, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldBytes);
   if (e != cudaSuccess) return e;
   // blocks of a row: until it fits, or the SMs have work
   int blocks = 1;
   auto part = [&] { return up(div_up(n, blocks), kPer); };
-  while (blocks < kMostCluster && ((part() + kPer) * es > kHeldBytes || (n_rows * blocks * 2 <= sms && part() > 8192))) blocks *= 2;
-  a.part = static_cast<int>(part());
-  a.held = (part() + kPer) * es <= kHeldBytes;
+  while (blocks < kMostCluster && ((part() + kPer) * es > room || (n_rows * blocks * 2 <= sms && part() > 8192))) blocks *= 2;
   if (n_rows * blocks > INT32_MAX) return cudaErrorInvalidValue;  // more bytes than any device has
-  const int64_t threads = std::min<int64_t>(1024, std::max<int64_t>(128, up(div_up(part(), 4 * kPer), 128)));
-  int block = 128;  // a power of two: bins are shared out evenly
-  while (block < threads) block *= 2;
-  return launch_chained(k_draw<TYPE>, static_cast<unsigned>(n_rows * blocks), block, a.held ? static_cast<size_t>((part() + kPer) * es) : 0,
-                        s, blocks, a);
+  a.part = static_cast<int>(part());
+  a.held = (part() + kPer) * es <= room;
+  const int64_t threads = std::min<int64_t>(1024, std::max<int64_t>(KEYS ? 256 : 128, up(div_up(part(), 4 * kPer), 128)));
+  const size_t smem = (KEYS ? kCountBytes : 0) + (a.held ? static_cast<size_t>((part() + kPer) * es) : 0);
+  return launch_chained(k_draw<TYPE, KEYS>, static_cast<unsigned>(n_rows * blocks), static_cast<unsigned>(threads), smem, s, blocks, a);
+}
+
+template <int TYPE>
+cudaError_t launch(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
+  if constexpr (TYPE != GM_LOSS_F32) {
+    if (a.n_classes >= kLeastCounted && a.n_classes <= kMostCounted * kMostCluster)
+      return launch_as<TYPE, true>(a, n_rows, sms, s);
+  }
+  return launch_as<TYPE, false>(a, n_rows, sms, s);
 }
 
 }  // namespace
