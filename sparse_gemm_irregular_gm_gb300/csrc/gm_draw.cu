@@ -34,6 +34,7 @@ using u64 = unsigned long long;
 constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) - kLog2e
 
 constexpr int kMostCluster = 8;
+constexpr int kFew = 512;  // classes that are compared each with each
 constexpr int kPer = 8;  // classes a thread takes at a time: 16 bytes of a 16-bit type
 constexpr int kTable = 33;
 
@@ -116,10 +117,9 @@ __device__ __forceinline__ u64 whole_times(float f, u64 n, bool& left) {
 }
 
 // ---- weights ---------------------------------------------------------------------------------------
-// t = (z - max) * (c + c_low) is formed to 48 bits or so: the difference with its rounding error, the product with its
-// own. Its fraction f in [-1/2, 1/2], in units of 2^-31, is split into the nearest 32nd, whose power is in a table of
-// 31-bit integers, and a rest g with |g| <= 1/64, whose 2^g - 1 = g ln 2 + (g ln 2)^2 / 2 + ... is at
-// most 0.011, so that fp32 gives it to 2^-31. About 30 instructions; exact at t = 0.
+// 2^(31 + f / 2^31) for f in [-2^30, 2^30], to about 2^-29 of itself: the nearest 32nd of f's range, whose power
+// is in a table of 32-bit integers, and a rest g with |g| <= 1/64, whose 2^g - 1 = g ln 2 + (g ln 2)^2 / 2 + ... is at
+// most 0.011, so that fp32 gives it to 2^-31. Exact at 0.
 // 2^(31 + (j - 16) / 32), rounded
 __constant__ uint32_t kPowers[kTable] = {
     1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u,
@@ -128,6 +128,17 @@ __constant__ uint32_t kPowers[kTable] = {
     2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
     2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u,
     2908241642u, 2971923842u, 3037000500u};
+__device__ __forceinline__ uint32_t power(int f, const uint32_t* table) {
+  const uint32_t x = static_cast<uint32_t>(f) + (1u << 30) + (1u << 25);
+  const uint32_t j = min(x >> 26, static_cast<uint32_t>(kTable - 1));
+  const float g = static_cast<float>(static_cast<int>(x - (j << 26)) - (1 << 25)) * 4.656612873077393e-10f;  // 2^-31
+  const float l = g * 0.693147180559945f;
+  const float q = l * fmaf(l, fmaf(l, fmaf(l, 0.0416666667f, 0.1666666667f), 0.5f), 1.f);
+  const uint32_t p = table[j];
+  return p + static_cast<uint32_t>(__float2int_rn(static_cast<float>(p) * q));
+}
+// w of a logit. t = (z - max) * (c + c_low) is formed to 48 bits or so: the difference with its rounding error, the product
+// with its own.
 struct Weigher {
   float top, c, c_low;
   uint32_t top_place;
@@ -142,19 +153,45 @@ struct Weigher {
     const float d_low = (z - (d - b)) - (top + b);
     const float t_low = fmaf(d, c, -t) + fmaf(d, c_low, d_low * c);
     const float whole = rintf(t);
-    const uint32_t x = static_cast<uint32_t>(__float2int_rn((t - whole) * 2147483648.f)) +
-                       static_cast<uint32_t>(__float2int_rn(t_low * 2147483648.f)) + (1u << 30) + (1u << 25);
-    const uint32_t j = min(x >> 26, static_cast<uint32_t>(kTable - 1));
-    const float g = static_cast<float>(static_cast<int>(x - (j << 26)) - (1 << 25)) * 4.656612873077393e-10f;  // 2^-31
-    const float l = g * 0.693147180559945f;
-    const float q = l * fmaf(l, fmaf(l, fmaf(l, 0.0416666667f, 0.1666666667f), 0.5f), 1.f);
-    const uint32_t p = table[j];
-    const uint32_t m = p + static_cast<uint32_t>(__float2int_rn(static_cast<float>(p) * q));
+    const uint32_t m = power(__float2int_rn((t - whole) * 2147483648.f) + __float2int_rn(t_low * 2147483648.f), table);
     const int shift = bits - 31 + static_cast<int>(whole);
     if (shift >= 0) return u64(m) << shift;
     return shift < -32 ? 0 : (u64(m) + (u64(1) << (-shift - 1))) >> -shift;
   }
 };
+
+// A value in two parts.
+struct Pair {
+  float x, low;
+};
+__device__ __forceinline__ Pair sum_of(float a, float b) {
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair times(Pair a, float x, float x_low) {
+  const float p = __fmul_rn(a.x, x);
+  return sum_of(p, fmaf(a.x, x, -p) + fmaf(a.x, x_low, a.low * x));
+}
+constexpr float kLn2 = 0.693147180559945f, kLn2Low = -1.9046543e-9f;
+// ln(m / 2^31 * 2^e) for m in [2^31, 2^32), to about 2^-29: log2f, put right by how far its power is from m.
+__device__ __forceinline__ Pair log_of(uint32_t m, int e, const uint32_t* table) {
+  const float y = log2f(static_cast<float>(m) * 4.656612873077393e-10f);  // 2^-31; in [0, 1]
+  const float whole = rintf(y);
+  const uint32_t p = power(__float2int_rn((y - whole) * 2147483648.f), table);
+  const float off = static_cast<float>(static_cast<int64_t>(m) - (static_cast<int64_t>(p) << static_cast<int>(whole))) / static_cast<float>(m);
+  Pair l = sum_of(static_cast<float>(e), y);
+  l.low = fmaf(off, 1.44269504f, l.low);
+  return times(l, kLn2, kLn2Low);
+}
+__device__ __forceinline__ Pair log_of(float x, const uint32_t* table) {  // 0 < x, finite
+  const uint32_t bits = __float_as_uint(x), e = bits >> 23, m = e ? (bits & 0x7fffffu) | 0x800000u : bits;
+  const int z = __clz(m);
+  return log_of(m << z, (e ? static_cast<int>(e) - 150 : -149) + 31 - z, table);
+}
+__device__ __forceinline__ Pair log_of(u64 n, int e, const uint32_t* table) {  // ln(n 2^e), n > 0
+  const int z = __clzll(static_cast<long long>(n));
+  return log_of(static_cast<uint32_t>((n << z) >> 32), e + 63 - z, table);
+}
 
 // ---- sums over the block and the cluster --------------------------------------------------------------
 constexpr int kGroups = 64;                          // of bins, or of lines: the first step of a search
@@ -177,19 +214,20 @@ template <bool KEYS>
 struct Shared {
   uint32_t table[kTable + 1];
   Share told[kMostCluster];
-  u64 told_ends[kMostCluster];
-  float least_log, least_log_low;  // T log(min_p)
-  double log_total;
+  u64 told_ends[kMostCluster], told_off[kMostCluster];
   Border border;
+  uint32_t cut;                    // the few largest: those with D up to this, where there are few
+  uint32_t n_few;
   uint32_t digit;                  // !KEYS: D's digits found so far
   bool found;
   u64 before, goal;
   u64 warp_sum[32];
   uint32_t warp_top[32], warp_last[32], warp_ties[32], warp_above[32];
   u64 coarse[kMostCluster][kGroups];
-  // !KEYS: counts, or the two words of sums; KEYS: sums of the lines
-  uint32_t low[KEYS ? 1 : kBins], high[KEYS ? 1 : kBins];
-  u64 line[KEYS ? kLines : 1];
+  alignas(16) uint32_t bins[KEYS ? 2 : 2 * kBins];  // !KEYS: histograms
+  alignas(16) u64 line[KEYS ? kLines : 1];
+  int n_lines;                     // lines that hold anything
+  uint16_t lines[KEYS ? kLines : 1];
 };
 
 __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
@@ -205,6 +243,11 @@ __device__ __forceinline__ u64 remote_u64(const void* p, uint32_t rank) {
 __device__ __forceinline__ void put_remote_u64(void* p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(map_to_rank(smem_addr(p), rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t add_remote_u32(void* p, uint32_t rank, uint32_t v) {
+  uint32_t was;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(was) : "r"(map_to_rank(smem_addr(p), rank)), "r"(v) : "memory");
+  return was;
+}
 // f(rank) for every block of the row, all under way before the first is used; their sum.
 template <class F>
 __device__ __forceinline__ u64 from_each(int blocks, F&& f) {
@@ -217,23 +260,28 @@ __device__ __forceinline__ u64 from_each(int blocks, F&& f) {
   return sum;
 }
 
-// A warp's way to the place at which a sum reaches the goal: the sum before what was found so far, the sum of all.
+// A warp's way to the place at which a sum reaches the goal: the sum before what was found so far, the sum of all, and
+// that of what was found.
 struct Search {
-  u64 before, total, goal;
+  u64 before, total, goal, in;
   // the first lane at which `before` and the sum of v up to and with it reach the goal (the last, where there is none)
   __device__ __forceinline__ uint32_t step(u64 v) {
     const u64 to = warp_inclusive_scan(v);
     const unsigned at = __ballot_sync(kFull, before + to >= goal);
     const int l = at ? __ffs(at) - 1 : 31;
     before += __shfl_sync(kFull, to - v, l);
+    in = __shfl_sync(kFull, v, l);
     return l;
   }
   // the same of two values a lane
   __device__ __forceinline__ uint32_t step2(u64 a, u64 b) {
     const uint32_t l = step(a + b);
     const u64 first = __shfl_sync(kFull, a, l);
-    if (before + first >= goal) return 2 * l;
-    before += first;
+    if (before + first >= goal) {
+      in = first;
+      return 2 * l;
+    }
+    before += first, in -= first;
     return 2 * l + 1;
   }
 };
@@ -244,6 +292,7 @@ struct Row {
   Shared<KEYS>& sh;
   const DrawArgs& a;
   uint32_t* counts;       // KEYS: of the values at each place, two a word
+  uint32_t *low, *high;   // histograms: counts, or the two words of sums
   int blocks, rank;       // of the cluster
   const void* data;       // of this block's part, from piece 0 on: places where they are held, else logits
   int n, phase;           // classes of the part, their first one's element in piece 0
@@ -330,15 +379,15 @@ struct Row {
     __syncthreads();
     for (int g = warp; g < kGroups; g += warps) {
       const int b = g * kGroupBins + lane;
-      tell(g, warp_reduce_sum(MASS ? u64(sh.low[b]) + (u64(sh.high[b]) << 32) : u64(sh.low[b])), lane);
+      tell(g, warp_reduce_sum(MASS ? u64(low[b]) + (u64(high[b]) << 32) : u64(low[b])), lane);
     }
     meet();
     if (warp == 0) {
-      Search s{before, 0, 0};
+      Search s{before, 0, 0, 0};
       const uint32_t g = group(s, goal_of), b = g * kGroupBins + lane;
       const u64 x = from_each(blocks, [&](int r) {
-        if (blocks == 1) return MASS ? u64(sh.low[b]) + (u64(sh.high[b]) << 32) : u64(sh.low[b]);
-        return MASS ? u64(remote_u32(&sh.low[b], r)) + (u64(remote_u32(&sh.high[b], r)) << 32) : u64(remote_u32(&sh.low[b], r));
+        if (blocks == 1) return MASS ? u64(low[b]) + (u64(high[b]) << 32) : u64(low[b]);
+        return MASS ? u64(remote_u32(&low[b], r)) + (u64(remote_u32(&high[b], r)) << 32) : u64(remote_u32(&low[b], r));
       });
       const uint32_t d = g * kGroupBins + s.step(x);
       then(s, d);
@@ -346,7 +395,7 @@ struct Row {
     meet();  // histograms and sums are read
   }
   __device__ __forceinline__ void clear() const {
-    for (int i = threadIdx.x; i < kBins; i += blockDim.x) sh.low[i] = sh.high[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += blockDim.x) low[i] = high[i] = 0;
     __syncthreads();
   }
 
@@ -360,10 +409,14 @@ struct Row {
       const uint32_t d = line * kLine + 2 * lane - top;  // wraps for values above the largest, whose counts are 0
       x = even ? value(d, even) : 0, y = odd ? value(d + 1, odd) : 0;
     };
-    // four lines at a time: eight lanes read one
+    // four lines at a time: eight lanes read one. Weights are formed of lines that hold anything, which the warps then share.
+    if constexpr (!COUNTS) {
+      if (threadIdx.x == 0) sh.n_lines = 0;
+      __syncthreads();
+    }
     for (int l = 4 * warp; l < kLines; l += 4 * warps) {
-      const uint4 c = reinterpret_cast<const uint4*>(counts)[l * 8 + lane];
       if constexpr (COUNTS) {
+        const uint4 c = reinterpret_cast<const uint4*>(counts)[l * 8 + lane];
         uint32_t n_ = 0;
 #pragma unroll
         for (const uint32_t w : {c.x, c.y, c.z, c.w}) n_ += (w & 0xffffu) + (w >> 16);
@@ -371,18 +424,23 @@ struct Row {
         for (int d = 4; d > 0; d >>= 1) n_ += __shfl_xor_sync(kFull, n_, d);
         if ((lane & 7) == 0) sh.line[l + lane / 8] = n_;
       } else {
+        if (lane < 4) sh.line[l + lane] = 0;
+        if (l + 3 < line0 || l > line1) continue;
+        const uint4 c = reinterpret_cast<const uint4*>(counts)[l * 8 + lane];
         const unsigned some = __ballot_sync(kFull, (c.x | c.y | c.z | c.w) != 0);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          u64 sum = 0;
-          if ((some >> (8 * i) & 0xffu) && l + i >= line0 && l + i <= line1) {
-            const uint32_t word = counts[(l + i) * 32 + lane];
-            u64 x, y;
-            of_line(l + i, word & 0xffffu, word >> 16, x, y);
-            sum = warp_reduce_sum(x + y);
-          }
-          if (lane == 0) sh.line[l + i] = sum;
-        }
+        if (lane < 4 && (some >> (8 * lane) & 0xffu) && l + lane >= line0 && l + lane <= line1)
+          sh.lines[atomicAdd(&sh.n_lines, 1)] = static_cast<uint16_t>(l + lane);
+      }
+    }
+    if constexpr (!COUNTS) {
+      __syncthreads();
+      for (int i = warp; i < sh.n_lines; i += warps) {
+        const int l = sh.lines[i];
+        const uint32_t word = counts[l * 32 + lane];
+        u64 x, y;
+        of_line(l, word & 0xffffu, word >> 16, x, y);
+        x = warp_reduce_sum(x + y);
+        if (lane == 0) sh.line[l] = x;
       }
     }
     __syncthreads();
@@ -394,7 +452,7 @@ struct Row {
     }
     meet();
     if (warp == 0) {
-      Search s{0, 0, 0};
+      Search s{0, 0, 0, 0};
       const uint32_t g = group(s, goal_of);
       const u64 x = from_each(blocks, [&](int r) {
         if (lane >= kGroupLines) return u64(0);
@@ -428,15 +486,16 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   const int64_t row_i = blockIdx.x / blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (threadIdx.x < kTable) sh.table[threadIdx.x] = kPowers[threadIdx.x];
+  if (threadIdx.x == 0) sh.n_few = 0;
   if constexpr (KEYS) {
     for (int i = threadIdx.x; i < kCountBytes / 16; i += blockDim.x) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   } else {
-    for (int i = threadIdx.x; i < kBins; i += blockDim.x) sh.low[i] = sh.high[i] = 0;
+    for (int i = threadIdx.x; i < 2 * kBins; i += blockDim.x) sh.bins[i] = 0;
   }
   chain_wait();
 
-  // the row's rule; T log(min_p), in 64 bits, is one thread's work while the row is on its way
+  // the row's rule
   const float temp = a.rule.temperature ? a.rule.temperature[row_i] : a.rule.all_temperature;
   const float top_p = a.rule.top_p ? a.rule.top_p[row_i] : a.rule.all_top_p;
   const float min_p = a.rule.min_p ? a.rule.min_p[row_i] : a.rule.all_min_p;
@@ -449,9 +508,10 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   const char* src = static_cast<const char*>(a.z) + (row_i * a.ld + first) * kBytes;
   const int phase = static_cast<int>(reinterpret_cast<uintptr_t>(src) % (kPer * kBytes) / kBytes);
   src -= phase * kBytes;  // piece 0
-  const R row{sh, a, counts, static_cast<int>(blocks), static_cast<int>(rank), a.held ? static_cast<const void*>(part_mem) : src, n, phase};
+  uint32_t* const bins = KEYS ? counts : sh.bins;
+  const R row{sh, a, counts, bins, bins + kBins, static_cast<int>(blocks), static_cast<int>(rank), a.held ? static_cast<const void*>(part_mem) : src, n, phase};
   const int pieces = row.pieces();
-  uint32_t top = 0xffffffffu, last = 0;
+  uint32_t top = 0xffffffffu, last = 0, n_counted = 0;
   constexpr int kAhead = TYPE == GM_LOSS_F32 ? 2 : 4;  // pieces of a thread under way
   for (int p0 = threadIdx.x; p0 < pieces; p0 += kAhead * blockDim.x) {
     uint32_t w[kAhead][kWords];
@@ -477,18 +537,16 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
           top = __vminu2(top, x), last = __vmaxu2(last, x);
         }
         if constexpr (KEYS) {
-          atomicAdd(&counts[(x & 0xffffu) >> 1], 1u + (x & 1u) * 0xffffu);
-          atomicAdd(&counts[x >> 17], 1u + (x >> 16 & 1u) * 0xffffu);
+          if (x != kNonePlace<TYPE> * 0x10001u) {  // two masked classes
+            n_counted += 2;
+            atomicAdd(&counts[(x & 0xffffu) >> 1], 1u + (x & 1u) * 0xffffu);
+            atomicAdd(&counts[x >> 17], 1u + (x >> 16 & 1u) * 0xffffu);
+          }
         }
       }
     }
   }
   if constexpr (TYPE != GM_LOSS_F32) top = min(top & 0xffffu, top >> 16), last = max(last & 0xffffu, last >> 16);
-  if (threadIdx.x == blockDim.x - 1 && min_p > 0.f) {
-    const double x = static_cast<double>(temp) * log(static_cast<double>(min_p));
-    sh.least_log = static_cast<float>(x);
-    sh.least_log_low = static_cast<float>(x - static_cast<double>(sh.least_log));
-  }
   top = __reduce_min_sync(kFull, top);
   last = __reduce_max_sync(kFull, last);
   if (lane == 0) sh.warp_top[warp] = top, sh.warp_last[warp] = last;
@@ -502,6 +560,30 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
       top = min(top, static_cast<uint32_t>(sh.told_ends[r]));
       last = max(last, static_cast<uint32_t>(sh.told_ends[r] >> 32));
     }
+  }
+
+  // KEYS: counts serve while none has passed 16 bits, which their sum would show: a carry takes 65536 away and adds 1 or
+  // nothing. Else, with tens of thousands of equal logits, the row is searched by digits.
+  bool by_counts = KEYS;
+  if (KEYS && a.part > 65535) {
+    int off = static_cast<int>(n_counted);
+    for (int i = threadIdx.x; i < kCountBytes / 16; i += blockDim.x) {
+      const uint4 c = reinterpret_cast<const uint4*>(counts)[i];
+#pragma unroll
+      for (const uint32_t w : {c.x, c.y, c.z, c.w}) off -= static_cast<int>((w & 0xffffu) + (w >> 16));
+    }
+    off = __reduce_add_sync(kFull, off);
+    if (lane == 0) sh.warp_above[warp] = off;
+    __syncthreads();
+    off = __reduce_add_sync(kFull, lane < warps ? sh.warp_above[lane] : 0);
+    if (blocks > 1) {
+      if (threadIdx.x < blocks) put_remote_u64(&sh.told_off[rank], threadIdx.x, off != 0);
+      cluster_sync_all();
+      for (int r = 0; r < blocks; ++r) off |= static_cast<int>(sh.told_off[r]);
+    }
+    by_counts = off == 0;
+    __syncthreads();
+    if (!by_counts) row.clear();
   }
 
   // log2(e) / T in two parts
@@ -520,26 +602,102 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   if (temp == 0.f) top_k = 1;
   const float top_z = value_of<TYPE>(top);
   const Weigher weigh{top_z, c_high, c_low, top, a.bits, sh.table};
+  // the row's results: a class, its place, the sum of what is kept, how many that are
+  auto answer = [&](int64_t index, uint32_t place, u64 sum, int64_t n_kept) {
+    const Pair l = log_of(sum, -a.bits, sh.table);
+    Pair w = {0.f, 0.f};
+    if (place != top) {
+      const Pair d = sum_of(value_of<TYPE>(place), -top_z);
+      w.x = d.x / temp;
+      w.low = (fmaf(-w.x, temp, d.x) + d.low) / temp;
+    }
+    a.index[row_i] = index;
+    const Pair x = sum_of(w.x, -l.x);
+    a.logprob[row_i] = x.x + (x.low + (w.low - l.low));
+    a.kept[row_i] = static_cast<int32_t>(n_kept);
+  };
   auto weight = [&](uint32_t d) { return weigh(top + d, value_of<TYPE>(top + d)); };
 
   // what is not -inf, and passes min-p
   Border border{kNonePlace<TYPE> - top - 1, INT64_MAX};
   uint32_t by_min = border.d;
   if (min_p > 0.f && temp > 0.f && top > kInfPlace<TYPE>) {
-    const uint32_t from = place_from<TYPE>(top_z, sh.least_log, sh.least_log_low);
+    const Pair l = times(log_of(min_p, sh.table), temp, 0.f);
+    const uint32_t from = place_from<TYPE>(top_z, l.x, l.low);
     by_min = min(by_min, max(from, top) - top);
   } else if (min_p > 0.f) {
     by_min = 0;  // T = 0, or +inf: w is 1 or 0
   }
+  // The few classes with D up to `cut`, the rule's kept ones among them: the row's first block takes them as a list and
+  // compares each with each, a thread a class.
+  auto of_few = [&](uint32_t cut) {
+    u64* list = KEYS ? sh.line : reinterpret_cast<u64*>(sh.bins);  // place and class; then weights
+    u64* w_few = list + kFew;
+    for (int p = threadIdx.x; p < pieces; p += blockDim.x) {
+      uint32_t q[kPer];
+      row.places(p, q);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (q[i] - top > cut) continue;
+        const u64 x = (u64(q[i]) << 32) | static_cast<uint32_t>(first + p * kPer - phase + i);
+        if (blocks == 1) list[atomicAdd(&sh.n_few, 1u)] = x;
+        else put_remote_u64(&list[add_remote_u32(&sh.n_few, 0, 1u)], 0, x);
+      }
+    }
+    row.meet();
+    if (rank != 0) return;
+    const int m = static_cast<int>(sh.n_few), i = threadIdx.x;
+    const u64 x = i < m ? list[i] : ~u64(0);
+    const uint32_t place = static_cast<uint32_t>(x >> 32);
+    const u64 w = i < m ? weigh(place, value_of<TYPE>(place)) : 0;
+    if (i < m) w_few[i] = w;
+    auto sum_all = [&](u64 v) {  // over the block
+      v = warp_reduce_sum(v);
+      __syncthreads();
+      if (lane == 0) sh.warp_sum[warp] = v;
+      __syncthreads();
+      return warp_reduce_sum(lane < warps ? sh.warp_sum[lane] : u64(0));
+    };
+    __syncthreads();
+    int n_before = 0;
+    u64 before = 0;
+    if (i < m) {
+#pragma unroll 4
+      for (int j = 0; j < m; ++j)
+        if (list[j] < x) ++n_before, before += w_few[j];  // equal places: by class
+    }
+    bool kept_here = i < m && (top_k == 0 || n_before < top_k);
+    const u64 all = sum_all(kept_here ? w : 0);
+    if (top_p < 1.f) {
+      bool left;
+      const u64 whole = whole_times(top_p, all, left);
+      kept_here = kept_here && (n_before == 0 || before < whole + left);
+    }
+    kept_here = kept_here && place - top <= by_min;
+    const u64 total = sum_all(kept_here ? w : 0);
+    const int n_kept = __syncthreads_count(kept_here);
+    if (i < m) w_few[i] = kept_here ? w : 0;
+    __syncthreads();
+    bool left;
+    const u64 goal = whole_times(u, total, left);
+    if (!kept_here) return;
+    u64 upto = 0;
+#pragma unroll 4
+    for (int j = 0; j < m; ++j)
+      if (static_cast<uint32_t>(list[j]) <= static_cast<uint32_t>(x)) upto += w_few[j];
+    if (upto > goal && upto - w <= goal) answer(static_cast<uint32_t>(x), place, total, n_kept);
+  };
   constexpr bool kLong = TYPE == GM_LOSS_F32;
   auto shift_of = [](int g) { return kLong ? (g == 0 ? 21 : g == 1 ? 10 : 0) : (g == 0 ? 5 : 0); };
 
   // ---- top-k
   if (top_k > 0 && top_k < a.n_classes) {
     auto goal = [&](u64) { return static_cast<u64>(top_k); };
-    if constexpr (KEYS) {
+    const u64 few = min(kFew, static_cast<int>(blockDim.x));
+    if (KEYS && by_counts) {
       row.template border_of<true>(top, 0xffffu, [](uint32_t, uint32_t count) { return u64(count); }, goal, [&](const Search& s, uint32_t d) {
-        if (lane == 0) sh.border = Border{d, top_k - static_cast<int64_t>(s.before)};
+        if (s.total < s.goal) d = 0xffffffffu;  // masked classes are not all counted
+        if (lane == 0) sh.border = Border{d, top_k - static_cast<int64_t>(s.before)}, sh.cut = d, sh.found = s.before + s.in <= few;
       });
     } else {
       uint32_t d = 0;
@@ -550,15 +708,23 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
         if (g > 0) row.clear();
         row.each([&](uint32_t q) {
           const uint32_t x = q - top;
-          if (g == 0 || (x >> done) == (d >> done)) atomicAdd(&sh.low[(x - d) >> shift], 1u);
+          if (g == 0 || (x >> done) == (d >> done)) atomicAdd(&row.low[(x - d) >> shift], 1u);
         });
         row.template digit<false>(before, goal, [&](const Search& s, uint32_t x) {
-          if (lane == 0) sh.border = Border{d + (x << shift), top_k - static_cast<int64_t>(s.before)}, sh.before = s.before;
+          if (lane == 0) {
+            sh.border = Border{d + (x << shift), top_k - static_cast<int64_t>(s.before)}, sh.before = s.before;
+            sh.cut = d + (x << shift) + ((1u << shift) - 1), sh.found = s.before + s.in <= few;
+          }
         });
+        if (sh.found) break;
         d = sh.border.d, before = sh.before;
       }
-      if (top_p < 1.f) row.clear();
     }
+    if (sh.found) {
+      of_few(min(sh.cut, border.d));
+      return;
+    }
+    if (!by_counts && top_p < 1.f) row.clear();
     if (sh.border.d <= border.d) border = sh.border;
   }
 
@@ -580,15 +746,15 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
       const u64 ties = w ? max(u64(1), (s.goal - from + w - 1) / w) : 1;
       if (lane == 0) sh.border = Border{d, static_cast<int64_t>(ties)};
     };
-    if constexpr (KEYS) {
+    if (KEYS && by_counts) {
       row.template border_of<false>(top, old.d, [&](uint32_t x, uint32_t count) {
         return x < old.d || (x == old.d && old.all()) ? weight(x) * count : u64(0);
       }, goal, at);
     } else {
       auto add = [&](uint32_t bin, u64 w) {
-        const uint32_t l = static_cast<uint32_t>(w), was = atomicAdd(&sh.low[bin], l);
+        const uint32_t l = static_cast<uint32_t>(w), was = atomicAdd(&row.low[bin], l);
         const uint32_t h = static_cast<uint32_t>(w >> 32) + (was + l < was);
-        if (h) atomicAdd(&sh.high[bin], h);
+        if (h) atomicAdd(&row.high[bin], h);
       };
       uint32_t d = 0;
       u64 before = 0, reach = 0;
@@ -628,7 +794,7 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   const bool whole = border.d + 2 <= kWeights;
   uint32_t above = 0, ties = 0;
   bool sparse = false;
-  if constexpr (KEYS) {
+  if (KEYS && by_counts) {
     ties = row.count_at(top + border.d);
     // classes above the border, eight places at a time
     uint32_t n_above = 0;
@@ -670,11 +836,11 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   const int p0 = min(warp * per_warp, pieces), p1 = min(p0 + per_warp, pieces);
   const u64 w_tie = weight(border.d);
   // weights above the border of a piece, and how many classes are at it
-  auto sum_of = [&](int p, uint32_t& n_ties, uint32_t& n_above) {
+  auto sum_piece = [&](int p, uint32_t& n_ties, uint32_t& n_above) {
     uint32_t q[kPer];
     row.places(p, q);
     u64 x = 0;
-    if (KEYS && !sparse) {
+    if (KEYS && by_counts && !sparse) {
       if (whole) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) x += weights[min(q[i] - top, border.d + 1)];
@@ -698,13 +864,13 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   };
   u64 sum = 0;
   uint32_t warp_ties = 0, warp_above = 0;
-  for (int p = p0 + lane; p < p1; p += 32) sum += sum_of(p, warp_ties, warp_above);
+  for (int p = p0 + lane; p < p1; p += 32) sum += sum_piece(p, warp_ties, warp_above);
   sum = warp_reduce_sum(sum);
   warp_ties = __reduce_add_sync(kFull, warp_ties);
-  if constexpr (!KEYS) warp_above = __reduce_add_sync(kFull, warp_above);
+  if (!by_counts) warp_above = __reduce_add_sync(kFull, warp_above);
   if (lane == 0) {
     sh.warp_sum[warp] = sum, sh.warp_ties[warp] = warp_ties;
-    if constexpr (!KEYS) sh.warp_above[warp] = warp_above;
+    if (!by_counts) sh.warp_above[warp] = warp_above;
   }
   __syncthreads();
   u64 sum_before, total;  // of this warp in its block, of the block
@@ -716,7 +882,7 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
     const uint32_t t_to = warp_inclusive_scan(t);
     sum_before = __shfl_sync(kFull, x_to - x, warp), ties_before = __shfl_sync(kFull, t_to - t, warp);
     total = __shfl_sync(kFull, x_to, 31), ties = __shfl_sync(kFull, t_to, 31);
-    if constexpr (!KEYS) above = __reduce_add_sync(kFull, lane < warps ? sh.warp_above[lane] : 0u);
+    if (!by_counts) above = __reduce_add_sync(kFull, lane < warps ? sh.warp_above[lane] : 0u);
   }
   int64_t all_ties = ties, kept = above;
   u64 part_from = 0, part_sum = total;  // of the row's sum: before this block's part, of the part
@@ -747,55 +913,45 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   sum_before += part_from + tied(part_ties_from, ties_before) * w_tie;
   sum += tied(part_ties_from + ties_before, warp_ties) * w_tie;
 
-  // ---- the one warp in which the sum passes u: 32 pieces at a time, then the lane, then the class. The logarithm
-  // of the sum is another warp's work meanwhile, in 64 bits.
-  const bool here = sum_before <= goal && sum_before + sum > goal;
-  int at_class = -1;
-  uint32_t at_place = 0;
-  if (here) {
-    int64_t tie = part_ties_from + ties_before;
-    u64 at = sum_before;
-    for (int p = p0; p < p1; p += 32) {
-      u64 own = 0;
-      uint32_t own_ties = 0, unused = 0;
-      if (p + lane < p1) own = sum_of(p + lane, own_ties, unused);
-      __syncwarp();
-      const uint32_t ties_to = warp_inclusive_scan(own_ties);
-      int64_t tie_at = tie + ties_to - own_ties;
-      own += tied(tie_at, own_ties) * w_tie;
-      const u64 to = warp_inclusive_scan(own);
-      const unsigned passed = __ballot_sync(kFull, at + to > goal);
-      if (!passed) {
-        at += __shfl_sync(kFull, to, 31);
-        tie += __shfl_sync(kFull, ties_to, 31);
-        continue;
-      }
-      if (lane == __ffs(passed) - 1) {
-        at += to - own;
-        uint32_t q[kPer];
-        row.places(p + lane, q);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const uint32_t d = q[i] - top;
-          u64 w = 0;
-          if (d < border.d) w = weigh(q[i], value_of<TYPE>(q[i]));
-          else if (d == border.d) w = tied(tie_at, 1) * w_tie, ++tie_at;
-          at += w;
-          if (at_class < 0 && w && at > goal) at_class = (p + lane) * kPer - phase + i, at_place = q[i];
-        }
-      }
-      break;
+  // ---- the one warp in which the sum passes u: 32 pieces at a time, then the lane, then the class
+  if (sum_before > goal || sum_before + sum <= goal) return;
+  int64_t tie = part_ties_from + ties_before;
+  u64 at = sum_before;
+  for (int p = p0; p < p1; p += 32) {
+    u64 own = 0;
+    uint32_t own_ties = 0, unused = 0;
+    if (p + lane < p1) own = sum_piece(p + lane, own_ties, unused);
+    __syncwarp();
+    const uint32_t ties_to = warp_inclusive_scan(own_ties);
+    int64_t tie_at = tie + ties_to - own_ties;
+    own += tied(tie_at, own_ties) * w_tie;
+    const u64 to = warp_inclusive_scan(own);
+    const unsigned passed = __ballot_sync(kFull, at + to > goal);
+    if (!passed) {
+      at += __shfl_sync(kFull, to, 31);
+      tie += __shfl_sync(kFull, ties_to, 31);
+      continue;
     }
-  } else if (lane == 0) {
-    // any warp but that one will do: all agree
-    if (warp == 0 || (warp == 1 && warps > 1)) sh.log_total = log(ldexp(static_cast<double>(total), -a.bits));
-  }
-  __syncthreads();
-  if (at_class >= 0) {
-    const double log_w = at_place == top ? 0.0 : (static_cast<double>(value_of<TYPE>(at_place)) - static_cast<double>(top_z)) / static_cast<double>(temp);
-    a.index[row_i] = first + at_class;
-    a.logprob[row_i] = static_cast<float>(log_w - sh.log_total);
-    a.kept[row_i] = static_cast<int32_t>(kept);
+    if (lane != __ffs(passed) - 1) return;
+    at += to - own;
+    uint32_t q[kPer];
+    row.places(p + lane, q);
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) {
+      uint32_t place = q[0];  // q[i], in registers
+#pragma unroll
+      for (int j = 1; j < kPer; ++j) place = i == j ? q[j] : place;
+      const uint32_t d = place - top;
+      u64 w = 0;
+      if (d < border.d) w = weigh(place, value_of<TYPE>(place));
+      else if (d == border.d) w = tied(tie_at, 1) * w_tie, ++tie_at;
+      at += w;
+      if (w && at > goal) {
+        answer(first + (p + lane) * kPer - phase + i, place, total, kept);
+        return;
+      }
+    }
+    return;
   }
 }
 
@@ -804,7 +960,6 @@ constexpr int64_t kMostClasses = int64_t(1) << 24;
 constexpr int kHeldBytes = 204800;          // of a block's shared memory: counts, and its part of the row
 // Rows from here on are searched by counts of all values: clearing and reading them costs what so many atomics do.
 constexpr int64_t kLeastCounted = 16384;
-constexpr int64_t kMostCounted = 65512;     // classes of a part: a value's count has 16 bits, up to 14 places are none's
 
 template <int TYPE, bool KEYS>
 cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
@@ -814,11 +969,11 @@ cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
   // blocks of a row: until it fits, or the SMs have work
   int blocks = 1;
   auto part = [&] { return up(div_up(n, blocks), kPer); };
-  while (blocks < kMostCluster && ((part() + kPer) * es > room || (n_rows * blocks * 2 <= sms && part() > 8192))) blocks *= 2;
+  while (blocks < kMostCluster && ((!KEYS && (part() + kPer) * es > room) || (n_rows * blocks * 2 <= sms && part() > 8192))) blocks *= 2;
   if (n_rows * blocks > INT32_MAX) return cudaErrorInvalidValue;  // more bytes than any device has
   a.part = static_cast<int>(part());
   a.held = (part() + kPer) * es <= room;
-  const int64_t threads = std::min<int64_t>(1024, std::max<int64_t>(KEYS ? 256 : 128, up(div_up(part(), 4 * kPer), 128)));
+  const int64_t threads = std::min<int64_t>(1024, std::max<int64_t>(KEYS ? 256 : 128, up(div_up(part(), 2 * kPer), 128)));
   const size_t smem = (KEYS ? kCountBytes : 0) + (a.held ? static_cast<size_t>((part() + kPer) * es) : 0);
   return launch_chained(k_draw<TYPE, KEYS>, static_cast<unsigned>(n_rows * blocks), static_cast<unsigned>(threads), smem, s, blocks, a);
 }
@@ -826,8 +981,7 @@ cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
 template <int TYPE>
 cudaError_t launch(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
   if constexpr (TYPE != GM_LOSS_F32) {
-    if (a.n_classes >= kLeastCounted && a.n_classes <= kMostCounted * kMostCluster)
-      return launch_as<TYPE, true>(a, n_rows, sms, s);
+    if (a.n_classes >= kLeastCounted) return launch_as<TYPE, true>(a, n_rows, sms, s);
   }
   return launch_as<TYPE, false>(a, n_rows, sms, s);
 }

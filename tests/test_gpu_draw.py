@@ -142,6 +142,30 @@ def test_equal_logits_are_taken_from_the_lowest_class_up(kind, classes):
     check(z, torch.rand(4, device="cuda"), top_k=classes // 3, top_p=0.75, most_unsure=0)
 
 
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("mask", ["none", "lowest", "both"])
+@pytest.mark.parametrize("rows", [2, 160])
+def test_rows_of_which_most_is_masked(kind, mask, rows):
+    """Tens of thousands of equal logits: more than a 16-bit count holds."""
+    classes = 200000 if rows == 2 else 140001
+    z, u = make(rows, classes, kind, masked=0.0, seed=5)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    hide = torch.rand(rows, classes, generator=g, device="cuda") < 0.97
+    hide[:, 1000] = False
+    low = torch.finfo(TYPES[kind]).min
+    z[hide] = -torch.inf if mask == "none" else low
+    if mask == "both":
+        z[:, ::3] = -torch.inf
+    z[:, 1000] = 1.0
+    check(z, u, temperature=0.9, top_p=0.9, most_unsure=1)
+    check(z, u, temperature=0.9, top_k=20, top_p=0.95, min_p=0.01, most_unsure=1)
+    check(z, u, most_unsure=1)
+    z[0] = low  # nothing but the mask
+    check(z[:2], u[:2], top_p=0.5)
+    check(z[:2], u[:2], top_k=70001)
+
+
 def test_zeros_of_both_signs_are_equal():
     z = torch.tensor([[0.0, -0.0, 0.0, -0.0, -1.0]], device="cuda").repeat(4, 1)
     u = torch.tensor([0.1, 0.3, 0.6, 0.9], device="cuda")
