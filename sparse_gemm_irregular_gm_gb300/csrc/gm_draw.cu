@@ -785,12 +785,12 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   if (by_min < border.d) border = Border{by_min, INT64_MAX};
 
   // KEYS: the weights of the values that occur in this part, in place of their counts, by D: those up to the border and a
-  // 0 after it; where the border lies further on, those nearest to the largest and those nearest to the border, backwards
-  // from it. What lies between, beyond 64 powers of two from either, is around 0 and rare; `sparse` where there is any. A class
-  // at the border has its mark in place of a weight.
+  // 0 after it; where the border lies further on, those nearest to the largest, those nearest to the border, backwards
+  // from it, and that of 0. What else lies between, beyond 64 powers of two from either, is rare; `sparse` where there is any.
+  // A class at the border has its mark in place of a weight.
   constexpr u64 kTie = u64(1) << 54;  // a thread sums at most 64 weights of 2^46
   const u64* weights = reinterpret_cast<const u64*>(counts);
-  constexpr uint32_t kNear = kWeights / 2;
+  constexpr uint32_t kNear = kWeights / 2, kOfZero = kWeights - 2, kNothing = kWeights - 1;
   const bool whole = border.d + 2 <= kWeights;
   uint32_t above = 0, ties = 0;
   bool sparse = false;
@@ -809,14 +809,14 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
         const uint32_t q = i * 8 + j, m = j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu, d = q - top;
         if (q >= end) continue;
         n_above += m;
-        between = between || (m && !whole && d >= kNear && end - q >= kNear - 1);
+        between = between || (m && !whole && d >= kNear && end - q >= kNear - 2 && q != kZero<TYPE>);
       }
     }
     n_above = __reduce_add_sync(kFull, n_above);
     if (lane == 0) sh.warp_above[warp] = n_above;
     auto d_of = [&](uint32_t i) { return whole || i < kNear ? i : border.d - (i - kNear); };
     u64 occurs = 0;
-    const uint32_t entries = whole ? border.d : kWeights - 1;
+    const uint32_t entries = whole ? border.d : kOfZero;
     for (uint32_t i = threadIdx.x, j = 0; i < entries; i += blockDim.x, ++j)
       if (row.count_at(top + d_of(i))) occurs |= u64(1) << j;
     sparse = __syncthreads_or(between);
@@ -826,7 +826,8 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
     __syncthreads();
     if (threadIdx.x == 0) {
       reinterpret_cast<u64*>(counts)[whole ? border.d : kNear] = kTie;
-      reinterpret_cast<u64*>(counts)[whole ? border.d + 1 : kWeights - 1] = 0;
+      reinterpret_cast<u64*>(counts)[whole ? border.d + 1 : kNothing] = 0;
+      if (!whole) reinterpret_cast<u64*>(counts)[kOfZero] = weigh(kZero<TYPE>, 0.f);
     }
     __syncthreads();
   }
@@ -848,7 +849,7 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const uint32_t d = q[i] - top;
-          x += weights[d < kNear ? d : d > border.d ? kWeights - 1 : kNear + border.d - d];
+          x += weights[d < kNear ? d : d > border.d ? kNothing : min(kNear + border.d - d, kOfZero)];
         }
       }
       n_ties += static_cast<uint32_t>(x / kTie);

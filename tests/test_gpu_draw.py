@@ -166,6 +166,19 @@ def test_rows_of_which_most_is_masked(kind, mask, rows):
     check(z[:2], u[:2], top_k=70001)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("tiny", [False, True])
+def test_zeros_and_tiny_logits_between_others(kind, tiny):
+    z, u = make(6, 30000, kind, spread=1.0, seed=12)
+    z[:, ::7] = 0.0
+    if tiny:
+        z[:, 3::11] = 2.0 ** -100 if kind == "bf16" else 2.0 ** -24
+        z[:, 5::13] = -2.0 ** -120 if kind == "bf16" else -2.0 ** -24
+    check(z, u, top_p=0.97, most_unsure=1)
+    check(z, u, temperature=0.5, most_unsure=1)
+    check(z, u, min_p=0.001, top_k=25000, most_unsure=1)
+
+
 def test_zeros_of_both_signs_are_equal():
     z = torch.tensor([[0.0, -0.0, 0.0, -0.0, -1.0]], device="cuda").repeat(4, 1)
     u = torch.tensor([0.1, 0.3, 0.6, 0.9], device="cuda")
