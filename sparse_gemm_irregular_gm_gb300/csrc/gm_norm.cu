@@ -1,12 +1,17 @@
 // gm_norm.cu -- the norms around a residual with its gate and scale (include/gm_layers.h), forward and
 // backward.
 //
-// Every element is read and written once: a group of threads holds a row in registers, the row's
-// means are the group's sums. Bound by memory. The backward pass also sums over rows (gradients of
-// weights, of a gate that is a vector): a thread keeps its columns from row to row, adds them up in
-// registers, and the blocks' sums are joined by a second kernel in a fixed order, so no value is
-// added atomically. Rows longer than a block holds (kHeldDim) are walked several times instead.
+// Every element is read and written once: a group of threads holds a row in registers, the row's means are the
+// group's sums. Memory should bound it; what stands in the way is the instructions an element takes, so what depends
+// on the column alone (after * gate, before) is formed once, and what depends on the row alone (1 / size, the
+// scale, the means) is gathered into factors of the row. The backward pass also sums over rows (gradients of
+// weights, of a gate that is a vector): a thread keeps its columns from row to row and adds them up in
+// shared memory, and the blocks' sums are joined by a second kernel in a fixed order, so no value is
+// added atomically. Two sums serve all where the gate is a vector or none: with A_j = sum over rows of dx n(f), B_j of dx,
+//   dafter = scale gate A, dgate = scale (after A + after_bias B), dafter_bias = scale gate B.
+// Rows longer than a block holds (kHeldDim) are walked several times instead.
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -21,10 +26,12 @@ namespace gm {
 
 namespace {
 
-constexpr int kPer = 8;           // elements of a row a thread holds together: 16 bytes of a 16-bit type
-constexpr int kHeldDim = 4096;    // of a row held by at most 512 threads
-constexpr int kSums = 5;          // over rows, at most: before, after, gate, before_bias, after_bias
-enum { kSumBefore, kSumAfter, kSumGate, kSumBeforeBias, kSumAfterBias };
+constexpr int kPer = 8;         // elements of a row a thread holds together: 16 bytes of a 16-bit type
+constexpr int kHeldDim = 8192;  // of a row held by at most 512 threads, 16 elements each
+constexpr int kLongBlock = 512;
+constexpr int kLeanThreads = 512;  // of the lean forward pass on an SM
+constexpr int kSums = 4;        // over rows, at most
+enum { kSumBefore, kSumA, kSumBeforeBias, kSumB };
 
 // Elements as they are in memory: 8 of them in 4 words (f32: 8).
 template <int TYPE>
@@ -66,12 +73,12 @@ __device__ __forceinline__ Raw<TYPE> pack(const float (&v)[kPer]) {
 // Columns of a thread: VEC (rows and vectors start and end on 16 bytes): 8 consecutive ones; else one
 // of every `group`, so that a warp's loads of single elements lie together.
 template <bool VEC>
-__device__ __forceinline__ int64_t column(int64_t t, int group, int i) {
-  return VEC ? t * kPer + i : t + static_cast<int64_t>(i) * group;
+__device__ __forceinline__ int column(int t, int group, int i) {
+  return VEC ? t * kPer + i : t + i * group;
 }
 // t: the thread's place in its group, plus kPer * group (VEC: group) for the next turn of a long row.
 template <int TYPE, bool VEC>
-__device__ __forceinline__ Raw<TYPE> load(const void* row, int64_t t, int group, int64_t dim) {
+__device__ __forceinline__ Raw<TYPE> load(const void* row, int t, int group, int dim) {
   Raw<TYPE> r;
 #pragma unroll
   for (int i = 0; i < kWords<TYPE>; ++i) r.w[i] = 0;
@@ -85,7 +92,7 @@ __device__ __forceinline__ Raw<TYPE> load(const void* row, int64_t t, int group,
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int64_t c = column<false>(t, group, i);
+      const int c = column<false>(t, group, i);
       if (c >= dim) continue;
       if constexpr (TYPE == GM_LOSS_F32) r.w[i] = static_cast<const uint32_t*>(row)[c];
       else r.w[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(row)[c]) << (i & 1 ? 16 : 0);
@@ -94,7 +101,7 @@ __device__ __forceinline__ Raw<TYPE> load(const void* row, int64_t t, int group,
   return r;
 }
 template <int TYPE, bool VEC>
-__device__ __forceinline__ void store(void* row, int64_t t, int group, int64_t dim, const float (&v)[kPer]) {
+__device__ __forceinline__ void store(void* row, int t, int group, int dim, const float (&v)[kPer]) {
   const Raw<TYPE> r = pack<TYPE>(v);
   if constexpr (VEC) {
 #pragma unroll
@@ -105,55 +112,124 @@ __device__ __forceinline__ void store(void* row, int64_t t, int group, int64_t d
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int64_t c = column<false>(t, group, i);
+      const int c = column<false>(t, group, i);
       if (c >= dim) continue;
       if constexpr (TYPE == GM_LOSS_F32) static_cast<uint32_t*>(row)[c] = r.w[i];
       else static_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(i & 1 ? r.w[i / 2] >> 16 : r.w[i / 2]);
     }
   }
 }
-template <int TYPE>
-__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld) {
-  return static_cast<const char*>(p) + row * ld * (TYPE == GM_LOSS_F32 ? 4 : 2);
-}
-template <int TYPE>
-__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t ld) {
-  return static_cast<char*>(p) + row * ld * (TYPE == GM_LOSS_F32 ? 4 : 2);
+// Row i of a matrix. SHORT: rows are less than 4 GB apart, so that one multiplication of 32 bits does.
+template <int TYPE, bool SHORT, class P>
+__device__ __forceinline__ P* row_at(P* m, int64_t ld, int64_t i) {
+  using Byte = std::conditional_t<std::is_const<P>::value, const char, char>;
+  constexpr int kBytes = TYPE == GM_LOSS_F32 ? 4 : 2;
+  if constexpr (SHORT) return static_cast<Byte*>(m) + static_cast<uint64_t>(static_cast<uint32_t>(i)) * static_cast<uint32_t>(ld * kBytes);
+  else return static_cast<Byte*>(m) + i * ld * kBytes;
 }
 
-// Threads that work on a row: 32 to 512 (long rows: 1024). Two sums over them, known to each. A group of one
-// warp needs no barrier; the others meet at one of their own, and the sums' places alternate, so that one
-// barrier a sum is enough.
+// Threads that work on a row. A group of one warp needs no barrier; the others meet at one of their own, and the sums' places
+// alternate, so that one barrier a sum is enough.
+template <int N>
+struct Sums {
+  float v[N];
+};
 struct Group {
   int size, id, t;
-  float2* sh;  // [2][32] of this group
+  float* sh;  // [2][2][16] of this group
   int turn = 0;
-  __device__ __forceinline__ Group(int size, float2* all) : size(size), id(threadIdx.x / size), t(threadIdx.x % size) {
+  __device__ __forceinline__ Group(int size, float* all) : size(size), id(threadIdx.x / size), t(threadIdx.x % size) {
     sh = all + id * 64;
   }
-  __device__ __forceinline__ float2 sum(float a, float b) {
+  template <int N>  // 1 or 2 sums over the group's threads, known to each
+  __device__ __forceinline__ Sums<N> sum(Sums<N> s) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      a += __shfl_xor_sync(kFull, a, d);
-      b += __shfl_xor_sync(kFull, b, d);
-    }
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int k = 0; k < N; ++k) s.v[k] += __shfl_xor_sync(kFull, s.v[k], d);
     if (size > 32) {
-      float2* at = sh + 32 * turn;
+      float* at = sh + 32 * turn;
       turn ^= 1;
-      if ((t & 31) == 0) at[t >> 5] = make_float2(a, b);
-      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(size) : "memory");
-      const int warps = size >> 5, lane = t & 31;
-      const float2 x = lane < warps ? at[lane] : make_float2(0.f, 0.f);
-      a = x.x, b = x.y;
+      if ((t & 31) == 0) {
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        a += __shfl_xor_sync(kFull, a, d);
-        b += __shfl_xor_sync(kFull, b, d);
+        for (int k = 0; k < N; ++k) at[16 * k + (t >> 5)] = s.v[k];
       }
+      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(size) : "memory");
+      const int warps = size >> 5, lane = t & 15;  // at most 16
+#pragma unroll
+      for (int k = 0; k < N; ++k) s.v[k] = lane < warps ? at[16 * k + lane] : 0.f;
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s.v[k] += __shfl_xor_sync(kFull, s.v[k], d);
     }
-    return make_float2(a, b);
+    return s;
   }
 };
+
+// Eight of a thread's columns: where they are, and which of them lie in the row.
+template <int TYPE, bool VEC>
+struct Columns {
+  int t, group, dim;
+  __device__ __forceinline__ void get(const void* p, float (&v)[kPer]) const { unpack<TYPE>(load<TYPE, VEC>(p, t, group, dim), v); }
+  __device__ __forceinline__ Raw<TYPE> raw(const void* p) const { return load<TYPE, VEC>(p, t, group, dim); }
+  __device__ __forceinline__ void put(void* p, const float (&v)[kPer]) const { store<TYPE, VEC>(p, t, group, dim, v); }
+  __device__ __forceinline__ bool inside(int i) const { return column<VEC>(t, group, i) < dim; }
+};
+// LEAN: no means taken off, no biases, a gate that is a vector or none: half the instructions of the general form.
+__device__ __forceinline__ bool is_matrix(const gm_norm& n) { return n.gate_kind == GM_GATE_MATRIX; }
+
+// What depends on the column alone: h = after * gate (that of a matrix comes with the row), hc = after_bias * gate,
+// before (as it is in memory) and its bias.
+template <int TYPE, bool VEC, bool LEAN>
+struct Weights {
+  float h[kPer], hc[LEAN ? 1 : kPer];
+  Raw<TYPE> before, before_bias;
+  __device__ __forceinline__ void read(const gm_norm& n, const Columns<TYPE, VEC>& c) {
+    // columns past the end have weights of 0
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) h[i] = n.f && c.inside(i) ? 1.f : 0.f;
+    if (n.after) c.get(n.after, h);
+    if constexpr (!LEAN) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) hc[i] = 0.f;
+      if (n.after_bias) c.get(n.after_bias, hc);
+    }
+    if (n.gate_kind == GM_GATE_VECTOR) {
+      float g[kPer];
+      c.get(n.gate, g);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) h[i] *= g[i];
+      if constexpr (!LEAN) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) hc[i] *= g[i];
+      }
+    }
+    before = before_bias = Raw<TYPE>{};
+    if (n.before) before = c.raw(n.before);
+    if (!LEAN && n.before_bias) before_bias = c.raw(n.before_bias);
+  }
+  // x' from x and f less its mean; factor: scale / size of f; g: the row's gates, of a matrix
+  __device__ __forceinline__ void update(const gm_norm& n, float (&x)[kPer], const float (&f)[kPer], float factor, const float (&g)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if constexpr (LEAN) {
+        x[i] = fmaf(f[i] * h[i], factor, x[i]);
+      } else {
+        const float p = fmaf(f[i] * h[i], factor, hc[i] * n.scale);
+        x[i] = is_matrix(n) ? fmaf(p, g[i], x[i]) : x[i] + p;
+      }
+    }
+  }
+};
+
+template <bool LEAN>
+__device__ __forceinline__ void less(float (&v)[kPer], float mean) {
+  if constexpr (!LEAN) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] -= mean;
+  }
+}
 
 struct NormArgs {
   gm_norm n;
@@ -163,122 +239,91 @@ struct NormArgs {
   float4* stats;
 };
 
-// What a thread does with its eight columns of a row; shared by the kernels that hold a row and those that
-// walk it.
-template <int TYPE, bool VEC>
-struct Columns {
-  const gm_norm& n;
-  int64_t t;
-  int group;
-  __device__ __forceinline__ void get(const void* p, float (&v)[kPer]) const {
-    unpack<TYPE>(load<TYPE, VEC>(p, t, group, n.dim), v);
-  }
-  __device__ __forceinline__ void row(const void* p, int64_t row, int64_t ld, float (&v)[kPer]) const {
-    get(row_at<TYPE>(p, row, ld), v);
-  }
-  __device__ __forceinline__ bool inside(int i) const { return column<VEC>(t, group, i) < n.dim; }
-  // scale * gate
-  __device__ __forceinline__ void factor(int64_t row_, float (&v)[kPer]) const {
-    if (n.gate_kind == GM_GATE_NONE) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = n.scale;
-      return;
-    }
-    row(n.gate, n.gate_kind == GM_GATE_MATRIX ? row_ : 0, n.gate_ld, v);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] *= n.scale;
-  }
-  // n(f) * after + after_bias
-  __device__ __forceinline__ void project(const float (&unit)[kPer], float (&p)[kPer]) const {
-    if (!n.after) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) p[i] = unit[i];
-      return;
-    }
-    weigh(n.after, n.after_bias, unit, p);
-  }
-  __device__ __forceinline__ void weigh(const void* weight, const void* bias, const float (&unit)[kPer],
-                                        float (&p)[kPer]) const {
-    float w[kPer];
-    get(weight, w);
-    if (bias) {
-      float b[kPer];
-      get(bias, b);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) p[i] = fmaf(unit[i], w[i], b[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) p[i] = unit[i] * w[i];
-    }
-  }
-  // x' from x and f, given f's statistics
-  __device__ __forceinline__ void update(int64_t row_, float2 of_f, const float (&f)[kPer], float (&x)[kPer]) const {
-    float u[kPer], g[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) u[i] = n.after ? (f[i] - of_f.x) * of_f.y : f[i];
-    project(u, u);
-    factor(row_, g);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = fmaf(g[i], u[i], x[i]);
-  }
-};
-
-// Mean and 1 / size of a row; SUM(g) gives the row's sum of g(i, value) over its elements.
-template <class SUM>
+// Mean and 1 / size of a row: sum(g) gives the sum of g(value) over its elements.
+template <bool LEAN, class SUM>
 __device__ __forceinline__ float2 statistics(const gm_norm& n, float inv_dim, SUM&& sum) {
   float mean = 0.f;
-  if (n.norm == GM_NORM_LAYER) mean = sum([](float v) { return v; }) * inv_dim;
-  const float square = sum([mean](float v) { return (v - mean) * (v - mean); }) * inv_dim;
+  if (!LEAN && n.norm == GM_NORM_LAYER) mean = sum([](float v) { return v; }) * inv_dim;
+  const float square = sum([mean](float v) { return LEAN ? v * v : (v - mean) * (v - mean); }) * inv_dim;
   return make_float2(mean, 1.f / sqrtf(square + n.eps));
 }
 
 // ---- forward -------------------------------------------------------------------------------------
 // A row in registers: NV turns of 8 columns a thread.
-template <int TYPE, bool VEC, int NV>
-__global__ void __launch_bounds__(512) k_norm_forward(const NormArgs a, int group) {
-  __shared__ float2 sh[512 / 32 * 64];
+template <int TYPE, bool VEC, int NV, bool LEAN>
+__global__ void __launch_bounds__(512, 1) k_norm_forward(const NormArgs a, int group) {
+  __shared__ float sh[16 * 64];
   chain_wait();
   Group g(group, sh);
-  const int groups = blockDim.x / group;
   const gm_norm& n = a.n;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id; row < n.n_rows;
-       row += static_cast<int64_t>(gridDim.x) * groups) {
-    float x[NV][kPer];
+  const int dim = static_cast<int>(n.dim), groups = blockDim.x / group;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  Columns<TYPE, VEC> c[NV];
+  Weights<TYPE, VEC, LEAN> w[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    c[k] = Columns<TYPE, VEC>{g.t + k * (VEC ? group : group * kPer), group, dim};
+    w[k].read(n, c[k]);
+  }
+  constexpr auto at = [](auto* m, int64_t ld, int64_t i) { return row_at<TYPE, LEAN>(m, ld, i); };
+  Raw<TYPE> x_next[NV], f_next[NV];
+  auto ask = [&](int64_t i) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      x_next[k] = c[k].raw(at(n.x, n.x_ld, i));
+      if (n.f) f_next[k] = c[k].raw(at(n.f, n.f_ld, i));
+    }
+  };
+  if (row < n.n_rows) ask(row);
+  for (; row < n.n_rows; row += step) {
     float2 of_f = make_float2(0.f, 1.f), of_x = make_float2(0.f, 1.f);
-    auto cols = [&](int v) { return Columns<TYPE, VEC>{n, g.t + int64_t(v) * (VEC ? group : group * kPer), group}; };
-    auto row_sum = [&](const float (&v)[NV][kPer]) {
-      return [&](auto&& f) {
-        float s = 0.f;
+    float x[NV][kPer], f[NV][kPer];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      unpack<TYPE>(x_next[k], x[k]);
+      if (n.f) unpack<TYPE>(f_next[k], f[k]);
+    }
+    if (row + step < n.n_rows) ask(row + step);
+    auto over = [&](const float (&v)[NV][kPer]) {
+      return [&](auto&& of) {
+        Sums<1> s = {{0.f}};
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) s += cols(k).inside(i) ? f(v[k][i]) : 0.f;
-        return g.sum(s, 0.f).x;
+          for (int i = 0; i < kPer; ++i) s.v[0] += LEAN || c[k].inside(i) ? of(v[k][i]) : 0.f;
+        return g.sum(s).v[0];
       };
     };
-#pragma unroll
-    for (int k = 0; k < NV; ++k) cols(k).row(n.x, row, n.x_ld, x[k]);
     if (n.f) {
-      float f[NV][kPer];
+      if (n.after) of_f = statistics<LEAN>(n, a.inv_dim, over(f));
 #pragma unroll
-      for (int k = 0; k < NV; ++k) cols(k).row(n.f, row, n.f_ld, f[k]);
-      if (n.after) of_f = statistics(n, a.inv_dim, row_sum(f));
-#pragma unroll
-      for (int k = 0; k < NV; ++k) cols(k).update(row, of_f, f[k], x[k]);
+      for (int k = 0; k < NV; ++k) {
+        float gate[kPer];
+        if (!LEAN && is_matrix(n)) c[k].get(at(n.gate, n.gate_ld, row), gate);
+        less<LEAN>(f[k], of_f.x);
+        w[k].update(n, x[k], f[k], n.scale * of_f.y, gate);
+      }
     }
     if (a.x_out) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        store<TYPE, VEC>(row_at<TYPE>(a.x_out, row, a.x_out_ld), cols(k).t, group, n.dim, x[k]);
+      for (int k = 0; k < NV; ++k) c[k].put(at(a.x_out, a.x_out_ld, row), x[k]);
     }
     if (a.y) {
-      of_x = statistics(n, a.inv_dim, row_sum(x));
+      of_x = statistics<LEAN>(n, a.inv_dim, over(x));
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
+        float b[kPer];
+        unpack<TYPE>(w[k].before, b);
+        less<LEAN>(x[k], of_x.x);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[k][i] = (x[k][i] - of_x.x) * of_x.y;
-        cols(k).weigh(n.before, n.before_bias, x[k], x[k]);
-        store<TYPE, VEC>(row_at<TYPE>(a.y, row, a.y_ld), cols(k).t, group, n.dim, x[k]);
+        for (int i = 0; i < kPer; ++i) x[k][i] = x[k][i] * of_x.y * b[i];
+        if constexpr (!LEAN) {
+          unpack<TYPE>(w[k].before_bias, b);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) x[k][i] += b[i];
+        }
+        c[k].put(at(a.y, a.y_ld, row), x[k]);
       }
     }
     if (a.stats && g.t == 0) a.stats[row] = make_float4(of_f.x, of_f.y, of_x.x, of_x.y);
@@ -288,52 +333,58 @@ __global__ void __launch_bounds__(512) k_norm_forward(const NormArgs a, int grou
 // Rows longer than that: a block walks its row once for each sum and once to write it. What it reads again
 // comes from L2. x is read for the last time before x_out is written, which may be the same memory.
 template <int TYPE, bool VEC>
-__global__ void __launch_bounds__(1024) k_norm_forward_long(const NormArgs a) {
-  __shared__ float2 sh[64];
+__global__ void __launch_bounds__(kLongBlock) k_norm_forward_long(const NormArgs a) {
+  constexpr bool LEAN = false;
+  __shared__ float sh[64];
   chain_wait();
-  const int group = blockDim.x;
-  Group g(group, sh);
+  Group g(kLongBlock, sh);
   const gm_norm& n = a.n;
+  const int dim = static_cast<int>(n.dim);
   for (int64_t row = blockIdx.x; row < n.n_rows; row += gridDim.x) {
+    auto at_row = [&](auto* m, int64_t ld) { return row_at<TYPE, false>(m, ld, row); };
     float2 of_f = make_float2(0.f, 1.f), of_x = make_float2(0.f, 1.f);
     auto walk = [&](auto&& body) {
-      for (int64_t at = 0; at < n.dim; at += group * kPer) {
-        const Columns<TYPE, VEC> c{n, g.t + (VEC ? at / kPer : at), group};
-        body(c);
-      }
-    };
-    auto updated = [&](const Columns<TYPE, VEC>& c, float (&x)[kPer]) {
-      c.row(n.x, row, n.x_ld, x);
-      if (!n.f) return;
-      float f[kPer];
-      c.row(n.f, row, n.f_ld, f);
-      c.update(row, of_f, f, x);
+      for (int at = 0; at < dim; at += kLongBlock * kPer)
+        body(Columns<TYPE, VEC>{g.t + (VEC ? at / kPer : at), kLongBlock, dim});
     };
     auto total = [&](auto&& values) {
-      return [&](auto&& f) {
-        float s = 0.f;
+      return [&](auto&& of) {
+        Sums<1> s = {{0.f}};
         walk([&](const Columns<TYPE, VEC>& c) {
           float v[kPer];
           values(c, v);
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) s += c.inside(i) ? f(v[i]) : 0.f;
+          for (int i = 0; i < kPer; ++i) s.v[0] += c.inside(i) ? of(v[i]) : 0.f;
         });
-        return g.sum(s, 0.f).x;
+        return g.sum(s).v[0];
       };
     };
-    if (n.after)
-      of_f = statistics(n, a.inv_dim, total([&](const Columns<TYPE, VEC>& c, float (&v)[kPer]) { c.row(n.f, row, n.f_ld, v); }));
-    if (a.y) of_x = statistics(n, a.inv_dim, total(updated));
+    Weights<TYPE, VEC, LEAN> w;
+    auto updated = [&](const Columns<TYPE, VEC>& c, float (&x)[kPer]) {
+      c.get(at_row(n.x, n.x_ld), x);
+      w.read(n, c);
+      if (!n.f) return;
+      float f[kPer], gate[kPer];
+      c.get(at_row(n.f, n.f_ld), f);
+      less<LEAN>(f, of_f.x);
+      if (is_matrix(n)) c.get(at_row(n.gate, n.gate_ld), gate);
+      w.update(n, x, f, n.scale * of_f.y, gate);
+    };
+    if (n.after) of_f = statistics<LEAN>(n, a.inv_dim, total([&](const Columns<TYPE, VEC>& c, float (&v)[kPer]) { c.get(at_row(n.f, n.f_ld), v); }));
+    if (a.y) of_x = statistics<LEAN>(n, a.inv_dim, total(updated));
     walk([&](const Columns<TYPE, VEC>& c) {
-      float x[kPer];
+      float x[kPer], b[kPer];
       updated(c, x);
-      if (a.x_out) store<TYPE, VEC>(row_at<TYPE>(a.x_out, row, a.x_out_ld), c.t, group, n.dim, x);
-      if (a.y) {
+      if (a.x_out) c.put(at_row(a.x_out, a.x_out_ld), x);
+      if (!a.y) return;
+      less<LEAN>(x, of_x.x);
+      unpack<TYPE>(w.before, b);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = (x[i] - of_x.x) * of_x.y;
-        c.weigh(n.before, n.before_bias, x, x);
-        store<TYPE, VEC>(row_at<TYPE>(a.y, row, a.y_ld), c.t, group, n.dim, x);
-      }
+      for (int i = 0; i < kPer; ++i) x[i] = x[i] * of_x.y * b[i];
+      unpack<TYPE>(w.before_bias, b);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] += b[i];
+      c.put(at_row(a.y, a.y_ld), x);
     });
     if (a.stats && g.t == 0) a.stats[row] = make_float4(of_f.x, of_f.y, of_x.x, of_x.y);
   }
@@ -352,259 +403,283 @@ struct BackArgs {
   float4* means;    // long rows: [row] the four means of the formulas
 };
 
-// A thread's columns of one row on the way back.
-template <int TYPE, bool VEC>
-struct Back {
-  float gy[kPer], unit[kPer], unit_f[kPer], p[kPer], factor[kPer], dx[kPer], dp[kPer];
-  // gy, n(x'), n(f), p, scale * gate
-  __device__ __forceinline__ void start(const BackArgs& a, const Columns<TYPE, VEC>& c, int64_t row, float4 st,
-                                        const Raw<TYPE>& x_raw, const Raw<TYPE>& f_raw, const Raw<TYPE>& gy_raw) {
-    const gm_norm& n = a.n;
-    float x[kPer];
-    unpack<TYPE>(x_raw, x);
-    unpack<TYPE>(gy_raw, gy);
-    if (n.f) {
-      unpack<TYPE>(f_raw, unit_f);
-      if (n.after) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) unit_f[i] = (unit_f[i] - st.x) * st.y;
-      }
-      c.project(unit_f, p);
-      c.factor(row, factor);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = fmaf(factor[i], p[i], x[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) unit[i] = (x[i] - st.z) * st.w;
-  }
-  // sums of d n(x') and of d, d = gy * before
-  __device__ __forceinline__ float2 sums_x(const BackArgs& a, const Columns<TYPE, VEC>& c, float (&d)[kPer]) const {
-    c.get(a.n.before, d);
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      d[i] *= gy[i];
-      s.x += c.inside(i) ? d[i] * unit[i] : 0.f;
-      s.y += d[i];
-    }
-    return s;
-  }
-  __device__ __forceinline__ void to_x(const BackArgs& a, const Raw<TYPE>& gx_raw, const float (&d)[kPer], float2 mean,
-                                       float4 st) {
-    unpack<TYPE>(gx_raw, dx);
-    if (!a.gy) return;
-    if (a.n.norm != GM_NORM_LAYER) mean.y = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) dx[i] = fmaf(d[i] - fmaf(unit[i], mean.x, mean.y), st.w, dx[i]);
-  }
-  // dp, and sums of e n(f) and of e, e = dp * after
-  __device__ __forceinline__ float2 sums_f(const BackArgs& a, const Columns<TYPE, VEC>& c, float (&e)[kPer]) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) dp[i] = factor[i] * dx[i];
-    float2 s = make_float2(0.f, 0.f);
-    if (!a.n.after) return s;
-    c.get(a.n.after, e);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      e[i] *= dp[i];
-      s.x += c.inside(i) ? e[i] * unit_f[i] : 0.f;
-      s.y += c.inside(i) ? e[i] : 0.f;
-    }
-    return s;
-  }
-  __device__ __forceinline__ void to_f(const BackArgs& a, const float (&e)[kPer], float2 mean, float4 st, float (&df)[kPer]) const {
-    if (a.n.norm != GM_NORM_LAYER) mean.y = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      df[i] = a.n.after ? (e[i] - fmaf(unit_f[i], mean.x, mean.y)) * st.y : dp[i];
-  }
-  // by the gate's elements
-  __device__ __forceinline__ void to_gate(const BackArgs& a, float (&dg)[kPer]) const {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) dg[i] = a.n.scale * dx[i] * p[i];
-  }
-  template <int N>
-  __device__ __forceinline__ void add(const BackArgs& a, float (&acc)[N][kPer]) const {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[kSumBefore][i] = fmaf(gy[i], unit[i], acc[kSumBefore][i]);
-    if constexpr (N > kSumBeforeBias) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[kSumBeforeBias][i] += gy[i];
-    }
-    if (!a.need_x || !a.n.f) return;
-    if (a.n.after) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[kSumAfter][i] = fmaf(dp[i], unit_f[i], acc[kSumAfter][i]);
-      if constexpr (N > kSumAfterBias) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[kSumAfterBias][i] += dp[i];
-      }
-    }
-    if (a.n.gate_kind == GM_GATE_VECTOR) {
-      float dg[kPer];
-      to_gate(a, dg);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[kSumGate][i] += dg[i];
-    }
-  }
-};
-
-// A row's four tensors as they are in memory.
+// Eight columns of a row as they are in memory.
 template <int TYPE>
 struct RowIn {
-  Raw<TYPE> x, f, gx, gy;
-  float4 st;
+  Raw<TYPE> x, f, gx, gy, gate;
 };
-template <int TYPE, bool VEC>
-__device__ __forceinline__ RowIn<TYPE> read_row(const BackArgs& a, int64_t t, int group, int64_t row) {
-  RowIn<TYPE> r = {};
-  const gm_norm& n = a.n;
-  r.st = a.stats[row];
-  r.x = load<TYPE, VEC>(row_at<TYPE>(n.x, row, n.x_ld), t, group, n.dim);
-  if (n.f) r.f = load<TYPE, VEC>(row_at<TYPE>(n.f, row, n.f_ld), t, group, n.dim);
-  if (a.gx) r.gx = load<TYPE, VEC>(row_at<TYPE>(a.gx, row, a.gx_ld), t, group, n.dim);
-  if (a.gy) r.gy = load<TYPE, VEC>(row_at<TYPE>(a.gy, row, a.gy_ld), t, group, n.dim);
-  return r;
+
+// A thread's eight columns of one row on the way back. What sums over rows is handed to add(which, values). Columns past the
+// row's end have weights, and so all terms of a row's sums, of 0.
+template <int TYPE, bool VEC, bool LEAN>
+struct Back {
+  const BackArgs& a;
+  const Weights<TYPE, VEC, LEAN>& w;
+  const RowIn<TYPE>& in;
+  float4 st;
+  // x: x' less its mean; d = gy * before; the row's sums of d x and of d
+  template <class ADD>
+  __device__ __forceinline__ void start(float (&x)[kPer], float (&d)[kPer], Sums<2>& s, ADD&& add) const {
+    unpack<TYPE>(in.x, x);
+    if (a.n.f) {
+      float f[kPer], gate[kPer];
+      unpack<TYPE>(in.f, f);
+      less<LEAN>(f, st.x);
+      if (!LEAN && is_matrix(a.n)) unpack<TYPE>(in.gate, gate);
+      w.update(a.n, x, f, a.n.scale * st.y, gate);
+    }
+    less<LEAN>(x, st.z);
+    if (!a.gy) return;
+    float t[kPer];
+    unpack<TYPE>(in.gy, d);
+    if constexpr (!LEAN) add(kSumBeforeBias, d, 1.f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t[i] = d[i] * x[i];
+    add(kSumBefore, t, st.w);
+    float b[kPer];
+    unpack<TYPE>(w.before, b);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      s.v[0] = fmaf(b[i], t[i], s.v[0]);
+      d[i] *= b[i];
+      if constexpr (!LEAN) s.v[1] += d[i];
+    }
+  }
+  // dx, in place of d. mean: of d n(x') and of d
+  __device__ __forceinline__ void to_x(const float (&x)[kPer], float (&d)[kPer], Sums<2> mean) const {
+    float gx[kPer];
+    unpack<TYPE>(in.gx, gx);
+    if (!a.gy) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) d[i] = gx[i];
+      return;
+    }
+    const float k = -mean.v[0] * st.w * st.w, m = -mean.v[1] * st.w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) d[i] = fmaf(x[i], k, fmaf(d[i], st.w, LEAN ? gx[i] : gx[i] + m));
+  }
+  // e = gate * after * dx, in place of dx; f less its mean; the row's sums of e f and of e
+  template <class ADD, class GATE>
+  __device__ __forceinline__ void past_gate(float (&d)[kPer], float (&f)[kPer], Sums<2>& s, ADD&& add, GATE&& gate_out) const {
+    const gm_norm& n = a.n;
+    unpack<TYPE>(in.f, f);
+    less<LEAN>(f, st.x);
+    if (!LEAN && is_matrix(n)) {
+      float t[kPer], gate[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        t[i] = fmaf(f[i] * st.y, w.h[i], w.hc[LEAN ? 0 : i]) * (n.scale * d[i]);
+      }
+      gate_out(t);
+      unpack<TYPE>(in.gate, gate);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) d[i] *= gate[i];
+    }
+    float t[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t[i] = d[i] * f[i];
+    add(kSumA, t, st.y);
+    if constexpr (!LEAN) add(kSumB, d, 1.f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      s.v[0] = fmaf(w.h[i], t[i], s.v[0]);
+      d[i] *= w.h[i];
+      if constexpr (!LEAN) s.v[1] += d[i];
+    }
+  }
+  // df, in place of e. mean: of e n(f) and of e
+  __device__ __forceinline__ void to_f(float (&e)[kPer], const float (&f)[kPer], Sums<2> mean) const {
+    const float r = a.n.scale * st.y, k = -mean.v[0] * r * st.y, m = -mean.v[1] * r;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = fmaf(f[i], k, LEAN ? e[i] * r : fmaf(e[i], r, m));
+  }
+};
+// The means that a row's two sums give; unit: what n() divided by, inverted. Without a norm: none.
+template <bool LEAN>
+__device__ __forceinline__ Sums<2> means_of(const gm_norm& n, Group& g, Sums<2> s, float inv_dim, float unit) {
+  if constexpr (LEAN) s.v[0] = g.sum(Sums<1>{{s.v[0]}}).v[0];
+  else s = g.sum(s);
+  s.v[0] *= inv_dim * unit, s.v[1] *= inv_dim;
+  if (LEAN || n.norm != GM_NORM_LAYER) s.v[1] = 0.f;
+  return s;
 }
 
-// Rows held by a group; the next row is under way while one is worked on. SUMS: 3 (no biases) or 5.
-template <int TYPE, bool VEC, int SUMS>
-__global__ void __launch_bounds__(512) k_norm_backward(const BackArgs a, int group) {
-  __shared__ float2 sh[512 / 32 * 64];
+// Rows held by a group: NV turns of 8 columns a thread, the next row under way. The sums over rows are kept in shared
+// memory, each thread's own columns.
+template <int TYPE, bool VEC, int NV, bool LEAN>
+__global__ void __launch_bounds__(512, 1) k_norm_backward(const BackArgs a, int group) {
+  __shared__ float sh[16 * 64];
+  extern __shared__ float4 acc[];  // [sum][turn][2][thread]
   chain_wait();
   Group g(group, sh);
-  const int groups = blockDim.x / group;
   const gm_norm& n = a.n;
-  const Columns<TYPE, VEC> c{n, g.t, group};
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  float acc[SUMS][kPer];
-#pragma unroll
-  for (int s = 0; s < SUMS; ++s)
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[s][i] = 0.f;
+  const int dim = static_cast<int>(n.dim), groups = blockDim.x / group;
+  constexpr int kHere = LEAN ? 2 : 4;
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id;
-  RowIn<TYPE> next;
-  if (row < n.n_rows) next = read_row<TYPE, VEC>(a, g.t, group, row);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  Columns<TYPE, VEC> c[NV];
+  Weights<TYPE, VEC, LEAN> w[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    c[k] = Columns<TYPE, VEC>{g.t + k * (VEC ? group : group * kPer), group, dim};
+    w[k].read(n, c[k]);
+  }
+  constexpr auto at = [](auto* m, int64_t ld, int64_t i) { return row_at<TYPE, LEAN>(m, ld, i); };
+  if (a.sums) {
+#pragma unroll
+    for (int s = 0; s < 2 * NV * kHere; ++s) acc[s * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  auto adder = [&](int k) {
+    return [&, k](int which, const float (&v)[kPer], float by) {
+      if (!a.sums) return;
+      float4* at = acc + 2 * (which * NV + k) * blockDim.x + threadIdx.x;
+      float4 x = at[0], y = at[blockDim.x];
+      x.x = fmaf(v[0], by, x.x), x.y = fmaf(v[1], by, x.y), x.z = fmaf(v[2], by, x.z), x.w = fmaf(v[3], by, x.w);
+      y.x = fmaf(v[4], by, y.x), y.y = fmaf(v[5], by, y.y), y.z = fmaf(v[6], by, y.z), y.w = fmaf(v[7], by, y.w);
+      at[0] = x, at[blockDim.x] = y;
+    };
+  };
+  RowIn<TYPE> next[NV];  // gx, wanted last, waits in L2
+  float4 st_next;
+  auto ask = [&](int64_t i) {
+    st_next = a.stats[i];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      next[k].x = c[k].raw(at(n.x, n.x_ld, i));
+      if (n.f) next[k].f = c[k].raw(at(n.f, n.f_ld, i));
+      if (a.gy) next[k].gy = c[k].raw(at(a.gy, a.gy_ld, i));
+      if (!LEAN && is_matrix(n)) next[k].gate = c[k].raw(at(n.gate, n.gate_ld, i));
+      if (VEC && a.gx && c[k].inside(0))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(at(a.gx, a.gx_ld, i)) + c[k].t * kPer * (TYPE == GM_LOSS_F32 ? 4 : 2)));
+    }
+  };
+  if (row < n.n_rows) ask(row);
   for (; row < n.n_rows; row += step) {
-    const RowIn<TYPE> in = next;
-    if (row + step < n.n_rows) next = read_row<TYPE, VEC>(a, g.t, group, row + step);
-    Back<TYPE, VEC> b;
-    b.start(a, c, row, in.st, in.x, in.f, in.gy);
+    RowIn<TYPE> in[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      in[k] = next[k];
+      in[k].gx = Raw<TYPE>{};
+      if (a.gx) in[k].gx = c[k].raw(at(a.gx, a.gx_ld, row));
+    }
+    const float4 st = st_next;
+    if (row + step < n.n_rows) ask(row + step);
+    using B = Back<TYPE, VEC, LEAN>;
+    float x[NV][kPer], d[NV][kPer];
+    Sums<2> s = {{0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) B{a, w[k], in[k], st}.start(x[k], d[k], s, adder(k));
     if (a.need_x) {
-      float d[kPer];
-      float2 mean = make_float2(0.f, 0.f);
-      if (a.gy) {
-        mean = b.sums_x(a, c, d);
-        mean = g.sum(mean.x, mean.y);
-        mean.x *= a.inv_dim, mean.y *= a.inv_dim;
+      if (a.gy) s = means_of<LEAN>(a.n, g, s, a.inv_dim, st.w);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        B{a, w[k], in[k], st}.to_x(x[k], d[k], s);
+        if (a.o.x) c[k].put(at(a.o.x, a.o.x_ld, row), d[k]);
       }
-      b.to_x(a, in.gx, d, mean, in.st);
-      if (a.o.x) store<TYPE, VEC>(row_at<TYPE>(a.o.x, row, a.o.x_ld), g.t, group, n.dim, b.dx);
       if (n.f) {
-        mean = b.sums_f(a, c, d);
-        if (n.after && a.o.f) {
-          mean = g.sum(mean.x, mean.y);
-          mean.x *= a.inv_dim, mean.y *= a.inv_dim;
-        }
+        s = Sums<2>{{0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          B{a, w[k], in[k], st}.past_gate(d[k], x[k], s, adder(k), [&](const float (&v)[kPer]) {
+            if (a.o.gate) c[k].put(at(a.o.gate, a.o.gate_ld, row), v);
+          });
         if (a.o.f) {
-          float df[kPer];
-          b.to_f(a, d, mean, in.st, df);
-          store<TYPE, VEC>(row_at<TYPE>(a.o.f, row, a.o.f_ld), g.t, group, n.dim, df);
-        }
-        if (a.o.gate && n.gate_kind == GM_GATE_MATRIX) {
-          b.to_gate(a, d);
-          store<TYPE, VEC>(row_at<TYPE>(a.o.gate, row, a.o.gate_ld), g.t, group, n.dim, d);
+          s = n.after ? means_of<LEAN>(a.n, g, s, a.inv_dim, st.y) : Sums<2>{{0.f, 0.f}};
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            B{a, w[k], in[k], st}.to_f(d[k], x[k], s);
+            c[k].put(at(a.o.f, a.o.f_ld, row), d[k]);
+          }
         }
       }
     }
-    if (a.sums) b.add(a, acc);
   }
   if (!a.sums) return;
-  // the block's groups one after another, in shared memory
-  extern __shared__ float block_sums[];  // [SUMS][dim] where a block has several groups
+  __syncthreads();
+  if (g.id != 0) return;  // one group adds the others' in their order
   float* out = a.sums + static_cast<int64_t>(blockIdx.x) * kSums * n.dim;
-  float* to = groups > 1 ? block_sums : out;
-  for (int k = 0; k < groups; ++k) {
-    if (g.id == k) {
 #pragma unroll
-      for (int s = 0; s < SUMS; ++s)
+  for (int s = 0; s < kHere; ++s)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (c.inside(i)) {
-            float* at = to + s * n.dim + column<VEC>(g.t, group, i);
-            *at = k > 0 ? *at + acc[s][i] : acc[s][i];
-          }
+    for (int k = 0; k < NV; ++k) {
+      float v[kPer] = {};
+      for (int j = 0; j < groups; ++j) {
+        const float4* at = acc + 2 * (s * NV + k) * blockDim.x + j * group + g.t;
+        const float4 x = at[0], y = at[blockDim.x];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (c[k].inside(i)) out[s * n.dim + column<VEC>(c[k].t, group, i)] = v[i];
     }
-    if (groups > 1) __syncthreads();
-  }
-  if (groups > 1)
-    for (int64_t i = threadIdx.x; i < SUMS * n.dim; i += blockDim.x) out[i] = block_sums[i];
+}
+
+// Eight columns of a row of the long ones, and their weights.
+template <int TYPE, bool VEC, bool LEAN>
+__device__ __forceinline__ void read_long(const BackArgs& a, const Columns<TYPE, VEC>& c, int64_t row, RowIn<TYPE>& in,
+                                          Weights<TYPE, VEC, LEAN>& w) {
+  const gm_norm& n = a.n;
+  auto get = [&](const void* m, int64_t ld) { return c.raw(row_at<TYPE, false>(m, ld, row)); };
+  in = RowIn<TYPE>{};
+  in.x = get(n.x, n.x_ld);
+  if (n.f) in.f = get(n.f, n.f_ld);
+  if (a.gy) in.gy = get(a.gy, a.gy_ld);
+  if (a.gx) in.gx = get(a.gx, a.gx_ld);
+  if (is_matrix(n)) in.gate = get(n.gate, n.gate_ld);
+  w.read(n, c);
 }
 
 // Rows longer than that: a block walks its row three times and leaves the row's means, by which
 // k_norm_columns sums over rows.
 template <int TYPE, bool VEC>
-__global__ void __launch_bounds__(512) k_norm_backward_long(const BackArgs a) {
-  __shared__ float2 sh[64];
+__global__ void __launch_bounds__(kLongBlock) k_norm_backward_long(const BackArgs a) {
+  constexpr bool LEAN = false;
+  __shared__ float sh[64];
   chain_wait();
-  const int group = blockDim.x;
-  Group g(group, sh);
+  Group g(kLongBlock, sh);
   const gm_norm& n = a.n;
+  const int dim = static_cast<int>(n.dim);
   for (int64_t row = blockIdx.x; row < n.n_rows; row += gridDim.x) {
-    float2 mean_x = make_float2(0.f, 0.f), mean_f = make_float2(0.f, 0.f);
+    const float4 st = a.stats[row];
+    auto at_row = [&](void* m, int64_t ld) { return row_at<TYPE, false>(m, ld, row); };
+    Sums<2> mean_x = {{0.f, 0.f}}, mean_f = {{0.f, 0.f}}, s = {{0.f, 0.f}}, unused = {{0.f, 0.f}};
+    auto none = [](int, const float (&)[kPer], float) {};
+    float x[kPer], d[kPer];
     auto walk = [&](auto&& body) {
-      for (int64_t at = 0; at < n.dim; at += group * kPer) {
-        const Columns<TYPE, VEC> c{n, g.t + (VEC ? at / kPer : at), group};
-        const RowIn<TYPE> in = read_row<TYPE, VEC>(a, c.t, group, row);
-        Back<TYPE, VEC> b;
-        b.start(a, c, row, in.st, in.x, in.f, in.gy);
-        body(c, b, in);
+      for (int at = 0; at < dim; at += kLongBlock * kPer) {
+        const Columns<TYPE, VEC> c{g.t + (VEC ? at / kPer : at), kLongBlock, dim};
+        RowIn<TYPE> in;
+        Weights<TYPE, VEC, LEAN> w;
+        read_long(a, c, row, in, w);
+        body(Back<TYPE, VEC, LEAN>{a, w, in, st}, c);
       }
     };
-    auto mean_of = [&](float2 s) {
-      s = g.sum(s.x, s.y);
-      return make_float2(s.x * a.inv_dim, s.y * a.inv_dim);
-    };
-    float2 s = make_float2(0.f, 0.f);
     if (a.gy) {
-      walk([&](const Columns<TYPE, VEC>& c, Back<TYPE, VEC>& b, const RowIn<TYPE>&) {
-        float d[kPer];
-        const float2 x = b.sums_x(a, c, d);
-        s.x += x.x, s.y += x.y;
-      });
-      mean_x = mean_of(s);
+      walk([&](const auto& b, const auto&) { b.start(x, d, s, none); });
+      mean_x = means_of<LEAN>(a.n, g, s, a.inv_dim, st.w);
     }
-    auto to_x = [&](const Columns<TYPE, VEC>& c, Back<TYPE, VEC>& b, const RowIn<TYPE>& in) {
-      float d[kPer];
-      if (a.gy) b.sums_x(a, c, d);
-      b.to_x(a, in.gx, d, mean_x, in.st);
-    };
     if (n.after && a.o.f) {
-      s = make_float2(0.f, 0.f);
-      walk([&](const Columns<TYPE, VEC>& c, Back<TYPE, VEC>& b, const RowIn<TYPE>& in) {
-        float e[kPer];
-        to_x(c, b, in);
-        const float2 x = b.sums_f(a, c, e);
-        s.x += x.x, s.y += x.y;
+      s = Sums<2>{{0.f, 0.f}};
+      walk([&](const auto& b, const auto&) {
+        b.start(x, d, unused, none);
+        b.to_x(x, d, mean_x);
+        b.past_gate(d, x, s, none, [](const float (&)[kPer]) {});
       });
-      mean_f = mean_of(s);
+      mean_f = means_of<LEAN>(a.n, g, s, a.inv_dim, st.y);
     }
-    walk([&](const Columns<TYPE, VEC>& c, Back<TYPE, VEC>& b, const RowIn<TYPE>& in) {
-      to_x(c, b, in);
-      if (a.o.x) store<TYPE, VEC>(row_at<TYPE>(a.o.x, row, a.o.x_ld), c.t, group, n.dim, b.dx);
+    walk([&](const auto& b, const auto& c) {
+      b.start(x, d, unused, none);
+      b.to_x(x, d, mean_x);
+      if (a.o.x) c.put(at_row(a.o.x, a.o.x_ld), d);
       if (!n.f) return;
-      float e[kPer], df[kPer];
-      b.sums_f(a, c, e);
-      if (a.o.f) {
-        b.to_f(a, e, mean_f, in.st, df);
-        store<TYPE, VEC>(row_at<TYPE>(a.o.f, row, a.o.f_ld), c.t, group, n.dim, df);
-      }
-      if (a.o.gate && n.gate_kind == GM_GATE_MATRIX) {
-        b.to_gate(a, df);
-        store<TYPE, VEC>(row_at<TYPE>(a.o.gate, row, a.o.gate_ld), c.t, group, n.dim, df);
-      }
+      b.past_gate(d, x, unused, none, [&](const float (&v)[kPer]) {
+        if (a.o.gate) c.put(at_row(a.o.gate, a.o.gate_ld), v);
+      });
+      if (!a.o.f) return;
+      b.to_f(d, x, mean_f);
+      c.put(at_row(a.o.f, a.o.f_ld), d);
     });
-    if (g.t == 0) a.means[row] = make_float4(mean_x.x, mean_x.y, mean_f.x, mean_f.y);
+    if (g.t == 0) a.means[row] = make_float4(mean_x.v[0], mean_x.v[1], mean_f.v[0], mean_f.v[1]);
   }
 }
 
@@ -612,30 +687,39 @@ __global__ void __launch_bounds__(512) k_norm_backward_long(const BackArgs a) {
 constexpr int kColumnWarps = 8, kColumns = 32 * kPer;
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(32 * kColumnWarps) k_norm_columns(const BackArgs a, int64_t rows_a_block) {
+  constexpr bool LEAN = false;
   __shared__ float sh[kSums][kColumns];
   chain_wait();
   const gm_norm& n = a.n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kColumns;
-  const Columns<TYPE, VEC> c{n, (VEC ? col0 / kPer : col0) + lane, 32};
+  const int col0 = blockIdx.x * kColumns;
+  const Columns<TYPE, VEC> c{(VEC ? col0 / kPer : col0) + lane, 32, static_cast<int>(n.dim)};
   float acc[kSums][kPer];
 #pragma unroll
   for (int s = 0; s < kSums; ++s)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[s][i] = 0.f;
+  auto add = [&](int which, const float (&v)[kPer], float by) {
+#pragma unroll
+    for (int s = 0; s < kSums; ++s)
+      if (s == which) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[s][i] = fmaf(v[i], by, acc[s][i]);
+      }
+  };
   const int64_t first = blockIdx.y * rows_a_block, end = min(n.n_rows, first + rows_a_block);
   for (int64_t row = first + warp; row < end; row += kColumnWarps) {
-    const RowIn<TYPE> in = read_row<TYPE, VEC>(a, c.t, 32, row);
-    Back<TYPE, VEC> b;
-    b.start(a, c, row, in.st, in.x, in.f, in.gy);
-    if (a.need_x) {
-      const float4 m = a.means[row];
-      float d[kPer];
-      if (a.gy) b.sums_x(a, c, d);
-      b.to_x(a, in.gx, d, make_float2(m.x, m.y), in.st);
-      if (n.f) b.sums_f(a, c, d);
-    }
-    b.add(a, acc);
+    RowIn<TYPE> in;
+    Weights<TYPE, VEC, LEAN> w;
+    read_long(a, c, row, in, w);
+    const Back<TYPE, VEC, LEAN> b{a, w, in, a.stats[row]};
+    float x[kPer], d[kPer];
+    Sums<2> unused = {{0.f, 0.f}};
+    b.start(x, d, unused, add);
+    if (!a.need_x || !n.f) continue;
+    const float4 m = a.means[row];
+    b.to_x(x, d, Sums<2>{{m.x, m.y}});
+    b.past_gate(d, x, unused, add, [](const float (&)[kPer]) {});
   }
   for (int k = 0; k < kColumnWarps; ++k) {
     if (warp == k) {
@@ -656,31 +740,51 @@ __global__ void __launch_bounds__(32 * kColumnWarps) k_norm_columns(const BackAr
   }
 }
 
-// The blocks' sums joined: 32 columns a block, its 8 warps every eighth part. blockIdx.y: which sum.
-struct JoinTo {
-  void* out[kSums];
-};
+// The blocks' sums joined, and the gradients that they give: 32 columns a block, its 32 warps every 32nd part.
+// blockIdx.y: before with its bias, or what comes from A and B.
 template <int TYPE>
-__global__ void __launch_bounds__(256) k_norm_join(const float* __restrict__ sums, int parts, int64_t dim, const JoinTo to) {
-  __shared__ float sh[8][32];
+__global__ void __launch_bounds__(1024) k_norm_join(const BackArgs a, int parts, bool biases) {
+  __shared__ float sh[2][32][33];
   chain_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.y;
-  void* out = to.out[s];
-  if (!out) return;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float x = 0.f;
-  if (col < dim) {
-    const float* p = sums + s * dim + col;
-#pragma unroll 8
-    for (int k = warp; k < parts; k += 8) x += p[static_cast<int64_t>(k) * kSums * dim];
+  const gm_norm& n = a.n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.y;
+  int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float x[2] = {0.f, 0.f};
+  if (col < n.dim) {
+    const float* p = a.sums + first * n.dim + col;
+#pragma unroll 4
+    for (int k = warp; k < parts; k += 32) {
+      x[0] += p[static_cast<int64_t>(k) * kSums * n.dim];
+      if (biases) x[1] += p[(static_cast<int64_t>(k) * kSums + 2) * n.dim];
+    }
   }
-  sh[warp][lane] = x;
+  sh[0][warp][lane] = x[0], sh[1][warp][lane] = x[1];
   __syncthreads();
-  if (warp != 0 || col >= dim) return;
-#pragma unroll
-  for (int k = 1; k < 8; ++k) x += sh[k][lane];
-  if constexpr (TYPE == GM_LOSS_F32) static_cast<float*>(out)[col] = x;
-  else static_cast<uint16_t*>(out)[col] = static_cast<uint16_t>(round16<TYPE>(x));
+  // a warp a column, its lanes the parts
+  x[0] = warp_reduce_sum(sh[0][lane][warp]);
+  x[1] = biases ? warp_reduce_sum(sh[1][lane][warp]) : 0.f;
+  col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane != 0 || col >= n.dim) return;
+  auto set = [&](void* out, float v) {
+    if (!out) return;
+    if constexpr (TYPE == GM_LOSS_F32) static_cast<float*>(out)[col] = v;
+    else static_cast<uint16_t*>(out)[col] = static_cast<uint16_t>(round16<TYPE>(v));
+  };
+  auto of = [&](const void* p, float none) {
+    if (!p) return none;
+    if constexpr (TYPE == GM_LOSS_F32) return static_cast<const float*>(p)[col];
+    else return lower16(static_cast<const uint16_t*>(p)[col], TYPE == GM_LOSS_BF16);
+  };
+  if (first == 0) {
+    set(a.o.before, x[0]);
+    set(a.o.before_bias, x[1]);
+  } else {
+    const bool vector = n.gate_kind == GM_GATE_VECTOR;
+    const float by = n.scale * (vector ? of(n.gate, 1.f) : 1.f);
+    set(a.o.after, by * x[0]);
+    set(a.o.after_bias, by * x[1]);
+    if (vector) set(a.o.gate, n.scale * fmaf(of(n.after, 1.f), x[0], of(n.after_bias, 0.f) * x[1]));
+  }
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -727,60 +831,67 @@ struct Sixteen {
   }
 };
 
-// Threads of a row held in registers, `turns` times 8 columns each.
-int group_of(int64_t dim, int turns) { return static_cast<int>(up(div_up(dim, kPer * turns), 32)); }
-
-template <class F>
-cudaError_t by_type(int32_t type, bool vec, F&& f) {
-  using std::integral_constant;
-#define GM_BY(T)                                                                                   \
-  return vec ? f(integral_constant<int, T>(), integral_constant<bool, true>()) : f(integral_constant<int, T>(), integral_constant<bool, false>())
-  switch (type) {
-    case GM_LOSS_F32: GM_BY(GM_LOSS_F32);
-    case GM_LOSS_BF16: GM_BY(GM_LOSS_BF16);
-    default: GM_BY(GM_LOSS_F16);
+// How a row is held: lean rows of 512 and more with 16 columns a thread where they are of 16 bits, others with 8.
+template <int TYPE, bool LEAN>
+constexpr int kTurns = LEAN && TYPE != GM_LOSS_F32 ? 2 : 1;
+struct Form {
+  bool vec, lean, held;
+  int turns, group;
+  Form(const gm_norm& n, bool vec, std::initializer_list<int64_t> lds) : vec(vec) {
+    const int wide = n.type == GM_LOSS_F32 ? 1 : 2;
+    lean = vec && n.dim >= 512 && n.dim <= kHeldDim / 2 * wide && n.norm == GM_NORM_RMS && !n.after_bias && !n.before_bias &&
+           n.gate_kind != GM_GATE_MATRIX;
+    for (int64_t ld : lds) lean = lean && ld * elem_bytes(n.type) <= UINT32_MAX;
+    turns = lean ? wide : 1;
+    held = lean || n.dim <= kHeldDim / 2;
+    group = static_cast<int>(up(div_up(n.dim, kPer * turns), 32));
   }
-#undef GM_BY
+};
+// f(type, rows by 16 bytes, lean) with constants
+template <class F>
+cudaError_t by_form(const gm_norm& n, const Form& form, F&& f) {
+  using std::integral_constant;
+  using Yes = std::true_type;
+  using No = std::false_type;
+  auto with = [&](auto t) { return form.lean ? f(t, Yes(), Yes()) : form.vec ? f(t, Yes(), No()) : f(t, No(), No()); };
+  return n.type == GM_LOSS_F32    ? with(integral_constant<int, GM_LOSS_F32>())
+         : n.type == GM_LOSS_BF16 ? with(integral_constant<int, GM_LOSS_BF16>())
+                                  : with(integral_constant<int, GM_LOSS_F16>());
 }
 
 gm_status done(cudaError_t e) { return cudaGetLastError() != cudaSuccess || e != cudaSuccess ? GM_ERR_CUDA : GM_OK; }
 
 gm_status norm_forward(const gm_norm& n, cudaStream_t s, void* x_out, int64_t x_out_ld, void* y, int64_t y_ld, float* stats) {
-  const bool vec = Sixteen(n)(x_out, x_out_ld)(y, y_ld).ok;
+  const int sms = sm_count(kMostBlocks);
+  if (sms <= 0) return done(cudaErrorUnknown);
+  const Form form(n, Sixteen(n)(x_out, x_out_ld)(y, y_ld).ok, {n.x_ld, n.f_ld, x_out_ld, y_ld});
   const NormArgs a{n, 1.f / static_cast<float>(n.dim), x_out, y, x_out_ld, y_ld, reinterpret_cast<float4*>(stats)};
-  return done(by_type(n.type, vec, [&](auto t, auto v) {
-    constexpr int T = decltype(t)::value;
-    constexpr bool V = decltype(v)::value;
-    if (n.dim > kHeldDim)
-      return launch_chained(k_norm_forward_long<T, V>, grid_for(n.n_rows, 1), n.dim > 2 * kHeldDim ? 1024 : 512, 0, s, 1, a);
-    // 4 turns for many long rows, so that several rows are under way on an SM; one thread a column group for few
-    const int turns = n.dim > 1024 && n.n_rows >= 512 ? 2 : 1;
-    const int group = group_of(n.dim, turns), block = std::max(group, 128) / group * group;
-    const unsigned grid = grid_for(n.n_rows, block / group, int64_t(1) << 30);
-    return turns == 2 ? launch_chained(k_norm_forward<T, V, 2>, grid, block, 0, s, 1, a, group)
-                      : launch_chained(k_norm_forward<T, V, 1>, grid, block, 0, s, 1, a, group);
+  return done(by_form(n, form, [&](auto t, auto v, auto l) {
+    constexpr int T = t;
+    constexpr bool V = v, L = l;
+    if (!form.held) return launch_chained(k_norm_forward_long<T, V>, grid_for(n.n_rows, 1), kLongBlock, 0, s, 1, a);
+    const int group = form.group, block = std::max(group, 128) / group * group;
+    const unsigned grid = grid_for(n.n_rows, block / group, int64_t(sms) * std::max(1, (L ? kLeanThreads : 1024) / block));
+    return launch_chained(k_norm_forward<T, V, kTurns<T, L>, L>, grid, block, 0, s, 1, a, group);
   }));
 }
 
 // How a backward call is cut, and where its workspace lies.
 struct NormPlan {
   Arena a;
-  bool long_rows;
-  int group = 0, block = 0;
+  int block = 0;
   int64_t parts, rows_a_part = 0;  // of the sums over rows
   size_t o_sums, o_means = 0;
-  NormPlan(const gm_norm& n, int sms) {
-    long_rows = n.dim > kHeldDim;
-    if (long_rows) {
+  NormPlan(const gm_norm& n, const Form& form, int sms) {
+    if (!form.held) {
       const int64_t slabs = div_up(n.dim, kColumns);
       parts = std::max<int64_t>(1, std::min<int64_t>(div_up(4 * sms, slabs), div_up(n.n_rows, 4 * kColumnWarps)));
       rows_a_part = div_up(n.n_rows, parts);
       parts = div_up(n.n_rows, rows_a_part);
       o_means = a.add(n.n_rows * 16);
     } else {
-      group = group_of(n.dim, 1);
-      block = std::max(group, 256) / group * group;
-      parts = std::min<int64_t>(div_up(n.n_rows, block / group), sms * std::max(1, 512 / block));
+      block = std::max(form.group, 256) / form.group * form.group;
+      parts = std::min<int64_t>(div_up(n.n_rows, block / form.group), int64_t(sms) * (512 / block));
     }
     o_sums = a.add(parts * kSums * n.dim * 4);
   }
@@ -789,56 +900,48 @@ struct NormPlan {
 gm_status norm_backward(const gm_norm& n, const gm_layer_config& cfg, cudaStream_t s, const float* stats, const void* gx,
                         int64_t gx_ld, const void* gy, int64_t gy_ld, const gm_norm_grads& o) {
   const int sms = sm_count(kMostBlocks);
-  if (sms <= 0) {
-    cudaGetLastError();
-    return GM_ERR_CUDA;
-  }
+  if (sms <= 0) return done(cudaErrorUnknown);
   const int64_t es = elem_bytes(n.type);
+  const bool vector = n.gate_kind == GM_GATE_VECTOR;
   if (n.n_rows == 0) {
-    for (void* p : {o.after, o.after_bias, o.before, o.before_bias, n.gate_kind == GM_GATE_VECTOR ? o.gate : nullptr})
+    for (void* p : {o.after, o.after_bias, o.before, o.before_bias, vector ? o.gate : nullptr})
       if (p && cudaMemsetAsync(p, 0, n.dim * es, s) != cudaSuccess) {
         cudaGetLastError();
         return GM_ERR_CUDA;
       }
     return GM_OK;
   }
-  NormPlan p(n, sms);
+  Sixteen all(n);
+  all(gx, gx_ld)(gy, gy_ld)(o.x, o.x_ld)(o.f, o.f_ld)(vector ? nullptr : o.gate, o.gate_ld);
+  const Form form(n, all.ok, {n.x_ld, n.f_ld, gx_ld, gy_ld, o.x_ld, o.f_ld});
+  NormPlan p(n, form, sms);
   const gm_status rc = p.a.open(cfg.workspace, cfg.workspace_bytes, s);
   if (rc != GM_OK) return rc;
-  JoinTo to = {};
-  to.out[kSumBefore] = o.before;
-  to.out[kSumAfter] = o.after;
-  to.out[kSumGate] = n.gate_kind == GM_GATE_VECTOR ? o.gate : nullptr;
-  to.out[kSumBeforeBias] = o.before_bias;
-  to.out[kSumAfterBias] = o.after_bias;
-  bool sums = false;
-  for (void* q : to.out) sums = sums || q;
-  const bool biases = o.before_bias || o.after_bias;
+  const bool sums = o.before || o.before_bias || o.after || o.after_bias || (vector && o.gate);
   BackArgs a{n, o, 1.f / static_cast<float>(n.dim), reinterpret_cast<const float4*>(stats), gx, gy, gx_ld, gy_ld};
   a.need_x = o.x || o.f || o.gate || o.after || o.after_bias;
   a.sums = sums ? p.a.at<float>(p.o_sums) : nullptr;
-  a.means = p.long_rows ? p.a.at<float4>(p.o_means) : nullptr;
-  Sixteen all(n);
-  all(gx, gx_ld)(gy, gy_ld)(o.x, o.x_ld)(o.f, o.f_ld)(o.gate, n.gate_kind == GM_GATE_MATRIX ? o.gate_ld : 0);
-  return done(by_type(n.type, all.ok, [&](auto t, auto v) {
-    constexpr int T = decltype(t)::value;
-    constexpr bool V = decltype(v)::value;
+  a.means = form.held ? nullptr : p.a.at<float4>(p.o_means);
+  return done(by_form(n, form, [&](auto t, auto v, auto l) {
+    constexpr int T = t;
+    constexpr bool V = v, L = l;
     cudaError_t e = cudaSuccess;
-    if (p.long_rows) {
-      if (a.need_x) e = launch_chained(k_norm_backward_long<T, V>, grid_for(n.n_rows, 1), 512, 0, s, 1, a);
+    if (!form.held) {
+      if (a.need_x) e = launch_chained(k_norm_backward_long<T, V>, grid_for(n.n_rows, 1), kLongBlock, 0, s, 1, a);
       if (e == cudaSuccess && sums) {
         const dim3 grid(static_cast<unsigned>(div_up(n.dim, kColumns)), static_cast<unsigned>(p.parts));
         e = launch_chained(k_norm_columns<T, V>, grid, 32 * kColumnWarps, 0, s, 1, a, p.rows_a_part);
       }
     } else {
-      const int groups = p.block / p.group;
-      const size_t smem = sums && groups > 1 ? (biases ? 5 : 3) * n.dim * 4 : 0;
-      e = biases ? launch_chained(k_norm_backward<T, V, 5>, static_cast<unsigned>(p.parts), p.block, smem, s, 1, a, p.group)
-                 : launch_chained(k_norm_backward<T, V, 3>, static_cast<unsigned>(p.parts), p.block, smem, s, 1, a, p.group);
+      constexpr int kBytes = (L ? 2 : 4) * 2 * 16 * kTurns<T, L>;  // of a thread
+      auto* k = k_norm_backward<T, V, kTurns<T, L>, L>;
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes * 512);
+      const size_t smem = sums ? size_t(kBytes) * p.block : 0;
+      if (e == cudaSuccess) e = launch_chained(k, static_cast<unsigned>(p.parts), p.block, smem, s, 1, a, form.group);
     }
     if (e == cudaSuccess && sums) {
-      const dim3 grid(static_cast<unsigned>(div_up(n.dim, 32)), biases ? 5 : 3);
-      e = launch_chained(k_norm_join<T>, grid, 256, 0, s, 1, a.sums, static_cast<int>(p.parts), n.dim, to);
+      const dim3 grid(static_cast<unsigned>(div_up(n.dim, 32)), n.f ? 2 : 1);
+      e = launch_chained(k_norm_join<T>, grid, 1024, 0, s, 1, a, static_cast<int>(p.parts), !L);
     }
     return e;
   }));
@@ -904,6 +1007,8 @@ extern "C" gm_status gm_norm_workspace(const gm_norm* n, int64_t* bytes) {
     cudaGetLastError();
     return GM_ERR_CUDA;
   }
-  *bytes = static_cast<int64_t>(gm::NormPlan(*n, sms).a.used);
+  // which form a call takes depends on its other arrays too
+  const gm::Form lean(*n, true, {}), general(*n, false, {});
+  *bytes = static_cast<int64_t>(std::max(gm::NormPlan(*n, lean, sms).a.used, gm::NormPlan(*n, general, sms).a.used));
   return GM_OK;
 }
