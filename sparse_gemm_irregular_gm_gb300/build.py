@@ -1,7 +1,8 @@
 """Builds libgm_spgemm.so (CUDA, sm_103a) in-tree with nvcc.
 
 Each translation unit compiles in its own nvcc process (in parallel), then one
-nvcc call links the shared library. Objects go to ``_build/`` next to this file.
+nvcc call links the shared library. Objects go to ``_build/`` next to this file. gm_marshal.so, the Python extension of the
+layers and the draw, is compiled beside it.
 ``build(checked=True)`` builds libgm_spgemm_checked.so instead, with
 GM_BOUNDS_CHECK defined: every write of C and of the chunk elements checks its
 index first and reports an index out of range as GM_ERR_INTERNAL (objects in
@@ -21,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgm_spgemm.so")
 LIB_CHECKED = os.path.join(HERE, "libgm_spgemm_checked.so")
+MARSHAL = os.path.join(HERE, "gm_marshal.so")
 SOURCES = ["gm_api.cu", "gm_analyze.cu", "gm_scan.cu", "gm_expand.cu", "gm_multisplit.cu", "gm_accum.cu", "gm_rowbitmap.cu",
            "gm_stream.cu", "gm_noalloc.cu", "gm_loss.cu", "gm_loss_prod.cu",
            "gm_loss_skinny.cu", "gm_linear.cu", "gm_norm.cu", "gm_draw.cu"]
@@ -39,12 +41,31 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_marshal() -> str:
+    """Compile gm_marshal.so, the Python extension that checks tensors and calls the library; needs no CUDA compiler."""
+    import sysconfig
+
+    import torch
+    at = os.path.dirname(torch.__file__)
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in inc), os.path.join(CSRC, "gm_marshal.cpp"), "-o", tmp, "-L" + os.path.join(at, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on gm_marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     """Compile (if stale) and return the path of libgm_spgemm.so (or, with checked,
     of libgm_spgemm_checked.so)."""
     lib = LIB_CHECKED if checked else LIB
     bdir = BUILD + "_checked" if checked else BUILD
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (lib, MARSHAL)):
         return lib
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
@@ -62,8 +83,10 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
             print(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        marshal = ex.submit(build_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs, "-ldl",  # NVTX loads a profiler's hooks
            "-Xlinker", "-rpath=/usr/local/cuda/lib64"]

@@ -4,7 +4,8 @@ epilogue, and the norms around a residual with its gate and scale; forward and b
 ``linear`` and ``residual_norm`` work under torch's autograd. ``linear_forward``, ``linear_backward``,
 ``residual_norm_forward`` and ``residual_norm_backward`` are the same without it; ``gm_*`` write into the caller's
 tensors under the names of the C interface. Matrices are rows of consecutive elements of bfloat16, float16 or float32;
-all tensors of a call have one type. Nothing waits for the GPU.
+all tensors of a call have one type. Nothing waits for the GPU. Arguments are checked, results made and the C interface called
+by a compiled extension (csrc/gm_marshal.cpp).
 """
 from __future__ import annotations
 
@@ -16,7 +17,7 @@ from torch.autograd.function import once_differentiable
 
 from . import binding
 from .binding import GmError
-from .losses import TYPES, _gradient, _like, _matrix, _On
+from .marshal import call, extension
 
 EXPORTS = ["gm_linear_forward", "gm_linear_backward", "gm_linear_workspace", "gm_norm_forward", "gm_norm_backward", "gm_norm_workspace"]
 NORMS = {"rms": 0, "layer": 1}
@@ -69,89 +70,46 @@ def load():
     return lib
 
 
-def _row(name, t, n, like):
-    """A contiguous vector of n elements as x's, or None: its address."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.shape != (n,) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of {n} elements of {like.dtype} on {like.device}")
-    return t.data_ptr()
-
-
-def _rows(name, t, like, shape=None):
-    return (None, 0) if t is None else _matrix(name, t, like, shape)
-
-
-def _check(rc, where):
+def _run(name, stream, x, *args):
+    """A function of the extension, on `stream` where one is given: what it returned after its status."""
+    rc, *out = call(getattr(extension(), name), stream, x, *args)
     if rc:
-        raise GmError(rc, where)
+        raise GmError(rc, "gm_" + name)
+    return out
 
 
-def _own(t):
-    """A matrix that was made for a result, as arguments."""
-    return (None, 0) if t is None else (t.data_ptr() or None, t.shape[1])
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(map(str, ACTIVATIONS))}, not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _norm(name):
+    if name not in NORMS:
+        raise ValueError(f"norm must be one of {', '.join(NORMS)}, not {name!r}")
+    return NORMS[name]
 
 
 # ---- product with bias, activation and residual ---------------------------------------------
-def _linear(x, w, activation):
-    xp, x_ld = _matrix("x", x)
-    wp, w_ld = _matrix("w", w, x)
-    n, dim = x.shape
-    if w.shape[1] != dim or dim < 1 or w.shape[0] < 1:
-        raise ValueError(f"x has rows of {dim} elements, w is {w.shape[0]} x {w.shape[1]}")
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {', '.join(map(str, ACTIVATIONS))}, not {activation!r}")
-    return gm_linear(n, dim, w.shape[0], xp, x_ld, wp, w_ld, TYPES[x.dtype], ACTIVATIONS[activation])
-
-
-def _linear_run(name, backward, a, device, s, *args):
-    lib, need = load(), ctypes.c_int64()
-    _check(lib.gm_linear_workspace(a, backward, need), name)
-    work = torch.empty(need.value, dtype=torch.uint8, device=device)
-    _check(getattr(lib, name)(a, gm_layer_config(work.data_ptr() or None, need.value), s, *args), name)
-
-
 def gm_linear_forward(x, w, bias, residual, y, z=None, *, activation=None, stream=None):
-    a = _linear(x, w, activation)
-    shape = (a.n_rows, a.n_outs)
-    args = (_row("bias", bias, a.n_outs, x), *_rows("residual", residual, x, shape), *_rows("y", y, x, shape), *_rows("z", z, x, shape))
-    with _On(x.device, stream) as s:
-        _linear_run("gm_linear_forward", 0, a, x.device, s, *args)
+    _run("linear_forward", stream, x, w, bias, _activation(activation), residual, False, y, z, False)
 
 
 def linear_forward(x, w, bias=None, *, activation=None, residual=None, keep=False, stream=None):
     """(y, z): y = residual + act(z), z = x w^T + bias (x: rows x dim, w: outs x dim). z is None unless ``keep`` and an
     activation, whose gradient reads it. ``activation``: relu, gelu, gelu_tanh, silu, or None."""
-    a = _linear(x, w, activation)
-    shape = (a.n_rows, a.n_outs)
-    args = _row("bias", bias, a.n_outs, x), *_rows("residual", residual, x, shape)
-    with _On(x.device, stream) as s:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
-        z = torch.empty_like(y) if keep and a.activation else None
-        _linear_run("gm_linear_forward", 0, a, x.device, s, *args, *_own(y), *_own(z))
-    return y, z
+    return tuple(_run("linear_forward", stream, x, w, bias, _activation(activation), residual, keep, None, None, True))
 
 
 def gm_linear_backward(x, w, grad, z, dx, dw, dbias, *, activation=None, stream=None):
-    a = _linear(x, w, activation)
-    shape = (a.n_rows, a.n_outs)
-    args = (*_matrix("grad", grad, x, shape), *_rows("z", z, x, shape), *_gradient("dx", dx, x), *_gradient("dw", dw, w),
-            _row("dbias", dbias, a.n_outs, x))
-    with _On(x.device, stream) as s:
-        _linear_run("gm_linear_backward", 1, a, x.device, s, *args)
+    _run("linear_backward", stream, x, w, grad, _activation(activation), z, dx, dw, dbias, False, False, False)
 
 
 def linear_backward(x, w, grad, *, activation=None, z=None, need_x=True, need_w=True, need_bias=False, stream=None):
     """(dx, dw, dbias) for the gradient by y; the residual's is that gradient itself. ``z``: linear_forward's, with an activation."""
-    a = _linear(x, w, activation)
-    shape = (a.n_rows, a.n_outs)
-    args = *_matrix("grad", grad, x, shape), *_rows("z", z, x, shape)
-    with _On(x.device, stream) as s:
-        dx, dw = _like(x, need_x), _like(w, need_w)
-        db = torch.empty(a.n_outs, dtype=x.dtype, device=x.device) if need_bias else None
-        if need_x or need_w or need_bias:
-            _linear_run("gm_linear_backward", 1, a, x.device, s, *args, *_own(dx), *_own(dw), None if db is None else db.data_ptr())
-    return dx, dw, db
+    if not (need_x or need_w or need_bias):
+        return None, None, None
+    return tuple(_run("linear_backward", stream, x, w, grad, _activation(activation), z, None, None, None, need_x, need_w, need_bias))
 
 
 class _Linear(torch.autograd.Function):
@@ -203,43 +161,9 @@ class NormGrads(NamedTuple):
     before_bias: torch.Tensor | None
 
 
-def _norm(x, f, norm, after, after_bias, gate, scale, before, before_bias, eps):
-    xp, x_ld = _matrix("x", x)
-    n, dim = x.shape
-    if dim < 1:
-        raise ValueError("x must have rows of an element at least")
-    if norm not in NORMS:
-        raise ValueError(f"norm must be one of {', '.join(NORMS)}, not {norm!r}")
-    if f is None and (after is not None or after_bias is not None or gate is not None):
-        raise ValueError("after, after_bias and gate belong to f, which is None")
-    if (after is None and after_bias is not None) or (before is None and before_bias is not None):
-        raise ValueError("a bias needs its norm's weight")
-    fp, f_ld = _rows("f", f, x, x.shape)
-    kind, gp, g_ld = 0, None, 0
-    if gate is not None:
-        if gate.dim() == 1:
-            kind, gp = 1, _row("gate", gate, dim, x)
-        else:
-            kind, (gp, g_ld) = 2, _matrix("gate", gate, x, x.shape)
-    return gm_norm(n, dim, TYPES[x.dtype], NORMS[norm], kind, scale, eps, xp, x_ld, fp, f_ld,
-                   _row("after", after, dim, x), _row("after_bias", after_bias, dim, x), gp, g_ld,
-                   _row("before", before, dim, x), _row("before_bias", before_bias, dim, x))
-
-
-def _stats(t, x):
-    if t is None:
-        return None
-    if t.shape != (x.shape[0], 4) or t.dtype != torch.float32 or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"stats must be a contiguous float32 tensor of {x.shape[0]} x 4 on {x.device}")
-    return t.data_ptr() or None
-
-
 def gm_norm_forward(x, f, x_out, y, stats=None, *, norm="rms", after=None, after_bias=None, gate=None, scale=1.0,
                     before=None, before_bias=None, eps=1e-6, stream=None):
-    a = _norm(x, f, norm, after, after_bias, gate, scale, before, before_bias, eps)
-    with _On(x.device, stream) as s:
-        _check(load().gm_norm_forward(a, s, *_rows("x_out", x_out, x, x.shape), *_rows("y", y, x, x.shape),
-                                      _stats(stats, x)), "gm_norm_forward")
+    _run("norm_forward", stream, x, f, _norm(norm), after, after_bias, gate, scale, before, before_bias, eps, x_out, y, stats, False)
 
 
 def residual_norm_forward(x, f=None, *, norm="rms", after=None, after_bias=None, gate=None, scale=1.0, before=None,
@@ -247,54 +171,32 @@ def residual_norm_forward(x, f=None, *, norm="rms", after=None, after_bias=None,
     """x' = x + scale * gate * (n(f) * after + after_bias) and y = n(x') * before + before_bias, a row at a time; n divides
     by the root mean square (``norm="rms"``) or takes the mean off first (``"layer"``). Without ``after``, f is taken as it
     is; without ``f``, x' is x; without ``before``, y is None. ``gate``: a vector, a matrix like x, or None."""
-    if f is None and before is None:
-        raise ValueError("there is nothing to compute without f and before")
-    a = _norm(x, f, norm, after, after_bias, gate, scale, before, before_bias, eps)
-    with _On(x.device, stream) as s:
-        x2, y = _like(x, f is not None), _like(x, before is not None)
-        stats = torch.empty((x.shape[0], 4), dtype=torch.float32, device=x.device)
-        _check(load().gm_norm_forward(a, s, *_own(x2), *_own(y), stats.data_ptr() or None), "gm_norm_forward")
+    x2, y, stats = _run("norm_forward", stream, x, f, _norm(norm), after, after_bias, gate, scale, before, before_bias, eps,
+                        None, None, None, True)
     return Normed(x if x2 is None else x2, y, stats)
 
 
 def gm_norm_backward(x, f, stats, grad_x, grad_y, grads: NormGrads, *, norm="rms", after=None, after_bias=None, gate=None,
                      scale=1.0, before=None, before_bias=None, eps=1e-6, stream=None):
-    a = _norm(x, f, norm, after, after_bias, gate, scale, before, before_bias, eps)
-    n = x.shape[1]
-    g = _gradient("grads.gate", grads.gate, x) if a.gate_kind == 2 else (_row("grads.gate", grads.gate, n, x), 0)
-    o = gm_norm_grads(*_gradient("grads.x", grads.x, x), *_gradient("grads.f", grads.f, x), *g,
-                      *(_row("grads." + k, getattr(grads, k), n, x) for k in ("after", "after_bias", "before", "before_bias")))
-    _norm_backward(a, x, stats, grad_x, grad_y, o, stream)
+    _run("norm_backward", stream, x, f, stats, grad_x, grad_y, _norm(norm), after, after_bias, gate, scale, before, before_bias,
+         eps, list(grads), False, 0)
 
 
-def _norm_backward(a, x, stats, grad_x, grad_y, o, stream):
-    lib, need = load(), ctypes.c_int64()
-    gx, gy = _rows("grad_x", grad_x, x, x.shape), _rows("grad_y", grad_y, x, x.shape)
-    with _On(x.device, stream) as s:
-        _check(lib.gm_norm_workspace(a, need), "gm_norm_backward")
-        work = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        cfg = gm_layer_config(work.data_ptr() or None, need.value)
-        _check(lib.gm_norm_backward(a, cfg, s, _stats(stats, x), *gx, *gy, o), "gm_norm_backward")
+_ALL = (1 << len(NormGrads._fields)) - 1
 
 
 def residual_norm_backward(x, f, grad_x, grad_y, stats, *, norm="rms", after=None, after_bias=None, gate=None, scale=1.0,
                            before=None, before_bias=None, eps=1e-6, need=None, stream=None) -> NormGrads:
     """Gradients by the inputs, from those by x' and by y (either may be None: zeros). ``need``: names of the inputs whose
     gradients are wanted (None: of all that are given)."""
-    a = _norm(x, f, norm, after, after_bias, gate, scale, before, before_bias, eps)
-    given = dict(x=x, f=f, gate=gate, after=after, after_bias=after_bias, before=before, before_bias=before_bias)
-    if need is not None and not set(need) <= set(given):
-        raise ValueError(f"need may hold {', '.join(given)}, not {', '.join(sorted(set(need) - set(given)))}")
-    with _On(x.device, stream):
-        out = {k: torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None and (need is None or k in need)
-               else None for k, t in given.items()}
-        if any(t is not None for t in out.values()):
-            v = {k: None if t is None else t.data_ptr() or None for k, t in out.items()}
-            d = x.shape[1]
-            _norm_backward(a, x, stats, grad_x, grad_y,
-                           gm_norm_grads(v["x"], d, v["f"], d, v["gate"], d, v["after"], v["after_bias"], v["before"],
-                                         v["before_bias"]), stream)
-    return NormGrads(**out)
+    bits = _ALL
+    if need is not None:
+        if not set(need) <= set(NormGrads._fields):
+            raise ValueError(f"need may hold {', '.join(NormGrads._fields)}, not {', '.join(sorted(set(need) - set(NormGrads._fields)))}")
+        bits = sum(1 << NormGrads._fields.index(k) for k in set(need))
+    (out,) = _run("norm_backward", stream, x, f, stats, grad_x, grad_y, _norm(norm), after, after_bias, gate, scale, before,
+                  before_bias, eps, [], True, bits)
+    return NormGrads(*out)
 
 
 class _ResidualNorm(torch.autograd.Function):

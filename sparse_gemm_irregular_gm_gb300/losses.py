@@ -107,32 +107,9 @@ def _same_device(stream, device):
     return stream
 
 
-class _On:
-    """``with`` makes a device and (unless None) a stream on it current, so that what torch allocates inside belongs to that
-    stream; gives the stream's handle."""
-
-    def __init__(self, device, stream):
-        self.device, self.given, self.on = device, stream, None
-
-    def __enter__(self):
-        if self.given is not None:
-            self.on = torch.cuda.stream(_same_device(self.given, self.device))  # also makes its device current
-        elif torch.cuda.current_device() != self.device.index:
-            self.on = torch.cuda.device(self.device)
-        if self.on is not None:
-            self.on.__enter__()
-        return self.handle()
-
-    def handle(self):
-        return (self.given if self.given is not None else torch.cuda.current_stream(self.device.index)).cuda_stream
-
-    def __exit__(self, *a):
-        if self.on is not None:
-            self.on.__exit__(*a)
-
-
 class _Call:
-    """One call's checked arguments; ``with`` makes its device and stream current."""
+    """One call's checked arguments; ``with`` makes its device and stream current, so that what torch
+    allocates inside belongs to that stream."""
 
     def __init__(self, h, w, target, ignore_index, teacher, check, workspace_cap_bytes, stream):
         hp, h_ld = _matrix("h", h)
@@ -148,7 +125,8 @@ class _Call:
             self.labels = gm_labels(p, ignore_index, target.dtype == torch.int32)
         self.cfg = gm_loss_config(workspace_cap_bytes, GM_LOSS_CHECK if check else 0, None, 0)
         self.teacher = self._teacher(teacher) if teacher is not None else None
-        self.on = _On(self.device, stream)
+        self.given = stream
+        self.on = None
 
     def _teacher(self, t):
         for name, x, kinds in (("row_ptr", t.row_ptr, _ROW_PTR), ("col", t.col, _COL), ("val", t.val, _VAL)):
@@ -161,11 +139,17 @@ class _Call:
         return t.desc(), _VAL[t.val.dtype], _ROW_PTR[t.row_ptr.dtype] | _COL[t.col.dtype]
 
     def __enter__(self):
-        self.on.__enter__()
+        if self.given is not None:
+            self.on = torch.cuda.stream(_same_device(self.given, self.device))  # also makes its device current
+        elif torch.cuda.current_device() != self.device.index:
+            self.on = torch.cuda.device(self.device)
+        if self.on is not None:
+            self.on.__enter__()
         return self
 
     def __exit__(self, *a):
-        self.on.__exit__(*a)
+        if self.on is not None:
+            self.on.__exit__(*a)
 
     def vectors(self, k):
         """k uninitialised results, a float a row."""
@@ -181,7 +165,7 @@ class _Call:
         work = torch.empty(size, dtype=torch.uint8, device=self.device)
         cfg.workspace = work.data_ptr() or None
         cfg.workspace_bytes = size
-        stream = self.on.handle()
+        stream = (self.given if self.given is not None else torch.cuda.current_stream(self.device.index)).cuda_stream
         if self.teacher is None:
             rc = getattr(lib, name)(z, self.labels, cfg, stream, *args)
         else:
