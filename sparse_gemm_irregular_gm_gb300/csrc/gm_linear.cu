@@ -110,8 +110,22 @@ __device__ __forceinline__ void read8(const void* p, int have, bool wide, bool b
   }
 }
 
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __half2 r = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 template <bool F32>
-__global__ void __launch_bounds__(32 * kDzWarps) k_dz(const DzArgs a) {
+__device__ __forceinline__ void times_slope(float (&g)[8], const float (&z)[8], int act) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] *= slope<F32>(z[i], act);
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a) {
   __shared__ float sh[kDzWarps][kDzColumns];
   chain_wait();
   constexpr int kBytes = F32 ? 4 : 2;
@@ -119,8 +133,12 @@ __global__ void __launch_bounds__(32 * kDzWarps) k_dz(const DzArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * kDzColumns + lane * 8;
   const int have = static_cast<int>(max(int64_t(0), min(int64_t(8), a.outs - col)));
-  const bool bf16 = a.type != GM_LOSS_F16;
+  const bool bf16 = a.type != GM_LOSS_F16, write = a.dz && col < a.ld;  // ld is a multiple of 8
   const int64_t first = blockIdx.y * a.rows_a_block, end = min(a.rows, first + a.rows_a_block);
+  const char* grad = static_cast<const char*>(a.grad) + ((first + warp) * a.grad_ld + col) * kBytes;
+  const char* z_at = static_cast<const char*>(a.z) + ((first + warp) * a.z_ld + col) * kBytes;
+  uint16_t* out = a.dz + (first + warp) * a.ld + col;
+  const int64_t grad_step = a.grad_ld * kBytes * kDzWarps, z_step = a.z_ld * kBytes * kDzWarps, out_step = a.ld * kDzWarps;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -128,47 +146,49 @@ __global__ void __launch_bounds__(32 * kDzWarps) k_dz(const DzArgs a) {
     float g[kAhead][8], z[kAhead][8];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int64_t r = r0 + k * kDzWarps;
-      const int in = r < end ? have : 0;
-      read8<F32>(static_cast<const char*>(a.grad) + (r * a.grad_ld + col) * kBytes, in, a.wide, bf16, g[k]);
-      if (a.z) read8<F32>(static_cast<const char*>(a.z) + (r * a.z_ld + col) * kBytes, in, a.wide, bf16, z[k]);
+      const int in = r0 + k * kDzWarps < end ? have : 0;  // what is not there is 0, and so is its dz
+      read8<F32>(grad, in, a.wide, bf16, g[k]);
+      if (a.z) read8<F32>(z_at, in, a.wide, bf16, z[k]);
+      grad += grad_step, z_at += z_step;
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t r = r0 + k * kDzWarps;
-      if (r >= end) break;
+    for (int k = 0; k < kAhead; ++k, out += out_step) {
       if (a.z) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[k][i] *= slope<F32>(z[k][i], a.act);
+        if (a.act == GM_ACT_GELU) times_slope<F32>(g[k], z[k], GM_ACT_GELU);
+        else if (a.act == GM_ACT_SILU) times_slope<F32>(g[k], z[k], GM_ACT_SILU);
+        else if (a.act == GM_ACT_GELU_TANH) times_slope<F32>(g[k], z[k], GM_ACT_GELU_TANH);
+        else times_slope<F32>(g[k], z[k], GM_ACT_RELU);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += i < have ? g[k][i] : 0.f;
-      if (a.dz && col < a.ld) {  // ld is a multiple of 8
+      for (int i = 0; i < 8; ++i) acc[i] += g[k][i];
+      if (!write || r0 + k * kDzWarps >= end) continue;
+      if (!F32 && a.planes == 1) {
+        *reinterpret_cast<uint4*>(out) = make_uint4(pack2(g[k][0], g[k][1], bf16), pack2(g[k][2], g[k][3], bf16),
+                                                    pack2(g[k][4], g[k][5], bf16), pack2(g[k][6], g[k][7], bf16));
+        continue;
+      }
 #pragma unroll 1
-        for (int p = 0; p < a.planes; ++p) {
-          uint32_t w[4];
+      for (int p = 0; p < a.planes; ++p) {
+        uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            float u[2] = {g[k][i], g[k][i + 1]};
-            uint32_t h[2];
+        for (int i = 0; i < 8; i += 2) {
+          uint32_t h[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (i + j >= have) u[j] = 0.f;
-              if constexpr (F32) {
-                h[j] = take_plane(u[j], p == 2, (__float_as_uint(u[j]) & INT32_MAX) < kRoundsPast);
-              } else if (bf16) {
-                const __nv_bfloat16 y = __float2bfloat16_rn(u[j]);
-                h[j] = __bfloat16_as_ushort(y), u[j] -= __bfloat162float(y);
-              } else {
-                const __half y = __float2half_rn(u[j]);
-                h[j] = __half_as_ushort(y), u[j] -= __half2float(y);
-              }
-              g[k][i + j] = u[j];
+          for (int j = 0; j < 2; ++j) {
+            float& u = g[k][i + j];
+            if constexpr (F32) {
+              h[j] = take_plane(u, p == 2, (__float_as_uint(u) & INT32_MAX) < kRoundsPast);
+            } else if (bf16) {
+              const __nv_bfloat16 y = __float2bfloat16_rn(u);
+              h[j] = __bfloat16_as_ushort(y), u -= __bfloat162float(y);
+            } else {
+              const __half y = __float2half_rn(u);
+              h[j] = __half_as_ushort(y), u -= __half2float(y);
             }
-            w[i / 2] = h[0] | (h[1] << 16);
           }
-          *reinterpret_cast<uint4*>(a.dz + p * a.plane + r * a.ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
+          w[i / 2] = h[0] | (h[1] << 16);
         }
+        *reinterpret_cast<uint4*>(out + p * a.plane) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }

@@ -231,6 +231,15 @@ struct FromTmem {
     }
     if constexpr (C + 32 >= COLS) done();
   }
+  __device__ __forceinline__ void get(int c, float (&v)[32]) {  // the same for a loop that is not unrolled
+    static_assert(AHEAD, "one group reads");
+    tmem_load_wait(ahead);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = ahead[j];
+    __syncwarp();
+    if (c + 32 < COLS) tmem_load32(at + c + 32, ahead);
+    else done();
+  }
 };
 template <int COLS>
 struct Held {
@@ -675,8 +684,7 @@ __device__ __forceinline__ void end_linear(const ProdArgs& g, const CUtensorMap*
     if constexpr (F32) box.put32(v);
     else box.put16(0, v, g.bf16, false, 0xffffffffu);
   };
-  each_32<kCols>([&](auto cc) {
-    constexpr int c = decltype(cc)::value;
+  auto columns = [&](int c, auto&& get) {
     const int64_t col = col0 + c;
     const int have = static_cast<int>(max(int64_t(0), min(int64_t(32), g.n - col)));
     Piece32<F32> res;
@@ -686,7 +694,7 @@ __device__ __forceinline__ void end_linear(const ProdArgs& g, const CUtensorMap*
     };
     if constexpr (!F32) read_residual();  // ahead of the sums; 32 words more than f32's registers hold
     float v[32];
-    src.template get<c>(v);
+    get(v);
     if (g.acc) {
       Outbox<false> box{buf, lane};
       box.open();
@@ -716,7 +724,17 @@ __device__ __forceinline__ void end_linear(const ProdArgs& g, const CUtensorMap*
       if (g.by_tma) box_y.send(map_o, static_cast<int>(col), static_cast<int>(row0), 0, false);
       else box_y.copy(g.out, g.out_ld, kBytes, row0, g.m, col, have);
     }
-  });
+  };
+  if constexpr (kHeld<Src>) {
+    each_32<kCols>([&](auto cc) {
+      columns(decltype(cc)::value, [&](float (&v)[32]) { src.template get<decltype(cc)::value>(v); });
+    });
+  } else {
+    // not unrolled: four copies of five activations are more instructions than the SM's cache holds (8192 x 1024 x 4096
+    // with gelu: 104 us so, most of it waiting for instructions)
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) columns(c, [&](float (&v)[32]) { src.get(c, v); });
+  }
 }
 
 template <Prod KIND, int CG, int BN, bool LAB, bool DIS, int ACC>
