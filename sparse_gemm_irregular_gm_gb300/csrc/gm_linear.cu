@@ -59,9 +59,38 @@ __global__ void __launch_bounds__(256) k_linear_join(const float* __restrict__ a
   }
 }
 
+// X and W laid out as operands where they cannot be read in place: in one launch, or by blocks of the next kernel's.
+struct Lay {
+  const void* src;  // null: nothing to lay out
+  int64_t rows, src_ld;
+  uint16_t* dst;
+  int dim, ld;
+  bool wide;        // rows of src start on 16-byte boundaries
+  unsigned blocks;
+};
+struct Lays {
+  Lay m[2];
+  unsigned blocks() const { return m[0].blocks + m[1].blocks; }
+};
+constexpr int kLayThreads = 256;
+
+template <bool F32>
+__device__ __forceinline__ void lay_out_all(const Lays& l, unsigned block) {
+  const Lay& m = l.m[block < l.m[0].blocks ? 0 : 1];
+  if (block >= l.m[0].blocks) block -= l.m[0].blocks;
+  const int64_t first = static_cast<int64_t>(block) * kLayThreads + threadIdx.x, stride = static_cast<int64_t>(m.blocks) * kLayThreads;
+  if (F32 && m.wide) lay_out<F32, true>(m.src, m.rows, m.dim, m.src_ld, m.dst, m.ld, first, stride);
+  else lay_out<F32, false>(m.src, m.rows, m.dim, m.src_ld, m.dst, m.ld, first, stride);
+}
+template <bool F32>
+__global__ void __launch_bounds__(kLayThreads) k_operands(const Lays l) {
+  chain_wait();
+  lay_out_all<F32>(l, blockIdx.x);
+}
+
 // dz = grad * act'(z), as an operand of the two products: 16 bits, with few rows a second plane of what rounding took; three
-// bf16 planes of f32. Sums of its columns over the block's rows, in fp32, go to sums[blockIdx.y]. A warp takes 256 columns of
-// a row, a thread 8 of them. Bound by memory.
+// bf16 planes of f32. Sums of its columns over the block's rows, in fp32, go to sums[part]. A warp takes 256 columns of
+// a row, a thread 8 of them. The blocks after these lay out X and W.
 struct DzArgs {
   const void *grad, *z;  // z null: dz is grad
   int64_t grad_ld, z_ld, rows, outs, rows_a_block;
@@ -71,36 +100,39 @@ struct DzArgs {
   int64_t ld, plane;
   int planes;
   float* sums;           // null: not wanted
+  unsigned slabs, blocks;
 };
-constexpr int kDzWarps = 8, kDzColumns = 256;
+constexpr int kDzWarps = kLayThreads / 32, kDzColumns = 256;
 
+// Eight elements as they are in memory; `have` of them, the others 0.
 template <bool F32>
-__device__ __forceinline__ void read8(const void* p, int have, bool wide, bool bf16, float (&v)[8]) {
+struct Raw8 {
+  uint32_t w[F32 ? 8 : 4];
+  __device__ __forceinline__ void read(const void* p, int have, bool wide) {
+    constexpr int kQuads = F32 ? 2 : 1;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  if constexpr (F32) {
+    for (int q = 0; q < 4 * kQuads; ++q) w[q] = 0;
     if (wide && have >= 8) {
-      const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < have) v[i] = static_cast<const float*>(p)[i];
-    }
-  } else {
-    uint32_t w[4];
-    if (wide && have >= 8) {
-      const uint4 a = *static_cast<const uint4*>(p);
-      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-    } else {
-      const uint16_t* s = static_cast<const uint16_t*>(p);
+      for (int q = 0; q < kQuads; ++q) {
+        const uint4 x = static_cast<const uint4*>(p)[q];
+        w[4 * q] = x.x, w[4 * q + 1] = x.y, w[4 * q + 2] = x.z, w[4 * q + 3] = x.w;
+      }
+    } else if (have > 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = (2 * i < have ? s[2 * i] : 0u) | (2 * i + 1 < have ? static_cast<uint32_t>(s[2 * i + 1]) << 16 : 0u);
+      for (int i = 0; i < 8; ++i) {
+        if (i >= have) continue;
+        if constexpr (F32) w[i] = static_cast<const uint32_t*>(p)[i];
+        else w[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << (i & 1 ? 16 : 0);
+      }
     }
+  }
+  __device__ __forceinline__ void get(bool bf16, float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (bf16) {
+      if constexpr (F32) {
+        v[2 * i] = __uint_as_float(w[2 * i]), v[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+      } else if (bf16) {
         v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
       } else {
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -108,7 +140,7 @@ __device__ __forceinline__ void read8(const void* p, int have, bool wide, bool b
       }
     }
   }
-}
+};
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
   if (bf16) {
@@ -125,16 +157,21 @@ __device__ __forceinline__ void times_slope(float (&g)[8], const float (&z)[8], 
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a) {
+__global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a, const Lays lays) {
   __shared__ float sh[kDzWarps][kDzColumns];
   chain_wait();
+  if (blockIdx.x >= a.blocks) {
+    lay_out_all<F32>(lays, blockIdx.x - a.blocks);
+    return;
+  }
   constexpr int kBytes = F32 ? 4 : 2;
-  constexpr int kAhead = 2;  // rows of a warp under way
+  constexpr int kAhead = F32 ? 2 : 4;  // rows of a warp under way
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * kDzColumns + lane * 8;
+  const unsigned slab = blockIdx.x % a.slabs, part = blockIdx.x / a.slabs;
+  const int64_t col = static_cast<int64_t>(slab) * kDzColumns + lane * 8;
   const int have = static_cast<int>(max(int64_t(0), min(int64_t(8), a.outs - col)));
   const bool bf16 = a.type != GM_LOSS_F16, write = a.dz && col < a.ld;  // ld is a multiple of 8
-  const int64_t first = blockIdx.y * a.rows_a_block, end = min(a.rows, first + a.rows_a_block);
+  const int64_t first = part * a.rows_a_block, end = min(a.rows, first + a.rows_a_block);
   const char* grad = static_cast<const char*>(a.grad) + ((first + warp) * a.grad_ld + col) * kBytes;
   const char* z_at = static_cast<const char*>(a.z) + ((first + warp) * a.z_ld + col) * kBytes;
   uint16_t* out = a.dz + (first + warp) * a.ld + col;
@@ -143,28 +180,32 @@ __global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   for (int64_t r0 = first + warp; r0 < end; r0 += kDzWarps * kAhead) {
-    float g[kAhead][8], z[kAhead][8];
+    Raw8<F32> g_raw[kAhead], z_raw[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int in = r0 + k * kDzWarps < end ? have : 0;  // what is not there is 0, and so is its dz
-      read8<F32>(grad, in, a.wide, bf16, g[k]);
-      if (a.z) read8<F32>(z_at, in, a.wide, bf16, z[k]);
+      g_raw[k].read(grad, in, a.wide);
+      if (a.z) z_raw[k].read(z_at, in, a.wide);
       grad += grad_step, z_at += z_step;
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k, out += out_step) {
+      float g[8];
+      g_raw[k].get(bf16, g);
       if (a.z) {
-        if (a.act == GM_ACT_GELU) times_slope<F32>(g[k], z[k], GM_ACT_GELU);
-        else if (a.act == GM_ACT_SILU) times_slope<F32>(g[k], z[k], GM_ACT_SILU);
-        else if (a.act == GM_ACT_GELU_TANH) times_slope<F32>(g[k], z[k], GM_ACT_GELU_TANH);
-        else times_slope<F32>(g[k], z[k], GM_ACT_RELU);
+        float z[8];
+        z_raw[k].get(bf16, z);
+        if (a.act == GM_ACT_GELU) times_slope<F32>(g, z, GM_ACT_GELU);
+        else if (a.act == GM_ACT_SILU) times_slope<F32>(g, z, GM_ACT_SILU);
+        else if (a.act == GM_ACT_GELU_TANH) times_slope<F32>(g, z, GM_ACT_GELU_TANH);
+        else times_slope<F32>(g, z, GM_ACT_RELU);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += g[k][i];
+      for (int i = 0; i < 8; ++i) acc[i] += g[i];
       if (!write || r0 + k * kDzWarps >= end) continue;
       if (!F32 && a.planes == 1) {
-        *reinterpret_cast<uint4*>(out) = make_uint4(pack2(g[k][0], g[k][1], bf16), pack2(g[k][2], g[k][3], bf16),
-                                                    pack2(g[k][4], g[k][5], bf16), pack2(g[k][6], g[k][7], bf16));
+        *reinterpret_cast<uint4*>(out) =
+            make_uint4(pack2(g[0], g[1], bf16), pack2(g[2], g[3], bf16), pack2(g[4], g[5], bf16), pack2(g[6], g[7], bf16));
         continue;
       }
 #pragma unroll 1
@@ -175,7 +216,7 @@ __global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a) {
           uint32_t h[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float& u = g[k][i + j];
+            float& u = g[i + j];
             if constexpr (F32) {
               h[j] = take_plane(u, p == 2, (__float_as_uint(u) & INT32_MAX) < kRoundsPast);
             } else if (bf16) {
@@ -196,11 +237,83 @@ __global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) sh[warp][lane * 8 + i] = acc[i];
   __syncthreads();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kDzColumns + threadIdx.x;
+  const int64_t c = static_cast<int64_t>(slab) * kDzColumns + threadIdx.x;
   float x = 0.f;
 #pragma unroll
   for (int w = 0; w < kDzWarps; ++w) x += sh[w][threadIdx.x];
-  if (c < a.outs) a.sums[blockIdx.y * a.outs + c] = x;
+  if (c < a.outs) a.sums[part * a.outs + c] = x;
+}
+
+// ---- few rows ------------------------------------------------------------------------------------
+// At most kFewRows rows of X: a warp reads kFewOuts rows of W once, 16 bytes a lane at a time (VEC; else single elements),
+// and multiplies in fp32. Bound by the bytes of W: 1 x 4096 x 4096 bf16, 33.6 MB.
+constexpr int kFewRows = 4, kFewOuts = 2, kFewWarps = 8;
+template <bool F32, bool VEC, int ROWS>
+__global__ void __launch_bounds__(32 * kFewWarps) k_linear_few(const gm_linear p, const LinearEnd e, void* y, int64_t y_ld) {
+  chain_wait();
+  constexpr int kBytes = F32 ? 4 : 2, kTurns = 4;  // turns under way
+  const int lane = threadIdx.x & 31, dim = static_cast<int>(p.dim);
+  const bool bf16 = p.type != GM_LOSS_F16;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kFewWarps * kFewOuts;
+  for (int64_t o0 = (static_cast<int64_t>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5)) * kFewOuts; o0 < p.n_outs; o0 += step) {
+    float acc[ROWS][kFewOuts] = {};
+    auto part = [&](const void* m, int64_t row, int64_t ld, int at, Raw8<F32>& v) {
+      const char* q = static_cast<const char*>(m) + row * ld * kBytes;
+      if constexpr (VEC) {
+        const int c = at + lane * 8;
+        v.read(q + static_cast<int64_t>(c) * kBytes, min(8, dim - c), true);  // dim is a multiple of 8
+      } else {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 8 : 4); ++i) v.w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = at + lane + 32 * i;
+          if (c >= dim) continue;
+          if constexpr (F32) v.w[i] = reinterpret_cast<const uint32_t*>(q)[c];
+          else v.w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(q)[c]) << (i & 1 ? 16 : 0);
+        }
+      }
+    };
+    for (int at = 0; at < dim; at += 256 * kTurns) {
+      Raw8<F32> w[kTurns][kFewOuts];
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t)
+#pragma unroll
+        for (int o = 0; o < kFewOuts; ++o) part(p.w, min(o0 + o, p.n_outs - 1), p.w_ld, at + t * 256, w[t][o]);
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t) {
+        float v[kFewOuts][8];
+#pragma unroll
+        for (int o = 0; o < kFewOuts; ++o) w[t][o].get(bf16, v[o]);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          Raw8<F32> x_raw;
+          float x[8];
+          part(p.x, r, p.x_ld, at + t * 256, x_raw);
+          x_raw.get(bf16, x);
+#pragma unroll
+          for (int o = 0; o < kFewOuts; ++o)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[r][o] = fmaf(x[i], v[o][i], acc[r][o]);
+        }
+      }
+    }
+    float mine = 0.f;  // lane r * kFewOuts + o has the sum of that row and out
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int o = 0; o < kFewOuts; ++o) {
+        const float sum = warp_reduce_sum(acc[r][o]);
+        if (lane == r * kFewOuts + o) mine = sum;
+      }
+    const int64_t row = lane / kFewOuts, out = o0 + lane % kFewOuts;
+    if (row >= ROWS || out >= p.n_outs) continue;
+    if (e.bias) mine += element(e.bias, out, p.type);
+    if (e.keep) set_element(e.z, row * e.z_ld + out, p.type, mine);
+    mine = activated(mine, e.act, F32);
+    if (e.residual) mine += element(e.residual, row * e.residual_ld + out, p.type);
+    set_element(y, row * y_ld + out, p.type, mine);
+  }
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -212,6 +325,9 @@ struct LinearCall {
   int* status = nullptr;
   int planes() const { return p.type == GM_LOSS_F32 ? 3 : 1; }
 };
+
+// Few rows go to a kernel that reads W once as it lies, instead of the tensor cores.
+bool few(const LinearCall& c) { return c.p.n_rows <= kFewRows; }
 
 gm_status check_matrix(const void* p, int64_t ld, int64_t cols, int64_t rows, int32_t type, bool needed) {
   if (!p) return needed && rows > 0 ? GM_ERR_INVALID_ARG : GM_OK;
@@ -244,6 +360,21 @@ gm_status begin(LinearCall& c) {
 }
 gm_status finish(bool launched) { return cudaGetLastError() != cudaSuccess || !launched ? GM_ERR_CUDA : GM_OK; }
 
+// How a source is laid out, and the operand that it is then.
+Lay lay_of(const Source& m, const Arena& a, int sms) {
+  Lay l = {};
+  if (!m.packed) return l;
+  l.src = m.p;
+  l.rows = m.rows;
+  l.src_ld = m.src_ld;
+  l.dst = a.at<uint16_t>(m.off);
+  l.dim = static_cast<int>(m.dim);
+  l.ld = static_cast<int>(m.ld);
+  l.wide = aligned(m.p, 16) && (m.rows <= 1 || m.src_ld * elem_bytes(m.type) % 16 == 0);
+  l.blocks = grid_for(m.rows * m.ld / 8, kLayThreads, int64_t(sms) * 16);
+  return l;
+}
+
 // Tiles of a product: blocks a tile, its columns, and how many parts its sum is cut into.
 struct Tiling {
   int cg = 1, bn = 64;
@@ -275,10 +406,11 @@ struct LinearForward {
   Arena a;
   Source x, w;
   Tiling t;
-  size_t o_lost, o_acc = 0;
+  size_t o_lost = 0, o_acc = 0;
   int64_t acc_ld = 0;
   explicit LinearForward(const LinearCall& c)
       : x(c.p.x, c.p.n_rows, c.p.dim, c.p.x_ld, c.p.type), w(c.p.w, c.p.n_outs, c.p.dim, c.p.w_ld, c.p.type) {
+    if (few(c)) return;
     o_lost = a.add(kMostBlocks);
     x.plan(a);
     w.plan(a);
@@ -300,14 +432,32 @@ bool linear_result(CUtensorMap* m, bool* by_tma, void* out, int64_t rows, int64_
   return encode(m, Operand{out, rows, cols, ld, rows * ld, 1, static_cast<int>(es)}, 32, static_cast<int>(32 * es));
 }
 
+template <bool F32, bool VEC>
+cudaError_t launch_few(const LinearCall& c, const LinearEnd& e, void* y, int64_t y_ld) {
+  const gm_linear& p = c.p;
+  const unsigned grid = grid_for(p.n_outs, kFewWarps * kFewOuts, int64_t(c.sms) * 16);
+  auto* k = p.n_rows == 1 ? k_linear_few<F32, VEC, 1> : p.n_rows == 2 ? k_linear_few<F32, VEC, 2> : p.n_rows == 3 ? k_linear_few<F32, VEC, 3> : k_linear_few<F32, VEC, 4>;
+  return launch_chained(k, grid, 32 * kFewWarps, 0, c.s, 1, p, e, y, y_ld);
+}
 gm_status forward(LinearCall& c, LinearEnd e, void* y, int64_t y_ld) {
   gm_status rc = begin(c);
   if (rc != GM_OK) return rc;
+  if (few(c)) {
+    const int64_t es = elem_bytes(c.p.type);
+    const bool vec = wide_rows(c.p.x, c.p.x_ld, c.p.n_rows, es) && wide_rows(c.p.w, c.p.w_ld, c.p.n_outs, es) && c.p.dim % 8 == 0;
+    const cudaError_t e4 = c.p.type == GM_LOSS_F32 ? (vec ? launch_few<true, true>(c, e, y, y_ld) : launch_few<true, false>(c, e, y, y_ld))
+                                                   : (vec ? launch_few<false, true>(c, e, y, y_ld) : launch_few<false, false>(c, e, y, y_ld));
+    return finish(e4 == cudaSuccess);
+  }
   const int64_t m = c.p.n_rows, n = c.p.n_outs, es = elem_bytes(c.p.type);
   LinearForward p(c);
   rc = p.a.open(c.cfg.workspace, c.cfg.workspace_bytes, c.s);
   if (rc != GM_OK) return rc;
-  const Operand ox = p.x.ready(p.a, c.s), ow = p.w.ready(p.a, c.s);
+  const Lays lays{{lay_of(p.x, p.a, c.sms), lay_of(p.w, p.a, c.sms)}};
+  if (lays.blocks() &&
+      launch_chained(c.p.type == GM_LOSS_F32 ? k_operands<true> : k_operands<false>, lays.blocks(), kLayThreads, 0, c.s, 1, lays) != cudaSuccess)
+    return finish(false);
+  const Operand ox = p.x.operand(p.a), ow = p.w.operand(p.a);
   ProdMaps maps;
   if (!encode(&maps.a, ox, prod_box_rows_a()) || !encode(&maps.b, ow, prod_box_rows_b(p.t.cg, p.t.bn))) return GM_ERR_CUDA;
   maps.o = maps.z = maps.a;
@@ -400,7 +550,7 @@ struct LinearBackward {
     dz_ld = up(n, 8);
     o_dz = a.add(dz_planes * m * dz_ld * 2);
     const int64_t slabs = div_up(n, kDzColumns);
-    parts = std::max<int64_t>(1, std::min(div_up(8 * c.sms, slabs), div_up(m, 4 * kDzWarps)));
+    parts = std::max<int64_t>(1, std::min(3 * c.sms / slabs, div_up(m, 4 * kDzWarps)));  // one round of blocks
     rows_a_part = div_up(m, parts);
     parts = div_up(m, rows_a_part);
     o_sums = a.add(parts * n * 4);
@@ -425,7 +575,11 @@ gm_status backward(LinearCall& c, const LinearGrads& q) {
   const bool in_place = !act && type != GM_LOSS_F32 && wide_rows(q.grad, q.grad_ld, m, 2);  // grad is dz, and an operand
   const bool products = q.dx || q.dw;
   Operand odz{q.grad, m, n, m <= 1 ? up(n, 8) : q.grad_ld, m * q.grad_ld, 1};
-  if ((products && !in_place) || q.db) {
+  Lays lays = {};
+  if (q.dx) lays.m[0] = lay_of(p.w, p.a, c.sms);
+  if (q.dw) lays.m[1] = lay_of(p.x, p.a, c.sms);
+  const bool dz_or_db = (products && !in_place) || q.db;
+  if (dz_or_db || lays.blocks()) {
     DzArgs d = {};
     d.grad = q.grad;
     d.grad_ld = q.grad_ld;
@@ -445,8 +599,9 @@ gm_status backward(LinearCall& c, const LinearGrads& q) {
       odz = Operand{d.dz, m, n, d.ld, d.plane, d.planes};
     }
     if (q.db) d.sums = p.a.at<float>(p.o_sums);
-    const dim3 grid(static_cast<unsigned>(div_up(n, kDzColumns)), static_cast<unsigned>(p.parts));
-    if (launch_chained(type == GM_LOSS_F32 ? k_dz<true> : k_dz<false>, grid, 32 * kDzWarps, 0, c.s, 1, d) != cudaSuccess)
+    d.slabs = static_cast<unsigned>(div_up(n, kDzColumns));
+    d.blocks = dz_or_db ? d.slabs * static_cast<unsigned>(p.parts) : 0;
+    if (launch_chained(type == GM_LOSS_F32 ? k_dz<true> : k_dz<false>, d.blocks + lays.blocks(), 32 * kDzWarps, 0, c.s, 1, d, lays) != cudaSuccess)
       return finish(false);
     if (q.db) sum_splits(d.sums, p.parts, 1, n, n, q.db, n, type, nullptr, c.s);
   }
@@ -484,8 +639,8 @@ gm_status backward(LinearCall& c, const LinearGrads& q) {
     return true;
   };
   uint8_t* lost = p.a.at<uint8_t>(p.o_lost);
-  if (q.dx) ok = product(Prod::kDh, p.dx, p.w.ready(p.a, c.s), m, q.dx, q.dx_ld, lost);
-  if (ok && q.dw) ok = product(Prod::kDw, p.dw, p.x.ready(p.a, c.s), n, q.dw, q.dw_ld, lost + kMostBlocks);
+  if (q.dx) ok = product(Prod::kDh, p.dx, p.w.operand(p.a), m, q.dx, q.dx_ld, lost);
+  if (ok && q.dw) ok = product(Prod::kDw, p.dw, p.x.operand(p.a), n, q.dw, q.dw_ld, lost + kMostBlocks);
   return finish(ok);
 }
 

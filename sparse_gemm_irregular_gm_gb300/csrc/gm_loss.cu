@@ -39,51 +39,8 @@ template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) k_pack(const void* __restrict__ src, int64_t rows, int dim, int64_t src_ld,
                                               uint16_t* __restrict__ dst, int ld) {
   chain_wait();
-  const unsigned per_row = static_cast<unsigned>(ld) / 8;
-  const int64_t n = rows * ld, pieces = rows * per_row, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
-    int64_t r;
-    int c;
-    if (pieces < (int64_t(1) << 32)) {
-      const unsigned q = static_cast<unsigned>(i) / per_row;
-      r = q, c = static_cast<int>((static_cast<unsigned>(i) - q * per_row) * 8);
-    } else {
-      r = i / per_row, c = static_cast<int>(i - r * per_row) * 8;
-    }
-    const int left = dim - c;  // at least 1
-    if constexpr (!F32) {
-      const uint16_t* p = static_cast<const uint16_t*>(src) + r * src_ld + c;
-      uint32_t x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[j] = (2 * j < left ? p[2 * j] : 0u) | (2 * j + 1 < left ? static_cast<uint32_t>(p[2 * j + 1]) << 16 : 0u);
-      *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(x[0], x[1], x[2], x[3]);
-    } else {
-      const float* p = static_cast<const float*>(src) + r * src_ld + c;
-      float x[8];
-      if (VEC && left >= 8) {
-        const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < left ? p[j] : 0.f;
-      }
-      uint32_t largest = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) largest = max(largest, __float_as_uint(x[j]) & INT32_MAX);
-      const bool ordinary = largest < kRoundsPast;
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        uint32_t y[4];
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const uint32_t a = take_plane(x[j], q == 2, ordinary), b = take_plane(x[j + 1], q == 2, ordinary);
-          y[j / 2] = a | (b << 16);
-        }
-        *reinterpret_cast<uint4*>(dst + q * n + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
-      }
-    }
-  }
+  lay_out<F32, VEC>(src, rows, dim, src_ld, dst, ld, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                    static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 // ---- the teacher's rows -----------------------------------------------------------------
@@ -436,10 +393,11 @@ Source::Source(const void* p, int64_t rows, int64_t dim, int64_t ld, int32_t typ
 void Source::plan(Arena& a) {
   if (packed) off = a.add(planes() * rows * ld * 2);
 }
+Operand Source::operand(const Arena& a) const {
+  return Operand{packed ? a.at<uint16_t>(off) : p, rows, dim, ld, rows * ld, planes()};
+}
 Operand Source::ready(const Arena& a, cudaStream_t s) const {
-  Operand o{p, rows, dim, ld, rows * ld, planes()};
   if (packed) {
-    o.p = a.at<uint16_t>(off);
     const unsigned grid = grid_for(rows * ld / 8, 256);
     uint16_t* dst = a.at<uint16_t>(off);
     const int d = static_cast<int>(dim), l = static_cast<int>(ld);
@@ -447,7 +405,7 @@ Operand Source::ready(const Arena& a, cudaStream_t s) const {
     launch_chained(type != GM_LOSS_F32 ? k_pack<false, false> : vec ? k_pack<true, true> : k_pack<true, false>, grid, 256,
                    0, s, 1, p, rows, d, src_ld, dst, l);
   }
-  return o;
+  return operand(a);
 }
 
 int group_of_tiles(int64_t m_tiles, int64_t tile_rows, int64_t dim, int planes) {

@@ -233,7 +233,8 @@ struct Source {
   Source(const void* p, int64_t rows, int64_t dim, int64_t ld, int32_t type);
   int planes() const { return type == GM_LOSS_F32 ? 3 : 1; }
   void plan(Arena& a);
-  Operand ready(const Arena& a, cudaStream_t s) const;
+  Operand operand(const Arena& a) const;                // once it is laid out
+  Operand ready(const Arena& a, cudaStream_t s) const;  // lays it out
 };
 // Where a result goes: by TMA where its rows start and end on 16-byte boundaries (a store
 // drops what lies outside the map by 16 bytes, not by elements).
