@@ -245,69 +245,73 @@ __global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a, const L
 }
 
 // ---- few rows ------------------------------------------------------------------------------------
-// At most kFewRows rows of X: a warp reads kFewOuts rows of W once, 16 bytes a lane at a time (VEC; else single elements),
-// and multiplies in fp32. Bound by the bytes of W: 1 x 4096 x 4096 bf16, 33.6 MB.
-constexpr int kFewRows = 4, kFewOuts = 2, kFewWarps = 8;
-template <bool F32, bool VEC, int ROWS>
-__global__ void __launch_bounds__(32 * kFewWarps) k_linear_few(const gm_linear p, const LinearEnd e, void* y, int64_t y_ld) {
+// One row of X, or up to 4 of f32 (whose tensor-core form reads and writes W four times more): a warp reads OUTS rows of W together, 16
+// bytes a lane (VEC; else single elements), eight such loads under way, and multiplies in fp32. Bound by the bytes of W
+// and, with 2^24 of them, by the launch. Two rows of 16 bits are as fast on the tensor cores (1024 x 32768: 36 us here, 26 there).
+constexpr int kFewWarps = 8;
+template <bool F32, bool VEC, int ROWS, int OUTS>
+__global__ void __launch_bounds__(32 * kFewWarps, ROWS == 1 ? 3 : 2) k_linear_few(const gm_linear p, const LinearEnd e, void* y, int64_t y_ld) {
   chain_wait();
-  constexpr int kBytes = F32 ? 4 : 2, kTurns = 4;  // turns under way
+  constexpr int kBytes = F32 ? 4 : 2, kTurns = (F32 ? 4 : 8) / OUTS;
   const int lane = threadIdx.x & 31, dim = static_cast<int>(p.dim);
   const bool bf16 = p.type != GM_LOSS_F16;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kFewWarps * kFewOuts;
-  for (int64_t o0 = (static_cast<int64_t>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5)) * kFewOuts; o0 < p.n_outs; o0 += step) {
-    float acc[ROWS][kFewOuts] = {};
-    auto part = [&](const void* m, int64_t row, int64_t ld, int at, Raw8<F32>& v) {
-      const char* q = static_cast<const char*>(m) + row * ld * kBytes;
-      if constexpr (VEC) {
-        const int c = at + lane * 8;
-        v.read(q + static_cast<int64_t>(c) * kBytes, min(8, dim - c), true);  // dim is a multiple of 8
-      } else {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kFewWarps * OUTS;
+  auto part = [&](const void* m, int64_t row, int64_t ld, int at, Raw8<F32>& v) {
+    const char* q = static_cast<const char*>(m) + row * ld * kBytes;
+    if constexpr (VEC) {
+      const int c = at + lane * 8;
+      v.read(q + static_cast<int64_t>(c) * kBytes, min(8, dim - c), true);  // dim is a multiple of 8
+    } else {
 #pragma unroll
-        for (int i = 0; i < (F32 ? 8 : 4); ++i) v.w[i] = 0;
+      for (int i = 0; i < (F32 ? 8 : 4); ++i) v.w[i] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = at + lane + 32 * i;
-          if (c >= dim) continue;
-          if constexpr (F32) v.w[i] = reinterpret_cast<const uint32_t*>(q)[c];
-          else v.w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(q)[c]) << (i & 1 ? 16 : 0);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int c = at + lane + 32 * i;
+        if (c >= dim) continue;
+        if constexpr (F32) v.w[i] = reinterpret_cast<const uint32_t*>(q)[c];
+        else v.w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(q)[c]) << (i & 1 ? 16 : 0);
       }
-    };
+    }
+  };
+  for (int64_t o0 = (static_cast<int64_t>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5)) * OUTS; o0 < p.n_outs; o0 += step) {
+    float acc[ROWS][OUTS] = {};
     for (int at = 0; at < dim; at += 256 * kTurns) {
-      Raw8<F32> w[kTurns][kFewOuts];
+      Raw8<F32> w[kTurns][OUTS], x_raw[kTurns];
 #pragma unroll
       for (int t = 0; t < kTurns; ++t)
 #pragma unroll
-        for (int o = 0; o < kFewOuts; ++o) part(p.w, min(o0 + o, p.n_outs - 1), p.w_ld, at + t * 256, w[t][o]);
+        for (int k = 0; k < OUTS; ++k) part(p.w, min(o0 + k, p.n_outs - 1), p.w_ld, at + t * 256, w[t][k]);
+      if constexpr (ROWS == 1) {
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) part(p.x, 0, p.x_ld, at + t * 256, x_raw[t]);
+      }
 #pragma unroll
       for (int t = 0; t < kTurns; ++t) {
-        float v[kFewOuts][8];
+        float v[OUTS][8];
 #pragma unroll
-        for (int o = 0; o < kFewOuts; ++o) w[t][o].get(bf16, v[o]);
+        for (int k = 0; k < OUTS; ++k) w[t][k].get(bf16, v[k]);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          Raw8<F32> x_raw;
           float x[8];
-          part(p.x, r, p.x_ld, at + t * 256, x_raw);
-          x_raw.get(bf16, x);
+          if constexpr (ROWS > 1) part(p.x, min(int64_t(r), p.n_rows - 1), p.x_ld, at + t * 256, x_raw[t]);
+          x_raw[t].get(bf16, x);
 #pragma unroll
-          for (int o = 0; o < kFewOuts; ++o)
+          for (int k = 0; k < OUTS; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[r][o] = fmaf(x[i], v[o][i], acc[r][o]);
+            for (int i = 0; i < 8; ++i) acc[r][k] = fmaf(x[i], v[k][i], acc[r][k]);
         }
       }
     }
-    float mine = 0.f;  // lane r * kFewOuts + o has the sum of that row and out
+    float mine = 0.f;  // lane r * OUTS + k has the sum of that row and out
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-      for (int o = 0; o < kFewOuts; ++o) {
-        const float sum = warp_reduce_sum(acc[r][o]);
-        if (lane == r * kFewOuts + o) mine = sum;
+      for (int k = 0; k < OUTS; ++k) {
+        const float sum = warp_reduce_sum(acc[r][k]);
+        if (lane == r * OUTS + k) mine = sum;
       }
-    const int64_t row = lane / kFewOuts, out = o0 + lane % kFewOuts;
-    if (row >= ROWS || out >= p.n_outs) continue;
+    const int64_t row = lane / OUTS, out = o0 + lane % OUTS;
+    if (row >= ROWS || row >= p.n_rows || out >= p.n_outs) continue;
     if (e.bias) mine += element(e.bias, out, p.type);
     if (e.keep) set_element(e.z, row * e.z_ld + out, p.type, mine);
     mine = activated(mine, e.act, F32);
@@ -327,7 +331,7 @@ struct LinearCall {
 };
 
 // Few rows go to a kernel that reads W once as it lies, instead of the tensor cores.
-bool few(const LinearCall& c) { return c.p.n_rows <= kFewRows; }
+bool few(const LinearCall& c) { return c.p.n_rows <= (c.p.type == GM_LOSS_F32 ? 4 : 1); }
 
 gm_status check_matrix(const void* p, int64_t ld, int64_t cols, int64_t rows, int32_t type, bool needed) {
   if (!p) return needed && rows > 0 ? GM_ERR_INVALID_ARG : GM_OK;
@@ -432,22 +436,29 @@ bool linear_result(CUtensorMap* m, bool* by_tma, void* out, int64_t rows, int64_
   return encode(m, Operand{out, rows, cols, ld, rows * ld, 1, static_cast<int>(es)}, 32, static_cast<int>(32 * es));
 }
 
-template <bool F32, bool VEC>
-cudaError_t launch_few(const LinearCall& c, const LinearEnd& e, void* y, int64_t y_ld) {
+template <bool F32, bool VEC, int ROWS>
+cudaError_t launch_few_rows(const LinearCall& c, const LinearEnd& e, void* y, int64_t y_ld) {
+  // short rows of W several at a time, so that the loads under way are as many
   const gm_linear& p = c.p;
-  const unsigned grid = grid_for(p.n_outs, kFewWarps * kFewOuts, int64_t(c.sms) * 16);
-  auto* k = p.n_rows == 1 ? k_linear_few<F32, VEC, 1> : p.n_rows == 2 ? k_linear_few<F32, VEC, 2> : p.n_rows == 3 ? k_linear_few<F32, VEC, 3> : k_linear_few<F32, VEC, 4>;
+  const int outs = p.dim > 1024 / (F32 ? 2 : 1) ? 1 : p.dim > 512 / (F32 ? 2 : 1) ? 2 : 4;
+  const unsigned grid = grid_for(p.n_outs, kFewWarps * outs, int64_t(c.sms) * 16);
+  auto* k = outs == 1 ? k_linear_few<F32, VEC, ROWS, 1> : outs == 2 ? k_linear_few<F32, VEC, ROWS, 2> : k_linear_few<F32, VEC, ROWS, 4>;
   return launch_chained(k, grid, 32 * kFewWarps, 0, c.s, 1, p, e, y, y_ld);
 }
+template <bool VEC>
+cudaError_t launch_few(const LinearCall& c, const LinearEnd& e, void* y, int64_t y_ld) {
+  if (c.p.type != GM_LOSS_F32) return launch_few_rows<false, VEC, 1>(c, e, y, y_ld);
+  return c.p.n_rows == 1 ? launch_few_rows<true, VEC, 1>(c, e, y, y_ld)
+         : c.p.n_rows == 2 ? launch_few_rows<true, VEC, 2>(c, e, y, y_ld) : launch_few_rows<true, VEC, 4>(c, e, y, y_ld);
+}
+
 gm_status forward(LinearCall& c, LinearEnd e, void* y, int64_t y_ld) {
   gm_status rc = begin(c);
   if (rc != GM_OK) return rc;
   if (few(c)) {
     const int64_t es = elem_bytes(c.p.type);
     const bool vec = wide_rows(c.p.x, c.p.x_ld, c.p.n_rows, es) && wide_rows(c.p.w, c.p.w_ld, c.p.n_outs, es) && c.p.dim % 8 == 0;
-    const cudaError_t e4 = c.p.type == GM_LOSS_F32 ? (vec ? launch_few<true, true>(c, e, y, y_ld) : launch_few<true, false>(c, e, y, y_ld))
-                                                   : (vec ? launch_few<false, true>(c, e, y, y_ld) : launch_few<false, false>(c, e, y, y_ld));
-    return finish(e4 == cudaSuccess);
+    return finish((vec ? launch_few<true>(c, e, y, y_ld) : launch_few<false>(c, e, y, y_ld)) == cudaSuccess);
   }
   const int64_t m = c.p.n_rows, n = c.p.n_outs, es = elem_bytes(c.p.type);
   LinearForward p(c);
