@@ -386,13 +386,13 @@ struct Tiling {
 };
 // The least of rounds of tiles times what a stage of one takes (in SM clocks: 64 bytes a clock from L2, or the products),
 // times stages, with a start and an end a round; parts cost their way through memory.
-Tiling tile_for(int64_t m, int64_t n, int64_t k_blocks, int planes, int sms) {
+Tiling tile_for(int64_t m, int64_t n, int64_t k_blocks, int planes, int sms, bool pairs = true) {
   Tiling best;
   double least = 1e300;
   struct Kind { int cg, bn; double stage; };
   const Kind kinds[] = {{2, 256, 512}, {1, 256, 768}, {1, 128, 512}, {1, 64, 384}};
   for (const Kind& k : kinds) {
-    if (planes == 3 && k.cg == 1 && k.bn == 256) continue;
+    if ((planes == 3 && k.cg == 1 && k.bn == 256) || (k.cg == 2 && !pairs)) continue;
     const int64_t slots = sms / k.cg, tiles = div_up(m, 128 * k.cg) * div_up(n, k.bn);
     const double stage = planes == 3 ? (k.cg == 2 ? 3200 : k.bn == 128 ? 2000 : 1400) : k.stage;
     for (int64_t want = 1; want <= 16; want *= 2) {
@@ -528,13 +528,10 @@ struct SumPlan {
   int cg, bn;
   int64_t splits, acc_ld, k_blocks;
   size_t o_acc = 0;
-  SumPlan(Arena& a, int64_t rows, int64_t cols, int64_t k, int planes, int sms) {
-    bn = prod_sums_cols(cols, rows, planes);
-    cg = bn == 256 && rows > 128 ? 2 : 1;
+  SumPlan(Arena& a, int64_t rows, int64_t cols, int64_t k, int planes, int sms, bool pairs) {
     k_blocks = div_up(k, 64);
-    const int64_t tiles = div_up(rows, 128 * cg) * div_up(cols, bn);
-    splits = std::max<int64_t>(1, std::min<int64_t>(sms / cg / tiles, k_blocks / 8));
-    splits = div_up(k_blocks, div_up(k_blocks, splits));
+    const Tiling t = tile_for(rows, cols, k_blocks, planes, sms, pairs);
+    cg = t.cg, bn = t.bn, splits = t.splits;
     acc_ld = up(cols, 32);
     if (splits > 1) o_acc = a.add(splits * rows * acc_ld * 4);
   }
@@ -552,8 +549,8 @@ struct LinearBackward {
         w(c.p.w, c.p.n_outs, c.p.dim, c.p.w_ld, c.p.type),
         planes(c.planes()),
         dz_planes(planes == 3 ? 3 : c.p.activation != GM_ACT_NONE && c.p.n_rows <= 128 ? 2 : 1),
-        dx(a, c.p.n_rows, c.p.dim, c.p.n_outs, planes, c.sms),
-        dw(a, c.p.n_outs, c.p.dim, c.p.n_rows, planes, c.sms) {
+        dx(a, c.p.n_rows, c.p.dim, c.p.n_outs, planes, c.sms, dz_planes != 2),  // no pairs of blocks for two planes of dz
+        dw(a, c.p.n_outs, c.p.dim, c.p.n_rows, planes, c.sms, dz_planes != 2) {
     const int64_t m = c.p.n_rows, n = c.p.n_outs;
     x.plan(a);
     w.plan(a);
@@ -644,6 +641,7 @@ gm_status backward(LinearCall& c, const LinearGrads& q) {
       set = encode(&maps.o, Operand{acc, rows, dim, t.acc_ld, rows * t.acc_ld, g.splits, 4}, 32);
     } else {
       set = set_result(&maps.o, g, out, rows, dim, out_ld, type);
+      if (t.bn == 64 && es == 2) g.by_tma = false;  // half a tile is less than a box
     }
     if (!set || launch_prod(kind, t.cg, t.bn, maps, g, c.sms, c.s) != cudaSuccess) return false;
     if (acc) sum_splits(acc, t.splits, rows, dim, t.acc_ld, out, out_ld, type, lost, c.s);
