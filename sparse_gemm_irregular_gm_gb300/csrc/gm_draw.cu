@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t place_from(float x, float y, float y_low) {
 // The whole part of f * n for f in [0, 1], and whether something is left: in integers, since 64-bit floating point is
 // 1 / 70 as fast as 32-bit here (all threads of a block dividing by T so took 5 us).
 __device__ __forceinline__ u64 whole_times(float f, u64 n, bool& left) {
-  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const uint32_t bits = __float_as_uint(f) & 0x7fffffffu, e = bits >> 23;  // -0 is 0
   const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits;
   const int s = e ? 150 - static_cast<int>(e) : 149;  // f = m 2^-s, 23 <= s
   const u64 lo = m * n, hi = __umul64hi(m, n);

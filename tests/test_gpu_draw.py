@@ -229,6 +229,38 @@ def test_rows_that_cannot_be_drawn_from_say_so_and_stay_alone(classes):
     assert sampling.draw(z, u, top_k=torch.tensor([0, -1] * 4, device="cuda", dtype=torch.int32)).kept[1::2].tolist() == [0] * 4
 
 
+def test_negative_zero_is_zero():
+    z, u = make(3, 500, "f32")
+    a = sampling.draw(z, torch.zeros_like(u), top_p=0.0, min_p=0.0)
+    b = sampling.draw(z, -torch.zeros_like(u), top_p=torch.full((3,), -0.0, device="cuda"), min_p=torch.full((3,), -0.0, device="cuda"))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert torch.equal(sampling.draw(z, u, temperature=torch.full((3,), -0.0, device="cuda")).index, z.argmax(1))
+
+
+def test_offsets_past_32_bits():
+    rows, classes = 17000, 131072  # 2.2e9 logits
+    z = torch.empty(rows, classes, device="cuda", dtype=torch.bfloat16)
+    z[:-3] = 0.0
+    z[-3:], u3 = make(3, classes, "bf16", seed=21)
+    u = torch.zeros(rows, device="cuda")
+    u[-3:] = u3
+    d = sampling.draw(z, u, top_k=50, top_p=0.9)
+    ref = sampling.draw(z[-3:].clone(), u3, top_k=50, top_p=0.9)
+    assert all(torch.equal(a[-3:], b) for a, b in zip(d, ref))
+    assert (d.index[:-3] == 0).all() and (d.kept[:-3] == 45).all()
+
+
+def test_calls_at_once_on_two_streams():
+    z, u = make(64, 50000, "bf16", seed=30)
+    ref = sampling.draw(z, u, top_p=0.8)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    out = [sampling.draw(z, u, top_p=0.8, stream=streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for d in out for a, b in zip(d, ref))
+
+
 def test_shares_are_those_of_the_softmax():
     """u through [0, 1) in even steps meets each class in proportion to its weight."""
     z = (torch.randn(1, 37, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) * 2).repeat(4096, 1)

@@ -172,6 +172,52 @@ def test_far_and_special_arguments(kind, act):
     assert (y2[3] == float("inf")).all()
 
 
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("rows", [1, 2, 4, 5])
+@pytest.mark.parametrize("dim,outs", [(8, 3), (200, 515), (512, 1030), (1024, 700), (2056, 129), (4096, 300), (1031, 77)])
+def test_few_rows(kind, rows, dim, outs):
+    x, w, b, r, grad = make(rows, dim, outs, kind, seed=dim)
+    both(x, w, b, r, grad, "gelu_tanh", kind)
+
+
+def test_offsets_past_32_bits():
+    outs, dim = 540000, 4096  # 2.2e9 weights; and as many results
+    x, w, b, _, _ = make(2, dim, 8, "bf16", residual=False)
+    big = torch.zeros(outs, dim, device="cuda", dtype=torch.bfloat16)
+    big[-8:] = w
+    bias = torch.zeros(outs, device="cuda", dtype=torch.bfloat16)
+    bias[-8:] = b
+    for rows in (1, 2):
+        y, _ = layers.linear_forward(x[:rows], big, bias, activation="silu")
+        ref, _ = layers.linear_forward(x[:rows], w, b, activation="silu")
+        assert torch.equal(y[:, -8:], ref) and (y[:, :-8] == 0).all()
+    del big
+    rows, outs = 70000, 32768
+    x, w, b, _, _ = make(rows, 64, outs, "bf16", residual=False)
+    y, _ = layers.linear_forward(x, w, b)
+    ref, _ = layers.linear_forward(x[-300:].clone(), w, b)
+    assert torch.equal(y[-300:], ref)
+    odd = torch.empty(rows * (outs + 1), device="cuda", dtype=torch.bfloat16).view(rows, outs + 1)[:, :outs]  # rows off 16 bytes
+    layers.gm_linear_forward(x, w, b, None, odd)
+    assert torch.equal(odd[-300:], ref)
+
+
+def test_calls_at_once_on_two_streams():
+    x, w, b, r, grad = make(300, 520, 264, "bf16")
+
+    def run(stream=None):
+        y, z = layers.linear_forward(x, w, b, activation="gelu", residual=r, keep=True, stream=stream)
+        return [y, z, *layers.linear_backward(x, w, grad, activation="gelu", z=z, need_bias=True, stream=stream)]
+
+    ref = run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    out = [run(streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for o in out for p, q in zip(o, ref))
+
+
 def test_no_rows():
     x, w, b, r, grad = make(0, 48, 72, "bf16")
     y, _ = layers.linear_forward(x, w, b, residual=r)

@@ -93,6 +93,40 @@ def test_parts(after, gate, before, bias, dim):
     assert set(got) == {"x", "dx", "df"} | ({"y"} if before else set()) | {"d" + k for k in rule}
 
 
+@pytest.mark.parametrize("rows,dim", [(1, 512), (700, 520), (33, 1024), (305, 1032), (9, 2056), (310, 4096), (5, 4104), (6, 8192), (3, 8184)])
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("after,gate,before", [(True, "vector", True), (True, None, True), (False, "vector", True), (True, "vector", False), (False, None, True)])
+def test_root_mean_squares_without_biases(rows, dim, kind, after, gate, before):
+    x, f, gx, gy, rule = make(rows, dim, kind, after=after, after_bias=False, gate=gate, before=before, before_bias=False, seed=dim)
+    both(x, f, gx, gy, dict(rule, scale=0.6), kind)
+    if before:
+        o = layers.residual_norm_forward(x, f, scale=0.6, **rule)
+        d = layers.residual_norm_backward(x, f, None, gy, o.stats, scale=0.6, **rule)  # no gradient by x' but through y
+        check(x, f, None, gy, dict(rule, scale=0.6), kind, {"d" + n: t for n, t in d._asdict().items() if t is not None})
+
+
+@pytest.mark.parametrize("dim", [512, 4096])
+def test_wide_strides_without_biases(dim):
+    x, f, gx, gy, rule = make(19, dim, "bf16", after_bias=False, before_bias=False, wide=24, offset=8)
+    both(x, f, gx, gy, rule, "bf16")
+
+
+def test_offsets_past_32_bits():
+    rows, dim = 540000, 4096  # 2.2e9 elements
+    x, f = (torch.zeros(rows, dim, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sx, sf, sgx, sgy, rule = make(3, dim, "bf16", after_bias=False, before_bias=False)
+    x[-3:], f[-3:] = sx, sf
+    o = layers.residual_norm_forward(x, f, **rule)
+    ref = layers.residual_norm_forward(sx, sf, **rule)
+    assert torch.equal(o.x[-3:], ref.x) and torch.equal(o.y[-3:], ref.y) and (o.x[:-3] == 0).all()
+    gx, gy = (torch.zeros(rows, dim, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    gx[-3:], gy[-3:] = sgx, sgy
+    d = layers.residual_norm_backward(x, f, gx, gy, o.stats, **rule)
+    e = layers.residual_norm_backward(sx, sf, sgx, sgy, ref.stats, **rule)
+    assert torch.equal(d.x[-3:], e.x) and torch.equal(d.f[-3:], e.f) and (d.x[:-3] == 0).all()
+    check(sx, sf, sgx, sgy, rule, "bf16", {"dafter": d.after, "dbefore": d.before, "dgate": d.gate})
+
+
 @pytest.mark.parametrize("dim", [40, 5000])
 @pytest.mark.parametrize("norm", ["rms", "layer"])
 def test_norm_alone(dim, norm):
@@ -214,6 +248,10 @@ def test_autograd_asks_only_for_what_is_wanted():
     assert torch.equal(f.grad, ref.f)
     y = layers.residual_norm(x.clone().requires_grad_(), before=rule["before"])
     assert y[0].shape == y[1].shape and y[1].grad_fn is not None
+    leaf = x.clone().requires_grad_()
+    xo, none = layers.residual_norm(leaf, f.detach(), gate=rule["gate"])  # no norm before the next block
+    xo.backward(gx)
+    assert none is None and torch.equal(leaf.grad, gx)
 
 
 def test_other_stream_and_graph():
