@@ -47,9 +47,15 @@ __device__ __forceinline__ float lower16(uint32_t x, bool bf16) {
 template <int TYPE>
 __device__ __forceinline__ void unpack(const Raw<TYPE>& r, float (&v)[kPer]) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if constexpr (TYPE == GM_LOSS_F32) v[i] = __uint_as_float(r.w[i]);
-    else v[i] = lower16(i & 1 ? r.w[i / 2] >> 16 : r.w[i / 2] & 0xffffu, TYPE == GM_LOSS_BF16);
+  for (int i = 0; i < kPer; i += 2) {
+    if constexpr (TYPE == GM_LOSS_F32) {
+      v[i] = __uint_as_float(r.w[i]), v[i + 1] = __uint_as_float(r.w[i + 1]);
+    } else if constexpr (TYPE == GM_LOSS_BF16) {
+      v[i] = __uint_as_float(r.w[i / 2] << 16), v[i + 1] = __uint_as_float(r.w[i / 2] & 0xffff0000u);
+    } else {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i / 2]));
+      v[i] = x.x, v[i + 1] = x.y;
+    }
   }
 }
 template <int TYPE>
@@ -65,7 +71,15 @@ __device__ __forceinline__ Raw<TYPE> pack(const float (&v)[kPer]) {
     for (int i = 0; i < kPer; ++i) r.w[i] = __float_as_uint(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) r.w[i / 2] = round16<TYPE>(v[i]) | (round16<TYPE>(v[i + 1]) << 16);
+    for (int i = 0; i < kPer; i += 2) {
+      if constexpr (TYPE == GM_LOSS_BF16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[i], v[i + 1]);
+        r.w[i / 2] = *reinterpret_cast<const uint32_t*>(&x);
+      } else {
+        const __half2 x = __floats2half2_rn(v[i], v[i + 1]);
+        r.w[i / 2] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
   }
   return r;
 }
@@ -175,6 +189,18 @@ struct Columns {
   __device__ __forceinline__ Raw<TYPE> raw(const void* p) const { return load<TYPE, VEC>(p, t, group, dim); }
   __device__ __forceinline__ void put(void* p, const float (&v)[kPer]) const { store<TYPE, VEC>(p, t, group, dim, v); }
   __device__ __forceinline__ bool inside(int i) const { return column<VEC>(t, group, i) < dim; }
+  // The same from the row's last columns where these lie past its end (their weights are 0): no load then waits for a
+  // comparison. For rows of whole pieces.
+  __device__ __forceinline__ Raw<TYPE> raw_or_last(const void* p) const {
+    Raw<TYPE> r;
+    const uint4* q = static_cast<const uint4*>(p) + min(t, dim / kPer - 1) * (kWords<TYPE> / 4);
+#pragma unroll
+    for (int h = 0; h < kWords<TYPE> / 4; ++h) {
+      const uint4 x = q[h];
+      r.w[4 * h] = x.x, r.w[4 * h + 1] = x.y, r.w[4 * h + 2] = x.z, r.w[4 * h + 3] = x.w;
+    }
+    return r;
+  }
 };
 // LEAN: no means taken off, no biases, a gate that is a vector or none: half the instructions of the general form.
 __device__ __forceinline__ bool is_matrix(const gm_norm& n) { return n.gate_kind == GM_GATE_MATRIX; }
@@ -506,16 +532,18 @@ __device__ __forceinline__ Sums<2> means_of(const gm_norm& n, Group& g, Sums<2> 
 
 // Rows held by a group: NV turns of 8 columns a thread, the next row under way. The sums over rows are kept in shared
 // memory, each thread's own columns.
-template <int TYPE, bool VEC, int NV, bool LEAN>
-__global__ void __launch_bounds__(512, 1) k_norm_backward(const BackArgs a, int group) {
+// ONE: a block has one group, so that a row's address is the same for all its threads.
+constexpr int kMostThreads = 512;
+template <int TYPE, bool VEC, int NV, bool LEAN, bool ONE>
+__global__ void __launch_bounds__(kMostThreads, 1) k_norm_backward(const BackArgs a, int group) {
   __shared__ float sh[16 * 64];
-  extern __shared__ float4 acc[];  // [sum][turn][2][thread]
+  extern __shared__ float4 acc[];  // [sum][turn][2][kMostThreads]
   chain_wait();
   Group g(group, sh);
   const gm_norm& n = a.n;
-  const int dim = static_cast<int>(n.dim), groups = blockDim.x / group;
+  const int dim = static_cast<int>(n.dim), groups = ONE ? 1 : blockDim.x / group;
   constexpr int kHere = LEAN ? 2 : 4;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id;
+  int64_t row = ONE ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * groups + g.id;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   Columns<TYPE, VEC> c[NV];
   Weights<TYPE, VEC, LEAN> w[NV];
@@ -527,28 +555,29 @@ __global__ void __launch_bounds__(512, 1) k_norm_backward(const BackArgs a, int 
   constexpr auto at = [](auto* m, int64_t ld, int64_t i) { return row_at<TYPE, LEAN>(m, ld, i); };
   if (a.sums) {
 #pragma unroll
-    for (int s = 0; s < 2 * NV * kHere; ++s) acc[s * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < 2 * NV * kHere; ++s) acc[s * kMostThreads + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   auto adder = [&](int k) {
     return [&, k](int which, const float (&v)[kPer], float by) {
       if (!a.sums) return;
-      float4* at = acc + 2 * (which * NV + k) * blockDim.x + threadIdx.x;
-      float4 x = at[0], y = at[blockDim.x];
+      float4* at = acc + 2 * (which * NV + k) * kMostThreads + threadIdx.x;
+      float4 x = at[0], y = at[kMostThreads];
       x.x = fmaf(v[0], by, x.x), x.y = fmaf(v[1], by, x.y), x.z = fmaf(v[2], by, x.z), x.w = fmaf(v[3], by, x.w);
       y.x = fmaf(v[4], by, y.x), y.y = fmaf(v[5], by, y.y), y.z = fmaf(v[6], by, y.z), y.w = fmaf(v[7], by, y.w);
-      at[0] = x, at[blockDim.x] = y;
+      at[0] = x, at[kMostThreads] = y;
     };
   };
+  auto get = [&](int k, const void* p) { return LEAN ? c[k].raw_or_last(p) : c[k].raw(p); };
   RowIn<TYPE> next[NV];  // gx, wanted last, waits in L2
   float4 st_next;
   auto ask = [&](int64_t i) {
     st_next = a.stats[i];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      next[k].x = c[k].raw(at(n.x, n.x_ld, i));
-      if (n.f) next[k].f = c[k].raw(at(n.f, n.f_ld, i));
-      if (a.gy) next[k].gy = c[k].raw(at(a.gy, a.gy_ld, i));
-      if (!LEAN && is_matrix(n)) next[k].gate = c[k].raw(at(n.gate, n.gate_ld, i));
+      next[k].x = get(k, at(n.x, n.x_ld, i));
+      if (n.f) next[k].f = get(k, at(n.f, n.f_ld, i));
+      if (a.gy) next[k].gy = get(k, at(a.gy, a.gy_ld, i));
+      if (!LEAN && is_matrix(n)) next[k].gate = get(k, at(n.gate, n.gate_ld, i));
       if (VEC && a.gx && c[k].inside(0))
         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(at(a.gx, a.gx_ld, i)) + c[k].t * kPer * (TYPE == GM_LOSS_F32 ? 4 : 2)));
     }
@@ -559,8 +588,8 @@ __global__ void __launch_bounds__(512, 1) k_norm_backward(const BackArgs a, int 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       in[k] = next[k];
-      in[k].gx = Raw<TYPE>{};
-      if (a.gx) in[k].gx = c[k].raw(at(a.gx, a.gx_ld, row));
+      if (a.gx) in[k].gx = get(k, at(a.gx, a.gx_ld, row));
+      else in[k].gx = Raw<TYPE>{};
     }
     const float4 st = st_next;
     if (row + step < n.n_rows) ask(row + step);
@@ -604,8 +633,8 @@ __global__ void __launch_bounds__(512, 1) k_norm_backward(const BackArgs a, int 
     for (int k = 0; k < NV; ++k) {
       float v[kPer] = {};
       for (int j = 0; j < groups; ++j) {
-        const float4* at = acc + 2 * (s * NV + k) * blockDim.x + j * group + g.t;
-        const float4 x = at[0], y = at[blockDim.x];
+        const float4* at = acc + 2 * (s * NV + k) * kMostThreads + j * group + g.t;
+        const float4 x = at[0], y = at[kMostThreads];
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
       }
 #pragma unroll
@@ -839,7 +868,7 @@ struct Form {
   int turns, group;
   Form(const gm_norm& n, bool vec, std::initializer_list<int64_t> lds) : vec(vec) {
     const int wide = n.type == GM_LOSS_F32 ? 1 : 2;
-    lean = vec && n.dim >= 512 && n.dim <= kHeldDim / 2 * wide && n.norm == GM_NORM_RMS && !n.after_bias && !n.before_bias &&
+    lean = vec && n.dim % kPer == 0 && n.dim >= 512 && n.dim <= kHeldDim / 2 * wide && n.norm == GM_NORM_RMS && !n.after_bias && !n.before_bias &&
            n.gate_kind != GM_GATE_MATRIX;
     for (int64_t ld : lds) lean = lean && ld * elem_bytes(n.type) <= UINT32_MAX;
     turns = lean ? wide : 1;
@@ -934,9 +963,12 @@ gm_status norm_backward(const gm_norm& n, const gm_layer_config& cfg, cudaStream
       }
     } else {
       constexpr int kBytes = (L ? 2 : 4) * 2 * 16 * kTurns<T, L>;  // of a thread
-      auto* k = k_norm_backward<T, V, kTurns<T, L>, L>;
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes * 512);
-      const size_t smem = sums ? size_t(kBytes) * p.block : 0;
+      auto* k = k_norm_backward<T, V, kTurns<T, L>, L, false>;
+      if constexpr (L) {
+        if (p.block == form.group) k = k_norm_backward<T, V, kTurns<T, L>, L, true>;
+      }
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes * kMostThreads);
+      const size_t smem = sums ? size_t(kBytes) * kMostThreads : 0;
       if (e == cudaSuccess) e = launch_chained(k, static_cast<unsigned>(p.parts), p.block, smem, s, 1, a, form.group);
     }
     if (e == cudaSuccess && sums) {
