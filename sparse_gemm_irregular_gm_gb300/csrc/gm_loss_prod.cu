@@ -76,21 +76,23 @@ __device__ __forceinline__ constexpr int pair_b(int p) {
 // a sum) is a chain of latencies that 2 warps a scheduler do not cover: with one group the
 // statistics of 512 x 256 x 1048576 took 332 us, the tensor cores 37 % busy. Two groups take
 // the tiles in turn, one accumulator each. Sums held in registers leave room for one group;
-// the gradients' results are only moved.
-template <Prod KIND, int ACC>
-constexpr int kGroups = !in_registers<ACC> && (KIND == Prod::kStats || KIND == Prod::kGrad) ? 2 : 1;
+// the gradients' results are only moved. Large tiles of X W^T: an activation and two results of each element take longer than
+// 16 stages of products (8192 x 1024 x 4096 bf16 with gelu: 63 us with one group).
+template <Prod KIND, int ACC, int CG = 2>
+constexpr int kGroups = !in_registers<ACC> && (KIND == Prod::kStats || KIND == Prod::kGrad ||
+                                               (KIND == Prod::kLinear && ACC == kWhole && CG == 2)) ? 2 : 1;
 
 template <Prod KIND, int CG, int BN, int ACC>
 struct Shape {
-  static constexpr int kThreads = 128 + 256 * kGroups<KIND, ACC>;
+  static constexpr int kThreads = 128 + 256 * kGroups<KIND, ACC, CG>;
   static constexpr int kABytes = 128 * 128;            // a plane of this block's 128 rows of A
   static constexpr int kBRows = BN / CG;               // its rows (columns) of B
   static constexpr int kBBytes = kBRows * 128;
   static constexpr int kStage = kPlanesA<ACC> * kABytes + kPlanesB<ACC> * kBBytes;
-  static constexpr int kMost = 196608 / kStage;        // 32 KB of the block's 227 hold results on their way out
+  static constexpr int kOut = KIND == Prod::kLinear && kGroups<KIND, ACC, CG> == 2 ? 65536 : 32768;  // results on their way out
+  static constexpr int kMost = (229376 - kOut) / kStage;  // of the block's 227 KB
   static constexpr int kStages = kMost > 8 ? 8 : kMost;
-  static constexpr int kBox = 4096 / kGroups<KIND, ACC>;  // a warp's results on their way out
-  static constexpr int kOut = 32768;
+  static constexpr int kBox = kOut / (8 * kGroups<KIND, ACC, CG>);  // a warp's
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kOut + 512;
   static_assert(kStages >= 2, "two stages at least");
 };
@@ -232,13 +234,18 @@ struct FromTmem {
     if constexpr (C + 32 >= COLS) done();
   }
   __device__ __forceinline__ void get(int c, float (&v)[32]) {  // the same for a loop that is not unrolled
-    static_assert(AHEAD, "one group reads");
-    tmem_load_wait(ahead);
+    if constexpr (AHEAD) {
+      tmem_load_wait(ahead);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = ahead[j];
-    __syncwarp();
-    if (c + 32 < COLS) tmem_load32(at + c + 32, ahead);
-    else done();
+      for (int j = 0; j < 32; ++j) v[j] = ahead[j];
+      __syncwarp();
+      if (c + 32 < COLS) tmem_load32(at + c + 32, ahead);
+    } else {
+      __syncwarp();
+      tmem_load32(at + c, v);
+      tmem_load_wait(v);
+    }
+    if (c + 32 >= COLS) done();
   }
 };
 template <int COLS>
@@ -907,7 +914,7 @@ __global__ void __launch_bounds__((Shape<KIND, CG, BN, ACC>::kThreads), 1) k_pro
     if constexpr (in_registers<ACC>) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
     // ---- results
     constexpr int kCols = BN / 2;
-    constexpr int kTurns = kGroups<KIND, ACC>;
+    constexpr int kTurns = kGroups<KIND, ACC, CG>;
     const int quad = warp & 3, half = ((warp - kEpiWarp0) >> 2) & 1;
     const int turn = kTurns == 2 ? (warp - kEpiWarp0) >> 3 : 0;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
