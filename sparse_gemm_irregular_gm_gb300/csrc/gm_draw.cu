@@ -400,7 +400,8 @@ struct Row {
   }
 
   // KEYS: the border's D, from the counts of values from place `top` to last_d further on. value(D, count): what so many
-  // classes of it add; COUNTS: their number. One warp calls then(search, D).
+  // classes of it add; COUNTS: their number. One warp calls then(search, D); D says nothing where all together fall short of
+  // the goal.
   template <bool COUNTS, class V, class G, class F>
   __device__ __forceinline__ void border_of(uint32_t top, uint32_t last_d, V&& value, G&& goal_of, F&& then) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -454,18 +455,19 @@ struct Row {
     if (warp == 0) {
       Search s{0, 0, 0, 0};
       const uint32_t g = group(s, goal_of);
-      const u64 x = from_each(blocks, [&](int r) {
+      const bool reached = s.total >= s.goal;  // else there is no line to look into
+      const u64 x = !reached ? 0 : from_each(blocks, [&](int r) {
         if (lane >= kGroupLines) return u64(0);
         return blocks == 1 ? sh.line[g * kGroupLines + lane] : remote_u64(&sh.line[g * kGroupLines + lane], r);
       });
-      const uint32_t line = g * kGroupLines + s.step(x);
-      const u64 both = from_each(blocks, [&](int r) {
+      const uint32_t line = g * kGroupLines + (reached ? s.step(x) : 0);  // one of the group's: its sums reach the goal
+      const u64 both = !reached ? 0 : from_each(blocks, [&](int r) {
         const uint32_t w = blocks == 1 ? counts[line * 32 + lane] : remote_u32(&counts[line * 32 + lane], r);
         return u64(w & 0xffffu) | (u64(w >> 16) << 32);
       });
       u64 even, odd;
       of_line(line, static_cast<uint32_t>(both), static_cast<uint32_t>(both >> 32), even, odd);
-      then(s, line * kLine + s.step2(even, odd) - top);
+      then(s, reached ? line * kLine + s.step2(even, odd) - top : 0);
     }
     meet();  // lines and sums are read
   }
@@ -696,8 +698,9 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
     const u64 few = min(kFew, static_cast<int>(blockDim.x));
     if (KEYS && by_counts) {
       row.template border_of<true>(top, 0xffffu, [](uint32_t, uint32_t count) { return u64(count); }, goal, [&](const Search& s, uint32_t d) {
-        if (s.total < s.goal) d = 0xffffffffu;  // masked classes are not all counted
-        if (lane == 0) sh.border = Border{d, top_k - static_cast<int64_t>(s.before)}, sh.cut = d, sh.found = s.before + s.in <= few;
+        const bool all = s.total < s.goal;  // masked classes are not all counted
+        if (all) d = 0xffffffffu;
+        if (lane == 0) sh.border = Border{d, top_k - static_cast<int64_t>(s.before)}, sh.cut = d, sh.found = (all ? s.total : s.before + s.in) <= few;
       });
     } else {
       uint32_t d = 0;

@@ -232,6 +232,18 @@ def test_rows_that_cannot_be_drawn_from_say_so_and_stay_alone(classes):
     assert sampling.draw(z, u, top_k=torch.tensor([0, -1] * 4, device="cuda", dtype=torch.int32)).kept[1::2].tolist() == [0] * 4
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,classes", [(1, 131072), (8, 131072), (40, 131072), (64, 131072), (100, 131072), (9, 524288), (30, 300000)])
+def test_shares_reached_only_by_some_of_the_classes_at_the_border(kind, rows, classes):
+    """Of many equal logits top-k keeps some, and top-p needs them: the sums without them fall short."""
+    z, u = make(rows, classes, kind, spread=1.0, seed=rows)
+    z[z < 2.5] = 2.5  # most are equal, and lowest
+    check(z, u, top_k=classes // 3, top_p=0.9, most_unsure=1)
+    check(z, u, top_k=classes // 2, top_p=0.999, min_p=0.01, most_unsure=1)
+    z[:, 40:] = -torch.inf  # fewer than top_k
+    check(z, u, top_k=700, top_p=0.95, most_unsure=1)
+
+
 def test_negative_zero_is_zero():
     z, u = make(3, 500, "f32")
     a = sampling.draw(z, torch.zeros_like(u), top_p=0.0, min_p=0.0)
