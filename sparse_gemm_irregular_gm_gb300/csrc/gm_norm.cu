@@ -29,7 +29,7 @@ namespace {
 constexpr int kPer = 8;         // elements of a row a thread holds together: 16 bytes of a 16-bit type
 constexpr int kHeldDim = 8192;  // of a row held by at most 512 threads, 16 elements each
 constexpr int kLongBlock = 512;
-constexpr int kLeanThreads = 512;  // of the lean forward pass on an SM
+constexpr int kSmThreads = 512;  // of the forward pass on an SM: by registers
 constexpr int kSums = 4;        // over rows, at most
 enum { kSumBefore, kSumA, kSumBeforeBias, kSumB };
 
@@ -188,7 +188,10 @@ struct Columns {
   __device__ __forceinline__ void get(const void* p, float (&v)[kPer]) const { unpack<TYPE>(load<TYPE, VEC>(p, t, group, dim), v); }
   __device__ __forceinline__ Raw<TYPE> raw(const void* p) const { return load<TYPE, VEC>(p, t, group, dim); }
   __device__ __forceinline__ void put(void* p, const float (&v)[kPer]) const { store<TYPE, VEC>(p, t, group, dim, v); }
-  __device__ __forceinline__ bool inside(int i) const { return column<VEC>(t, group, i) < dim; }
+  // rows of whole 16 bytes: the same for all that lie in one 16
+  __device__ __forceinline__ bool inside(int i) const {
+    return column<VEC>(t, group, !VEC ? i : TYPE == GM_LOSS_F32 ? i & 4 : 0) < dim;
+  }
   // The same from the row's last columns where these lie past its end (their weights are 0): no load then waits for a
   // comparison. For rows of whole pieces.
   __device__ __forceinline__ Raw<TYPE> raw_or_last(const void* p) const {
@@ -249,6 +252,29 @@ struct Weights {
   }
 };
 
+// The weights of a thread's columns, read once and kept; by the general form with 16 columns a thread, whose registers they
+// would fill, at each use, from L1. That form does not ask for the next row either.
+template <int TYPE, bool VEC, int NV, bool LEAN>
+struct Kept {
+  static constexpr bool kAll = LEAN || NV == 1;
+  Weights<TYPE, VEC, LEAN> w[kAll ? NV : 1];
+  __device__ __forceinline__ void read(const gm_norm& n, const Columns<TYPE, VEC> (&c)[NV]) {
+    if constexpr (kAll) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) w[k].read(n, c[k]);
+    }
+  }
+  __device__ __forceinline__ Weights<TYPE, VEC, LEAN> of(const gm_norm& n, const Columns<TYPE, VEC> (&c)[NV], int k) const {
+    if constexpr (kAll) {
+      return w[k];
+    } else {
+      Weights<TYPE, VEC, LEAN> x;
+      x.read(n, c[k]);
+      return x;
+    }
+  }
+};
+
 template <bool LEAN>
 __device__ __forceinline__ void less(float (&v)[kPer], float mean) {
   if constexpr (!LEAN) {
@@ -286,31 +312,33 @@ __global__ void __launch_bounds__(512, 1) k_norm_forward(const NormArgs a, int g
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   Columns<TYPE, VEC> c[NV];
-  Weights<TYPE, VEC, LEAN> w[NV];
+  Kept<TYPE, VEC, NV, LEAN> w;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    c[k] = Columns<TYPE, VEC>{g.t + k * (VEC ? group : group * kPer), group, dim};
-    w[k].read(n, c[k]);
-  }
+  for (int k = 0; k < NV; ++k) c[k] = Columns<TYPE, VEC>{g.t + k * (VEC ? group : group * kPer), group, dim};
+  w.read(n, c);
   constexpr auto at = [](auto* m, int64_t ld, int64_t i) { return row_at<TYPE, LEAN>(m, ld, i); };
-  Raw<TYPE> x_next[NV], f_next[NV];
+  Raw<TYPE> x_next[NV], f_next[NV], gate_next[NV];
   auto ask = [&](int64_t i) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       x_next[k] = c[k].raw(at(n.x, n.x_ld, i));
       if (n.f) f_next[k] = c[k].raw(at(n.f, n.f_ld, i));
+      if (!LEAN && is_matrix(n)) gate_next[k] = c[k].raw(at(n.gate, n.gate_ld, i));
     }
   };
-  if (row < n.n_rows) ask(row);
+  if (row < n.n_rows && w.kAll) ask(row);
   for (; row < n.n_rows; row += step) {
+    if (!w.kAll) ask(row);
     float2 of_f = make_float2(0.f, 1.f), of_x = make_float2(0.f, 1.f);
     float x[NV][kPer], f[NV][kPer];
+    Raw<TYPE> gates[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      gates[k] = gate_next[k];
       unpack<TYPE>(x_next[k], x[k]);
       if (n.f) unpack<TYPE>(f_next[k], f[k]);
     }
-    if (row + step < n.n_rows) ask(row + step);
+    if (row + step < n.n_rows && w.kAll) ask(row + step);
     auto over = [&](const float (&v)[NV][kPer]) {
       return [&](auto&& of) {
         Sums<1> s = {{0.f}};
@@ -326,9 +354,9 @@ __global__ void __launch_bounds__(512, 1) k_norm_forward(const NormArgs a, int g
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         float gate[kPer];
-        if (!LEAN && is_matrix(n)) c[k].get(at(n.gate, n.gate_ld, row), gate);
+        if (!LEAN && is_matrix(n)) unpack<TYPE>(gates[k], gate);
         less<LEAN>(f[k], of_f.x);
-        w[k].update(n, x[k], f[k], n.scale * of_f.y, gate);
+        w.of(n, c, k).update(n, x[k], f[k], n.scale * of_f.y, gate);
       }
     }
     if (a.x_out) {
@@ -340,12 +368,13 @@ __global__ void __launch_bounds__(512, 1) k_norm_forward(const NormArgs a, int g
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         float b[kPer];
-        unpack<TYPE>(w[k].before, b);
+        const Weights<TYPE, VEC, LEAN> own = w.of(n, c, k);
+        unpack<TYPE>(own.before, b);
         less<LEAN>(x[k], of_x.x);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) x[k][i] = x[k][i] * of_x.y * b[i];
         if constexpr (!LEAN) {
-          unpack<TYPE>(w[k].before_bias, b);
+          unpack<TYPE>(own.before_bias, b);
 #pragma unroll
           for (int i = 0; i < kPer; ++i) x[k][i] += b[i];
         }
@@ -546,12 +575,10 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_norm_backward(const BackArg
   int64_t row = ONE ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * groups + g.id;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   Columns<TYPE, VEC> c[NV];
-  Weights<TYPE, VEC, LEAN> w[NV];
+  Kept<TYPE, VEC, NV, LEAN> w;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    c[k] = Columns<TYPE, VEC>{g.t + k * (VEC ? group : group * kPer), group, dim};
-    w[k].read(n, c[k]);
-  }
+  for (int k = 0; k < NV; ++k) c[k] = Columns<TYPE, VEC>{g.t + k * (VEC ? group : group * kPer), group, dim};
+  w.read(n, c);
   constexpr auto at = [](auto* m, int64_t ld, int64_t i) { return row_at<TYPE, LEAN>(m, ld, i); };
   if (a.sums) {
 #pragma unroll
@@ -582,8 +609,9 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_norm_backward(const BackArg
         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(at(a.gx, a.gx_ld, i)) + c[k].t * kPer * (TYPE == GM_LOSS_F32 ? 4 : 2)));
     }
   };
-  if (row < n.n_rows) ask(row);
+  if (row < n.n_rows && w.kAll) ask(row);
   for (; row < n.n_rows; row += step) {
+    if (!w.kAll) ask(row);
     RowIn<TYPE> in[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -592,31 +620,31 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_norm_backward(const BackArg
       else in[k].gx = Raw<TYPE>{};
     }
     const float4 st = st_next;
-    if (row + step < n.n_rows) ask(row + step);
+    if (row + step < n.n_rows && w.kAll) ask(row + step);
     using B = Back<TYPE, VEC, LEAN>;
     float x[NV][kPer], d[NV][kPer];
     Sums<2> s = {{0.f, 0.f}};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) B{a, w[k], in[k], st}.start(x[k], d[k], s, adder(k));
+    for (int k = 0; k < NV; ++k) B{a, w.of(n, c, k), in[k], st}.start(x[k], d[k], s, adder(k));
     if (a.need_x) {
       if (a.gy) s = means_of<LEAN>(a.n, g, s, a.inv_dim, st.w);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        B{a, w[k], in[k], st}.to_x(x[k], d[k], s);
+        B{a, w.of(n, c, k), in[k], st}.to_x(x[k], d[k], s);
         if (a.o.x) c[k].put(at(a.o.x, a.o.x_ld, row), d[k]);
       }
       if (n.f) {
         s = Sums<2>{{0.f, 0.f}};
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-          B{a, w[k], in[k], st}.past_gate(d[k], x[k], s, adder(k), [&](const float (&v)[kPer]) {
+          B{a, w.of(n, c, k), in[k], st}.past_gate(d[k], x[k], s, adder(k), [&](const float (&v)[kPer]) {
             if (a.o.gate) c[k].put(at(a.o.gate, a.o.gate_ld, row), v);
           });
         if (a.o.f) {
           s = n.after ? means_of<LEAN>(a.n, g, s, a.inv_dim, st.y) : Sums<2>{{0.f, 0.f}};
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
-            B{a, w[k], in[k], st}.to_f(d[k], x[k], s);
+            B{a, w.of(n, c, k), in[k], st}.to_f(d[k], x[k], s);
             c[k].put(at(a.o.f, a.o.f_ld, row), d[k]);
           }
         }
@@ -861,8 +889,7 @@ struct Sixteen {
 };
 
 // How a row is held: lean rows of 512 and more with 16 columns a thread where they are of 16 bits, others with 8.
-template <int TYPE, bool LEAN>
-constexpr int kTurns = LEAN && TYPE != GM_LOSS_F32 ? 2 : 1;
+// The others with 16 where a block does not hold them else.
 struct Form {
   bool vec, lean, held;
   int turns, group;
@@ -871,18 +898,24 @@ struct Form {
     lean = vec && n.dim % kPer == 0 && n.dim >= 512 && n.dim <= kHeldDim / 2 * wide && n.norm == GM_NORM_RMS && !n.after_bias && !n.before_bias &&
            n.gate_kind != GM_GATE_MATRIX;
     for (int64_t ld : lds) lean = lean && ld * elem_bytes(n.type) <= UINT32_MAX;
-    turns = lean ? wide : 1;
-    held = lean || n.dim <= kHeldDim / 2;
+    turns = lean ? wide : n.dim > kHeldDim / 2 ? 2 : 1;
+    held = n.dim <= kHeldDim;
     group = static_cast<int>(up(div_up(n.dim, kPer * turns), 32));
   }
 };
-// f(type, rows by 16 bytes, lean) with constants
+// f(type, rows by 16 bytes, lean, turns) with constants
 template <class F>
 cudaError_t by_form(const gm_norm& n, const Form& form, F&& f) {
   using std::integral_constant;
   using Yes = std::true_type;
   using No = std::false_type;
-  auto with = [&](auto t) { return form.lean ? f(t, Yes(), Yes()) : form.vec ? f(t, Yes(), No()) : f(t, No(), No()); };
+  using One = integral_constant<int, 1>;
+  using Two = integral_constant<int, 2>;
+  auto with = [&](auto t) {
+    if (form.lean) return f(t, Yes(), Yes(), integral_constant<int, t == GM_LOSS_F32 ? 1 : 2>());
+    auto turned = [&](auto v) { return form.turns == 1 ? f(t, v, No(), One()) : f(t, v, No(), Two()); };
+    return form.vec ? turned(Yes()) : turned(No());
+  };
   return n.type == GM_LOSS_F32    ? with(integral_constant<int, GM_LOSS_F32>())
          : n.type == GM_LOSS_BF16 ? with(integral_constant<int, GM_LOSS_BF16>())
                                   : with(integral_constant<int, GM_LOSS_F16>());
@@ -895,13 +928,13 @@ gm_status norm_forward(const gm_norm& n, cudaStream_t s, void* x_out, int64_t x_
   if (sms <= 0) return done(cudaErrorUnknown);
   const Form form(n, Sixteen(n)(x_out, x_out_ld)(y, y_ld).ok, {n.x_ld, n.f_ld, x_out_ld, y_ld});
   const NormArgs a{n, 1.f / static_cast<float>(n.dim), x_out, y, x_out_ld, y_ld, reinterpret_cast<float4*>(stats)};
-  return done(by_form(n, form, [&](auto t, auto v, auto l) {
-    constexpr int T = t;
+  return done(by_form(n, form, [&](auto t, auto v, auto l, auto turns) {
+    constexpr int T = t, N = turns;
     constexpr bool V = v, L = l;
     if (!form.held) return launch_chained(k_norm_forward_long<T, V>, grid_for(n.n_rows, 1), kLongBlock, 0, s, 1, a);
     const int group = form.group, block = std::max(group, 128) / group * group;
-    const unsigned grid = grid_for(n.n_rows, block / group, int64_t(sms) * std::max(1, (L ? kLeanThreads : 1024) / block));
-    return launch_chained(k_norm_forward<T, V, kTurns<T, L>, L>, grid, block, 0, s, 1, a, group);
+    const unsigned grid = grid_for(n.n_rows, block / group, int64_t(sms) * std::max(1, kSmThreads / block));
+    return launch_chained(k_norm_forward<T, V, N, L>, grid, block, 0, s, 1, a, group);
   }));
 }
 
@@ -951,8 +984,8 @@ gm_status norm_backward(const gm_norm& n, const gm_layer_config& cfg, cudaStream
   a.need_x = o.x || o.f || o.gate || o.after || o.after_bias;
   a.sums = sums ? p.a.at<float>(p.o_sums) : nullptr;
   a.means = form.held ? nullptr : p.a.at<float4>(p.o_means);
-  return done(by_form(n, form, [&](auto t, auto v, auto l) {
-    constexpr int T = t;
+  return done(by_form(n, form, [&](auto t, auto v, auto l, auto turns) {
+    constexpr int T = t, N = turns;
     constexpr bool V = v, L = l;
     cudaError_t e = cudaSuccess;
     if (!form.held) {
@@ -962,10 +995,10 @@ gm_status norm_backward(const gm_norm& n, const gm_layer_config& cfg, cudaStream
         e = launch_chained(k_norm_columns<T, V>, grid, 32 * kColumnWarps, 0, s, 1, a, p.rows_a_part);
       }
     } else {
-      constexpr int kBytes = (L ? 2 : 4) * 2 * 16 * kTurns<T, L>;  // of a thread
-      auto* k = k_norm_backward<T, V, kTurns<T, L>, L, false>;
+      constexpr int kBytes = (L ? 2 : 4) * 2 * 16 * N;  // of a thread
+      auto* k = k_norm_backward<T, V, N, L, false>;
       if constexpr (L) {
-        if (p.block == form.group) k = k_norm_backward<T, V, kTurns<T, L>, L, true>;
+        if (p.block == form.group) k = k_norm_backward<T, V, N, L, true>;
       }
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes * kMostThreads);
       const size_t smem = sums ? size_t(kBytes) * kMostThreads : 0;
