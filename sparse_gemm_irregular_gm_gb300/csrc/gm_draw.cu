@@ -34,7 +34,7 @@ using u64 = unsigned long long;
 constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) - kLog2e
 
 constexpr int kMostCluster = 8;
-constexpr int kFew = 512;  // classes that are compared each with each
+constexpr int kFew = 256;  // classes that are compared each with each
 constexpr int kPer = 8;  // classes a thread takes at a time: 16 bytes of a 16-bit type
 constexpr int kTable = 33;
 
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
 constexpr int64_t kMostClasses = int64_t(1) << 24;
 constexpr int kHeldBytes = 204800;          // of a block's shared memory: counts, and its part of the row
 // Rows from here on are searched by counts of all values: clearing and reading them costs what so many atomics do.
-constexpr int64_t kLeastCounted = 16384;
+constexpr int64_t kLeastCounted = 12288;
 
 template <int TYPE, bool KEYS>
 cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
@@ -985,7 +985,9 @@ cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
 template <int TYPE>
 cudaError_t launch(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
   if constexpr (TYPE != GM_LOSS_F32) {
-    if (a.n_classes >= kLeastCounted) return launch_as<TYPE, true>(a, n_rows, sms, s);
+    const bool warm = a.rule.temperature || a.rule.all_temperature != 0.f;
+    const bool border = warm && (a.rule.top_k || a.rule.all_top_k > 0 || a.rule.top_p || a.rule.all_top_p < 1.f);
+    if (border && a.n_classes >= kLeastCounted) return launch_as<TYPE, true>(a, n_rows, sms, s);
   }
   return launch_as<TYPE, false>(a, n_rows, sms, s);
 }
