@@ -34,7 +34,10 @@ using u64 = unsigned long long;
 constexpr float kLog2eLow = 1.92596299e-8f;  // log2(e) - kLog2e
 
 constexpr int kMostCluster = 8;
-constexpr int kFew = 256;  // classes that are compared each with each
+// Classes that are compared each with each: so many steps of each thread, where a search would take its rounds over the
+// cluster. 1 x 131072, top-k and top-p, us: 50 classes 19 (search 27), 128: 21 (27), 256: 27 (27.5); 64 rows: 29 (39), 31 (39),
+// 37 (40), and 512 classes 47 (40).
+constexpr int kFew = 256;
 constexpr int kPer = 8;  // classes a thread takes at a time: 16 bytes of a 16-bit type
 constexpr int kTable = 33;
 
@@ -962,22 +965,47 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
 // ---- host ---------------------------------------------------------------------------------------------
 constexpr int64_t kMostClasses = int64_t(1) << 24;
 constexpr int kHeldBytes = 204800;          // of a block's shared memory: counts, and its part of the row
-// Rows from here on are searched by counts of all values: clearing and reading them costs what so many atomics do.
-constexpr int64_t kLeastCounted = 12288;
+constexpr int64_t kSharedBytes = 90112;     // of a part, of which two lie in an SM's shared memory
+// Rows of 16 bits are searched by counts of all values, or by digits. Counting takes one atomic a class, and 128 KB to clear and
+// to walk, so that an SM has one row at a time; digits take up to two atomics, and for top-p a weight, a class. us, counts /
+// digits: top-p at 512 x 8192: 62 / 42, 12288: 64 / 75, 20000: 70 / 101, 131072: 175 / 474; top-k = 50 at 20000: 54 / 35,
+// 50000: 73 / 73, 131072: 138 / 184; 1 x 131072: top-p 23 / 31, top-k 19 / 19. Without either there is no border: at
+// 512 x 131072 364 / 296.
+constexpr int64_t kLeastShared = 12288;   // with top-p
+constexpr int64_t kLeastCounted = 49152;  // with top-k alone
+
+// Threads of a block that has `part` classes, `bytes` of them, where an SM gets `rows` of such blocks: the 1024 that its
+// registers hold, shared between the rows, 8 to 32 classes a thread: a block's steps wait for one another, so that blocks
+// side by side fill an SM better than threads of one. By powers of two, of which two, four or eight blocks
+// fill it. 2000 x 12288 bf16, top-k = 50: 84 us with 512 threads, 134 with 768 (one block an SM); 300 x 8192 top-p: 35 with 512,
+// 64 with 128.
+int64_t threads_for(int64_t part, int64_t bytes, int64_t rows) {
+  auto power_from = [](int64_t x) {
+    int64_t p = 128;
+    while (p < x && p < 1024) p *= 2;
+    return p;
+  };
+  if (bytes > kSharedBytes) return power_from(div_up(part, kPer));
+  const int64_t least = std::min<int64_t>(power_from(div_up(part, 4 * kPer)), 512), most = power_from(div_up(part, kPer));
+  int64_t threads = most;
+  while (threads > least && threads * rows > 1024) threads /= 2;
+  return threads;
+}
 
 template <int TYPE, bool KEYS>
 cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
   const int64_t es = TYPE == GM_LOSS_F32 ? 4 : 2, n = a.n_classes, room = kHeldBytes - (KEYS ? kCountBytes : 0);
   const cudaError_t e = cudaFuncSetAttribute(k_draw<TYPE, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldBytes);
   if (e != cudaSuccess) return e;
-  // blocks of a row: until it fits, or the SMs have work
+  // Blocks of a row: until it fits, or the SMs have work. 131072 bf16 by 1, 2, 4, 8 blocks, us: one row 48, 36, 27, 26;
+  // 40 rows 48, 38, 45, 59.
   int blocks = 1;
   auto part = [&] { return up(div_up(n, blocks), kPer); };
   while (blocks < kMostCluster && ((!KEYS && (part() + kPer) * es > room) || (n_rows * blocks * 2 <= sms && part() > 8192))) blocks *= 2;
   if (n_rows * blocks > INT32_MAX) return cudaErrorInvalidValue;  // more bytes than any device has
   a.part = static_cast<int>(part());
   a.held = (part() + kPer) * es <= room;
-  const int64_t threads = std::min<int64_t>(1024, std::max<int64_t>(KEYS ? 256 : 128, up(div_up(part(), 2 * kPer), 128)));
+  const int64_t threads = KEYS ? 1024 : threads_for(part(), (part() + kPer) * es, div_up(n_rows * blocks, sms));
   const size_t smem = (KEYS ? kCountBytes : 0) + (a.held ? static_cast<size_t>((part() + kPer) * es) : 0);
   return launch_chained(k_draw<TYPE, KEYS>, static_cast<unsigned>(n_rows * blocks), static_cast<unsigned>(threads), smem, s, blocks, a);
 }
@@ -985,9 +1013,9 @@ cudaError_t launch_as(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
 template <int TYPE>
 cudaError_t launch(DrawArgs& a, int64_t n_rows, int sms, cudaStream_t s) {
   if constexpr (TYPE != GM_LOSS_F32) {
-    const bool warm = a.rule.temperature || a.rule.all_temperature != 0.f;
-    const bool border = warm && (a.rule.top_k || a.rule.all_top_k > 0 || a.rule.top_p || a.rule.all_top_p < 1.f);
-    if (border && a.n_classes >= kLeastCounted) return launch_as<TYPE, true>(a, n_rows, sms, s);
+    const bool warm = a.rule.temperature || a.rule.all_temperature != 0.f, by_share = a.rule.top_p || a.rule.all_top_p < 1.f;
+    const bool border = by_share || a.rule.top_k || a.rule.all_top_k > 0;
+    if (warm && border && a.n_classes >= (by_share ? kLeastShared : kLeastCounted)) return launch_as<TYPE, true>(a, n_rows, sms, s);
   }
   return launch_as<TYPE, false>(a, n_rows, sms, s);
 }
