@@ -40,22 +40,79 @@ __device__ __forceinline__ float activated(float z, int act, bool fine) {
   return z;
 }
 
-// y and z from the parts of X W^T, a thread an element.
+// Four elements from i on, `have` of them; wide: they lie together on a boundary of their own.
+__device__ __forceinline__ void get_four(const void* p, int64_t i, int type, bool wide, int have, float (&v)[4]) {
+  if (wide && type == GM_LOSS_F32) {
+    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else if (wide) {
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 y = type == GM_LOSS_BF16 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u))
+                                            : __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      v[2 * j] = y.x, v[2 * j + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < have ? element(p, i + j, type) : 0.f;
+  }
+}
+__device__ __forceinline__ void set_four(void* p, int64_t i, int type, bool wide, int have, const float (&v)[4]) {
+  if (wide && type == GM_LOSS_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (wide) {
+    uint32_t w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (type == GM_LOSS_BF16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&x);
+      } else {
+        const __half2 x = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < have) set_element(p, i + j, type, v[j]);
+  }
+}
+
+// y and z from the parts of X W^T, a thread four columns: 512 x 4096 in two parts, 25 MB, 6 us; an element a thread, found by a
+// division of 64 bits, took 14. Parts are made of so few tiles that 32 bits count the fours.
 __global__ void __launch_bounds__(256) k_linear_join(const float* __restrict__ acc, int splits, int64_t rows, int64_t outs,
-                                                     int64_t acc_ld, const LinearEnd e, void* y, int64_t y_ld, int type) {
+                                                     int64_t acc_ld, const LinearEnd e, void* y, int64_t y_ld, int type, bool wide) {
   chain_wait();
-  const int64_t n = rows * outs, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
-    const int64_t r = i / outs, c = i - r * outs;
+  const uint32_t a_row = static_cast<uint32_t>(acc_ld / 4), n = static_cast<uint32_t>(rows) * a_row, stride = gridDim.x * blockDim.x;
+  for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
+    const int64_t r = i / a_row, c = int64_t(i - static_cast<uint32_t>(r) * a_row) * 4;
+    const int have = static_cast<int>(outs - c);
+    if (have <= 0) continue;
     const float* p = acc + r * acc_ld + c;
-    float v = 0.f;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, t[4];
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) v += p[s * rows * acc_ld];
-    if (e.bias) v += element(e.bias, c, type);
-    if (e.keep) set_element(e.z, r * e.z_ld + c, type, v);
-    v = activated(v, e.act, type == GM_LOSS_F32);
-    if (e.residual) v += element(e.residual, r * e.residual_ld + c, type);
-    set_element(y, r * y_ld + c, type, v);
+    for (int s = 0; s < splits; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(p + s * rows * acc_ld);  // columns from outs on are not written: not used
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    }
+    if (e.bias) {
+      get_four(e.bias, c, type, wide, have, t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += t[j];
+    }
+    if (e.keep) set_four(e.z, r * e.z_ld + c, type, wide, have, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = activated(v[j], e.act, type == GM_LOSS_F32);
+    if (e.residual) {
+      get_four(e.residual, r * e.residual_ld + c, type, wide, have, t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += t[j];
+    }
+    set_four(y, r * y_ld + c, type, wide, have, v);
   }
 }
 
@@ -90,7 +147,8 @@ __global__ void __launch_bounds__(kLayThreads) k_operands(const Lays l) {
 
 // dz = grad * act'(z), as an operand of the two products: 16 bits, with few rows a second plane of what rounding took; three
 // bf16 planes of f32. Sums of its columns over the block's rows, in fp32, go to sums[part]. A warp takes 256 columns of
-// a row, a thread 8 of them. The blocks after these lay out X and W.
+// a row, a thread 8 of them. The blocks after these lay out X and W. Bound by memory and by gelu's slope together: 8192 x 4096 bf16,
+// 201 MB, 42 us, 4.8 TB/s or 71 % of what a copy reaches.
 struct DzArgs {
   const void *grad, *z;  // z null: dz is grad
   int64_t grad_ld, z_ld, rows, outs, rows_a_block;
@@ -384,22 +442,25 @@ struct Tiling {
   int cg = 1, bn = 64;
   int64_t splits = 1;
 };
-// The least of rounds of tiles times what a stage of one takes (in SM clocks: 64 bytes a clock from L2, or the products),
-// times stages, with a start and an end a round; parts cost their way through memory.
+// The least of rounds of tiles times what a stage of one takes (SM clocks, measured: 16 bits, and three planes of f32, whose
+// pairs hold two stages only), times stages, with a start and an end a round; parts cost a launch and their way through memory.
+// us, forward with gelu, by tiles of 2 x 256 (pairs), 256, 128 and 64 columns: 8192 x 1024 x 4096 bf16: 54, 60, 69, 107;
+// 512 x 4096 x 4096: 33, 31, 23, 33; 24 x 1024 x 32768: 27, 21, 25, 33; 4096 x 1024 x 1024 f32: 99, -, 71, 85.
+// In 1, 2, 4, 8 parts: 24 x 16384 x 1024 by 128: 59, 35, 23, 17; 512 x 4096 x 4096: 23, 29, 32, 38.
 Tiling tile_for(int64_t m, int64_t n, int64_t k_blocks, int planes, int sms, bool pairs = true) {
   Tiling best;
   double least = 1e300;
-  struct Kind { int cg, bn; double stage; };
-  const Kind kinds[] = {{2, 256, 512}, {1, 256, 768}, {1, 128, 512}, {1, 64, 384}};
+  struct Kind { int cg, bn; double stage, stage32; };
+  const Kind kinds[] = {{2, 256, 600, 10400}, {1, 256, 700, 0}, {1, 128, 456, 3400}, {1, 64, 375, 2060}};
   for (const Kind& k : kinds) {
     if ((planes == 3 && k.cg == 1 && k.bn == 256) || (k.cg == 2 && !pairs)) continue;
     const int64_t slots = sms / k.cg, tiles = div_up(m, 128 * k.cg) * div_up(n, k.bn);
-    const double stage = planes == 3 ? (k.cg == 2 ? 3200 : k.bn == 128 ? 2000 : 1400) : k.stage;
+    const double stage = planes == 3 ? k.stage32 : k.stage;
     for (int64_t want = 1; want <= 16; want *= 2) {
       if (want > 1 && (tiles * want > slots || k_blocks / want < 8)) break;
       const int64_t per = div_up(k_blocks, want), parts = div_up(k_blocks, per);
       const double cost = div_up(tiles * parts, slots) * (per * stage + 2500.0 + 12.0 * k.bn) +
-                          (parts > 1 ? 6000.0 + static_cast<double>(m) * n * parts * 8 / (sms * 32.0) : 0.0);
+                          (parts > 1 ? 6000.0 + static_cast<double>(m) * n * parts * 0.0025 : 0.0);
       if (cost < least) least = cost, best = Tiling{k.cg, k.bn, parts};
     }
   }
@@ -505,9 +566,12 @@ gm_status forward(LinearCall& c, LinearEnd e, void* y, int64_t y_ld) {
   if (!set) return GM_ERR_CUDA;
   g.lin = e;
   bool ok = launch_prod(Prod::kLinear, p.t.cg, p.t.bn, maps, g, c.sms, c.s) == cudaSuccess;
-  if (ok && acc)
-    ok = launch_chained(k_linear_join, grid_for(m * n, 256), 256, 0, c.s, 1, static_cast<const float*>(acc), g.splits, m, n,
-                        p.acc_ld, e, y, y_ld, static_cast<int>(c.p.type)) == cudaSuccess;
+  if (ok && acc) {
+    auto four = [&](const void* q, int64_t ld) { return !q || (aligned(q, 4 * es) && (m <= 1 || ld % 4 == 0)); };
+    const bool wide = n % 4 == 0 && four(y, y_ld) && four(e.keep ? e.z : nullptr, e.z_ld) && four(e.residual, e.residual_ld) && four(e.bias, 0);
+    ok = launch_chained(k_linear_join, grid_for(m * (p.acc_ld / 4), 256), 256, 0, c.s, 1, static_cast<const float*>(acc), g.splits, m, n,
+                        p.acc_ld, e, y, y_ld, static_cast<int>(c.p.type), wide) == cudaSuccess;
+  }
   return finish(ok);
 }
 

@@ -10,6 +10,12 @@
 // added atomically. Two sums serve all where the gate is a vector or none: with A_j = sum over rows of dx n(f), B_j of dx,
 //   dafter = scale gate A, dgate = scale (after A + after_bias B), dafter_bias = scale gate B.
 // Rows longer than a block holds (kHeldDim) are walked several times instead.
+//
+// 8192 x 4096 bf16, rms, after, gate vector: forward 47 us for 268 MB, 5.7 TB/s or 85 % of what a copy reaches; backward 78 us
+// for 403 MB, 5.2 TB/s or 76 %, and 7 us to join the blocks' sums. 24 % of the warps fit (registers); what they wait for is
+// divided between memory, the sums' exchanges and shared memory. The general form, with twice the instructions an element: layer norm
+// with biases 97 and 131 us (four sums one after another), a matrix of gates 78 and 143. One row of 4096: 6 us, a launch and three
+// trips to memory.
 #include <cmath>
 #include <type_traits>
 
@@ -205,7 +211,8 @@ struct Columns {
     return r;
   }
 };
-// LEAN: no means taken off, no biases, a gate that is a vector or none: half the instructions of the general form.
+// LEAN: no means taken off, no biases, a gate that is a vector or none: half the instructions of the general form
+// (8192 x 4096 bf16 backward: 78 us, 131 with layer norm and biases).
 __device__ __forceinline__ bool is_matrix(const gm_norm& n) { return n.gate_kind == GM_GATE_MATRIX; }
 
 // What depends on the column alone: h = after * gate (that of a matrix comes with the row), hc = after_bias * gate,
@@ -253,7 +260,8 @@ struct Weights {
 };
 
 // The weights of a thread's columns, read once and kept; by the general form with 16 columns a thread, whose registers they
-// would fill, at each use, from L1. That form does not ask for the next row either.
+// would fill, at each use, from L1. That form does not ask for the next row either. Backward, 4096 x 8192 layer norm with biases:
+// bf16 156 us, f32 276; with all kept (spilled) 199 and 551. Forward and backward 275 bf16; walked, as longer rows are, 932 (8192 x 4104).
 template <int TYPE, bool VEC, int NV, bool LEAN>
 struct Kept {
   static constexpr bool kAll = LEAN || NV == 1;

@@ -293,3 +293,31 @@ def test_refusals_of_the_device_side_arguments():
         layers.residual_norm_forward(x, f, scale=float("nan"), **rule)
     with pytest.raises(GmError):
         layers.residual_norm_forward(x, f, eps=-1.0, **rule)
+
+
+# Rows of more than 8192 are walked; the forms between 4096 and 8192 hold 16 columns a thread.
+@pytest.mark.parametrize("dim", [8200, 8201])
+def test_walked_rows_as_the_others(dim):
+    for norm in ("rms", "layer"):
+        test_norm_alone(dim, norm)
+    test_in_place_residual(dim)
+    test_rows_that_are_all_zero_or_not_finite_stay_alone(dim)
+    test_results_into_the_callers_rows(dim, 5, 0)
+    test_results_into_the_callers_rows(dim, 8, 8)
+    for after, gate, before, bias in PARTS:
+        test_parts(after, gate, before, bias, dim)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("rows,dim", [(1, 4097), (309, 4100), (6, 5000), (4, 6001), (7, 8191), (3, 8192), (5, 8193)])
+@pytest.mark.parametrize("norm,gate", [("layer", "vector"), ("rms", "matrix"), ("layer", None)])
+def test_long_rows_in_every_form(rows, dim, kind, norm, gate):
+    x, f, gx, gy, rule = make(rows, dim, kind, gate=gate, seed=dim)
+    both(x, f, gx, gy, dict(rule, norm=norm, scale=0.7), kind)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("wide,offset", [(8, 0), (3, 0), (0, 1), (5, 2)])
+@pytest.mark.parametrize("dim", [8190, 8200])
+def test_strides_of_long_rows(kind, wide, offset, dim):
+    test_strides(kind, wide, offset, dim)
