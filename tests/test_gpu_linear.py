@@ -291,3 +291,12 @@ def test_refusals():
             bad()
     with pytest.raises(GmError):
         layers.linear_backward(x, w, grad, activation="gelu")  # without z
+
+
+# Few rows of long ones: the parts are joined by a kernel of their own, four columns a thread where all rows allow it.
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("wide,offset", [(0, 0), (4, 4), (2, 2), (1, 0), (0, 1)])
+@pytest.mark.parametrize("rows,dim,outs", [(24, 4104, 256), (24, 4100, 255), (5, 4096, 70), (130, 4096, 260)])
+def test_joined_parts(kind, wide, offset, rows, dim, outs):
+    both(*make(rows, dim, outs, kind, wide=wide, offset=offset), ACTS[(outs + wide) % 5], kind)
+    both(*make(rows, dim, outs, kind, bias=False, wide=wide, offset=offset), "none", kind)
