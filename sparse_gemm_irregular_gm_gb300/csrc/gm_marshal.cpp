@@ -243,8 +243,15 @@ std::tuple<int, std::vector<Opt>> norm_backward(const Tensor& x, const Opt& f, c
 // A value of the rule: a number, or a tensor of one a row.
 template <class T>
 void value_of(const char* name, const pybind11::object& v, int64_t n, const Tensor& z, at::ScalarType type, const T** rows, T* all) {
-  if (THPVariable_Check(v.ptr())) *rows = static_cast<const T*>(vector(name, THPVariable_Unpack(v.ptr()), n, type, z.device()));
-  else *all = v.cast<T>();
+  if (THPVariable_Check(v.ptr())) {
+    *rows = static_cast<const T*>(vector(name, THPVariable_Unpack(v.ptr()), n, type, z.device()));
+    return;
+  }
+  try {
+    *all = v.cast<T>();
+  } catch (const pybind11::cast_error&) {
+    refuse(name, type == at::kInt ? " must be a whole number of 32 bits" : " must be a number", ", or a tensor of one a row");
+  }
 }
 
 std::tuple<int, Tensor, Tensor, Tensor> draw(const Tensor& z, const Tensor& u, const pybind11::object& temperature, const pybind11::object& top_k,
@@ -254,11 +261,7 @@ std::tuple<int, Tensor, Tensor, Tensor> draw(const Tensor& z, const Tensor& u, c
   if (z.size(1) < 1) refuse("logits must have a class at least");
   gm_draw_rule r = {};
   value_of("temperature", temperature, n, z, at::kFloat, &r.temperature, &r.all_temperature);
-  try {
-    value_of("top_k", top_k, n, z, at::kInt, &r.top_k, &r.all_top_k);
-  } catch (const pybind11::cast_error&) {
-    refuse("top_k must be a whole number of 32 bits");
-  }
+  value_of("top_k", top_k, n, z, at::kInt, &r.top_k, &r.all_top_k);
   value_of("top_p", top_p, n, z, at::kFloat, &r.top_p, &r.all_top_p);
   value_of("min_p", min_p, n, z, at::kFloat, &r.min_p, &r.all_min_p);
   const float* pu = static_cast<const float*>(vector("u", u, n, at::kFloat, z.device()));

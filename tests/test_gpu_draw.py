@@ -327,3 +327,17 @@ def test_results_into_the_callers_tensors_and_refusals():
             sampling.draw(z, bad)
     with pytest.raises(ValueError):
         sampling.draw(z.t(), u)
+
+
+@pytest.mark.parametrize("name", ["temperature", "top_k", "top_p", "min_p"])
+@pytest.mark.parametrize("value", [None, "a", [0.5]])
+def test_values_that_are_no_numbers_are_refused(name, value):
+    z, u = make(3, 100, "bf16")
+    with pytest.raises(ValueError, match=name):
+        sampling.draw(z, u, **{name: value})
+
+
+def test_a_whole_number_of_top_k():
+    z, u = make(3, 100, "bf16")
+    with pytest.raises(ValueError, match="top_k"):
+        sampling.draw(z, u, top_k=1.5)
