@@ -1,8 +1,9 @@
 // gm_draw.cu -- a class drawn from each row of logits (include/gm_sampling.h).
 //
-// A row is read from memory once, into the shared memory of a block or of a cluster of blocks, and
-// everything else works there: its maximum; for top-k and top-p a border found by histograms, never a
-// sort; the kept weights' sum; the class at which u is passed. Nothing is written but the results.
+// A row is read from memory once, into the shared memory of a block or of a cluster of blocks where it fits (beside the
+// counts up to 36856 classes a block; else its later passes read it from L2), and everything else works there: its maximum; for
+// top-k and top-p a border found by histograms, never a sort; the kept weights' sum; the class at which u is passed. Nothing is
+// written but the results.
 //
 // Borders. Classes are compared by D, the distance of their ordered bits from the row's largest: 16 bits, or 32 of
 // f32. A border is a D and how many of the classes that have just that D are kept, in class order.
@@ -11,6 +12,10 @@
 //   computed for each value that occurs, not for each class, and looked up when classes are summed.
 //   Others: a histogram of D's upper 11 bits shows the digit in which the border lies, one of the next
 //   11 bits within that digit its next, until D is known.
+//
+// Bound by the shared memory's operations and the barriers between steps, far from memory's rate: 256 x 131072 bf16 with top-p
+// 100 us (67 MB; plain 8240), of a row's clocks 36 % reading and counting, 19 % the search, 25 % the sums; 1 x 131072 with
+// all four rules 15 us back to back, 19 alone.
 //
 // Weights are integers: w = 2^(t), t = (z - max) log2(e) / T <= 0, as a multiple of 2^-B with B such that all of a row
 // add up in 64 bits. So sums are exact, in any order, and every pass sees the same ones.

@@ -4,6 +4,7 @@
 //
 // The functions of the C interface are handed in by address (init): which build of the library they
 // come from is the binding's choice. Arguments that do not fit raise ValueError; statuses are returned.
+#include <algorithm>
 #include <cstdint>
 #include <optional>
 #include <sstream>

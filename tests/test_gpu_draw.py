@@ -341,3 +341,11 @@ def test_a_whole_number_of_top_k():
     z, u = make(3, 100, "bf16")
     with pytest.raises(ValueError, match="top_k"):
         sampling.draw(z, u, top_k=1.5)
+
+
+# more rows than SMs: blocks of 128 to 512 threads share one
+@pytest.mark.parametrize("rows,classes", [(310, 1029), (320, 9000), (500, 4100), (170, 16001), (160, 49152), (160, 12288)])
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("rule", [dict(), dict(top_k=70), dict(top_p=0.8), dict(min_p=0.01), dict(top_k=400, top_p=0.95)])
+def test_rows_that_share_an_sm(rows, classes, kind, rule):
+    check(*make(rows, classes, kind, seed=classes), temperature=0.9, most_unsure=1, **rule)
