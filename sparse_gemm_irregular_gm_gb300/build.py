@@ -52,7 +52,7 @@ def build_marshal() -> str:
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{d}" for d in inc), os.path.join(CSRC, "gm_marshal.cpp"), "-o", tmp, "-L" + os.path.join(at, "lib"),
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on gm_marshal.cpp:\n{r.stdout}\n{r.stderr}")

@@ -14,7 +14,7 @@
 #include <vector>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -83,7 +83,11 @@ void* vector(const char* name, const Tensor& t, int64_t n, at::ScalarType type, 
 void* vector(const char* name, const Opt& t, int64_t n, const Tensor& like) {
   return t ? vector(name, *t, n, like.scalar_type(), like.device()) : nullptr;
 }
-Tensor rows_like(const Tensor& x, int64_t rows, int64_t cols) { return at::empty({rows, cols}, x.options()); }
+// From torch's allocator, on x's device. Straight from its CUDA function: by way of the dispatcher three results take 2.4 us longer.
+Tensor made(const Tensor& x, at::IntArrayRef size, at::ScalarType type) {
+  return Tensor(at::detail::empty_cuda(size, type, x.device(), std::nullopt));
+}
+Tensor rows_like(const Tensor& x, int64_t rows, int64_t cols) { return made(x, {rows, cols}, x.scalar_type()); }
 
 struct Here {  // the tensors' device, and its current stream
   c10::cuda::CUDAGuard guard;
@@ -96,7 +100,7 @@ struct Work {
   gm_layer_config cfg = {};
   Work(const Tensor& x, int64_t bytes) {
     if (!bytes) return;
-    t = at::empty({bytes}, x.options().dtype(at::kByte));
+    t = made(x, {bytes}, at::kByte);
     cfg.workspace = t.data_ptr();
     cfg.workspace_bytes = bytes;
   }
@@ -138,7 +142,7 @@ std::tuple<int, Opt, Opt, Opt> linear_backward(const Tensor& x, const Tensor& w,
   const Here here(x);
   if (make_x) dx = rows_like(x, p.n_rows, p.dim);
   if (make_w) dw = rows_like(x, p.n_outs, p.dim);
-  if (make_b) db = at::empty({p.n_outs}, x.options());
+  if (make_b) db = made(x, {p.n_outs}, x.scalar_type());
   const Matrix mx = matrix("dx", dx, &x, p.n_rows, p.dim), mw = matrix("dw", dw, &x, p.n_outs, p.dim);
   void* b = vector("dbias", db, p.n_outs, x);
   int64_t bytes = 0;
@@ -193,7 +197,7 @@ std::tuple<int, Opt, Opt, Opt> norm_forward(const Tensor& x, const Opt& f, int n
     if (!f && !before) refuse("there is nothing to compute without f and before");
     if (f) x_out = rows_like(x, n.n_rows, n.dim);
     if (before) y = rows_like(x, n.n_rows, n.dim);
-    stats = at::empty({n.n_rows, 4}, x.options().dtype(at::kFloat));
+    stats = made(x, {n.n_rows, 4}, at::kFloat);
   }
   const Matrix o = matrix("x_out", x_out, &x, n.n_rows, n.dim), my = matrix("y", y, &x, n.n_rows, n.dim);
   const int rc = fn.norm_forward(&n, here.stream, o.p, o.ld, my.p, my.ld, stats_of(stats, x));
@@ -213,7 +217,7 @@ std::tuple<int, std::vector<Opt>> norm_backward(const Tensor& x, const Opt& f, c
     grads.assign(7, Opt());
     bool any = false;
     for (int i = 0; i < 7; ++i)
-      if (all[i] && (need >> i & 1)) grads[i] = at::empty(all[i]->sizes(), x.options()), any = true;
+      if (all[i] && (need >> i & 1)) grads[i] = made(x, all[i]->sizes(), x.scalar_type()), any = true;
     if (!any) return {GM_OK, std::move(grads)};
   } else if (grads.size() != 7) {
     refuse("grads must be seven");
@@ -268,9 +272,9 @@ std::tuple<int, Tensor, Tensor, Tensor> draw(const Tensor& z, const Tensor& u, c
   const float* pu = static_cast<const float*>(vector("u", u, n, at::kFloat, z.device()));
   const Here here(z);
   if (!index) {
-    index = at::empty({n}, z.options().dtype(at::kLong));
-    logprob = at::empty({n}, z.options().dtype(at::kFloat));
-    kept = at::empty({n}, z.options().dtype(at::kInt));
+    index = made(z, {n}, at::kLong);
+    logprob = made(z, {n}, at::kFloat);
+    kept = made(z, {n}, at::kInt);
   }
   const int rc = fn.draw(m.p, n, z.size(1), m.ld, type_of(z), &r, pu, here.stream,
                          static_cast<int64_t*>(vector("index", *index, n, at::kLong, z.device())),

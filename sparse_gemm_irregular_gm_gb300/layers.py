@@ -72,7 +72,8 @@ def load():
 
 def _run(name, stream, x, *args):
     """A function of the extension, on `stream` where one is given: what it returned after its status."""
-    rc, *out = call(getattr(extension(), name), stream, x, *args)
+    f = getattr(extension(), name)
+    rc, *out = f(x, *args) if stream is None else call(f, stream, x, *args)
     if rc:
         raise GmError(rc, "gm_" + name)
     return out

@@ -49,7 +49,8 @@ class Drawn(NamedTuple):
 
 
 def _draw(stream, logits, u, rule, out):
-    rc, *out = call(extension().draw, stream, logits, u, *rule, *out)
+    f = extension().draw
+    rc, *out = f(logits, u, *rule, *out) if stream is None else call(f, stream, logits, u, *rule, *out)
     if rc:
         raise GmError(rc, "gm_draw")
     return out
