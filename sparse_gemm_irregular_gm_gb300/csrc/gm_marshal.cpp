@@ -1,6 +1,6 @@
 // gm_marshal.cpp -- what the Python binding of the layers and of the draw does for each call: checks tensors, makes the
 // results, fills the descriptors of the C interface and calls it on the current stream. Compiled because a call of one row
-// takes the GPU a few microseconds, and the same in Python took 20 (8 so).
+// takes the GPU a few microseconds, and the same in Python took 20 (a product 5 so, a norm 8).
 //
 // The functions of the C interface are handed in by address (init): which build of the library they
 // come from is the binding's choice. Arguments that do not fit raise ValueError; statuses are returned.
