@@ -300,3 +300,10 @@ def test_refusals():
 def test_joined_parts(kind, wide, offset, rows, dim, outs):
     both(*make(rows, dim, outs, kind, wide=wide, offset=offset), ACTS[(outs + wide) % 5], kind)
     both(*make(rows, dim, outs, kind, bias=False, wide=wide, offset=offset), "none", kind)
+
+
+# more tiles than SMs, in every width of tile that the rule takes for such sizes
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("rows,dim,outs", [(2600, 700, 1500), (700, 1536, 2600), (1500, 96, 5200)])
+def test_blocks_that_walk_several_tiles(kind, rows, dim, outs):
+    both(*make(rows, dim, outs, kind, seed=9), "silu", kind)
