@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   uint32_t blocks;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(blocks));
   const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
+  if (blocks > 1) cluster_arrive();  // waited for before another block's shared memory is used: it must have started
   const int64_t row_i = blockIdx.x / blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (threadIdx.x < kTable) sh.table[threadIdx.x] = kPowers[threadIdx.x];
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   top = __reduce_min_sync(kFull, sh.warp_top[lane < warps ? lane : 0]);
   last = __reduce_max_sync(kFull, sh.warp_last[lane < warps ? lane : 0]);
   if (blocks > 1) {
+    cluster_wait();  // all blocks run; the reading of the row lies between
     if (threadIdx.x < blocks) put_remote_u64(&sh.told_ends[rank], threadIdx.x, (u64(last) << 32) | top);
     cluster_sync_all();
     for (int r = 0; r < blocks; ++r) {

@@ -78,3 +78,15 @@ def test_no_rows_is_no_work(lib, rule):
 def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         sampling.draw(torch.zeros(2, 3), torch.zeros(2))
+
+
+def test_blocks_of_a_cluster_wait_until_all_have_started():
+    """Another block's shared memory may be used only once that block is known to run: the kernel arrives at a barrier of the
+    cluster and waits there before its first use. Read from the source: a run cannot show it."""
+    src = open(os.path.join(ROOT, "sparse_gemm_irregular_gm_gb300", "csrc", "gm_draw.cu")).read()
+    kernel = src[src.index("k_draw(const __grid_constant__"):src.index("// ---- host")]
+    kernel = re.sub(r"//[^\n]*", "", kernel)
+    uses = [kernel.find(f + "(") for f in ("put_remote_u64", "add_remote_u32", "remote_u32", "remote_u64", "map_to_rank", "cluster_sync_all")]
+    first = min(i for i in uses if i >= 0)
+    arrive, wait = kernel.find("cluster_arrive()"), kernel.find("cluster_wait()")
+    assert 0 <= arrive < wait < first
