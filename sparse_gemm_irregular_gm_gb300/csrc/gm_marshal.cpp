@@ -259,8 +259,11 @@ void value_of(const char* name, const pybind11::object& v, int64_t n, const Tens
   }
 }
 
+// index, logprob and kept: the caller's, or with make made.
 std::tuple<int, Tensor, Tensor, Tensor> draw(const Tensor& z, const Tensor& u, const pybind11::object& temperature, const pybind11::object& top_k,
-                                             const pybind11::object& top_p, const pybind11::object& min_p, Opt index, Opt logprob, Opt kept) {
+                                             const pybind11::object& top_p, const pybind11::object& min_p, Opt index, Opt logprob, Opt kept,
+                                             bool make) {
+  if (!make && (!index || !logprob || !kept)) refuse("index, logprob and kept must be tensors");
   const Matrix m = matrix("logits", z);
   const int64_t n = z.size(0);
   if (z.size(1) < 1) refuse("logits must have a class at least");
@@ -271,7 +274,7 @@ std::tuple<int, Tensor, Tensor, Tensor> draw(const Tensor& z, const Tensor& u, c
   value_of("min_p", min_p, n, z, at::kFloat, &r.min_p, &r.all_min_p);
   const float* pu = static_cast<const float*>(vector("u", u, n, at::kFloat, z.device()));
   const Here here(z);
-  if (!index) {
+  if (make) {
     index = made(z, {n}, at::kLong);
     logprob = made(z, {n}, at::kFloat);
     kept = made(z, {n}, at::kInt);

@@ -48,20 +48,20 @@ class Drawn(NamedTuple):
     kept: torch.Tensor
 
 
-def _draw(stream, logits, u, rule, out):
+def _draw(stream, logits, u, rule, out, make):
     f = extension().draw
-    rc, *out = f(logits, u, *rule, *out) if stream is None else call(f, stream, logits, u, *rule, *out)
+    rc, *out = f(logits, u, *rule, *out, make) if stream is None else call(f, stream, logits, u, *rule, *out, make)
     if rc:
         raise GmError(rc, "gm_draw")
     return out
 
 
 def gm_draw(logits, u, index, logprob, kept, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
-    _draw(stream, logits, u, (temperature, top_k, top_p, min_p), (index, logprob, kept))
+    _draw(stream, logits, u, (temperature, top_k, top_p, min_p), (index, logprob, kept), False)
 
 
 def draw(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None) -> Drawn:
     """A class a row of ``logits`` (rows x classes; bfloat16, float16 or float32) by the random numbers ``u`` (float32, one
     a row, in [0, 1)). ``temperature`` (0: the largest logit), ``top_k`` (0: off), ``top_p`` (1: off) and ``min_p`` (0: off)
     are numbers, or tensors of one value a row (float32; top_k int32)."""
-    return Drawn(*_draw(stream, logits, u, (temperature, top_k, top_p, min_p), (None, None, None)))
+    return Drawn(*_draw(stream, logits, u, (temperature, top_k, top_p, min_p), (None, None, None), True))

@@ -349,3 +349,12 @@ def test_a_whole_number_of_top_k():
 @pytest.mark.parametrize("rule", [dict(), dict(top_k=70), dict(top_p=0.8), dict(min_p=0.01), dict(top_k=400, top_p=0.95)])
 def test_rows_that_share_an_sm(rows, classes, kind, rule):
     check(*make(rows, classes, kind, seed=classes), temperature=0.9, most_unsure=1, **rule)
+
+
+@pytest.mark.parametrize("missing", [(0,), (1,), (2,), (1, 2), (0, 1, 2)])
+def test_results_that_are_missing_are_refused_and_the_others_left(missing):
+    out = [torch.full((6,), 9, device="cuda", dtype=t) for t in (torch.int64, torch.float32, torch.int32)]
+    given = [None if i in missing else t for i, t in enumerate(out)]
+    with pytest.raises(ValueError):
+        sampling.gm_draw(torch.zeros(6, 50, device="cuda"), torch.zeros(6, device="cuda"), *given)
+    assert all((t == 9).all() for t in out)

@@ -90,3 +90,12 @@ def test_blocks_of_a_cluster_wait_until_all_have_started():
     first = min(i for i in uses if i >= 0)
     arrive, wait = kernel.find("cluster_arrive()"), kernel.find("cluster_wait()")
     assert 0 <= arrive < wait < first
+
+
+@pytest.mark.parametrize("missing", [(0,), (1,), (2,), (0, 1), (0, 2), (1, 2), (0, 1, 2)])
+def test_binding_refuses_results_that_are_missing(lib, missing):
+    out = [torch.zeros(2, dtype=t) for t in (torch.int64, torch.float32, torch.int32)]
+    for i in missing:
+        out[i] = None
+    with pytest.raises(ValueError, match="index, logprob and kept"):
+        sampling.gm_draw(torch.zeros(2, 3), torch.zeros(2), *out)
