@@ -53,20 +53,31 @@ __device__ __forceinline__ float logistic(float x) {
 constexpr float kTanhA = 1.5957691216f, kTanhB = 0.044715f;
 __device__ __forceinline__ float gelu_tanh_arg(float z) { return z * fmaf(z * z, kTanhA * kTanhB, kTanhA); }
 
-// act'(z)
+// z, or the end of [-most, most] that it lies beyond; NaN stays.
+__device__ __forceinline__ float within(float z, float most) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(most));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(-most));
+  return y;
+}
+
+// act'(z). It is 0 or 1 in fp32 well before the ends that z is brought within, where the terms of an infinite z (a finite one
+// kept in f16 may be) would give NaN.
 template <bool FINE>
 __device__ __forceinline__ float slope(float z, int act) {
   if (act == GM_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (act == GM_ACT_GELU) {
+    z = within(z, 30.f);
     const float b = bell<FINE>(z);
     return fmaf(z * 0.3989422804f, b, normal_below<FINE>(z, b));
   }
   if (act == GM_ACT_GELU_TANH) {
-    z = z > 30.f ? 30.f : z < -30.f ? -30.f : z;  // 1 and 0 long before; z^2 stays finite
+    z = within(z, 30.f);
     const float s = logistic<FINE>(gelu_tanh_arg(z));
     return fmaf(z * s * (1.f - s), fmaf(z * z, 3.f * kTanhA * kTanhB, kTanhA), s);
   }
   if (act == GM_ACT_SILU) {
+    z = within(z, 128.f);
     const float s = logistic<FINE>(z);
     return s * fmaf(z, 1.f - s, 1.f);
   }

@@ -307,3 +307,42 @@ def test_joined_parts(kind, wide, offset, rows, dim, outs):
 @pytest.mark.parametrize("rows,dim,outs", [(2600, 700, 1500), (700, 1536, 2600), (1500, 96, 5200)])
 def test_blocks_that_walk_several_tiles(kind, rows, dim, outs):
     both(*make(rows, dim, outs, kind, seed=9), "silu", kind)
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("rows", [4, 200])
+def test_arguments_past_the_range_in_which_they_are_kept(act, rows):
+    """Finite x and W of f16 whose z is past its range: kept as an infinity, at which the slopes are 0 and 1."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.rand(rows, 8, device="cuda", generator=g).add_(0.5).half()
+    w = torch.randn(16, 8, device="cuda", generator=g).half()
+    w[3], w[7] = -30000.0, 30000.0  # z from -360000 to -120000, and the same above 0
+    grad = torch.randn(rows, 16, device="cuda", generator=g).half()
+    y, z = layers.linear_forward(x, w, activation=act, keep=True)
+    assert (z[:, 3] == -torch.inf).all() and (z[:, 7] == torch.inf).all() and z[:, :3].isfinite().all()
+    assert (y[:, 3] == 0).all() and (y[:, 7] == torch.inf).all()
+    got = layers.linear_backward(x, w, grad, activation=act, z=z, need_bias=True)
+    X, W, G, kept = (wide_of(t) for t in (x, w, grad, z.clamp(-1000, 1000)))  # slopes are 0 or 1 from there on
+    s = layer_oracle.act(kept, act)[1]
+    assert (s[:, 3] == 0).all() and (s[:, 7] == 1).all()
+    dz = G * s
+    dz_room = np.abs(G) * 2.0 ** -21 * (1 + np.abs(kept)) * (s != 0) * (s != 1) + HALF["f16"] * np.abs(dz) + 2 * LEAST["f16"]
+    # f16 ends at 65504, its steps there are 32: what is 65520 or more, within the room, is rightly an infinity
+    ref, room = dz @ W, dz_room @ np.abs(W) + sum_room(16, np.abs(dz) @ np.abs(W))
+    past = np.isinf(wide_of(got[0])) & (np.sign(wide_of(got[0])) * ref + room >= 65520)
+    check(torch.where(torch.tensor(past, device="cuda"), 0, got[0]), np.where(past, 0, ref), room, "f16")
+    check(got[1], dz.T @ X, dz_room.T @ np.abs(X) + sum_room(rows, np.abs(dz).T @ np.abs(X)), "f16")
+    check(got[2], dz.sum(0), dz_room.sum(0) + EPS32 * (rows / 8 + 600) * np.abs(dz).sum(0), "f16")
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_slopes_at_infinity_and_no_number(kind, act):
+    x, w, _, _, _ = make(3, 24, 8, kind)
+    z = torch.tensor([[torch.inf, -torch.inf] * 4, [1.0, -1.0] * 4, [torch.nan] * 8], device="cuda", dtype=TYPES[kind])
+    _, _, db = layers.linear_backward(x[:2], w, torch.ones_like(z[:2]), activation=act, z=z[:2], need_bias=True)
+    ref = layer_oracle.act(np.array([1.0, -1.0] * 4), act)[1] + np.array([1.0, 0.0] * 4)
+    check(db, ref, 2.0 ** -20, kind)
+    dx, _, _ = layers.linear_backward(x, w, torch.ones_like(z), activation=act, z=z, need_w=False)
+    assert dx[:2].isfinite().all()
+    assert dx[2].isnan().all() or act == "relu"
