@@ -25,7 +25,9 @@
  *     (gm_layer_config.workspace) or comes through gm_set_allocator's hooks, in stream order.
  *   - Every call returns a gm_status; nothing is thrown across the ABI.
  *   - Arithmetic and sums are fp32, results are rounded once, but: dz is rounded to a 16-bit
- *     operand type before the two products that read it (db is summed before that), and the slope
+ *     operand type before the two products that read it (db is summed before that); f16's is scaled
+ *     by a power of two first, so that its steps are at most 2^-37 of the largest finite gradient by y where
+ *     they are not a rounding of dz itself. The slope
  *     of an activation is taken at z as it was kept, rounded to the operand type. Products on the
  *     tensor cores cut sums as gm_losses.h says; f32 operands are three bf16 parts each. No value is
  *     added atomically: results do not depend on the launch.

@@ -346,3 +346,52 @@ def test_slopes_at_infinity_and_no_number(kind, act):
     dx, _, _ = layers.linear_backward(x, w, torch.ones_like(z), activation=act, z=z, need_w=False)
     assert dx[:2].isfinite().all()
     assert dx[2].isnan().all() or act == "relu"
+
+
+def small_gradients(x, w, grad, act, z, inside=slice(None), columns=slice(None)):
+    """f16: dz is kept in steps of at most half of 2^-25 / 2^13 of the largest finite gradient, or rounded once; slopes to 2^-21."""
+    rows = x.shape[0]
+    got = layers.linear_backward(x, w, grad, activation=act, z=z, need_bias=True)
+    X, W, G, kept = (wide_of(t) for t in (x, w, grad, z))
+    most = np.abs(G[np.isfinite(G)]).max()
+    G = np.where(np.isfinite(G), G, 0)
+    dz = G * layer_oracle.act(kept, act)[1]
+    own = np.abs(G) * 2.0 ** -21  # of the slope alone: db is summed before dz is rounded
+    dz_room = own + (HALF["f16"] ** 2 if rows <= 128 else HALF["f16"]) * np.abs(dz) + 2.0 ** -38 * most
+    k = W.shape[0]
+    check(got[0][inside], (dz @ W)[inside], (dz_room @ np.abs(W) + sum_room(k, np.abs(dz) @ np.abs(W)))[inside], "f16")
+    check(got[1][columns], (dz.T @ X)[columns], (dz_room.T @ np.abs(X) + sum_room(rows, np.abs(dz).T @ np.abs(X)))[columns], "f16")
+    check(got[2][columns], dz.sum(0)[columns], (own.sum(0) + EPS32 * (rows / 8 + 600) * np.abs(dz).sum(0))[columns], "f16")
+    return got
+
+
+@pytest.mark.parametrize("size", [1e-5, 1e-4, 1.0])
+@pytest.mark.parametrize("rows,dim,outs,wide", [(1000, 72, 136, 0), (100, 72, 136, 0), (333, 40, 77, 3), (1, 64, 520, 0)])
+@pytest.mark.parametrize("act,far", [("gelu", 4.0), ("gelu_tanh", 4.0), ("silu", 10.0)])
+def test_small_gradients_of_f16_keep_their_digits(act, far, rows, dim, outs, wide, size):
+    x, w, _, _, grad = make(rows, dim, outs, "f16", wide=wide, seed=5)
+    w.mul_(0.1)
+    b = -torch.linspace(0, far, outs, device="cuda").half()  # slopes from a half to 5e-4
+    _, z = layers.linear_forward(x, w, b, activation=act, keep=True)
+    grad.mul_(4 * size)
+    small_gradients(x, w, grad, act, z)
+
+
+@pytest.mark.parametrize("rows", [60, 300])
+def test_large_gradients_of_f16_stay_finite_past_a_steep_slope(rows):
+    x, w, _, _, grad = make(rows, 64, 96, "f16", seed=6)
+    w.mul_(2.0 ** -10)
+    x.mul_(2.0 ** -10)
+    z = torch.full((rows, 96), 1.5, device="cuda").half()  # gelu's slope is 1.128 there
+    grad[:, 5] = 65504.0
+    dx, dw, _ = small_gradients(x, w, grad, "gelu", z, columns=[i for i in range(96) if i != 5])  # db[5] is past f16
+    assert dx.isfinite().all() and dw.isfinite().all()
+
+
+@pytest.mark.parametrize("rows", [60, 300])
+def test_an_infinite_gradient_does_not_cost_the_others_digits(rows):
+    x, w, b, _, grad = make(rows, 64, 96, "f16", seed=7)
+    _, z = layers.linear_forward(x, w, b, activation="silu", keep=True)
+    grad.mul_(1e-4)
+    grad[2, 9] = torch.inf
+    small_gradients(x, w, grad, "silu", z, inside=[i for i in range(rows) if i != 2], columns=[i for i in range(96) if i != 9])
