@@ -346,10 +346,10 @@ __global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a, const L
               h[j] = take_plane(u, p == 2, (__float_as_uint(u) & INT32_MAX) < kRoundsPast);
             } else if (bf16) {
               const __nv_bfloat16 y = __float2bfloat16_rn(u);
-              h[j] = __bfloat16_as_ushort(y), u -= __bfloat162float(y);
+              h[j] = __bfloat16_as_ushort(y), u = (h[j] & 0x7f80u) == 0x7f80u ? 0.f : u - __bfloat162float(y);  // of inf: nothing
             } else {
               const __half y = __float2half_rn(u);
-              h[j] = __half_as_ushort(y), u -= __half2float(y);
+              h[j] = __half_as_ushort(y), u = (h[j] & 0x7c00u) == 0x7c00u ? 0.f : u - __half2float(y);
             }
           }
           w[i / 2] = h[0] | (h[1] << 16);

@@ -395,3 +395,20 @@ def test_an_infinite_gradient_does_not_cost_the_others_digits(rows):
     grad.mul_(1e-4)
     grad[2, 9] = torch.inf
     small_gradients(x, w, grad, "silu", z, inside=[i for i in range(rows) if i != 2], columns=[i for i in range(96) if i != 9])
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("rows", [3, 100, 200])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_an_infinite_gradient_gives_infinities(kind, rows, act):
+    x, w, b, _, grad = make(rows, 48, 56, kind, seed=8)
+    _, z = layers.linear_forward(x, w, b, activation=act, keep=True)
+    if z is not None:
+        z[1, 4] = 2.0  # slope over 0
+    grad[1, 4] = -torch.inf
+    w[4, 3] = x[1, 3] = 1.0
+    dx, dw, db = layers.linear_backward(x, w, grad, activation=act, z=z, need_bias=True)
+    assert torch.equal(dx[1], -torch.inf * w[4].sign()) and torch.equal(dw[4], -torch.inf * x[1].sign()) and db[4] == -torch.inf
+    for t, i in ((dx, 1), (dw, 4), (db, 4)):
+        t[i] = 0
+        assert t.isfinite().all()
