@@ -612,6 +612,7 @@ gm_status forward(LinearCall& c, LinearEnd e, void* y, int64_t y_ld) {
   g.k_blocks = static_cast<int>(div_up(c.p.dim, 64));
   g.k_per_split = static_cast<int>(div_up(g.k_blocks, p.t.splits));
   g.splits = static_cast<int>(div_up(g.k_blocks, g.k_per_split));
+  g.chunk = kChunk;
   g.group = group_of_tiles(g.m_tiles, 128 * p.t.cg, c.p.dim, g.planes);
   g.status = c.status;
   g.lost = p.a.at<uint8_t>(p.o_lost);
@@ -781,6 +782,8 @@ gm_status backward(LinearCall& c, const LinearGrads& q) {
     g.k_blocks = static_cast<int>(t.k_blocks);
     g.k_per_split = static_cast<int>(div_up(t.k_blocks, t.splits));
     g.splits = static_cast<int>(t.splits);
+    g.chunk = kChunk;
+    g.parts = true;
     g.group = 1;
     g.status = c.status;
     g.lost = lost;

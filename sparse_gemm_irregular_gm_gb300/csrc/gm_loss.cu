@@ -591,10 +591,6 @@ struct TeacherPlan {
   }
 };
 
-// Stages (64 elements each) of a row of Z summed in TMEM at a time: 1024 elements leave an error
-// under 4e-7 of the row's log-sum; summing every stage apart would read TMEM 16 times as often.
-constexpr int kChunk = 16;
-
 void set_logits_args(ProdArgs& g, const Call& c, const Arena& a, const TeacherPlan& t) {
   g.tgt = targets_of(c);
   g.status = c.status;

@@ -41,31 +41,34 @@ constexpr int kBK = 64;  // summed elements a stage: one 128-byte swizzled row
 //   kWhole: in TMEM from the first stage to the last. The tensor cores cut each sum to
 //     24 bits instead of rounding it, so the error grows with the number of stages: 3.3e-7
 //     of a row's log-sum at dim 1024, 1.6e-6 at 4096 (the fp32 form: 4e-8).
-//   kParts: in TMEM over `chunk` stages, the parts added in registers, rounded: for logits of
+//   kParts: in TMEM over `chunk` stages, the parts added in registers, rounded: for the layers' products, and for logits of
 //     long rows, whose error goes into the losses as it is.
 //   kSplit: fp32 operands as three bf16 planes a stage, six products of planes a stage, in TMEM
 //     over one stage, the stages added in registers.
 //   kSplitWhole: the same, but in TMEM to the end: logits of at most two stages.
 //   kTwo: 16-bit operands, but G in two planes: gradients of few rows (see g_planes).
-enum { kWhole = 0, kParts = 1, kSplit = 2, kSplitWhole = 3, kTwo = 4 };
+//   kTwoParts: the same, in TMEM over `chunk` stages.
+enum { kWhole = 0, kParts = 1, kSplit = 2, kSplitWhole = 3, kTwo = 4, kTwoParts = 5 };
 constexpr int kWholeBlocks = 2;
 template <int ACC>
 constexpr bool three_planes = ACC == kSplit || ACC == kSplitWhole;
 template <int ACC>
-constexpr int kPlanesA = three_planes<ACC> ? 3 : ACC == kTwo ? 2 : 1;
+constexpr bool two_planes = ACC == kTwo || ACC == kTwoParts;
+template <int ACC>
+constexpr int kPlanesA = three_planes<ACC> ? 3 : two_planes<ACC> ? 2 : 1;
 template <int ACC>
 constexpr int kPlanesB = three_planes<ACC> ? 3 : 1;
 template <int ACC>
 constexpr int kPairs = three_planes<ACC> ? 6 : kPlanesA<ACC>;  // products of planes a stage
 template <int ACC>
-constexpr bool in_registers = ACC == kParts || ACC == kSplit;
+constexpr bool in_registers = ACC == kParts || ACC == kSplit || ACC == kTwoParts;
 
 // Products of planes of split operands (x = x0 + x1 + x2 by falling size), the small ones
 // first, so that they meet a small accumulator; x1 y2, x2 y1 and x2 y2 lie under 2^-24
 // of x y and are left out.
 template <int ACC>
 __device__ __forceinline__ constexpr int pair_a(int p) {
-  return ACC == kTwo ? 1 - p : !three_planes<ACC> ? 0 : p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 1 : 0;
+  return two_planes<ACC> ? 1 - p : !three_planes<ACC> ? 0 : p == 0 ? 2 : p == 1 ? 0 : p == 2 ? 1 : p == 3 ? 1 : 0;
 }
 template <int ACC>
 __device__ __forceinline__ constexpr int pair_b(int p) {
@@ -1054,39 +1057,41 @@ cudaError_t launch_logits(int cg, const ProdMaps& maps, const ProdArgs& a, int n
                  : launch_modes<KIND, 1, 256, kWhole>(maps, a, num_sms, s);
 }
 
+template <Prod KIND, int ACC, bool PAIRS>
+cudaError_t launch_tile(int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
+  if constexpr (PAIRS) {
+    if (bn == 256 && cg == 2) return launch_one<KIND, 2, 256, false, false, ACC>(maps, a, num_sms, s);
+  }
+  return bn == 256   ? launch_one<KIND, 1, 256, false, false, ACC>(maps, a, num_sms, s)
+         : bn == 128 ? launch_one<KIND, 1, 128, false, false, ACC>(maps, a, num_sms, s)
+                     : launch_one<KIND, 1, 64, false, false, ACC>(maps, a, num_sms, s);
+}
+// Three planes: no room for two stages of one block's 256 columns.
+template <Prod KIND, int ACC>
+cudaError_t launch_split(int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
+  return cg == 2     ? launch_one<KIND, 2, 256, false, false, ACC>(maps, a, num_sms, s)
+         : bn == 128 ? launch_one<KIND, 1, 128, false, false, ACC>(maps, a, num_sms, s)
+                     : launch_one<KIND, 1, 64, false, false, ACC>(maps, a, num_sms, s);
+}
+
 template <Prod KIND>
 cudaError_t launch_sums(int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
-  if (a.planes == 3)
-    return cg == 2     ? launch_one<KIND, 2, 256, false, false, kSplit>(maps, a, num_sms, s)
-           : bn == 128 ? launch_one<KIND, 1, 128, false, false, kSplit>(maps, a, num_sms, s)
-                       : launch_one<KIND, 1, 64, false, false, kSplit>(maps, a, num_sms, s);
-  if (a.g_planes == 2)
-    return bn == 128  ? launch_one<KIND, 1, 128, false, false, kTwo>(maps, a, num_sms, s)
-           : bn == 64 ? launch_one<KIND, 1, 64, false, false, kTwo>(maps, a, num_sms, s)
-           : KIND == Prod::kDw && cg == 2 ? launch_one<Prod::kDw, 2, 256, false, false, kTwo>(maps, a, num_sms, s)
-                                          : launch_one<KIND, 1, 256, false, false, kTwo>(maps, a, num_sms, s);
-  if (bn == 256) {
-    if (cg == 1) return launch_one<KIND, 1, 256, false, false, kWhole>(maps, a, num_sms, s);
-    return launch_one<KIND, 2, 256, false, false, kWhole>(maps, a, num_sms, s);
+  const bool parts = a.parts && a.chunk < a.k_per_split;
+  if (a.planes == 3) return launch_split<KIND, kSplit>(cg, bn, maps, a, num_sms, s);
+  if (a.g_planes == 2) {  // at most 128 rows: one block's of dH, two stages of dW's sums
+    if constexpr (KIND == Prod::kDh) {
+      if (parts) return launch_tile<KIND, kTwoParts, false>(cg, bn, maps, a, num_sms, s);
+    }
+    return launch_tile<KIND, kTwo, KIND == Prod::kDw>(cg, bn, maps, a, num_sms, s);
   }
-  return bn == 128 ? launch_one<KIND, 1, 128, false, false, kWhole>(maps, a, num_sms, s)
-                   : launch_one<KIND, 1, 64, false, false, kWhole>(maps, a, num_sms, s);
+  return parts ? launch_tile<KIND, kParts, true>(cg, bn, maps, a, num_sms, s) : launch_tile<KIND, kWhole, true>(cg, bn, maps, a, num_sms, s);
 }
 
 cudaError_t launch_linear(int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms, cudaStream_t s) {
   constexpr Prod K = Prod::kLinear;
-  if (a.planes == 3 && a.k_blocks <= kWholeBlocks)
-    return cg == 2     ? launch_one<K, 2, 256, false, false, kSplitWhole>(maps, a, num_sms, s)
-           : bn == 128 ? launch_one<K, 1, 128, false, false, kSplitWhole>(maps, a, num_sms, s)
-                       : launch_one<K, 1, 64, false, false, kSplitWhole>(maps, a, num_sms, s);
-  if (a.planes == 3)
-    return cg == 2     ? launch_one<K, 2, 256, false, false, kSplit>(maps, a, num_sms, s)
-           : bn == 128 ? launch_one<K, 1, 128, false, false, kSplit>(maps, a, num_sms, s)
-                       : launch_one<K, 1, 64, false, false, kSplit>(maps, a, num_sms, s);
-  return cg == 2     ? launch_one<K, 2, 256, false, false, kWhole>(maps, a, num_sms, s)
-         : bn == 256 ? launch_one<K, 1, 256, false, false, kWhole>(maps, a, num_sms, s)
-         : bn == 128 ? launch_one<K, 1, 128, false, false, kWhole>(maps, a, num_sms, s)
-                     : launch_one<K, 1, 64, false, false, kWhole>(maps, a, num_sms, s);
+  if (a.planes == 3 && a.k_blocks <= kWholeBlocks) return launch_split<K, kSplitWhole>(cg, bn, maps, a, num_sms, s);
+  if (a.planes == 3) return launch_split<K, kSplit>(cg, bn, maps, a, num_sms, s);
+  return a.chunk < a.k_per_split ? launch_tile<K, kParts, true>(cg, bn, maps, a, num_sms, s) : launch_tile<K, kWhole, true>(cg, bn, maps, a, num_sms, s);
 }
 
 }  // namespace

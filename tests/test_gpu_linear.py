@@ -412,3 +412,50 @@ def test_an_infinite_gradient_gives_infinities(kind, rows, act):
     for t, i in ((dx, 1), (dw, 4), (db, 4)):
         t[i] = 0
         assert t.isfinite().all()
+
+
+# Sums of 16-bit operands: up to 1024 elements are added 16 at a time, each addition cut to 24 bits, off by 2^-23 of the sum
+# so far at most, two such additions where dz has two planes; the parts are added in fp32.
+def long_sum_room(length, size, planes=1):
+    return (planes * 64 * 2.0 ** -23 + (length / 1024 + 17) * 2.0 ** -24) * size
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,dim,outs", [(4096, 16384, 2560), (300, 65536, 520), (24, 262144, 64), (2, 1 << 20, 40)])
+def test_long_rows_of_one_sign(kind, rows, dim, outs):
+    """The residual takes z away but for its last digits, so that y shows the sum's own error, not its rounding."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x = torch.rand(rows, dim, device="cuda", generator=g).add_(0.5).to(TYPES[kind])
+    w = torch.rand(outs, dim, device="cuda", generator=g).add_(0.5).div_(dim).to(TYPES[kind])
+    z = torch.cat([x[i:i + 256].double() @ w.double().T for i in range(0, rows, 256)])
+    r = -z.to(TYPES[kind])
+    y, _ = layers.linear_forward(x, w, residual=r)
+    check(y, wide_of(z + r), long_sum_room(dim, wide_of(z)), kind)
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("rows,dim,outs", [(4096, 2560, 65536), (128, 20480, 65536)])
+def test_long_sums_of_gradients_by_x(rows, dim, outs, act):
+    """The second half takes away what the first one gave: what is left is the sum's own error."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    half = outs // 2
+    w = torch.rand(half, dim, device="cuda", generator=g).half().repeat(2, 1)
+    grad = torch.rand(rows, half, device="cuda", generator=g).half()
+    grad = torch.cat([grad, -grad], 1)
+    x = torch.zeros(rows, dim, device="cuda").half()
+    z = None if act == "none" else torch.full_like(grad, 1.0)
+    dx, _, _ = layers.linear_backward(x, w, grad, activation=act, z=z, need_w=False)
+    size = 1.09 * grad.float().abs() @ w.float()  # gelu's slope at 1 is 1.083
+    planes = 2 if rows <= 128 and act != "none" else 1
+    check(dx, np.zeros((rows, dim)), long_sum_room(outs, wide_of(size), planes), "f16")
+
+
+def test_long_sums_of_gradients_by_w():
+    rows, dim, outs = 65536, 2560, 4096
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.rand(rows // 2, dim, device="cuda", generator=g).half().repeat(2, 1)
+    grad = torch.rand(rows // 2, outs, device="cuda", generator=g).half()
+    grad = torch.cat([grad, -grad])
+    w = torch.zeros(outs, dim, device="cuda").half()
+    _, dw, _ = layers.linear_backward(x, w, grad, need_x=False)
+    check(dw, np.zeros((outs, dim)), long_sum_room(rows, wide_of(grad.float().abs().T @ x.float())), "f16")
