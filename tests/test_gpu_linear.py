@@ -459,3 +459,24 @@ def test_long_sums_of_gradients_by_w():
     w = torch.zeros(outs, dim, device="cuda").half()
     _, dw, _ = layers.linear_backward(x, w, grad, need_x=False)
     check(dw, np.zeros((outs, dim)), long_sum_room(rows, wide_of(grad.float().abs().T @ x.float())), "f16")
+
+
+@pytest.mark.parametrize("kind,least", [("bf16", 2.0 ** -120), ("f16", 2.0 ** -24)])
+@pytest.mark.parametrize("act,far", [("gelu", 12.5), ("gelu_tanh", 9.5), ("silu", 80.0)])
+@pytest.mark.parametrize("rows", [1, 150])
+def test_tails_of_activations_are_rounded_once(kind, least, act, far, rows):
+    """An activation is within 2^-15 of itself before it is rounded (its form, and roundings of an exponent up to 2^7)."""
+    z = -torch.linspace(0.05, far, 5000, device="cuda").to(TYPES[kind])
+    x = torch.ones(rows, 1, device="cuda").to(TYPES[kind])
+    y, _ = layers.linear_forward(x, z[:, None].contiguous(), activation=act)  # z as it is: one term
+    v = wide_of(z)
+    if act == "gelu":
+        ref = np.array([t * 0.5 * math.erfc(-t / math.sqrt(2)) for t in v])
+    elif act == "silu":
+        ref = v / (1 + np.exp(-v))
+    else:
+        ref = v / (1 + np.exp(-2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))
+    got = wide_of(y)
+    room = np.abs(ref) * (HALF[kind] * 1.01 + 2.0 ** -15) + least / 2
+    bad = ~(np.abs(got - ref) <= room)
+    assert not bad.any(), (int(bad.sum()), v[np.argwhere(bad)[:5, 1]], got[bad][:5], ref[np.argwhere(bad)[:5, 1]])
