@@ -85,8 +85,10 @@ __device__ __forceinline__ void set_four(void* p, int64_t i, int type, bool wide
 // y and z from the parts of X W^T, a thread four columns: 512 x 4096 in two parts, 25 MB, 6 us; an element a thread, found by a
 // division of 64 bits, took 14. Parts are made of so few tiles that 32 bits count the fours.
 __global__ void __launch_bounds__(256) k_linear_join(const float* __restrict__ acc, int splits, int64_t rows, int64_t outs,
-                                                     int64_t acc_ld, const LinearEnd e, void* y, int64_t y_ld, int type, bool wide) {
+                                                     int64_t acc_ld, const LinearEnd e, void* y, int64_t y_ld, int type, bool wide,
+                                                     const uint8_t* __restrict__ lost) {
   chain_wait();
+  const bool gone = __any_sync(kFull, lost_word(lost) != 0);  // parts that were never written: NaN, not what lies there
   const uint32_t a_row = static_cast<uint32_t>(acc_ld / 4), n = static_cast<uint32_t>(rows) * a_row, stride = gridDim.x * blockDim.x;
   for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
     const int64_t r = i / a_row, c = int64_t(i - static_cast<uint32_t>(r) * a_row) * 4;
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const float* __restrict__ a
       const float4 x = *reinterpret_cast<const float4*>(p + s * rows * acc_ld);  // columns from outs on are not written: not used
       v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
     }
+    if (gone) v[0] = v[1] = v[2] = v[3] = NAN;
     if (e.bias) {
       get_four(e.bias, c, type, wide, have, t);
 #pragma unroll
@@ -639,7 +642,7 @@ gm_status forward(LinearCall& c, LinearEnd e, void* y, int64_t y_ld) {
     auto four = [&](const void* q, int64_t ld) { return !q || (aligned(q, 4 * es) && (m <= 1 || ld % 4 == 0)); };
     const bool wide = n % 4 == 0 && four(y, y_ld) && four(e.keep ? e.z : nullptr, e.z_ld) && four(e.residual, e.residual_ld) && four(e.bias, 0);
     ok = launch_chained(k_linear_join, grid_for(m * (p.acc_ld / 4), 256), 256, 0, c.s, 1, static_cast<const float*>(acc), g.splits, m, n,
-                        p.acc_ld, e, y, y_ld, static_cast<int>(c.p.type), wide) == cudaSuccess;
+                        p.acc_ld, e, y, y_ld, static_cast<int>(c.p.type), wide, static_cast<const uint8_t*>(g.lost)) == cudaSuccess;
   }
   return finish(ok);
 }

@@ -229,13 +229,6 @@ __global__ void __launch_bounds__(32 * kTeacherWarps, 2) k_teacher(const Teacher
   }
 }
 
-// This lane's part of a call's `lost` (gm_loss_prod.cu): not 0 where a product gave up. A warp that writes
-// results reads all of it, early, and asks once it has its sums. lost null: kernels that wait for nothing.
-__device__ __forceinline__ uint64_t lost_word(const uint8_t* lost) {
-  static_assert(kMostBlocks == 8 * 32, "a word a lane");
-  return lost ? reinterpret_cast<const uint64_t*>(lost)[threadIdx.x & 31] : 0;
-}
-
 // ---- joining the half tiles of a row -----------------------------------------------------
 struct JoinArgs {
   float4* carry;  // [row]: the sums so far, of a piece that is not the last; null: results

@@ -224,6 +224,13 @@ int prod_grad_row_bytes(int planes, int chunk, int k_blocks);
 cudaError_t launch_prod(Prod kind, int cg, int bn, const ProdMaps& maps, const ProdArgs& a, int num_sms,
                         cudaStream_t s);
 
+// This lane's part of a call's `lost` (gm_loss_prod.cu): not 0 where a product gave up. A warp that writes
+// results reads all of it, early, and asks once it has its sums. lost null: kernels that wait for nothing.
+__device__ __forceinline__ uint64_t lost_word(const uint8_t* lost) {
+  static_assert(kMostBlocks == 8 * 32, "a word a lane");
+  return lost ? reinterpret_cast<const uint64_t*>(lost)[threadIdx.x & 31] : 0;
+}
+
 // ---- around the products (gm_loss.cu) ------------------------------------------------------
 // Report word of the current device; null when it cannot be had.
 int* loss_status_word();
