@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(1024) k_draw(const __grid_constant__ DrawArgs 
   Border border{kNonePlace<TYPE> - top - 1, INT64_MAX};
   uint32_t by_min = border.d;
   if (min_p > 0.f && temp > 0.f && top > kInfPlace<TYPE>) {
-    const Pair l = times(log_of(min_p, sh.table), temp, 0.f);
+    Pair l = times(log_of(min_p, sh.table), temp, 0.f);
+    if (!(l.x > -INFINITY)) l = Pair{-INFINITY, 0.f};  // T ln(min_p) past fp32, whose parts would be inf - inf: nothing falls short
     const uint32_t from = place_from<TYPE>(top_z, l.x, l.low);
     by_min = min(by_min, max(from, top) - top);
   } else if (min_p > 0.f) {

@@ -358,3 +358,17 @@ def test_results_that_are_missing_are_refused_and_the_others_left(missing):
     with pytest.raises(ValueError):
         sampling.gm_draw(torch.zeros(6, 50, device="cuda"), torch.zeros(6, device="cuda"), *given)
     assert all((t == 9).all() for t in out)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("classes", [100, 20000])
+@pytest.mark.parametrize("temperature", [1e30, 5e37, 3.4e38])
+@pytest.mark.parametrize("min_p", [0.999, 0.5, 1e-10, 1e-44])
+def test_temperatures_near_the_end_of_the_range(kind, classes, temperature, min_p):
+    """All weights are 1 but for 1e-28 of them, whatever T ln(min_p) comes to."""
+    z, u = make(3, classes, kind, seed=2)
+    alive = (z > -torch.inf).sum(1)
+    for rule in (dict(), dict(top_k=classes), dict(top_p=1.0)):
+        d = sampling.draw(z, u, temperature=temperature, min_p=min_p, **rule)
+        assert torch.equal(d.kept.long(), alive)
+        assert (d.logprob + alive.float().log()).abs().max() <= 1e-6 * math.log(classes)
