@@ -11,6 +11,7 @@
 #include <stdexcept>
 #include <string>
 #include <tuple>
+#include <type_traits>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
@@ -154,6 +155,11 @@ std::tuple<int, Opt, Opt, Opt> linear_backward(const Tensor& x, const Tensor& w,
   return {rc, dx, dw, db};
 }
 
+// A number that 32 bits would take to 0 means something else than 0 does.
+void still_a_number(const char* name, double v) {
+  if (v != 0 && static_cast<float>(v) == 0) refuse(name, " is ", v, ": 0 in 32 bits");
+}
+
 // ---- norms around a residual -----------------------------------------------------------------
 struct Rule {
   int norm;
@@ -168,6 +174,7 @@ gm_norm norm_of(const Tensor& x, const Opt& f, const Rule& r) {
   if (dim < 1) refuse("x must have rows of an element at least");
   if (!f && (r.after || r.after_bias || r.gate)) refuse("after, after_bias and gate belong to f, which is None");
   if ((!r.after && r.after_bias) || (!r.before && r.before_bias)) refuse("a bias needs its norm's weight");
+  still_a_number("eps", r.eps);
   const Matrix mf = matrix("f", f, &x, n, dim);
   int kind = GM_GATE_NONE;
   Matrix g;
@@ -254,6 +261,7 @@ void value_of(const char* name, const pybind11::object& v, int64_t n, const Tens
   }
   try {
     *all = v.cast<T>();
+    if (std::is_floating_point_v<T>) still_a_number(name, v.cast<double>());
   } catch (const pybind11::cast_error&) {
     refuse(name, type == at::kInt ? " must be a whole number of 32 bits" : " must be a number", ", or a tensor of one a row");
   }

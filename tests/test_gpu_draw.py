@@ -372,3 +372,12 @@ def test_temperatures_near_the_end_of_the_range(kind, classes, temperature, min_
         d = sampling.draw(z, u, temperature=temperature, min_p=min_p, **rule)
         assert torch.equal(d.kept.long(), alive)
         assert (d.logprob + alive.float().log()).abs().max() <= 1e-6 * math.log(classes)
+
+
+@pytest.mark.parametrize("name,value", [("temperature", 1e-46), ("temperature", 1e-300), ("top_p", 1e-46), ("min_p", 1e-60)])
+def test_numbers_that_32_bits_take_to_zero_are_refused(name, value):
+    """Else a temperature over 0 would take the first of equal logits always, and a min-p be off."""
+    z, u = make(2, 50, "f32")
+    with pytest.raises(ValueError, match=name):
+        sampling.draw(z, u, **{name: value})
+    sampling.draw(z, u, **{name: 0.0})

@@ -321,3 +321,10 @@ def test_long_rows_in_every_form(rows, dim, kind, norm, gate):
 @pytest.mark.parametrize("dim", [8190, 8200])
 def test_strides_of_long_rows(kind, wide, offset, dim):
     test_strides(kind, wide, offset, dim)
+
+
+def test_an_eps_that_32_bits_take_to_zero_is_refused():
+    x, before = torch.zeros(2, 16, device="cuda"), torch.ones(16, device="cuda")
+    with pytest.raises(ValueError, match="eps"):
+        layers.residual_norm_forward(x, before=before, eps=1e-46)
+    assert (layers.residual_norm_forward(x, before=before, eps=2e-45).y == 0).all()
