@@ -480,3 +480,14 @@ def test_tails_of_activations_are_rounded_once(kind, least, act, far, rows):
     room = np.abs(ref) * (HALF[kind] * 1.01 + 2.0 ** -15) + least / 2
     bad = ~(np.abs(got - ref) <= room)
     assert not bad.any(), (int(bad.sum()), v[np.argwhere(bad)[:5, 1]], got[bad][:5], ref[np.argwhere(bad)[:5, 1]])
+
+
+# Sums longer than 1024 elements on every tile that the rule takes for them, in one part and in several; a, b: rows and columns
+# of a result, n: the length of its sums.
+@pytest.mark.parametrize("act,kind", [("none", "bf16"), ("silu", "f16")])
+@pytest.mark.parametrize("role", ["y", "dx", "dw"])
+@pytest.mark.parametrize("a,n,b", [(24, 1100, 64), (24, 5000, 4100), (24, 1100, 20000), (300, 1100, 4100), (520, 1100, 4100), (1024, 5000, 264),
+                                   (200, 5000, 1100)])
+def test_sums_in_parts_on_every_tile(act, kind, role, a, n, b):
+    rows, dim, outs = {"y": (a, n, b), "dx": (a, b, n), "dw": (n, b, a)}[role]
+    both(*make(rows, dim, outs, kind, seed=n), act, kind)
