@@ -30,8 +30,9 @@
  *   - Every call returns a gm_status; nothing is thrown across the ABI.
  *   - One row, or up to 8 of f32, of dim up to 4096: fp32 arithmetic throughout, G too.
  *     Others: products on the tensor cores with fp32 sums, which are cut, not rounded,
- *     to 24 bits for up to 1024 elements at a time; bf16 and f16 operands as they are, f32
- *     operands as three bf16 parts each. Before the gradient products G is rounded to
+ *     to 24 bits: Z's for up to 1024 elements at a time, those of dH and dW of 16-bit operands over
+ *     all the classes or rows of a piece; bf16 and f16 operands as they are, f32
+ *     operands as three bf16 parts each, 64 elements at a time. Before the gradient products G is rounded to
  *     the operands' 16-bit type; with at most 128 rows the remainder is kept beside it in that
  *     type, and f32's G is three bf16 parts. Maxima, sums of exponentials and losses
  *     are fp32; dH and dW are rounded once, from fp32 sums. The results do not depend

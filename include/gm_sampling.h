@@ -12,8 +12,9 @@
  *   times the sum of all kept w.
  * A logit of -inf is never kept. Where the largest is +inf, w is 1 there and 0 elsewhere. T = 0 keeps the largest alone.
  *
- * The weights are within 2^-29 of w relatively (or 2^-40 of the largest, up to 2^22 classes) and are summed exactly, as
- * 64-bit integers: a border between two classes is met to about nine digits, and results do not depend on the launch.
+ * The weights are within 2^-28 of w relatively (or 2^-40 of the largest, up to 2^22 classes) and are summed exactly, as
+ * 64-bit integers: a border between two classes is met to more than eight digits, and results do not depend on the launch.
+ * z_j - max z is formed in fp32: a difference past 3.4e38 counts as infinite.
  */
 #ifndef GM_SAMPLING_H
 #define GM_SAMPLING_H

@@ -13,9 +13,10 @@
 //   Others: a histogram of D's upper 11 bits shows the digit in which the border lies, one of the next
 //   11 bits within that digit its next, until D is known.
 //
-// Bound by the shared memory's operations and the barriers between steps, far from memory's rate: 256 x 131072 bf16 with top-p
-// 100 us (67 MB; plain 8240), of a row's clocks 36 % reading and counting, 19 % the search, 25 % the sums; 1 x 131072 with
-// all four rules 15 us back to back, 19 alone.
+// Bound by latency, far from memory's rate: with counts an SM has one row, whose warps wait for shared memory and at barriers
+// with nothing beside them (LSU 26 % busy, DRAM 7 %, 43 % of the warps). 256 x 131072 bf16 with top-p 101 us (67 MB; plain 8240),
+// of a row's clocks 36 % reading and counting, 19 % the search, 25 % the sums; 1 x 131072 with all four rules 15 us back to
+// back, 19 alone.
 //
 // Weights are integers: w = 2^(t), t = (z - max) log2(e) / T <= 0, as a multiple of 2^-B with B such that all of a row
 // add up in 64 bits. So sums are exact, in any order, and every pass sees the same ones.
@@ -125,7 +126,7 @@ __device__ __forceinline__ u64 whole_times(float f, u64 n, bool& left) {
 }
 
 // ---- weights ---------------------------------------------------------------------------------------
-// 2^(31 + f / 2^31) for f in [-2^30, 2^30], to about 2^-29 of itself: the nearest 32nd of f's range, whose power
+// 2^(31 + f / 2^31) for f in [-2^30, 2^30], to 2^-28 of itself: the nearest 32nd of f's range, whose power
 // is in a table of 32-bit integers, and a rest g with |g| <= 1/64, whose 2^g - 1 = g ln 2 + (g ln 2)^2 / 2 + ... is at
 // most 0.011, so that fp32 gives it to 2^-31. Exact at 0.
 // 2^(31 + (j - 16) / 32), rounded
@@ -181,7 +182,7 @@ __device__ __forceinline__ Pair times(Pair a, float x, float x_low) {
   return sum_of(p, fmaf(a.x, x, -p) + fmaf(a.x, x_low, a.low * x));
 }
 constexpr float kLn2 = 0.693147180559945f, kLn2Low = -1.9046543e-9f;
-// ln(m / 2^31 * 2^e) for m in [2^31, 2^32), to about 2^-29: log2f, put right by how far its power is from m.
+// ln(m / 2^31 * 2^e) for m in [2^31, 2^32), to about 2^-28: log2f, put right by how far its power is from m.
 __device__ __forceinline__ Pair log_of(uint32_t m, int e, const uint32_t* table) {
   const float y = log2f(static_cast<float>(m) * 4.656612873077393e-10f);  // 2^-31; in [0, 1]
   const float whole = rintf(y);

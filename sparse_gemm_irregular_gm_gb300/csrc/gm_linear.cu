@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kLayThreads) k_operands(const Lays l) {
 // dz = grad * act'(z), as an operand of the two products: 16 bits, with few rows a second plane of what rounding took; three
 // bf16 planes of f32. Sums of its columns over the block's rows, in fp32, go to sums[part]. A warp takes 256 columns of
 // a row, a thread 8 of them. The blocks after these lay out X and W. Bound by memory and by gelu's slope together: 8192 x 4096 bf16,
-// 201 MB, 37 us, 5.4 TB/s or 80 % of what a copy reaches (42 with all rows of a turn asked for before any is worked on).
+// 201 MB, 41 us, 4.9 TB/s or 72 % of what a copy reaches (5 longer with all rows of a turn asked for before any is worked on).
 struct DzArgs {
   const void *grad, *z;  // z null: dz is grad
   int64_t grad_ld, z_ld, rows, outs, rows_a_block;
@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(32 * kDzWarps, 3) k_dz(const DzArgs a, const L
 // ---- few rows ------------------------------------------------------------------------------------
 // One row of X, or up to 4 of f32 (whose tensor-core form reads and writes W four times more): a warp reads OUTS rows of W together, 16
 // bytes a lane (VEC; else single elements), eight such loads under way, and multiplies in fp32. Bound by the bytes of W
-// and, with 2^24 of them, by the launch: 1 x 4096 x 4096 bf16 11 us from memory, 3 TB/s (21 on the tensor cores); four rows of
-// f32 65 (five on the tensor cores: 85). Two rows of 16 bits are faster on the tensor cores (1024 x 32768: 36 us here, 26 there).
+// and, with 2^24 of them, by the launch: 1 x 4096 x 4096 bf16 11 us from memory, 3 TB/s (21 on the tensor cores); 1024 x 32768
+// f32, 134 MB: one row 34, two 40, four 56 (five, on the tensor cores, 124). Two rows of 16 bits are faster on the tensor cores
+// (1024 x 32768: 36 us here, 26 there).
 constexpr int kFewWarps = 8;
 template <bool F32, bool VEC, int ROWS, int OUTS>
 __global__ void __launch_bounds__(32 * kFewWarps, ROWS == 1 ? 3 : 2) k_linear_few(const gm_linear p, const LinearEnd e, void* y, int64_t y_ld) {
@@ -687,6 +688,8 @@ struct LinearBackward {
       : x(c.p.x, c.p.n_rows, c.p.dim, c.p.x_ld, c.p.type),
         w(c.p.w, c.p.n_outs, c.p.dim, c.p.w_ld, c.p.type),
         planes(c.planes()),
+        // Rounding dz costs digits (8192 x 1024 x 4096 bf16 gelu: gradients 2.4e-3 from 64 bits, 1.7e-3 without); a second plane doubles
+        // the products' time, 90 us of 188 there, but none where they wait for W and dW
         dz_planes(planes == 3 ? 3 : c.p.activation != GM_ACT_NONE && c.p.n_rows <= 128 ? 2 : 1),
         dx(a, c.p.n_rows, c.p.dim, c.p.n_outs, planes, c.sms, dz_planes != 2),  // no pairs of blocks for two planes of dz
         dw(a, c.p.n_outs, c.p.dim, c.p.n_rows, planes, c.sms, dz_planes != 2) {

@@ -123,3 +123,28 @@ def test_a_copied_module_of_parameters_trains():
     for k in ("down", "after", "table", "first"):
         assert torch.equal(q[k].grad, ref[k]) or (q[k].grad.double() - ref[k].double()).norm() <= 1e-6 * ref[k].double().norm(), k
     assert q["up"].grad is None and q["gate"].grad is None
+
+
+def test_gradients_of_leaves_in_a_graph():
+    """backward() captured with no eager graph of the leaves alive: each replay writes their gradients."""
+    p, x, target = weights(torch.bfloat16)
+    p = {k: v.requires_grad_() for k, v in p.items()}
+
+    def step():
+        _, h = block(p, x)
+        losses.cross_entropy(h, p["table"], target)[0].sum().backward()
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    ref = {k: v.grad.clone() for k, v in p.items() if v.grad is not None}
+    for v in p.values():
+        v.grad = None
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(2):
+        g.replay()
+        assert ref and all(torch.equal(p[k].grad, r) for k, r in ref.items())
