@@ -180,3 +180,11 @@ def test_oracle_of_the_activations_against_differences(act):
     a, s = layer_oracle.act(z, act)
     up, down = layer_oracle.act(z + 1e-6, act)[0], layer_oracle.act(z - 1e-6, act)[0]
     assert np.allclose((up - down) / 2e-6, s, atol=1e-8)
+
+
+def test_every_struct_of_the_header_is_bound():
+    src = open(os.path.join(ROOT, "include", "gm_layers.h")).read()
+    names = re.findall(r"^typedef struct (gm_\w+) \{", src, flags=re.M)
+    assert len(names) == 4
+    for n in names:
+        assert issubclass(getattr(layers, n), ctypes.Structure)
